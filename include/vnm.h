@@ -66,7 +66,13 @@ typedef enum vnm_status {
     VNM_ERR_INTERNAL = 6     /* a kernel found an inconsistent internal state */
 } vnm_status;
 
-typedef enum vnm_dtype { VNM_F16 = 0, VNM_F32 = 1 } vnm_dtype;
+/* VNM_BF16 is a type of the norm, the 8-bit quantiser and the 8-bit Linear
+ * layer only; the V:N:M and bitmap entry points take VNM_F16 and VNM_F32. */
+typedef enum vnm_dtype { VNM_F16 = 0, VNM_F32 = 1, VNM_BF16 = 2 } vnm_dtype;
+
+/* 8-bit floating-point formats: e4m3 (no infinities, largest value 448) and
+ * e5m2 (largest finite value 57344). */
+typedef enum vnm_fp8 { VNM_E4M3 = 0, VNM_E5M2 = 1 } vnm_fp8;
 
 /* Which kernel family serves an SpMM. */
 typedef enum vnm_path {
@@ -390,6 +396,111 @@ vnm_status vnm_spmm_with_plan(vnm_matrix A, const vnm_spmm_plan* plan, const voi
 vnm_status vnm_spmm_noalloc(int64_t R, int64_t K, int32_t V, int32_t M, const void* values, const void* meta,
                             const void* colidx, const void* B, int64_t ld_b, int64_t N, void* C, int64_t ld_c,
                             vnm_dtype c_type, int32_t* status, vnm_stream_t stream);
+
+/* ---- the dense neighbours of a pruned layer: norm, 8-bit form, 8-bit Linear layer ----
+ *
+ * Block-scaled 8-bit form of a matrix: fp8 values q (row-major, one byte an
+ * element) and fp32 scales s, one for each group of 128 consecutive columns
+ * of a row (1 x 128, activations and gradients) or for each 128 x 128 block
+ * (weights); the last group or block of an edge is shorter. An element stands
+ * for q * s. For a group with largest magnitude m:
+ *   s = max(m / F, 2^-100), F = 448 (e4m3) or 57344 (e5m2),
+ *   q = the nearest fp8 value to y * (1 / s) (ties to even, saturating);
+ * a group that holds an Inf or a NaN gets s = NaN and q = NaN throughout.
+ * Scales are addressed with two strides in elements: the scale of row (or row
+ * block) i and column group g is s[i * s_rs + g * s_cs].
+ * These entry points run on the current device and take no handle.
+ */
+
+/*
+ * RMS norm of T rows of D features, with the residual's addition and an
+ * output in 8 bits:
+ *   h = x + residual      (added in fp32, rounded once to `type`)
+ *   rstd = 1 / sqrt(mean over the row of h^2 + eps)      (fp32)
+ *   y = h * rstd * weight                                (fp32)
+ * with h as rounded (what is stored is what is normalised). Outputs, each
+ * NULL when not wanted (but y or q is): h (T x D, type; needs residual), y
+ * (T x D, rounded once to type), rstd (fp32 [T], for the backward pass), and q
+ * with q_scale: the unrounded y in the block-scaled 8-bit form, groups of
+ * 1 x 128 (q_scale is needed with q). weight: [D] of type, NULL for all ones.
+ * x, residual, h, y share `type` (VNM_F16, VNM_BF16 or VNM_F32) and are
+ * row-major with leading dimensions ld_* >= D; ld_* of a NULL matrix is
+ * ignored. Any alignment of the type; 16-byte aligned rows run faster.
+ * h may be x or residual themselves, and so may y where h is not (same pointer
+ * and leading dimension); no other overlap.
+ * A NaN in a row makes its y, rstd and groups NaN. eps >= 0.
+ * Errors: VNM_ERR_INVALID_ARG (pointers, alignment, leading dimensions, types,
+ * eps, h without residual, neither y nor q), VNM_ERR_CUDA.
+ */
+vnm_status vnm_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual, const void* weight,
+                       float eps, int64_t T, int64_t D, vnm_dtype type, void* h, int64_t ld_h, void* y, int64_t ld_y,
+                       float* rstd, void* q, int64_t ld_q, vnm_fp8 q_type, float* q_scale, int64_t s_rs, int64_t s_cs,
+                       vnm_stream_t stream);
+
+/*
+ * Backward pass of vnm_rmsnorm. dy: gradient of y; h: the normalised sum (x
+ * itself without a residual); rstd as the forward pass wrote it; dresidual:
+ * the gradient that reaches h past the norm (NULL for none). With g = dy * weight:
+ *   dh = dresidual + rstd * (g - h * rstd^2 * mean over the row of g * h)
+ * which is the gradient of x and of residual alike (T x D, type), and
+ *   dweight[d] = sum over the rows of dy * h * rstd      (fp32 [D])
+ * Either output may be NULL. dh may be dy or dresidual (same pointer and
+ * leading dimension). Sums are fp32 and their order is fixed: the same inputs
+ * give the same bits. workspace: vnm_rmsnorm_backward_workspace_size bytes,
+ * 16-byte aligned (NULL when dweight is NULL). T = 0 writes dweight = 0.
+ * Errors: VNM_ERR_INVALID_ARG, VNM_ERR_CUDA.
+ */
+vnm_status vnm_rmsnorm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, const void* weight,
+                                const float* rstd, const void* dresidual, int64_t ld_dresidual, int64_t T, int64_t D,
+                                vnm_dtype type, void* dh, int64_t ld_dh, float* dweight, void* workspace,
+                                size_t workspace_bytes, vnm_stream_t stream);
+
+/* Bytes of workspace vnm_rmsnorm_backward needs for dweight (host only). */
+vnm_status vnm_rmsnorm_backward_workspace_size(int64_t T, int64_t D, size_t* bytes);
+
+/*
+ * The block-scaled 8-bit form of X (R x C, type, ld_x >= C), plain and/or
+ * transposed, in one pass over X.
+ *   block_rows = 1: q (R x C) has a scale for each 1 x 128 group, s is
+ *     R x ceil(C/128); qt (C x R) holds X^T in groups of 128 along R, st is
+ *     C x ceil(R/128): the two roundings are independent.
+ *   block_rows = 128: one scale for each 128 x 128 block, s is ceil(R/128) x
+ *     ceil(C/128); qt holds the same values transposed, st (ceil(C/128) x
+ *     ceil(R/128)) is s transposed.
+ * q with s, or qt with st, may be NULL (both of a pair together), not all
+ * four. Any alignment; 16-byte aligned rows run faster (and vnm_fp8_linear
+ * wants them).
+ * Errors: VNM_ERR_INVALID_ARG, VNM_ERR_CUDA.
+ */
+vnm_status vnm_fp8_quantize(const void* X, int64_t ld_x, int64_t R, int64_t C, vnm_dtype type, int32_t block_rows,
+                            vnm_fp8 q_type, void* q, int64_t ld_q, float* s, int64_t s_rs, int64_t s_cs, void* qt,
+                            int64_t ld_qt, float* st, int64_t st_rs, int64_t st_cs, vnm_stream_t stream);
+
+/*
+ * Dense Linear layer on block-scaled 8-bit operands:
+ *   Y[t][r] = act(sum over groups b of x_scale[t, b] * w_scale[r', b] *
+ *                 (sum over k in b of xq[t][k] * wq[r][k]) + bias[r])
+ * with r' = r for w_block_rows = 1 and r / 128 for 128. X: T x K with 1 x 128
+ * scales; W: R x K. All sums are fp32; Y (T x R, ld_y >= R; VNM_F16, VNM_BF16 or
+ * VNM_F32) is rounded once, bias ([R], bias_type, or NULL) and act are
+ * applied in fp32 before that. The gradients are products of the same form:
+ *   dX = dY . W:   X := dY (1 x 128 along R), W := W^T (vnm_fp8_quantize's qt, st);
+ *   dW = dY^T . X: X := dY^T, W := X^T (both qt, st with block_rows = 1).
+ * xq and wq: 16-byte aligned with ld % 16 == 0 (elements past K in the
+ * rows' padding are not used). The product of an x_scale and a w_scale has to
+ * be a finite fp32 number. The result does not depend on timing: no atomics.
+ * status: optional device pointer to 3 zeroed int32 words (first error code,
+ * detail, count): a bounded wait that runs out records VNM_ERR_TIMEOUT there
+ * (Y is then undefined); NULL: not recorded.
+ * T = 0 or R = 0 is a no-op; K = 0 gives act(bias).
+ * Errors: VNM_ERR_INVALID_ARG (pointers, alignment, leading dimensions, types,
+ * w_block_rows), VNM_ERR_CUDA.
+ */
+vnm_status vnm_fp8_linear(const void* xq, int64_t ld_x, vnm_fp8 x_type, const float* x_scale, int64_t xs_rs,
+                          int64_t xs_cs, const void* wq, int64_t ld_w, vnm_fp8 w_type, const float* w_scale,
+                          int64_t ws_rs, int64_t ws_cs, int32_t w_block_rows, int64_t T, int64_t R, int64_t K,
+                          const void* bias, vnm_dtype bias_type, vnm_activation act, void* Y, int64_t ld_y,
+                          vnm_dtype y_type, int32_t* status, vnm_stream_t stream);
 
 /*
  * Synchronise `stream`, then return and clear the first error any kernel

@@ -26,6 +26,21 @@ vnm_status vnm_testing_spmm_skip_stage(vnm_matrix A, const void* B, int64_t ld_b
                                        int64_t ld_c, vnm_dtype c_type, void* workspace, size_t workspace_bytes,
                                        int32_t skip_stage, vnm_stream_t stream);
 
+/*
+ * vnm_fp8_linear, except that the first CTA never issues the TMA loads of its
+ * pipeline stage number `skip_stage` (counted over the tiles it takes): its
+ * bounded waits run out after about 1 s, VNM_ERR_TIMEOUT goes to `status`
+ * (needed here), and Y is unspecified; the device stays usable.
+ * Errors: as vnm_fp8_linear, plus VNM_ERR_INVALID_ARG for skip_stage < 0 or no status.
+ */
+vnm_status vnm_testing_fp8_linear_skip_stage(const void* xq, int64_t ld_x, vnm_fp8 x_type, const float* x_scale,
+                                             int64_t xs_rs, int64_t xs_cs, const void* wq, int64_t ld_w,
+                                             vnm_fp8 w_type, const float* w_scale, int64_t ws_rs, int64_t ws_cs,
+                                             int32_t w_block_rows, int64_t T, int64_t R, int64_t K, const void* bias,
+                                             vnm_dtype bias_type, vnm_activation act, void* Y, int64_t ld_y,
+                                             vnm_dtype y_type, int32_t* status, int32_t skip_stage,
+                                             vnm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

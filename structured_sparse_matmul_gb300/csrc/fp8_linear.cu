@@ -1,0 +1,563 @@
+// Dense Linear layer on block-scaled 8-bit operands:
+//
+//   Y[t][r] = act(sum_b xs[t, b] ws[r', b] (sum_{k in b} xq[t][k] wq[r][k]) + bias[r])
+//
+// The inner sums are 8-bit tensor-core products of one K block of 128
+// (tcgen05.mma kind::f8f6f4, 4 MMAs of K = 32) into a TMEM buffer of their own;
+// the outer sum is formed in registers, where each element of the buffer is
+// scaled as it is added in fp32. So the MMAs of block b + 1 run while block b
+// is added up, and no scale ever has to be a power of two.
+//
+// The kernel sees P (128 rows a tile, the MMA's M side) times Q (BN rows a tile,
+// the N side): P = X, Q = W for many tokens, P = W, Q = X for few of them, where
+// the weights' rows then fill the tensor cores' rows and BN fits the tokens.
+// Few tiles split K over the CTAs of a cluster, which add their sums up through
+// distributed shared memory in rank order.
+//
+//   warp 0     TMA producer: a stage is 128 rows of P and BN rows of Q by 128
+//              bytes of K, 128B swizzle.
+//   warp 1     TMEM owner and MMA issuer (one thread).
+//   warp 2     the K block's scales, 128 of P and BN of Q, into a shared-memory
+//              ring by 4-byte cp.async (any strides).
+//   warps 3..  add up: thread = row of P; 4 warps, or 8 with half the columns each.
+// Every mbarrier wait is bounded.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "vnm_dense.h"
+#include "vnm_fp8.cuh"
+#include "vnm_internal.h"
+#include "vnm_ptx.cuh"
+
+namespace vnm {
+namespace {
+
+constexpr int kTileM = 128;
+constexpr int kMaxSplits = 8;
+constexpr int kMaxDevicesFl = 64;
+
+template <int BN>
+struct FlCfg {
+    static constexpr int kPBytes = kTileM * 128;
+    static constexpr int kQBytes = BN * 128;
+    static constexpr int kStageBytes = kPBytes + kQBytes;
+    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+    static constexpr int kAcc = BN == 256 ? 2 : 4;  // TMEM buffers
+    static constexpr int kTmemCols = kAcc * BN;
+    static constexpr int kAddWarps = BN >= 128 ? 8 : 4;
+    static constexpr int kCols = BN * 4 / kAddWarps;  // columns a thread adds up
+    static constexpr int kThreads = 32 * (3 + kAddWarps);
+    static constexpr int kScaleSlots = 4;
+    static constexpr int kScaleFloats = kTileM + BN;
+    // over half an SM's shared memory, so that a second CTA never waits for TMEM
+    // that the first one holds
+    static constexpr int kSmem = kStages * kStageBytes + kScaleSlots * kScaleFloats * 4 + 1024;
+    static_assert(kSmem > 116 * 1024 && kSmem <= 227 * 1024, "one CTA an SM");
+    static_assert(kTileM * BN * 4 <= kStages * kStageBytes, "the split's sums fit the stage ring");
+};
+
+struct FlArgs {
+    int64_t m, n;
+    int num_kb, splits, kb_per_split;
+    int m_tiles, n_tiles, tiles;
+    uint32_t idesc;
+    ScaleView ps, qs;
+    void* y;
+    int64_t y_ms, y_ns;
+    int y_type;
+    int y_align;  // bytes by which rows of 16 outputs are aligned (y_ns == 1)
+    const void* bias;
+    int bias_type;
+    bool bias_on_m;
+    int act;
+    int* status;
+    int skip_stage;  // tests of the bounded waits only (-1: none)
+};
+
+// Instruction descriptor of kind::f8f6f4 with an fp32 accumulator, both
+// operands K-major: bits 4-5 D format (1 = f32), 7-9 / 10-12 A / B format
+// (0 = e4m3, 1 = e5m2), 17-22 N >> 3, 24-28 M >> 4.
+constexpr uint32_t fp8_idesc(int m, int n, bool a_e5m2, bool b_e5m2) {
+    return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((b_e5m2 ? 1u : 0u) << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// D[tmem] (+)= A[smem] x B[smem], 8-bit inputs, fp32 D.
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// The wait names the registers, so that no use of them can move above it.
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+// 4-byte asynchronous copy global -> shared (0 where !valid).
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, bool valid) {
+    const uint32_t n = valid ? 4u : 0u;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ float load_any(const void* p, int type, int64_t i) {
+    if (type == VNM_F32) return static_cast<const float*>(p)[i];
+    if (type == VNM_F16) return __half2float(static_cast<const __half*>(p)[i]);
+    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+__device__ __forceinline__ void store_any(void* p, int type, int64_t i, float v) {
+    if (type == VNM_F32)
+        static_cast<float*>(p)[i] = v;
+    else if (type == VNM_F16)
+        static_cast<__half*>(p)[i] = __float2half_rn(v);
+    else
+        static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+__device__ __forceinline__ float activate(int act, float v) {
+    // a comparison rather than fmaxf, which would turn NaN into 0
+    if (act == VNM_ACT_RELU) return v < 0.f ? 0.f : v;
+    if (act == VNM_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+    return v;
+}
+
+// Output (m, n) from its sum.
+__device__ __forceinline__ void store_one(const FlArgs& a, int64_t m, int64_t n, float v) {
+    if (a.bias) v += load_any(a.bias, a.bias_type, a.bias_on_m ? m : n);
+    store_any(a.y, a.y_type, m * a.y_ms + n * a.y_ns, activate(a.act, v));
+}
+
+// 16 neighbouring outputs of row m from column n on (y_ns == 1).
+__device__ __forceinline__ void store_row16(const FlArgs& a, int64_t m, int64_t n, const float* v) {
+    if (n + 16 > a.n || a.y_align < 16) {
+        for (int u = 0; u < 16; ++u)
+            if (n + u < a.n) store_one(a, m, n + u, v[u]);
+        return;
+    }
+    float t[16];
+    const float bm = a.bias && a.bias_on_m ? load_any(a.bias, a.bias_type, m) : 0.f;
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+        t[u] = activate(a.act, v[u] + (a.bias && !a.bias_on_m ? load_any(a.bias, a.bias_type, n + u) : bm));
+    uint32_t w[16];
+    uint8_t* dst = static_cast<uint8_t*>(a.y) + (m * a.y_ms + n) * (a.y_type == VNM_F32 ? 4 : 2);
+    if (a.y_type == VNM_F32) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u) w[u] = __float_as_uint(t[u]);
+    } else if (a.y_type == VNM_F16) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const __half2 h = __floats2half2_rn(t[2 * u], t[2 * u + 1]);
+            w[u] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(t[2 * u], t[2 * u + 1]);
+            w[u] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+    if (a.y_align >= 32) {
+        st_global_v8(dst, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+        if (a.y_type == VNM_F32) st_global_v8(dst + 32, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
+    } else {
+        uint4* d = reinterpret_cast<uint4*>(dst);
+        d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        if (a.y_type == VNM_F32) {
+            d[2] = make_uint4(w[8], w[9], w[10], w[11]);
+            d[3] = make_uint4(w[12], w[13], w[14], w[15]);
+        }
+    }
+}
+
+// Tiles in groups of kGroupM row tiles, row tiles fastest: the CTAs that run
+// together share a few tiles of both operands in L2.
+constexpr int kGroupM = 16;
+__device__ __forceinline__ void tile_at(const FlArgs& a, int tile, int& mt, int& nt) {
+    const int per_group = kGroupM * a.n_tiles;
+    const int g = tile / per_group, r = tile - g * per_group;
+    const int rows = min(kGroupM, a.m_tiles - g * kGroupM);
+    nt = r / rows;
+    mt = g * kGroupM + (r - nt * rows);
+}
+
+template <int BN>
+__global__ void __launch_bounds__(FlCfg<BN>::kThreads, 1)
+    fp8_linear_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
+                      const FlArgs a) {
+    using Cfg = FlCfg<BN>;
+    constexpr int ST = Cfg::kStages, ACC = Cfg::kAcc, SS = Cfg::kScaleSlots, COLS = Cfg::kCols;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full_bar[ST], empty_bar[ST];      // operand stages
+    __shared__ __align__(8) uint64_t accf_bar[ACC], acce_bar[ACC];     // TMEM buffers
+    __shared__ __align__(8) uint64_t scf_bar[SS], sce_bar[SS];         // scale slots
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+
+    const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* const smem_gen = smem_raw + (smem_base - smem_u32(smem_raw));
+    float* const scales = reinterpret_cast<float*>(smem_gen + ST * Cfg::kStageBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(smem_u32(&full_bar[s]), 1);
+            mbar_init(smem_u32(&empty_bar[s]), 1);
+        }
+        for (int s = 0; s < ACC; ++s) {
+            mbar_init(smem_u32(&accf_bar[s]), 1);
+            mbar_init(smem_u32(&acce_bar[s]), Cfg::kAddWarps);
+        }
+        for (int s = 0; s < SS; ++s) {
+            mbar_init(smem_u32(&scf_bar[s]), 32);
+            mbar_init(smem_u32(&sce_bar[s]), Cfg::kAddWarps);
+        }
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (threadIdx.x == 64) {
+        tma_prefetch_desc(&tm_p);
+        tma_prefetch_desc(&tm_q);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&tmem_slot), Cfg::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    volatile int* abort = &abort_flag;
+
+    // this CTA's tiles and K blocks: every role walks the same sequence
+    const int rank = a.splits > 1 ? static_cast<int>(blockIdx.x) % a.splits : 0;
+    const int tile0 = static_cast<int>(blockIdx.x) / a.splits;
+    const int tile_step = a.splits > 1 ? a.tiles : static_cast<int>(gridDim.x);
+    const int kb0 = rank * a.kb_per_split;
+    const int kb1 = min(a.num_kb, kb0 + a.kb_per_split);
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int it = 0;
+            bool run = true;
+            for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
+                int mt, nt;
+                tile_at(a, tile, mt, nt);
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int slot = it % ST;
+                    if (!mbar_wait(smem_u32(&empty_bar[slot]), (static_cast<uint32_t>(it / ST) & 1u) ^ 1u, abort)) {
+                        run = false;
+                        break;
+                    }
+                    if (it == a.skip_stage && blockIdx.x == 0) continue;
+                    const uint32_t fb = smem_u32(&full_bar[slot]);
+                    const uint32_t sp = smem_base + slot * Cfg::kStageBytes;
+                    mbar_arrive_expect_tx(fb, Cfg::kStageBytes);
+                    tma_load_2d(sp, &tm_p, kb * 128, mt * kTileM, fb);
+                    tma_load_2d(sp + Cfg::kPBytes, &tm_q, kb * 128, nt * BN, fb);
+                }
+            }
+            if (*abort) {
+                // every copy issued must land before the CTA exits
+                for (int k = it > ST ? it - ST : 0; k < it; ++k)
+                    if (k != a.skip_stage || blockIdx.x != 0) mbar_drain(smem_u32(&full_bar[k % ST]), static_cast<uint32_t>(k / ST) & 1u);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            // both operands K-major, 128B swizzle, 128-byte rows, 8-row groups 1024 bytes
+            // apart; MMA k-step s (K = 32) takes bytes 32s .. 32s + 31 of every row
+            const uint64_t pdesc = make_smem_desc(smem_base, 16, 1024, kLayoutSw128);
+            const uint64_t qdesc = make_smem_desc(smem_base + Cfg::kPBytes, 16, 1024, kLayoutSw128);
+            int it = 0, last_acc = -1;
+            bool run = true;
+            for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int slot = it % ST, acc = it % ACC;
+                    if (!mbar_wait(smem_u32(&acce_bar[acc]), (static_cast<uint32_t>(it / ACC) & 1u) ^ 1u, abort) ||
+                        !mbar_wait(smem_u32(&full_bar[slot]), static_cast<uint32_t>(it / ST) & 1u, abort)) {
+                        run = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint64_t off = static_cast<uint64_t>((slot * Cfg::kStageBytes) >> 4);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        tc_mma_f8(tmem + acc * BN, pdesc + off + 2 * s, qdesc + off + 2 * s, a.idesc, s > 0 ? 1u : 0u);
+                    tc_commit(smem_u32(&empty_bar[slot]));
+                    tc_commit(smem_u32(&accf_bar[acc]));
+                    last_acc = it;
+                }
+            }
+            // every MMA issued is done before TMEM goes back
+            if (last_acc >= 0)
+                mbar_drain(smem_u32(&accf_bar[last_acc % ACC]), static_cast<uint32_t>(last_acc / ACC) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------ scales
+        int it = 0;
+        bool run = true;
+        for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
+            int mt, nt;
+            tile_at(a, tile, mt, nt);
+            const int64_t m0 = static_cast<int64_t>(mt) * kTileM, n0 = static_cast<int64_t>(nt) * BN;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int slot = it % SS;
+                if (!mbar_wait_warp(smem_u32(&sce_bar[slot]), (static_cast<uint32_t>(it / SS) & 1u) ^ 1u, abort)) {
+                    run = false;
+                    break;
+                }
+                const uint32_t dst = smem_u32(scales + slot * Cfg::kScaleFloats);
+#pragma unroll
+                for (int i = lane; i < kTileM; i += 32) {
+                    const int64_t r = m0 + i;
+                    const bool in = r < a.m;
+                    cp_async_4(dst + 4 * i, a.ps.p + (in ? (r >> a.ps.shift) * a.ps.rs + kb * a.ps.cs : 0), in);
+                }
+                for (int i = lane; i < BN; i += 32) {
+                    const int64_t r = n0 + i;
+                    const bool in = r < a.n;
+                    cp_async_4(dst + 4 * (kTileM + i), a.qs.p + (in ? (r >> a.qs.shift) * a.qs.rs + kb * a.qs.cs : 0),
+                               in);
+                }
+                cp_async_arrive_noinc(smem_u32(&scf_bar[slot]));
+            }
+        }
+        cp_async_wait_all();
+    } else {
+        // ------------------------------------------------ adding up
+        const int quarter = warp & 3;                   // TMEM lanes 32 quarter ..
+        const int row = 32 * quarter + lane;            // row of the tile
+        const int col0 = ((warp - 3) >> 2) * COLS;      // first column of the tile
+        const uint32_t lane_addr = static_cast<uint32_t>(32 * quarter) << 16;
+        int it = 0;
+        bool run = true;
+        for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
+            float sum[COLS];
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) sum[c] = 0.f;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int acc = it % ACC, slot = it % SS;
+                if (!mbar_wait_warp(smem_u32(&scf_bar[slot]), static_cast<uint32_t>(it / SS) & 1u, abort) ||
+                    !mbar_wait_warp(smem_u32(&accf_bar[acc]), static_cast<uint32_t>(it / ACC) & 1u, abort)) {
+                    run = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const float* sc = scales + slot * Cfg::kScaleFloats;
+                const float sp = sc[row];
+                const float* sq = sc + kTileM + col0;
+                const uint32_t taddr = tmem + lane_addr + acc * BN + col0;
+#pragma unroll
+                for (int c = 0; c < COLS; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(taddr + c, v);
+                    tmem_wait_ld16(v);
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) sum[c + u] = fmaf(__uint_as_float(v[u]), sp * sq[c + u], sum[c + u]);
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&acce_bar[acc]));
+                    mbar_arrive(smem_u32(&sce_bar[slot]));
+                }
+            }
+            if (!run) break;
+            if (a.splits > 1) {
+                // the stage ring is free: this tile's MMAs are done with it
+                float* part = reinterpret_cast<float*>(smem_gen);
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) part[(col0 + c) * kTileM + row] = sum[c];
+                continue;
+            }
+            int mt, nt;
+            tile_at(a, tile, mt, nt);
+            const int64_t m = static_cast<int64_t>(mt) * kTileM + row;
+            const int64_t n0 = static_cast<int64_t>(nt) * BN + col0;
+            if (m >= a.m) continue;
+            if (a.y_ns == 1) {
+#pragma unroll
+                for (int c = 0; c < COLS; c += 16) store_row16(a, m, n0 + c, sum + c);
+            } else {
+#pragma unroll
+                for (int c = 0; c < COLS; ++c)
+                    if (n0 + c < a.n) store_one(a, m, n0 + c, sum[c]);
+            }
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (a.splits > 1) {
+        // add the cluster's sums, in rank order; each CTA takes its share of the columns
+        cluster_sync_all();
+        int mt, nt;
+        tile_at(a, tile0, mt, nt);
+        const int share = BN / a.splits;
+        for (int i = threadIdx.x; i < share * kTileM; i += Cfg::kThreads) {
+            const int c = rank * share + i / kTileM, row = i % kTileM;
+            const uint32_t addr = smem_base + 4 * (c * kTileM + row);
+            float v[kMaxSplits];
+#pragma unroll
+            for (int s = 0; s < kMaxSplits; ++s) v[s] = s < a.splits ? dsmem_ld_f32(dsmem_map(addr, s)) : 0.f;
+            float sum = v[0];
+#pragma unroll
+            for (int s = 1; s < kMaxSplits; ++s)
+                if (s < a.splits) sum += v[s];
+            const int64_t m = static_cast<int64_t>(mt) * kTileM + row, n = static_cast<int64_t>(nt) * BN + c;
+            if (m < a.m && n < a.n) store_one(a, m, n, sum);
+        }
+        cluster_sync_all();  // no CTA leaves while others read its sums
+    }
+    if (threadIdx.x == 0 && abort_flag && a.status) record_error(a.status, VNM_ERR_TIMEOUT, 12);
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, Cfg::kTmemCols);
+    }
+}
+
+// K = 0: act(bias).
+__global__ void fp8_linear_empty_kernel(const FlArgs a) {
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.m * a.n;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+        store_one(a, i / a.n, i % a.n, 0.f);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// An operand's bytes as boxes of 128 bytes of K x `rows` rows; past its edges it reads as 0.
+bool encode(CUtensorMap* tm, const void* base, int64_t k, int64_t rows, int64_t ld, int box_rows) {
+    auto enc = encoder();
+    if (enc == nullptr) return false;
+    const cuuint64_t dim[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(ld)};
+    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t step[2] = {1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dim, stride, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN>
+cudaError_t run(const Fp8LinearArgs& g, FlArgs a, int splits, int sm_count, cudaStream_t stream) {
+    using Cfg = FlCfg<BN>;
+    a.m_tiles = static_cast<int>((g.m + kTileM - 1) / kTileM);
+    a.n_tiles = static_cast<int>((g.n + BN - 1) / BN);
+    const int64_t tiles = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
+    if (tiles * kMaxSplits > INT32_MAX) return cudaErrorInvalidValue;
+    a.tiles = static_cast<int>(tiles);
+    a.splits = splits;
+    a.kb_per_split = (a.num_kb + splits - 1) / splits;
+    a.idesc = fp8_idesc(kTileM, BN, g.p_e5m2, g.q_e5m2);
+    CUtensorMap tm_p, tm_q;
+    if (!encode(&tm_p, g.p, g.k, g.m, g.ld_p, kTileM) || !encode(&tm_q, g.q, g.k, g.n, g.ld_q, BN))
+        return cudaErrorInvalidValue;
+    static std::atomic<bool> attr_set[kMaxDevicesFl];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevicesFl) return cudaErrorInvalidDevice;
+    if (!attr_set[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(fp8_linear_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(true, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(splits > 1 ? tiles * splits : std::min<int64_t>(tiles, sm_count)));
+    cfg.blockDim = dim3(Cfg::kThreads);
+    cfg.dynamicSmemBytes = Cfg::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(splits);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fp8_linear_kernel<BN>, tm_p, tm_q, a);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const ScaleView& xs, const void* wq,
+                              int64_t ld_w, bool w_e5m2, const ScaleView& ws, int64_t T, int64_t R, int64_t K,
+                              const void* bias, vnm_dtype bias_type, int act, void* y, int64_t ld_y, vnm_dtype y_type,
+                              int* status, int skip_stage, int sm_count, cudaStream_t stream) {
+    auto ceil_div = [](int64_t p, int64_t q) { return (p + q - 1) / q; };
+    // Many tiles of 128 tokens x 256 outputs: X on the M side. Otherwise W on the
+    // M side, the narrowest tile that holds the tokens (128 at most), and K split
+    // while the tiles leave SMs idle.
+    const bool wide = ceil_div(T, kTileM) * ceil_div(R, 256) >= sm_count;
+    Fp8LinearArgs g{};
+    if (wide)
+        g = Fp8LinearArgs{xq, wq, ld_x, ld_w, x_e5m2, w_e5m2, xs, ws, T, R, K, y, ld_y, 1, y_type, bias, bias_type,
+                          false, act, status};
+    else
+        g = Fp8LinearArgs{wq, xq, ld_w, ld_x, w_e5m2, x_e5m2, ws, xs, R, T, K, y, 1, ld_y, y_type, bias, bias_type,
+                          true, act, status};
+    FlArgs a{};
+    a.m = g.m;
+    a.n = g.n;
+    a.num_kb = static_cast<int>(ceil_div(K, 128));
+    a.ps = g.ps;
+    a.qs = g.qs;
+    a.y = y;
+    a.y_ms = g.y_ms;
+    a.y_ns = g.y_ns;
+    a.y_type = y_type;
+    const uintptr_t align = reinterpret_cast<uintptr_t>(y) | (static_cast<uintptr_t>(ld_y) * (y_type == VNM_F32 ? 4 : 2));
+    a.y_align = align % 32 == 0 ? 32 : align % 16 == 0 ? 16 : 1;
+    a.bias = bias;
+    a.bias_type = bias_type;
+    a.bias_on_m = g.bias_on_m;
+    a.act = act;
+    a.status = status;
+    a.skip_stage = skip_stage;
+    if (K == 0) {
+        const int64_t n = std::min<int64_t>(ceil_div(T * R, 256), 16 * sm_count);
+        fp8_linear_empty_kernel<<<static_cast<unsigned>(n), 256, 0, stream>>>(a);
+        return cudaGetLastError();
+    }
+    if (wide) return run<256>(g, a, 1, sm_count, stream);
+    const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+    const int64_t tiles = ceil_div(R, kTileM) * ceil_div(T, bn);
+    int splits = 1;
+    while (splits < kMaxSplits && tiles * splits * 2 <= sm_count && a.num_kb >= 2 * splits) splits *= 2;
+    switch (bn) {
+        case 16: return run<16>(g, a, splits, sm_count, stream);
+        case 32: return run<32>(g, a, splits, sm_count, stream);
+        case 64: return run<64>(g, a, splits, sm_count, stream);
+        default: return run<128>(g, a, splits, sm_count, stream);
+    }
+}
+
+}  // namespace vnm

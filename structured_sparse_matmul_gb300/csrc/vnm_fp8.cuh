@@ -1,0 +1,61 @@
+// Device helpers of the block-scaled 8-bit form: the scale rule, fp8
+// conversions, and element types widened to fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+namespace vnm {
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(__half v) { return __half2float(v); }
+__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T>
+__device__ __forceinline__ T narrow(float v);
+template <>
+__device__ __forceinline__ float narrow<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Largest finite values of the two formats.
+constexpr float kMaxE4m3 = 448.f;
+constexpr float kMaxE5m2 = 57344.f;
+// Smallest scale: a group of zeros (or of values below 2^-100 of the format's
+// range) keeps a finite reciprocal.
+constexpr float kMinScale = 0x1p-100f;
+
+// Magnitudes compare as the integers of their bits, which orders
+// finite < Inf < NaN: one integer maximum then finds both the largest magnitude
+// of a group and whether it holds a non-finite value.
+__device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// Scale of a group whose largest magnitude has these bits, and its reciprocal
+// (both NaN for a group with a non-finite value, so that its q are NaN too).
+// Elements are multiplied by the rounded reciprocal rather than divided by the
+// scale: an element within 2^-23 of the middle between two fp8 values may round
+// to the other one, which is 2^-19 of its rounding error at most.
+__device__ __forceinline__ float group_scale(uint32_t bits, bool e5m2, float& inv) {
+    if (bits >= 0x7F800000u) {
+        inv = __uint_as_float(0x7FC00000u);
+        return inv;
+    }
+    const float s = fmaxf(__fdiv_rn(__uint_as_float(bits), e5m2 ? kMaxE5m2 : kMaxE4m3), kMinScale);
+    inv = __frcp_rn(s);
+    return s;
+}
+
+// Two fp32 values to fp8 (nearest even, saturating, NaN kept), `lo` in the low byte.
+__device__ __forceinline__ uint32_t to_fp8x2(float lo, float hi, bool e5m2) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
+}
+
+__device__ __forceinline__ uint32_t to_fp8x4(float a, float b, float c, float d, bool e5m2) {
+    return to_fp8x2(a, b, e5m2) | (to_fp8x2(c, d, e5m2) << 16);
+}
+
+}  // namespace vnm

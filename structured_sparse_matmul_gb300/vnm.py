@@ -26,6 +26,10 @@ VNM_ERR_INTERNAL = 6
 
 VNM_F16 = 0
 VNM_F32 = 1
+VNM_BF16 = 2
+
+VNM_E4M3 = 0
+VNM_E5M2 = 1
 
 VNM_PATH_NONE = 0
 VNM_PATH_TC = 1
@@ -77,6 +81,14 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.vnm_get_status.argtypes = [p, p]
     L.vnm_spmm_noalloc.argtypes = [i64, i64, i32, i32, p, p, p, p, i64, i64, p, i64, ctypes.c_int, p, p]
     L.vnm_testing_spmm_skip_stage.argtypes = [p, p, i64, i64, p, i64, ctypes.c_int, p, sz, i32, p]
+    f32, dt = ctypes.c_float, ctypes.c_int
+    L.vnm_rmsnorm.argtypes = [p, i64, p, i64, p, f32, i64, i64, dt, p, i64, p, i64, p, p, i64, dt, p, i64, i64, p]
+    L.vnm_rmsnorm_backward.argtypes = [p, i64, p, i64, p, p, p, i64, i64, i64, dt, p, i64, p, p, sz, p]
+    L.vnm_rmsnorm_backward_workspace_size.argtypes = [i64, i64, p]
+    L.vnm_fp8_quantize.argtypes = [p, i64, i64, i64, dt, i32, dt, p, i64, p, i64, i64, p, i64, p, i64, i64, p]
+    L.vnm_fp8_linear.argtypes = [p, i64, dt, p, i64, i64, p, i64, dt, p, i64, i64, i32, i64, i64, i64, p, dt, dt, p, i64,
+                                 dt, p, p]
+    L.vnm_testing_fp8_linear_skip_stage.argtypes = L.vnm_fp8_linear.argtypes[:-1] + [i32, p]
     for name in ("vnm_sizes", "vnm_matrix_create", "vnm_matrix_destroy", "vnm_compress", "vnm_decompress",
                  "vnm_spmm", "vnm_spmm_workspace_size", "vnm_spmm_plan_query", "vnm_spmm_with_plan",
                  "vnm_get_status", "vnm_spmm_noalloc", "vnm_testing_spmm_skip_stage"):
@@ -437,3 +449,177 @@ def vnm_spmm_noalloc(R: int, K: int, V: int, M: int, values: torch.Tensor, meta:
                                   colidx.data_ptr() or None, B.data_ptr() or None, _rowmajor(B, "B"), N,
                                   C.data_ptr() or None, _rowmajor(C, "C"), _c_type(C), sp, _stream_ptr(stream)),
            "vnm_spmm_noalloc")
+
+
+# ---- the dense neighbours of a pruned layer: norm, 8-bit form, 8-bit Linear layer ----
+
+_DTYPES = {torch.float16: VNM_F16, torch.float32: VNM_F32, torch.bfloat16: VNM_BF16}
+_FP8 = {torch.float8_e4m3fn: VNM_E4M3, torch.float8_e5m2: VNM_E5M2}
+
+
+def _groups(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be fp16, bf16 or fp32")
+    return code
+
+
+def _fp8(t: torch.Tensor, name: str) -> int:
+    code = _FP8.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float8_e4m3fn or float8_e5m2")
+    return code
+
+
+def _shaped(t: Optional[torch.Tensor], name: str, shape, like: torch.Tensor, dtype=None):
+    """(pointer, leading dimension) of an operand of a given shape on like's
+    device; (None, 1) where it is None. A vector has to be contiguous."""
+    if t is None:
+        return None, 1
+    if t.shape != shape or t.device != like.device or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be a tensor of shape {tuple(shape)}{f' and type {dtype}' if dtype else ''} on {like.device}")
+    if len(shape) == 1:
+        if t.stride(0) != 1 and t.numel() > 1:
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr() or None, 1
+    return t.data_ptr() or None, _rowmajor(t, name) if t.numel() else max(int(shape[1]), 1)
+
+
+def _scales(t: Optional[torch.Tensor], name: str, shape, like: torch.Tensor):
+    """(pointer, strides) of fp32 scales: any strides."""
+    if t is None:
+        return None, 0, 0
+    if t.shape != shape or t.dtype != torch.float32 or t.device != like.device:
+        raise ValueError(f"{name} must be an fp32 tensor of shape {tuple(shape)} on {like.device}")
+    return t.data_ptr() or None, int(t.stride(0)), int(t.stride(1))
+
+
+def _on_current_device(t: torch.Tensor, name: str) -> None:
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a CUDA matrix")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+
+
+def vnm_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float, residual: Optional[torch.Tensor] = None,
+                h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                rstd: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                q_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """h = x + residual, y = h * rstd * weight with rstd = 1 / sqrt(mean h^2 + eps).
+
+    x, residual, h, y: T x D of one type (fp16, bf16, fp32); weight (D,) or None;
+    rstd fp32 (T,); q: T x D float8 and q_scale fp32 (T, ceil(D / 128)), the
+    8-bit form of y. Outputs that are None are not written (y or q is needed)."""
+    _on_current_device(x, "x")
+    T, D = x.shape
+    dt, code = x.dtype, _dtype(x, "x")
+    xp, ld_x = _shaped(x, "x", x.shape, x)
+    rp, ld_r = _shaped(residual, "residual", x.shape, x, dt)
+    wp, _ = _shaped(weight, "weight", (D,), x, dt)
+    hp, ld_h = _shaped(h, "h", x.shape, x, dt)
+    yp, ld_y = _shaped(y, "y", x.shape, x, dt)
+    sp, _ = _shaped(rstd, "rstd", (T,), x, torch.float32)
+    qp, ld_q = _shaped(q, "q", x.shape, x)
+    qt = _fp8(q, "q") if q is not None else VNM_E4M3
+    cp, c_rs, c_cs = _scales(q_scale, "q_scale", (T, _groups(D)), x)
+    _check(lib().vnm_rmsnorm(xp, ld_x, rp, ld_r, wp, eps, T, D, code, hp, ld_h, yp, ld_y, sp, qp, ld_q, qt, cp, c_rs,
+                             c_cs, _stream_ptr(stream)), "vnm_rmsnorm")
+
+
+def vnm_rmsnorm_backward_workspace_size(T: int, D: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().vnm_rmsnorm_backward_workspace_size(T, D, ctypes.byref(n)), "vnm_rmsnorm_backward_workspace_size")
+    return int(n.value)
+
+
+def vnm_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: Optional[torch.Tensor], rstd: torch.Tensor,
+                         dh: Optional[torch.Tensor], dweight: Optional[torch.Tensor],
+                         dresidual: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         stream=None) -> None:
+    """Gradients of vnm_rmsnorm: dh (T x D, of x and residual alike; dresidual
+    added where given) and dweight (fp32 (D,)); either may be None."""
+    _on_current_device(dy, "dy")
+    T, D = dy.shape
+    dt, code = dy.dtype, _dtype(dy, "dy")
+    yp, ld_dy = _shaped(dy, "dy", dy.shape, dy)
+    hp, ld_h = _shaped(h, "h", dy.shape, dy, dt)
+    wp, _ = _shaped(weight, "weight", (D,), dy, dt)
+    sp, _ = _shaped(rstd, "rstd", (T,), dy, torch.float32)
+    rp, ld_r = _shaped(dresidual, "dresidual", dy.shape, dy, dt)
+    op, ld_o = _shaped(dh, "dh", dy.shape, dy, dt)
+    gp, _ = _shaped(dweight, "dweight", (D,), dy, torch.float32)
+    if workspace is None and dweight is not None:
+        workspace = torch.empty(vnm_rmsnorm_backward_workspace_size(T, D), dtype=torch.uint8, device=dy.device)
+    ws_ptr = (workspace.data_ptr() or None) if workspace is not None else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().vnm_rmsnorm_backward(yp, ld_dy, hp, ld_h, wp, sp, rp, ld_r, T, D, code, op, ld_o, gp, ws_ptr, ws_bytes,
+                                      _stream_ptr(stream)), "vnm_rmsnorm_backward")
+
+
+def vnm_fp8_quantize(X: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None,
+                     qt: Optional[torch.Tensor] = None, st: Optional[torch.Tensor] = None, block_rows: int = 1,
+                     stream=None) -> None:
+    """The block-scaled 8-bit form of X (R x C; fp16, bf16, fp32): q (R x C
+    float8) with s, and/or of X^T: qt (C x R) with st. Scales (fp32, any strides)
+    are (rows / block_rows, ceil(columns / 128)); block_rows 1 or 128."""
+    _on_current_device(X, "X")
+    R, C = X.shape
+    code = _dtype(X, "X")
+    rows = max(int(block_rows), 1)
+    xp, ld_x = _shaped(X, "X", X.shape, X)
+    qp, ld_q = _shaped(q, "q", (R, C), X)
+    tp, ld_t = _shaped(qt, "qt", (C, R), X)
+    kinds = {_fp8(t, n) for t, n in ((q, "q"), (qt, "qt")) if t is not None}
+    if len(kinds) > 1:
+        raise ValueError("q and qt must have the same type")
+    sp, s_rs, s_cs = _scales(s, "s", (-(-R // rows), _groups(C)), X)
+    up, u_rs, u_cs = _scales(st, "st", (-(-C // rows), _groups(R)), X)
+    _check(lib().vnm_fp8_quantize(xp, ld_x, R, C, code, int(block_rows), kinds.pop() if kinds else VNM_E4M3, qp, ld_q,
+                                  sp, s_rs, s_cs, tp, ld_t, up, u_rs, u_cs, _stream_ptr(stream)), "vnm_fp8_quantize")
+
+
+def vnm_fp8_linear(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, Y: torch.Tensor,
+                   bias: Optional[torch.Tensor] = None, act: int = VNM_ACT_NONE,
+                   status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Y = act(X . W^T + bias) on block-scaled 8-bit operands: xq (T x K
+    float8) with x_scale (T, ceil(K / 128)); wq (R x K float8) with w_scale of
+    (R or ceil(R / 128), ceil(K / 128)); Y T x R (fp16, bf16, fp32); bias (R,) of
+    those types. ``status``: optional int32 CUDA tensor of 3 zeroed words that
+    receives kernel errors."""
+    _check(lib().vnm_fp8_linear(*_fp8_linear_args(xq, x_scale, wq, w_scale, Y, bias, act, status), _stream_ptr(stream)),
+           "vnm_fp8_linear")
+
+
+def vnm_testing_fp8_linear_skip_stage(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
+                                      Y: torch.Tensor, skip_stage: int, status: torch.Tensor, stream=None) -> None:
+    """Test support: vnm_fp8_linear with the first CTA's loads of one pipeline
+    stage never issued (include/vnm_testing.h)."""
+    _check(lib().vnm_testing_fp8_linear_skip_stage(*_fp8_linear_args(xq, x_scale, wq, w_scale, Y, None, VNM_ACT_NONE, status),
+                                                   int(skip_stage), _stream_ptr(stream)),
+           "vnm_testing_fp8_linear_skip_stage")
+
+
+def _fp8_linear_args(xq, x_scale, wq, w_scale, Y, bias, act, status):
+    _on_current_device(xq, "xq")
+    T, K = xq.shape
+    R = int(wq.shape[0])
+    xp, ld_x = _shaped(xq, "xq", xq.shape, xq)
+    wp, ld_w = _shaped(wq, "wq", (R, K), xq)
+    yp, ld_y = _shaped(Y, "Y", (T, R), xq)
+    block = 1 if w_scale.shape[0] == R else 128
+    sp, s_rs, s_cs = _scales(x_scale, "x_scale", (T, _groups(K)), xq)
+    vp, v_rs, v_cs = _scales(w_scale, "w_scale", (R if block == 1 else _groups(R), _groups(K)), xq)
+    bp, b_code = None, VNM_F32
+    if bias is not None:
+        bp, b_code = _shaped(bias, "bias", (R,), xq)[0], _dtype(bias, "bias")
+    stp = None
+    if status is not None:
+        if status.dtype != torch.int32 or not status.is_cuda or status.numel() < 3:
+            raise ValueError("status must be a CUDA int32 tensor of at least 3 words")
+        stp = status.data_ptr()
+    return (xp, ld_x, _fp8(xq, "xq"), sp, s_rs, s_cs, wp, ld_w, _fp8(wq, "wq"), vp, v_rs, v_cs, block, T, R, K, bp,
+            b_code, int(act), yp, ld_y, _dtype(Y, "Y"), stp)
