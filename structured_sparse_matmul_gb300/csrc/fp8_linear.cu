@@ -8,18 +8,20 @@
 // scaled as it is added in fp32. So the MMAs of block b + 1 run while block b
 // is added up, and no scale ever has to be a power of two.
 //
-// The kernel sees P (128 rows a tile, the MMA's M side) times Q (BN rows a tile,
+// The kernel sees P (128 rows a CTA, the MMA's M side) times Q (BN rows a tile,
 // the N side): P = X, Q = W for many tokens, P = W, Q = X for few of them, where
 // the weights' rows then fill the tensor cores' rows and BN fits the tokens.
 // Few tiles split K over the CTAs of a cluster, which add their sums up through
-// distributed shared memory in rank order.
+// distributed shared memory in rank order. Many tiles are taken by pairs of CTAs
+// (cta_group::2): 256 x 256 outputs a pair, each CTA loading its own 128 rows of
+// P and half of Q, so that a K block costs an SM 32 KB of loads instead of 48.
 //
-//   warp 0     TMA producer: a stage is 128 rows of P and BN rows of Q by 128
-//              bytes of K, 128B swizzle.
-//   warp 1     TMEM owner and MMA issuer (one thread).
-//   warp 2     the K block's scales, 128 of P and BN of Q, into a shared-memory
-//              ring by 4-byte cp.async (any strides).
-//   warps 3..  add up: thread = row of P; 4 warps, or 8 with half the columns each.
+//   warp 0     TMA producer: a stage is 128 rows of P and the CTA's rows of Q by
+//              128 bytes of K, 128B swizzle.
+//   warp 1     TMEM owner and MMA issuer (one thread; of a pair, the first CTA's).
+//   warp 2     the K block's scales into a shared-memory ring by 4-byte cp.async
+//              (any strides).
+//   warps 4..  add up: thread = row of P; 4 warps, or 8 with half the columns each.
 // Every mbarrier wait is bounded.
 #include <cudaTypedefs.h>
 
@@ -37,26 +39,41 @@ namespace {
 
 constexpr int kTileM = 128;
 constexpr int kMaxSplits = 8;
+constexpr int kHelpers = 4;  // warps before the adding ones (the fourth is idle)
 constexpr int kMaxDevicesFl = 64;
 
-template <int BN>
+// BN: columns of the tile; ONE: every thread's columns lie in one 128-row block
+// of Q, with one scale; CG: CTAs of a tile (1, or 2 for a pair).
+template <int BN, bool ONE, int CG>
 struct FlCfg {
     static constexpr int kPBytes = kTileM * 128;
-    static constexpr int kQBytes = BN * 128;
+    static constexpr int kQRows = BN / CG;
+    static constexpr int kQBytes = kQRows * 128;
     static constexpr int kStageBytes = kPBytes + kQBytes;
-    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+    static constexpr int kStages = CG == 2 ? 5 : BN == 128 ? 6 : 8;
     static constexpr int kAcc = BN == 256 ? 2 : 4;  // TMEM buffers
     static constexpr int kTmemCols = kAcc * BN;
     static constexpr int kAddWarps = BN >= 128 ? 8 : 4;
     static constexpr int kCols = BN * 4 / kAddWarps;  // columns a thread adds up
-    static constexpr int kThreads = 32 * (3 + kAddWarps);
-    static constexpr int kScaleSlots = 4;
-    static constexpr int kScaleFloats = kTileM + BN;
+    static constexpr int kThreads = 32 * (kHelpers + kAddWarps);
+    // Registers: 128 sums and two loads of 16 columns do not fit the 168 that 12
+    // warps get; the adding warps take what the helper warps leave. The shares
+    // add up to the launch's (in warps: 4 x 72 + 8 x 216 = 12 x 168).
+    static constexpr bool kSplitRegs = kAddWarps == 8 && kCols == 128;
+    static constexpr int kLaunchRegs = 168, kHelperRegs = 72, kAddRegs = 216;
+    static_assert(!kSplitRegs || kHelpers * kHelperRegs + kAddWarps * kAddRegs == (kHelpers + kAddWarps) * kLaunchRegs,
+                  "register shares");
+    // a scale takes about as long to arrive as an operand stage
+    static constexpr int kScaleSlots = 8;
+    static constexpr int kQScales = ONE ? (BN + 127) / 128 : BN;
+    static constexpr int kScaleFloats = kTileM + (kQScales + 3) / 4 * 4;
+    // a pair's outputs leave by TMA stores, from 32 rows x 128 bytes for each adding warp
+    static constexpr int kStoreBytes = CG == 2 ? kAddWarps * 32 * 128 : 0;
     // over half an SM's shared memory, so that a second CTA never waits for TMEM
     // that the first one holds
-    static constexpr int kSmem = kStages * kStageBytes + kScaleSlots * kScaleFloats * 4 + 1024;
-    static_assert(kSmem > 116 * 1024 && kSmem <= 227 * 1024, "one CTA an SM");
-    static_assert(kTileM * BN * 4 <= kStages * kStageBytes, "the split's sums fit the stage ring");
+    static constexpr int kSmem = kStages * kStageBytes + kStoreBytes + kScaleSlots * kScaleFloats * 4 + 1024;
+    static_assert(kSmem > 116 * 1024 && kSmem <= 226 * 1024, "one CTA an SM");
+    static_assert(CG == 2 || kTileM * BN * 4 <= kStages * kStageBytes, "the split's sums fit the stage ring");
 };
 
 struct FlArgs {
@@ -68,7 +85,8 @@ struct FlArgs {
     void* y;
     int64_t y_ms, y_ns;
     int y_type;
-    int y_align;  // bytes by which rows of 16 outputs are aligned (y_ns == 1)
+    int y_align;   // bytes by which rows of 16 outputs are aligned (y_ns == 1)
+    bool y_tma;    // Y is written by TMA stores (pairs)
     const void* bias;
     int bias_type;
     bool bias_on_m;
@@ -85,15 +103,98 @@ constexpr uint32_t fp8_idesc(int m, int n, bool a_e5m2, bool b_e5m2) {
            (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] x B[smem], 8-bit inputs, fp32 D.
+// D[tmem] (+)= A[smem] x B[smem], 8-bit inputs, fp32 D; CG = 2: of a pair, each
+// CTA holding half the rows of A, of B and of D at the same addresses.
+template <int CG>
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                           uint32_t accumulate) {
+    if (CG == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// Arrive on `bar` (of a pair: on both CTAs') when the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void tc_commit_group(uint32_t bar) {
+    if (CG == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+    else
+        tc_commit(bar);
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_alloc_group(uint32_t dst_smem, uint32_t ncols) {
+    if (CG == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        tmem_alloc(dst_smem, ncols);
+        tmem_relinquish();
+    }
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_dealloc_group(uint32_t taddr, uint32_t ncols) {
+    if (CG == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+    else
+        tmem_dealloc(taddr, ncols);
+}
+
+// As tma_load_2d, of a pair: into this CTA's memory, signalling the first CTA's barrier.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* tm, int32_t x, int32_t y,
+                                                 uint32_t cluster_bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(cluster_bar)
+        : "memory");
+}
+
+// Store of a box from shared memory; it belongs to the thread's bulk group.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, int32_t x, int32_t y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(tm)),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// The thread's stores have read their shared memory / are complete.
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Arrive on a barrier of any CTA of the cluster (address from dsmem_map).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// Wait for a phase to which the other CTA of a pair may have arrived.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
         : "memory");
+    return ok != 0;
 }
 
 // The wait names the registers, so that no use of them can move above it.
@@ -103,6 +204,44 @@ __device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :
                  : "memory");
+}
+
+// One thread of a converged warp. Unlike a test of the lane number it keeps the
+// branch uniform for the compiler, which matters to the tcgen05 instructions:
+// their operands live in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // 4-byte asynchronous copy global -> shared (0 where !valid).
@@ -139,36 +278,33 @@ __device__ __forceinline__ void store_one(const FlArgs& a, int64_t m, int64_t n,
     store_any(a.y, a.y_type, m * a.y_ms + n * a.y_ns, activate(a.act, v));
 }
 
-// 16 neighbouring outputs of row m from column n on (y_ns == 1).
-__device__ __forceinline__ void store_row16(const FlArgs& a, int64_t m, int64_t n, const float* v) {
-    if (n + 16 > a.n || a.y_align < 16) {
-        for (int u = 0; u < 16; ++u)
-            if (n + u < a.n) store_one(a, m, n + u, v[u]);
-        return;
-    }
-    float t[16];
-    const float bm = a.bias && a.bias_on_m ? load_any(a.bias, a.bias_type, m) : 0.f;
+// 16 sums rounded to Y's type, as 8 (16-bit) or 16 words.
+__device__ __forceinline__ void narrow16(int y_type, const float (&v)[16], uint32_t (&w)[16]) {
+    if (y_type == VNM_F32) {
 #pragma unroll
-    for (int u = 0; u < 16; ++u)
-        t[u] = activate(a.act, v[u] + (a.bias && !a.bias_on_m ? load_any(a.bias, a.bias_type, n + u) : bm));
-    uint32_t w[16];
-    uint8_t* dst = static_cast<uint8_t*>(a.y) + (m * a.y_ms + n) * (a.y_type == VNM_F32 ? 4 : 2);
-    if (a.y_type == VNM_F32) {
-#pragma unroll
-        for (int u = 0; u < 16; ++u) w[u] = __float_as_uint(t[u]);
-    } else if (a.y_type == VNM_F16) {
+        for (int u = 0; u < 16; ++u) w[u] = __float_as_uint(v[u]);
+    } else if (y_type == VNM_F16) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const __half2 h = __floats2half2_rn(t[2 * u], t[2 * u + 1]);
+            const __half2 h = __floats2half2_rn(v[2 * u], v[2 * u + 1]);
             w[u] = *reinterpret_cast<const uint32_t*>(&h);
         }
     } else {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(t[2 * u], t[2 * u + 1]);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * u], v[2 * u + 1]);
             w[u] = *reinterpret_cast<const uint32_t*>(&h);
         }
     }
+}
+
+// 16 neighbouring outputs of row m as the sums themselves (no bias, no
+// activation; y_ns == 1, aligned, all inside): the code is short enough to stand
+// in the unrolled loop over a thread's columns.
+__device__ __forceinline__ void store_row16_plain(const FlArgs& a, int64_t m, int64_t n, const float (&v)[16]) {
+    uint32_t w[16];
+    uint8_t* dst = static_cast<uint8_t*>(a.y) + (m * a.y_ms + n) * (a.y_type == VNM_F32 ? 4 : 2);
+    narrow16(a.y_type, v, w);
     if (a.y_align >= 32) {
         st_global_v8(dst, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
         if (a.y_type == VNM_F32) st_global_v8(dst + 32, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
@@ -183,9 +319,39 @@ __device__ __forceinline__ void store_row16(const FlArgs& a, int64_t m, int64_t 
     }
 }
 
+// The bias and the activation of 16 neighbouring columns of row m. One copy of
+// this code: unrolled over a thread's columns, the activations' code alone is
+// tens of KB, and fetching it took 20 us a tile.
+__device__ __noinline__ void finish16(const FlArgs& a, int64_t m, int64_t n, float (&v)[16]) {
+    if (a.bias && a.bias_on_m) {
+        const float b = load_any(a.bias, a.bias_type, m);
+#pragma unroll
+        for (int u = 0; u < 16; ++u) v[u] += b;
+    } else if (a.bias) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+            if (n + u < a.n) v[u] += load_any(a.bias, a.bias_type, n + u);
+    }
+    if (a.act != VNM_ACT_NONE) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u) v[u] = activate(a.act, v[u]);
+    }
+}
+
+// Any 16 outputs of row m, n .. n + 15, from their finished sums.
+__device__ __noinline__ void store_any16(const FlArgs& a, int64_t m, int64_t n, float (&v)[16]) {
+    if (a.y_ns == 1 && a.y_align >= 16 && n + 16 <= a.n) {
+        store_row16_plain(a, m, n, v);
+    } else {
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+            if (n + u < a.n) store_any(a.y, a.y_type, m * a.y_ms + (n + u) * a.y_ns, v[u]);
+    }
+}
+
 // Tiles in groups of kGroupM row tiles, row tiles fastest: the CTAs that run
 // together share a few tiles of both operands in L2.
-constexpr int kGroupM = 16;
+constexpr int kGroupM = 8;
 __device__ __forceinline__ void tile_at(const FlArgs& a, int tile, int& mt, int& nt) {
     const int per_group = kGroupM * a.n_tiles;
     const int g = tile / per_group, r = tile - g * per_group;
@@ -194,33 +360,33 @@ __device__ __forceinline__ void tile_at(const FlArgs& a, int tile, int& mt, int&
     mt = g * kGroupM + (r - nt * rows);
 }
 
-template <int BN>
-__global__ void __launch_bounds__(FlCfg<BN>::kThreads, 1)
+template <int BN, bool ONE, int CG>
+__global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, 1)
     fp8_linear_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
-                      const FlArgs a) {
-    using Cfg = FlCfg<BN>;
+                      const __grid_constant__ CUtensorMap tm_y, const FlArgs a) {
+    using Cfg = FlCfg<BN, ONE, CG>;
     constexpr int ST = Cfg::kStages, ACC = Cfg::kAcc, SS = Cfg::kScaleSlots, COLS = Cfg::kCols;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full_bar[ST], empty_bar[ST];      // operand stages
-    __shared__ __align__(8) uint64_t accf_bar[ACC], acce_bar[ACC];     // TMEM buffers
-    __shared__ __align__(8) uint64_t scf_bar[SS], sce_bar[SS];         // scale slots
+    __shared__ __align__(8) uint64_t full_bar[ST];   // the stage's operands have landed (a pair's: in the first CTA)
+    // the MMAs of the stage are done: its TMEM buffer is full and its operands are free
+    __shared__ __align__(8) uint64_t done_bar[ST];
+    __shared__ __align__(8) uint64_t acce_bar[ACC];  // the TMEM buffer has been read (a pair's: in the first CTA)
+    __shared__ __align__(8) uint64_t scf_bar[SS], sce_bar[SS];  // the scales have landed, have been read
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
 
     const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* const smem_gen = smem_raw + (smem_base - smem_u32(smem_raw));
-    float* const scales = reinterpret_cast<float*>(smem_gen + ST * Cfg::kStageBytes);
+    float* const scales = reinterpret_cast<float*>(smem_gen + ST * Cfg::kStageBytes + Cfg::kStoreBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int pair_rank = CG == 2 ? static_cast<int>(blockIdx.x & 1) : 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(smem_u32(&full_bar[s]), 1);
-            mbar_init(smem_u32(&empty_bar[s]), 1);
+            mbar_init(smem_u32(&done_bar[s]), 1);
         }
-        for (int s = 0; s < ACC; ++s) {
-            mbar_init(smem_u32(&accf_bar[s]), 1);
-            mbar_init(smem_u32(&acce_bar[s]), Cfg::kAddWarps);
-        }
+        for (int s = 0; s < ACC; ++s) mbar_init(smem_u32(&acce_bar[s]), CG * Cfg::kAddWarps);
         for (int s = 0; s < SS; ++s) {
             mbar_init(smem_u32(&scf_bar[s]), 32);
             mbar_init(smem_u32(&sce_bar[s]), Cfg::kAddWarps);
@@ -232,84 +398,111 @@ __global__ void __launch_bounds__(FlCfg<BN>::kThreads, 1)
         tma_prefetch_desc(&tm_p);
         tma_prefetch_desc(&tm_q);
     }
-    if (warp == 1) {
-        tmem_alloc(smem_u32(&tmem_slot), Cfg::kTmemCols);
-        tmem_relinquish();
-    }
+    if (warp == 1) tmem_alloc_group<CG>(smem_u32(&tmem_slot), Cfg::kTmemCols);
     tc_fence_before_sync();
     __syncthreads();
+    if (CG == 2) cluster_sync_all();  // both CTAs' barriers and TMEM exist
     tc_fence_after_sync();
     const uint32_t tmem = tmem_slot;
     volatile int* abort = &abort_flag;
 
     // this CTA's tiles and K blocks: every role walks the same sequence
-    const int rank = a.splits > 1 ? static_cast<int>(blockIdx.x) % a.splits : 0;
-    const int tile0 = static_cast<int>(blockIdx.x) / a.splits;
-    const int tile_step = a.splits > 1 ? a.tiles : static_cast<int>(gridDim.x);
+    const int rank = CG == 1 && a.splits > 1 ? static_cast<int>(blockIdx.x) % a.splits : 0;
+    const int tile0 = static_cast<int>(blockIdx.x) / (CG == 2 ? 2 : a.splits);
+    const int tile_step = a.splits > 1 ? a.tiles : static_cast<int>(gridDim.x) / CG;
     const int kb0 = rank * a.kb_per_split;
     const int kb1 = min(a.num_kb, kb0 + a.kb_per_split);
 
+    if (Cfg::kSplitRegs && warp < kHelpers) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kHelperRegs));
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
-        if (lane == 0) {
-            int it = 0;
-            bool run = true;
-            for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
-                int mt, nt;
-                tile_at(a, tile, mt, nt);
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int slot = it % ST;
-                    if (!mbar_wait(smem_u32(&empty_bar[slot]), (static_cast<uint32_t>(it / ST) & 1u) ^ 1u, abort)) {
-                        run = false;
-                        break;
-                    }
-                    if (it == a.skip_stage && blockIdx.x == 0) continue;
+        int it = 0, slot = 0;
+        uint32_t phase = 1;
+        bool run = true;
+        for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
+            int mt, nt;
+            tile_at(a, tile, mt, nt);
+            const int prow = (mt * CG + pair_rank) * kTileM, qrow = nt * BN + pair_rank * Cfg::kQRows;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                if (!mbar_wait_warp(smem_u32(&done_bar[slot]), phase, abort)) {
+                    run = false;
+                    break;
+                }
+                if (elect_one() && (it != a.skip_stage || blockIdx.x != 0)) {
                     const uint32_t fb = smem_u32(&full_bar[slot]);
                     const uint32_t sp = smem_base + slot * Cfg::kStageBytes;
-                    mbar_arrive_expect_tx(fb, Cfg::kStageBytes);
-                    tma_load_2d(sp, &tm_p, kb * 128, mt * kTileM, fb);
-                    tma_load_2d(sp + Cfg::kPBytes, &tm_q, kb * 128, nt * BN, fb);
+                    if (CG == 2) {
+                        // the second CTA's bytes may arrive before the first CTA expects them: the
+                        // phase cannot end before that CTA's own arrival
+                        const uint32_t lead = dsmem_map(fb, 0);
+                        if (pair_rank == 0) mbar_arrive_expect_tx(fb, 2 * Cfg::kStageBytes);
+                        tma_load_2d_pair(sp, &tm_p, kb * 128, prow, lead);
+                        tma_load_2d_pair(sp + Cfg::kPBytes, &tm_q, kb * 128, qrow, lead);
+                    } else {
+                        mbar_arrive_expect_tx(fb, Cfg::kStageBytes);
+                        tma_load_2d(sp, &tm_p, kb * 128, prow, fb);
+                        tma_load_2d(sp + Cfg::kPBytes, &tm_q, kb * 128, qrow, fb);
+                    }
+                }
+                __syncwarp();
+                if (++slot == ST) {
+                    slot = 0;
+                    phase ^= 1;
                 }
             }
-            if (*abort) {
-                // every copy issued must land before the CTA exits
+        }
+        if (*abort) {
+            // every copy issued must land before the CTA exits; the second CTA of a pair has no
+            // barrier of its own to wait on, and gives its copies a millisecond
+            if (pair_rank == 0) {
                 for (int k = it > ST ? it - ST : 0; k < it; ++k)
-                    if (k != a.skip_stage || blockIdx.x != 0) mbar_drain(smem_u32(&full_bar[k % ST]), static_cast<uint32_t>(k / ST) & 1u);
+                    if (k != a.skip_stage || blockIdx.x != 0)
+                        mbar_drain(smem_u32(&full_bar[k % ST]), static_cast<uint32_t>(k / ST) & 1u);
+            } else {
+                const uint64_t t0 = global_timer_ns();
+                for (int i = 0; i < (1 << 20) && global_timer_ns() - t0 < 1000000; ++i) __nanosleep(1000);
             }
         }
-        __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            // both operands K-major, 128B swizzle, 128-byte rows, 8-row groups 1024 bytes
-            // apart; MMA k-step s (K = 32) takes bytes 32s .. 32s + 31 of every row
-            const uint64_t pdesc = make_smem_desc(smem_base, 16, 1024, kLayoutSw128);
-            const uint64_t qdesc = make_smem_desc(smem_base + Cfg::kPBytes, 16, 1024, kLayoutSw128);
-            int it = 0, last_acc = -1;
-            bool run = true;
-            for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const int slot = it % ST, acc = it % ACC;
-                    if (!mbar_wait(smem_u32(&acce_bar[acc]), (static_cast<uint32_t>(it / ACC) & 1u) ^ 1u, abort) ||
-                        !mbar_wait(smem_u32(&full_bar[slot]), static_cast<uint32_t>(it / ST) & 1u, abort)) {
-                        run = false;
-                        break;
-                    }
-                    tc_fence_after_sync();
+        // both operands K-major, 128B swizzle, 128-byte rows, 8-row groups 1024 bytes
+        // apart; MMA k-step s (K = 32) takes bytes 32s .. 32s + 31 of every row
+        const uint64_t pdesc = make_smem_desc(smem_base, 16, 1024, kLayoutSw128);
+        const uint64_t qdesc = make_smem_desc(smem_base + Cfg::kPBytes, 16, 1024, kLayoutSw128);
+        int it = 0, slot = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 1;
+        bool run = pair_rank == 0;
+        for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                if (!mbar_wait_warp(smem_u32(&full_bar[slot]), phase, abort) ||
+                    !mbar_wait_warp(smem_u32(&acce_bar[acc]), acc_phase, abort)) {
+                    run = false;
+                    break;
+                }
+                // (a phase that is over: this only orders the other CTA's TMEM reads before the MMAs)
+                if (CG == 2) mbar_try_wait_cluster(smem_u32(&acce_bar[acc]), acc_phase);
+                tc_fence_after_sync();
+                if (elect_one()) {
                     const uint64_t off = static_cast<uint64_t>((slot * Cfg::kStageBytes) >> 4);
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
-                        tc_mma_f8(tmem + acc * BN, pdesc + off + 2 * s, qdesc + off + 2 * s, a.idesc, s > 0 ? 1u : 0u);
-                    tc_commit(smem_u32(&empty_bar[slot]));
-                    tc_commit(smem_u32(&accf_bar[acc]));
-                    last_acc = it;
+                        tc_mma_f8<CG>(tmem + acc * BN, pdesc + off + 2 * s, qdesc + off + 2 * s, a.idesc,
+                                      s > 0 ? 1u : 0u);
+                    tc_commit_group<CG>(smem_u32(&done_bar[slot]));
+                }
+                __syncwarp();
+                if (++slot == ST) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+                if (++acc == ACC) {
+                    acc = 0;
+                    acc_phase ^= 1;
                 }
             }
-            // every MMA issued is done before TMEM goes back
-            if (last_acc >= 0)
-                mbar_drain(smem_u32(&accf_bar[last_acc % ACC]), static_cast<uint32_t>(last_acc / ACC) & 1u);
         }
-        __syncwarp();
+        // every MMA issued is done before TMEM goes back
+        if (it > 0) mbar_drain(smem_u32(&done_bar[(it - 1) % ST]), static_cast<uint32_t>((it - 1) / ST) & 1u);
     } else if (warp == 2) {
         // ------------------------------------------------ scales
         int it = 0;
@@ -317,7 +510,7 @@ __global__ void __launch_bounds__(FlCfg<BN>::kThreads, 1)
         for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
             int mt, nt;
             tile_at(a, tile, mt, nt);
-            const int64_t m0 = static_cast<int64_t>(mt) * kTileM, n0 = static_cast<int64_t>(nt) * BN;
+            const int64_t m0 = static_cast<int64_t>(mt * CG + pair_rank) * kTileM, n0 = static_cast<int64_t>(nt) * BN;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int slot = it % SS;
                 if (!mbar_wait_warp(smem_u32(&sce_bar[slot]), (static_cast<uint32_t>(it / SS) & 1u) ^ 1u, abort)) {
@@ -331,8 +524,8 @@ __global__ void __launch_bounds__(FlCfg<BN>::kThreads, 1)
                     const bool in = r < a.m;
                     cp_async_4(dst + 4 * i, a.ps.p + (in ? (r >> a.ps.shift) * a.ps.rs + kb * a.ps.cs : 0), in);
                 }
-                for (int i = lane; i < BN; i += 32) {
-                    const int64_t r = n0 + i;
+                for (int i = lane; i < Cfg::kQScales; i += 32) {
+                    const int64_t r = n0 + (ONE ? 128 * i : i);
                     const bool in = r < a.n;
                     cp_async_4(dst + 4 * (kTileM + i), a.qs.p + (in ? (r >> a.qs.shift) * a.qs.rs + kb * a.qs.cs : 0),
                                in);
@@ -341,72 +534,144 @@ __global__ void __launch_bounds__(FlCfg<BN>::kThreads, 1)
             }
         }
         cp_async_wait_all();
-    } else {
+    } else if (warp >= kHelpers) {
         // ------------------------------------------------ adding up
+        if (Cfg::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kAddRegs));
         const int quarter = warp & 3;                   // TMEM lanes 32 quarter ..
         const int row = 32 * quarter + lane;            // row of the tile
-        const int col0 = ((warp - 3) >> 2) * COLS;      // first column of the tile
+        const int col0 = ((warp - kHelpers) >> 2) * COLS;  // first column of the tile
         const uint32_t lane_addr = static_cast<uint32_t>(32 * quarter) << 16;
         int it = 0;
         bool run = true;
         for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
-            float sum[COLS];
+            uint64_t sum[COLS / 2];
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) sum[c] = 0.f;
+            for (int c = 0; c < COLS / 2; ++c) sum[c] = 0;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int acc = it % ACC, slot = it % SS;
                 if (!mbar_wait_warp(smem_u32(&scf_bar[slot]), static_cast<uint32_t>(it / SS) & 1u, abort) ||
-                    !mbar_wait_warp(smem_u32(&accf_bar[acc]), static_cast<uint32_t>(it / ACC) & 1u, abort)) {
+                    !mbar_wait_warp(smem_u32(&done_bar[it % ST]), static_cast<uint32_t>(it / ST) & 1u, abort)) {
                     run = false;
                     break;
                 }
                 tc_fence_after_sync();
                 const float* sc = scales + slot * Cfg::kScaleFloats;
                 const float sp = sc[row];
-                const float* sq = sc + kTileM + col0;
+                const float* sq = sc + kTileM + (ONE ? col0 / 128 : col0);
+                const uint64_t sp2 = ONE ? pack2(sp * sq[0], sp * sq[0]) : pack2(sp, sp);
                 const uint32_t taddr = tmem + lane_addr + acc * BN + col0;
+                // the next 16 columns are on their way while these are added
+                uint32_t v[2][16];
+                tmem_ld_32x32b_x16(taddr, v[0]);
 #pragma unroll
                 for (int c = 0; c < COLS; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld_32x32b_x16(taddr + c, v);
-                    tmem_wait_ld16(v);
+                    uint32_t(&cur)[16] = v[(c / 16) & 1];
+                    tmem_wait_ld16(cur);
+                    if (c + 16 < COLS) {
+                        tmem_ld_32x32b_x16(taddr + c + 16, v[(c / 16 + 1) & 1]);
+                    } else {
+                        // all read: the MMAs may have the buffer back
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (elect_one()) {
+                            if (CG == 2)
+                                mbar_arrive_cluster(dsmem_map(smem_u32(&acce_bar[acc]), 0));
+                            else
+                                mbar_arrive(smem_u32(&acce_bar[acc]));
+                        }
+                    }
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) sum[c + u] = fmaf(__uint_as_float(v[u]), sp * sq[c + u], sum[c + u]);
+                    for (int u = 0; u < 16; u += 4) {
+                        uint64_t s0 = sp2, s1 = sp2;
+                        if (!ONE) {
+                            const float4 q4 = *reinterpret_cast<const float4*>(sq + c + u);
+                            s0 = mul2(sp2, pack2(q4.x, q4.y));
+                            s1 = mul2(sp2, pack2(q4.z, q4.w));
+                        }
+                        sum[(c + u) / 2] = fma2(pack2(cur[u], cur[u + 1]), s0, sum[(c + u) / 2]);
+                        sum[(c + u) / 2 + 1] = fma2(pack2(cur[u + 2], cur[u + 3]), s1, sum[(c + u) / 2 + 1]);
+                    }
                 }
-                tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&acce_bar[acc]));
-                    mbar_arrive(smem_u32(&sce_bar[slot]));
-                }
+                if (elect_one()) mbar_arrive(smem_u32(&sce_bar[slot]));
             }
             if (!run) break;
-            if (a.splits > 1) {
+            if (CG == 1 && a.splits > 1) {
                 // the stage ring is free: this tile's MMAs are done with it
                 float* part = reinterpret_cast<float*>(smem_gen);
 #pragma unroll
-                for (int c = 0; c < COLS; ++c) part[(col0 + c) * kTileM + row] = sum[c];
+                for (int c = 0; c < COLS; c += 2) {
+                    float lo, hi;
+                    unpack2(sum[c / 2], lo, hi);
+                    part[(col0 + c) * kTileM + row] = lo;
+                    part[(col0 + c + 1) * kTileM + row] = hi;
+                }
                 continue;
             }
             int mt, nt;
             tile_at(a, tile, mt, nt);
-            const int64_t m = static_cast<int64_t>(mt) * kTileM + row;
+            const int64_t m0 = static_cast<int64_t>(mt * CG + pair_rank) * kTileM + 32 * quarter, m = m0 + lane;
             const int64_t n0 = static_cast<int64_t>(nt) * BN + col0;
+            const bool finish = a.bias || a.act != VNM_ACT_NONE;
+            if (CG == 2 && a.y_tma) {
+                // 128 bytes of 32 rows at a time, 128B-swizzled, then one TMA store (which
+                // leaves out what lies past Y's edges)
+                const int words = a.y_type == VNM_F32 ? 16 : 8;  // words of 16 columns
+                const uint32_t buf = smem_base + ST * Cfg::kStageBytes + (warp - kHelpers) * 4096;
+                int chunk = 0;  // 16-byte chunks of the 128 bytes that are filled
+                int64_t x = n0;
+#pragma unroll
+                for (int c = 0; c < COLS; c += 16) {
+                    float v[16];
+                    uint32_t w[16];
+#pragma unroll
+                    for (int u = 0; u < 16; u += 2) unpack2(sum[(c + u) / 2], v[u], v[u + 1]);
+                    if (finish && m < a.m) finish16(a, m, n0 + c, v);
+                    narrow16(a.y_type, v, w);
+                    if (chunk == 0) {
+                        if (lane == 0) tma_store_wait_read();
+                        __syncwarp();
+                    }
+                    const uint32_t dst = buf + 128 * lane;
+#pragma unroll
+                    for (int u = 0; u < 16; u += 4)
+                        if (u < words)
+                            st_shared_v4(dst + 16 * ((chunk + u / 4) ^ (lane & 7)), w[u], w[u + 1], w[u + 2], w[u + 3]);
+                    chunk += words / 4;
+                    if (chunk == 8) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && m0 < a.m && x < a.n)
+                            tma_store_2d(&tm_y, static_cast<int32_t>(x), static_cast<int32_t>(m0), buf);
+                        chunk = 0;
+                        x = n0 + c + 16;
+                    }
+                }
+                continue;
+            }
             if (m >= a.m) continue;
-            if (a.y_ns == 1) {
+            const bool plain = a.y_ns == 1 && a.y_align >= 16 && !finish && n0 + COLS <= a.n;
 #pragma unroll
-                for (int c = 0; c < COLS; c += 16) store_row16(a, m, n0 + c, sum + c);
-            } else {
+            for (int c = 0; c < COLS; c += 16) {
+                float v[16];
 #pragma unroll
-                for (int c = 0; c < COLS; ++c)
-                    if (n0 + c < a.n) store_one(a, m, n0 + c, sum[c]);
+                for (int u = 0; u < 16; u += 2) unpack2(sum[(c + u) / 2], v[u], v[u + 1]);
+                if (plain) {
+                    store_row16_plain(a, m, n0 + c, v);
+                } else {
+                    if (finish) finish16(a, m, n0 + c, v);
+                    store_any16(a, m, n0 + c, v);
+                }
             }
         }
+        if (CG == 2 && lane == 0) tma_store_wait();
     }
 
     tc_fence_before_sync();
     __syncthreads();
-    if (a.splits > 1) {
+    if (CG == 2) {
+        cluster_sync_all();  // neither CTA leaves while the other's arrivals or MMAs may reach it
+    } else if (a.splits > 1) {
         // add the cluster's sums, in rank order; each CTA takes its share of the columns
         cluster_sync_all();
         int mt, nt;
@@ -430,7 +695,7 @@ __global__ void __launch_bounds__(FlCfg<BN>::kThreads, 1)
     if (threadIdx.x == 0 && abort_flag && a.status) record_error(a.status, VNM_ERR_TIMEOUT, 12);
     if (warp == 1) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem, Cfg::kTmemCols);
+        tmem_dealloc_group<CG>(tmem, Cfg::kTmemCols);
     }
 }
 
@@ -455,55 +720,73 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-// An operand's bytes as boxes of 128 bytes of K x `rows` rows; past its edges it reads as 0.
-bool encode(CUtensorMap* tm, const void* base, int64_t k, int64_t rows, int64_t ld, int box_rows) {
+// A row-major matrix as boxes of 128 bytes x `box_rows` rows, 128B swizzle; past
+// its edges it reads as 0.
+bool encode(CUtensorMap* tm, CUtensorMapDataType type, int elem, const void* base, int64_t cols, int64_t rows, int64_t ld,
+            int box_rows) {
     auto enc = encoder();
     if (enc == nullptr) return false;
-    const cuuint64_t dim[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(ld)};
-    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+    const cuuint64_t dim[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(ld * elem)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t step[2] = {1, 1};
-    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dim, stride, box, step,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return enc(tm, type, 2, const_cast<void*>(base), dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN>
+template <int BN, bool ONE, int CG>
 cudaError_t run(const Fp8LinearArgs& g, FlArgs a, int splits, int sm_count, cudaStream_t stream) {
-    using Cfg = FlCfg<BN>;
-    a.m_tiles = static_cast<int>((g.m + kTileM - 1) / kTileM);
+    using Cfg = FlCfg<BN, ONE, CG>;
+    a.m_tiles = static_cast<int>((g.m + CG * kTileM - 1) / (CG * kTileM));
     a.n_tiles = static_cast<int>((g.n + BN - 1) / BN);
     const int64_t tiles = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
     if (tiles * kMaxSplits > INT32_MAX) return cudaErrorInvalidValue;
     a.tiles = static_cast<int>(tiles);
     a.splits = splits;
     a.kb_per_split = (a.num_kb + splits - 1) / splits;
-    a.idesc = fp8_idesc(kTileM, BN, g.p_e5m2, g.q_e5m2);
-    CUtensorMap tm_p, tm_q;
-    if (!encode(&tm_p, g.p, g.k, g.m, g.ld_p, kTileM) || !encode(&tm_q, g.q, g.k, g.n, g.ld_q, BN))
+    a.idesc = fp8_idesc(CG * kTileM, BN, g.p_e5m2, g.q_e5m2);
+    CUtensorMap tm_p, tm_q, tm_y;
+    if (!encode(&tm_p, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.p, g.k, g.m, g.ld_p, kTileM) ||
+        !encode(&tm_q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.q, g.k, g.n, g.ld_q, Cfg::kQRows))
         return cudaErrorInvalidValue;
+    tm_y = tm_p;  // not used, unless:
+    a.y_tma = CG == 2 && a.y_ns == 1 && a.y_align >= 16;
+    if (a.y_tma) {
+        const CUtensorMapDataType t = a.y_type == VNM_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                      : a.y_type == VNM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        if (!encode(&tm_y, t, a.y_type == VNM_F32 ? 4 : 2, a.y, g.n, g.m, a.y_ms, 32)) return cudaErrorInvalidValue;
+    }
     static std::atomic<bool> attr_set[kMaxDevicesFl];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevicesFl) return cudaErrorInvalidDevice;
     if (!attr_set[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(fp8_linear_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+        e = cudaFuncSetAttribute(fp8_linear_kernel<BN, ONE, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
         if (e != cudaSuccess) return e;
+        if (Cfg::kSplitRegs) {
+            // the shares are drawn from the launch's registers: never ask for more
+            cudaFuncAttributes fa;
+            if ((e = cudaFuncGetAttributes(&fa, fp8_linear_kernel<BN, ONE, CG>)) != cudaSuccess) return e;
+            if (fa.numRegs != Cfg::kLaunchRegs) return cudaErrorInvalidConfiguration;
+        }
         attr_set[dev].store(true, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(splits > 1 ? tiles * splits : std::min<int64_t>(tiles, sm_count)));
+    const int64_t ctas = splits > 1 ? tiles * splits : CG * std::min<int64_t>(tiles, std::max(1, sm_count / CG));
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(Cfg::kThreads);
     cfg.dynamicSmemBytes = Cfg::kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(splits);
+    attr.val.clusterDim.x = static_cast<unsigned>(splits * CG);
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = splits > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fp8_linear_kernel<BN>, tm_p, tm_q, a);
+    cfg.numAttrs = splits * CG > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fp8_linear_kernel<BN, ONE, CG>, tm_p, tm_q, tm_y, a);
 }
 
 }  // namespace
@@ -513,10 +796,10 @@ cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const S
                               const void* bias, vnm_dtype bias_type, int act, void* y, int64_t ld_y, vnm_dtype y_type,
                               int* status, int skip_stage, int sm_count, cudaStream_t stream) {
     auto ceil_div = [](int64_t p, int64_t q) { return (p + q - 1) / q; };
-    // Many tiles of 128 tokens x 256 outputs: X on the M side. Otherwise W on the
+    // Many tiles of 256 tokens x 256 outputs: X on the M side, pairs of CTAs. Otherwise W on the
     // M side, the narrowest tile that holds the tokens (128 at most), and K split
     // while the tiles leave SMs idle.
-    const bool wide = ceil_div(T, kTileM) * ceil_div(R, 256) >= sm_count;
+    const bool wide = 3 * ceil_div(T, 256) * ceil_div(R, 256) >= sm_count;
     Fp8LinearArgs g{};
     if (wide)
         g = Fp8LinearArgs{xq, wq, ld_x, ld_w, x_e5m2, w_e5m2, xs, ws, T, R, K, y, ld_y, 1, y_type, bias, bias_type,
@@ -547,16 +830,17 @@ cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const S
         fp8_linear_empty_kernel<<<static_cast<unsigned>(n), 256, 0, stream>>>(a);
         return cudaGetLastError();
     }
-    if (wide) return run<256>(g, a, 1, sm_count, stream);
+    if (wide)
+        return ws.shift ? run<256, true, 2>(g, a, 1, sm_count, stream) : run<256, false, 2>(g, a, 1, sm_count, stream);
     const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
     const int64_t tiles = ceil_div(R, kTileM) * ceil_div(T, bn);
     int splits = 1;
     while (splits < kMaxSplits && tiles * splits * 2 <= sm_count && a.num_kb >= 2 * splits) splits *= 2;
     switch (bn) {
-        case 16: return run<16>(g, a, splits, sm_count, stream);
-        case 32: return run<32>(g, a, splits, sm_count, stream);
-        case 64: return run<64>(g, a, splits, sm_count, stream);
-        default: return run<128>(g, a, splits, sm_count, stream);
+        case 16: return run<16, false, 1>(g, a, splits, sm_count, stream);
+        case 32: return run<32, false, 1>(g, a, splits, sm_count, stream);
+        case 64: return run<64, false, 1>(g, a, splits, sm_count, stream);
+        default: return run<128, false, 1>(g, a, splits, sm_count, stream);
     }
 }
 
