@@ -19,9 +19,10 @@
 //   warp 0     TMA producer: a stage is 128 rows of P and the CTA's rows of Q by
 //              128 bytes of K, 128B swizzle.
 //   warp 1     TMEM owner and MMA issuer (one thread; of a pair, the first CTA's).
-//   warp 2     the K block's scales into a shared-memory ring by 4-byte cp.async
-//              (any strides).
-//   warps 4..  add up: thread = row of P; 4 warps, or 8 with half the columns each.
+//   warp 2     the K block's scales of Q into a shared-memory ring by 4-byte
+//              cp.async (any strides), where the tile has more than one or two.
+//   warps 4..  add up: thread = row of P, whose scale it loads two blocks ahead; 4
+//              warps, or 8 with half the columns each.
 // Every mbarrier wait is bounded.
 #include <cudaTypedefs.h>
 
@@ -41,6 +42,7 @@ constexpr int kTileM = 128;
 constexpr int kMaxSplits = 8;
 constexpr int kHelpers = 4;  // warps before the adding ones (the fourth is idle)
 constexpr int kMaxDevicesFl = 64;
+constexpr int kStoreBox = 32 * 128;  // bytes of a TMA store: 32 rows x 128 bytes
 
 // BN: columns of the tile; ONE: every thread's columns lie in one 128-row block
 // of Q, with one scale; CG: CTAs of a tile (1, or 2 for a pair).
@@ -55,23 +57,22 @@ struct FlCfg {
     static constexpr int kTmemCols = kAcc * BN;
     static constexpr int kAddWarps = BN >= 128 ? 8 : 4;
     static constexpr int kCols = BN * 4 / kAddWarps;  // columns a thread adds up
+    static constexpr int kLoad = kCols < 32 ? kCols : 32;  // columns of one TMEM load
     static constexpr int kThreads = 32 * (kHelpers + kAddWarps);
-    // Registers: 128 sums and two loads of 16 columns do not fit the 168 that 12
+    // Registers: 128 sums and two loads of 32 columns do not fit the 168 that 12
     // warps get; the adding warps take what the helper warps leave. The shares
     // add up to the launch's (in warps: 4 x 72 + 8 x 216 = 12 x 168).
-    static constexpr bool kSplitRegs = kAddWarps == 8 && kCols == 128;
+    static constexpr bool kSplitRegs = kCols == 128;
     static constexpr int kLaunchRegs = 168, kHelperRegs = 72, kAddRegs = 216;
     static_assert(!kSplitRegs || kHelpers * kHelperRegs + kAddWarps * kAddRegs == (kHelpers + kAddWarps) * kLaunchRegs,
                   "register shares");
-    // a scale takes about as long to arrive as an operand stage
-    static constexpr int kScaleSlots = 8;
-    static constexpr int kQScales = ONE ? (BN + 127) / 128 : BN;
-    static constexpr int kScaleFloats = kTileM + (kQScales + 3) / 4 * 4;
+    // Q's scales (ONE reads its one scale itself); they take about as long to arrive as an operand stage
+    static constexpr int kScaleSlots = ONE ? 0 : 8;
     // a pair's outputs leave by TMA stores, from 32 rows x 128 bytes for each adding warp
-    static constexpr int kStoreBytes = CG == 2 ? kAddWarps * 32 * 128 : 0;
+    static constexpr int kStoreBytes = CG == 2 ? kAddWarps * kStoreBox : 0;
     // over half an SM's shared memory, so that a second CTA never waits for TMEM
     // that the first one holds
-    static constexpr int kSmem = kStages * kStageBytes + kStoreBytes + kScaleSlots * kScaleFloats * 4 + 1024;
+    static constexpr int kSmem = kStages * kStageBytes + kStoreBytes + kScaleSlots * BN * 4 + 1024;
     static_assert(kSmem > 116 * 1024 && kSmem <= 226 * 1024, "one CTA an SM");
     static_assert(CG == 2 || kTileM * BN * 4 <= kStages * kStageBytes, "the split's sums fit the stage ring");
 };
@@ -179,31 +180,44 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, int32_t x, i
 __device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// Arrive on a barrier of any CTA of the cluster (address from dsmem_map).
+// Arrive on a barrier of any CTA of the cluster (address from dsmem_map). The
+// arrival releases TMEM reads that have already completed and no memory writes;
+// releasing at cluster scope cost 1 us a K block here.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
-// Wait for a phase to which the other CTA of a pair may have arrived.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// The wait names the registers, so that no use of them can move above it.
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+// The waits name the registers, so that no use of them can move above.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :
                  : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+// Each thread of the warp reads 16 or 32 consecutive 32-bit columns of its lane.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(taddr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
 }
 
 // One thread of a converged warp. Unlike a test of the lane number it keeps the
@@ -217,31 +231,6 @@ __device__ __forceinline__ bool elect_one() {
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(p));
     return p != 0;
-}
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 
 // 4-byte asynchronous copy global -> shared (0 where !valid).
@@ -278,45 +267,13 @@ __device__ __forceinline__ void store_one(const FlArgs& a, int64_t m, int64_t n,
     store_any(a.y, a.y_type, m * a.y_ms + n * a.y_ns, activate(a.act, v));
 }
 
-// 16 sums rounded to Y's type, as 8 (16-bit) or 16 words.
-__device__ __forceinline__ void narrow16(int y_type, const float (&v)[16], uint32_t (&w)[16]) {
-    if (y_type == VNM_F32) {
-#pragma unroll
-        for (int u = 0; u < 16; ++u) w[u] = __float_as_uint(v[u]);
-    } else if (y_type == VNM_F16) {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const __half2 h = __floats2half2_rn(v[2 * u], v[2 * u + 1]);
-            w[u] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-    } else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * u], v[2 * u + 1]);
-            w[u] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-    }
+__device__ __forceinline__ uint32_t to_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
-
-// 16 neighbouring outputs of row m as the sums themselves (no bias, no
-// activation; y_ns == 1, aligned, all inside): the code is short enough to stand
-// in the unrolled loop over a thread's columns.
-__device__ __forceinline__ void store_row16_plain(const FlArgs& a, int64_t m, int64_t n, const float (&v)[16]) {
-    uint32_t w[16];
-    uint8_t* dst = static_cast<uint8_t*>(a.y) + (m * a.y_ms + n) * (a.y_type == VNM_F32 ? 4 : 2);
-    narrow16(a.y_type, v, w);
-    if (a.y_align >= 32) {
-        st_global_v8(dst, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
-        if (a.y_type == VNM_F32) st_global_v8(dst + 32, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
-    } else {
-        uint4* d = reinterpret_cast<uint4*>(dst);
-        d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        d[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        if (a.y_type == VNM_F32) {
-            d[2] = make_uint4(w[8], w[9], w[10], w[11]);
-            d[3] = make_uint4(w[12], w[13], w[14], w[15]);
-        }
-    }
+__device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // The bias and the activation of 16 neighbouring columns of row m. One copy of
@@ -338,10 +295,25 @@ __device__ __noinline__ void finish16(const FlArgs& a, int64_t m, int64_t n, flo
     }
 }
 
-// Any 16 outputs of row m, n .. n + 15, from their finished sums.
+// 16 neighbouring outputs of row m from their finished sums: 16-byte stores where
+// Y's rows allow them.
 __device__ __noinline__ void store_any16(const FlArgs& a, int64_t m, int64_t n, float (&v)[16]) {
     if (a.y_ns == 1 && a.y_align >= 16 && n + 16 <= a.n) {
-        store_row16_plain(a, m, n, v);
+        uint4* d = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.y) + (m * a.y_ms + n) * (a.y_type == VNM_F32 ? 4 : 2));
+        if (a.y_type == VNM_F32) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                d[u] = make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]), __float_as_uint(v[4 * u + 2]),
+                                  __float_as_uint(v[4 * u + 3]));
+        } else {
+            const bool bf16 = a.y_type == VNM_BF16;
+            uint32_t w[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                w[u] = bf16 ? to_bf16x2(v[2 * u], v[2 * u + 1]) : to_f16x2(v[2 * u], v[2 * u + 1]);
+            d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
     } else {
 #pragma unroll
         for (int u = 0; u < 16; ++u)
@@ -360,24 +332,26 @@ __device__ __forceinline__ void tile_at(const FlArgs& a, int tile, int& mt, int&
     mt = g * kGroupM + (r - nt * rows);
 }
 
-template <int BN, bool ONE, int CG>
+// F32: Y is fp32 (for a pair's staged output).
+template <int BN, bool ONE, int CG, bool F32>
 __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, 1)
     fp8_linear_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_y, const FlArgs a) {
     using Cfg = FlCfg<BN, ONE, CG>;
-    constexpr int ST = Cfg::kStages, ACC = Cfg::kAcc, SS = Cfg::kScaleSlots, COLS = Cfg::kCols;
+    constexpr int ST = Cfg::kStages, ACC = Cfg::kAcc, SS = Cfg::kScaleSlots, COLS = Cfg::kCols, LD = Cfg::kLoad;
+    constexpr int SSB = SS > 0 ? SS : 1;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[ST];   // the stage's operands have landed (a pair's: in the first CTA)
     // the MMAs of the stage are done: its TMEM buffer is full and its operands are free
     __shared__ __align__(8) uint64_t done_bar[ST];
     __shared__ __align__(8) uint64_t acce_bar[ACC];  // the TMEM buffer has been read (a pair's: in the first CTA)
-    __shared__ __align__(8) uint64_t scf_bar[SS], sce_bar[SS];  // the scales have landed, have been read
+    __shared__ __align__(8) uint64_t scf_bar[SSB], sce_bar[SSB];  // Q's scales have landed, have been read
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
 
     const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* const smem_gen = smem_raw + (smem_base - smem_u32(smem_raw));
-    float* const scales = reinterpret_cast<float*>(smem_gen + ST * Cfg::kStageBytes + Cfg::kStoreBytes);
+    float* const scales = reinterpret_cast<float*>(smem_gen + ST * Cfg::kStageBytes + Cfg::kStoreBytes);  // [SS][BN]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int pair_rank = CG == 2 ? static_cast<int>(blockIdx.x & 1) : 0;
 
@@ -474,13 +448,11 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, 1)
         bool run = pair_rank == 0;
         for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                if (!mbar_wait_warp(smem_u32(&full_bar[slot]), phase, abort) ||
-                    !mbar_wait_warp(smem_u32(&acce_bar[acc]), acc_phase, abort)) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait2(smem_u32(&full_bar[slot]), phase, smem_u32(&acce_bar[acc]),
+                                                        acc_phase, abort))) {
                     run = false;
                     break;
                 }
-                // (a phase that is over: this only orders the other CTA's TMEM reads before the MMAs)
-                if (CG == 2) mbar_try_wait_cluster(smem_u32(&acce_bar[acc]), acc_phase);
                 tc_fence_after_sync();
                 if (elect_one()) {
                     const uint64_t off = static_cast<uint64_t>((slot * Cfg::kStageBytes) >> 4);
@@ -503,32 +475,25 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, 1)
         }
         // every MMA issued is done before TMEM goes back
         if (it > 0) mbar_drain(smem_u32(&done_bar[(it - 1) % ST]), static_cast<uint32_t>((it - 1) / ST) & 1u);
-    } else if (warp == 2) {
-        // ------------------------------------------------ scales
+    } else if (warp == 2 && !ONE) {
+        // ------------------------------------------------ scales of Q
         int it = 0;
         bool run = true;
         for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
             int mt, nt;
             tile_at(a, tile, mt, nt);
-            const int64_t m0 = static_cast<int64_t>(mt * CG + pair_rank) * kTileM, n0 = static_cast<int64_t>(nt) * BN;
+            const int64_t n0 = static_cast<int64_t>(nt) * BN;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int slot = it % SS;
-                if (!mbar_wait_warp(smem_u32(&sce_bar[slot]), (static_cast<uint32_t>(it / SS) & 1u) ^ 1u, abort)) {
+                const int slot = it % SSB;
+                if (!mbar_wait_warp(smem_u32(&sce_bar[slot]), (static_cast<uint32_t>(it / SSB) & 1u) ^ 1u, abort)) {
                     run = false;
                     break;
                 }
-                const uint32_t dst = smem_u32(scales + slot * Cfg::kScaleFloats);
-#pragma unroll
-                for (int i = lane; i < kTileM; i += 32) {
-                    const int64_t r = m0 + i;
-                    const bool in = r < a.m;
-                    cp_async_4(dst + 4 * i, a.ps.p + (in ? (r >> a.ps.shift) * a.ps.rs + kb * a.ps.cs : 0), in);
-                }
-                for (int i = lane; i < Cfg::kQScales; i += 32) {
-                    const int64_t r = n0 + (ONE ? 128 * i : i);
+                const uint32_t dst = smem_u32(scales + slot * BN);
+                for (int i = lane; i < BN; i += 32) {
+                    const int64_t r = n0 + i;
                     const bool in = r < a.n;
-                    cp_async_4(dst + 4 * (kTileM + i), a.qs.p + (in ? (r >> a.qs.shift) * a.qs.rs + kb * a.qs.cs : 0),
-                               in);
+                    cp_async_4(dst + 4 * i, a.qs.p + (in ? (r >> a.qs.shift) * a.qs.rs + kb * a.qs.cs : 0), in);
                 }
                 cp_async_arrive_noinc(smem_u32(&scf_bar[slot]));
             }
@@ -541,127 +506,169 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, 1)
         const int row = 32 * quarter + lane;            // row of the tile
         const int col0 = ((warp - kHelpers) >> 2) * COLS;  // first column of the tile
         const uint32_t lane_addr = static_cast<uint32_t>(32 * quarter) << 16;
-        int it = 0;
+        const uint32_t acce_lead = CG == 2 ? dsmem_map(smem_u32(&acce_bar[0]), 0) : 0;
+        // The scales of this thread's row and, of a ONE tile, of its columns are loaded two
+        // K blocks ahead, over the end of the tile as well. Rows and columns past the
+        // edges take the last one's: their sums are not stored.
+        const float *cur_p = a.ps.p, *cur_q = a.qs.p, *next_p = a.ps.p, *next_q = a.qs.p;
+        int m0 = 0, n0 = 0, next_m0 = 0, next_n0 = 0;  // the warp's first row, the thread's first column
+        auto point = [&](int tile) {
+            int mt, nt;
+            tile_at(a, tile, mt, nt);
+            next_m0 = (mt * CG + pair_rank) * kTileM + 32 * quarter;
+            next_n0 = nt * BN + col0;
+            next_p = a.ps.p + (min(static_cast<int64_t>(next_m0) + lane, a.m - 1) >> a.ps.shift) * a.ps.rs + kb0 * a.ps.cs;
+            if (ONE) next_q = a.qs.p + (min(static_cast<int64_t>(next_n0), a.n - 1) >> a.qs.shift) * a.qs.rs + kb0 * a.qs.cs;
+        };
+        float p1 = 0.f, p2 = 0.f, q1 = 0.f, q2 = 0.f;  // of the next K block and the one after it
+        point(tile0);
+        cur_p = next_p;
+        cur_q = next_q;
+        const bool two = kb1 - kb0 >= 2;
+        if (kb0 < kb1) {
+            p1 = *cur_p;
+            if (ONE) q1 = *cur_q;
+        }
+        if (two) {
+            p2 = *(cur_p += a.ps.cs);
+            if (ONE) q2 = *(cur_q += a.qs.cs);
+        }
+        int it = 0, stage = 0;
+        uint32_t phase = 0;
         bool run = true;
         for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
-            uint64_t sum[COLS / 2];
+            m0 = next_m0;
+            n0 = next_n0;
+            if (tile + tile_step < a.tiles) point(tile + tile_step);
+            float sum[COLS];
 #pragma unroll
-            for (int c = 0; c < COLS / 2; ++c) sum[c] = 0;
+            for (int c = 0; c < COLS; ++c) sum[c] = 0.f;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int acc = it % ACC, slot = it % SS;
-                if (!mbar_wait_warp(smem_u32(&scf_bar[slot]), static_cast<uint32_t>(it / SS) & 1u, abort) ||
-                    !mbar_wait_warp(smem_u32(&done_bar[it % ST]), static_cast<uint32_t>(it / ST) & 1u, abort)) {
+                const int acc = it % ACC, slot = it % SSB;
+                const float sp = p1, sq1 = q1;
+                p1 = p2;
+                q1 = q2;
+                if (kb + 2 == kb1 || !two) {
+                    cur_p = next_p;
+                    cur_q = next_q;
+                } else {
+                    cur_p += a.ps.cs;
+                    cur_q += a.qs.cs;
+                }
+                p2 = *cur_p;
+                if (ONE) q2 = *cur_q;
+                if (!two) {  // one block a tile: the next tile's is the next one
+                    p1 = p2;
+                    q1 = q2;
+                }
+                const uint32_t done = smem_u32(&done_bar[stage]);
+                const bool ok = ONE ? mbar_wait(done, phase, abort)
+                                    : mbar_wait2(smem_u32(&scf_bar[slot]), static_cast<uint32_t>(it / SSB) & 1u, done,
+                                                 phase, abort);
+                if (++stage == ST) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
                     run = false;
                     break;
                 }
                 tc_fence_after_sync();
-                const float* sc = scales + slot * Cfg::kScaleFloats;
-                const float sp = sc[row];
-                const float* sq = sc + kTileM + (ONE ? col0 / 128 : col0);
-                const uint64_t sp2 = ONE ? pack2(sp * sq[0], sp * sq[0]) : pack2(sp, sp);
+                const float* sq = scales + slot * BN + col0;
+                const float s1 = ONE ? sp * sq1 : sp;
                 const uint32_t taddr = tmem + lane_addr + acc * BN + col0;
-                // the next 16 columns are on their way while these are added
-                uint32_t v[2][16];
-                tmem_ld_32x32b_x16(taddr, v[0]);
+                // the next columns are on their way while these are added
+                uint32_t v[2][LD];
+                tmem_ld(taddr, v[0]);
 #pragma unroll
-                for (int c = 0; c < COLS; c += 16) {
-                    uint32_t(&cur)[16] = v[(c / 16) & 1];
-                    tmem_wait_ld16(cur);
-                    if (c + 16 < COLS) {
-                        tmem_ld_32x32b_x16(taddr + c + 16, v[(c / 16 + 1) & 1]);
+                for (int c = 0; c < COLS; c += LD) {
+                    uint32_t(&cur)[LD] = v[(c / LD) & 1];
+                    tmem_wait_ld(cur);
+                    if (c + LD < COLS) {
+                        tmem_ld(taddr + c + LD, v[(c / LD + 1) & 1]);
                     } else {
                         // all read: the MMAs may have the buffer back
                         tc_fence_before_sync();
                         __syncwarp();
                         if (elect_one()) {
                             if (CG == 2)
-                                mbar_arrive_cluster(dsmem_map(smem_u32(&acce_bar[acc]), 0));
+                                mbar_arrive_cluster(acce_lead + 8 * acc);
                             else
                                 mbar_arrive(smem_u32(&acce_bar[acc]));
                         }
                     }
 #pragma unroll
-                    for (int u = 0; u < 16; u += 4) {
-                        uint64_t s0 = sp2, s1 = sp2;
-                        if (!ONE) {
-                            const float4 q4 = *reinterpret_cast<const float4*>(sq + c + u);
-                            s0 = mul2(sp2, pack2(q4.x, q4.y));
-                            s1 = mul2(sp2, pack2(q4.z, q4.w));
-                        }
-                        sum[(c + u) / 2] = fma2(pack2(cur[u], cur[u + 1]), s0, sum[(c + u) / 2]);
-                        sum[(c + u) / 2 + 1] = fma2(pack2(cur[u + 2], cur[u + 3]), s1, sum[(c + u) / 2 + 1]);
+                    for (int u = 0; u < LD; u += 4) {
+                        float4 q4 = make_float4(1.f, 1.f, 1.f, 1.f);
+                        if (!ONE) q4 = *reinterpret_cast<const float4*>(sq + c + u);
+                        sum[c + u] = fmaf(__uint_as_float(cur[u]), ONE ? s1 : s1 * q4.x, sum[c + u]);
+                        sum[c + u + 1] = fmaf(__uint_as_float(cur[u + 1]), ONE ? s1 : s1 * q4.y, sum[c + u + 1]);
+                        sum[c + u + 2] = fmaf(__uint_as_float(cur[u + 2]), ONE ? s1 : s1 * q4.z, sum[c + u + 2]);
+                        sum[c + u + 3] = fmaf(__uint_as_float(cur[u + 3]), ONE ? s1 : s1 * q4.w, sum[c + u + 3]);
                     }
                 }
-                __syncwarp();
-                if (elect_one()) mbar_arrive(smem_u32(&sce_bar[slot]));
+                if (!ONE) {
+                    __syncwarp();
+                    if (elect_one()) mbar_arrive(smem_u32(&sce_bar[slot]));
+                }
             }
             if (!run) break;
             if (CG == 1 && a.splits > 1) {
                 // the stage ring is free: this tile's MMAs are done with it
                 float* part = reinterpret_cast<float*>(smem_gen);
 #pragma unroll
-                for (int c = 0; c < COLS; c += 2) {
-                    float lo, hi;
-                    unpack2(sum[c / 2], lo, hi);
-                    part[(col0 + c) * kTileM + row] = lo;
-                    part[(col0 + c + 1) * kTileM + row] = hi;
-                }
+                for (int c = 0; c < COLS; ++c) part[(col0 + c) * kTileM + row] = sum[c];
                 continue;
             }
-            int mt, nt;
-            tile_at(a, tile, mt, nt);
-            const int64_t m0 = static_cast<int64_t>(mt * CG + pair_rank) * kTileM + 32 * quarter, m = m0 + lane;
-            const int64_t n0 = static_cast<int64_t>(nt) * BN + col0;
+            const int64_t m = static_cast<int64_t>(m0) + lane;
             const bool finish = a.bias || a.act != VNM_ACT_NONE;
-            if (CG == 2 && a.y_tma) {
-                // 128 bytes of 32 rows at a time, 128B-swizzled, then one TMA store (which
-                // leaves out what lies past Y's edges)
-                const int words = a.y_type == VNM_F32 ? 16 : 8;  // words of 16 columns
-                const uint32_t buf = smem_base + ST * Cfg::kStageBytes + (warp - kHelpers) * 4096;
-                int chunk = 0;  // 16-byte chunks of the 128 bytes that are filled
-                int64_t x = n0;
+            if (finish && m < a.m) {
 #pragma unroll
                 for (int c = 0; c < COLS; c += 16) {
                     float v[16];
-                    uint32_t w[16];
 #pragma unroll
-                    for (int u = 0; u < 16; u += 2) unpack2(sum[(c + u) / 2], v[u], v[u + 1]);
-                    if (finish && m < a.m) finish16(a, m, n0 + c, v);
-                    narrow16(a.y_type, v, w);
-                    if (chunk == 0) {
-                        if (lane == 0) tma_store_wait_read();
-                        __syncwarp();
-                    }
-                    const uint32_t dst = buf + 128 * lane;
+                    for (int u = 0; u < 16; ++u) v[u] = sum[c + u];
+                    finish16(a, m, n0 + c, v);
 #pragma unroll
-                    for (int u = 0; u < 16; u += 4)
-                        if (u < words)
-                            st_shared_v4(dst + 16 * ((chunk + u / 4) ^ (lane & 7)), w[u], w[u + 1], w[u + 2], w[u + 3]);
-                    chunk += words / 4;
-                    if (chunk == 8) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0 && m0 < a.m && x < a.n)
-                            tma_store_2d(&tm_y, static_cast<int32_t>(x), static_cast<int32_t>(m0), buf);
-                        chunk = 0;
-                        x = n0 + c + 16;
+                    for (int u = 0; u < 16; ++u) sum[c + u] = v[u];
+                }
+            }
+            if (CG == 2 && a.y_tma) {
+                // 128 bytes of 32 rows at a time, 128B-swizzled, then one TMA store (which
+                // leaves out what lies past Y's edges)
+                constexpr int kBoxCols = F32 ? 32 : 64;
+                const bool bf16 = a.y_type == VNM_BF16;
+                const uint32_t buf = smem_base + ST * Cfg::kStageBytes + (warp - kHelpers) * kStoreBox;
+                const uint32_t dst = buf + 128 * lane, flip = lane & 7;
+#pragma unroll
+                for (int c = 0; c < COLS; c += kBoxCols) {
+                    if (lane == 0) tma_store_wait_read();
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {  // 16 bytes each
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = c + j * kBoxCols / 8 + (F32 ? i : 2 * i);
+                            w[i] = F32    ? __float_as_uint(sum[e])
+                                   : bf16 ? to_bf16x2(sum[e], sum[e + 1])
+                                          : to_f16x2(sum[e], sum[e + 1]);
+                        }
+                        st_shared_v4(dst + 16 * (j ^ flip), w[0], w[1], w[2], w[3]);
                     }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && m0 < a.m && n0 + c < a.n) tma_store_2d(&tm_y, n0 + c, m0, buf);
                 }
                 continue;
             }
             if (m >= a.m) continue;
-            const bool plain = a.y_ns == 1 && a.y_align >= 16 && !finish && n0 + COLS <= a.n;
 #pragma unroll
             for (int c = 0; c < COLS; c += 16) {
                 float v[16];
 #pragma unroll
-                for (int u = 0; u < 16; u += 2) unpack2(sum[(c + u) / 2], v[u], v[u + 1]);
-                if (plain) {
-                    store_row16_plain(a, m, n0 + c, v);
-                } else {
-                    if (finish) finish16(a, m, n0 + c, v);
-                    store_any16(a, m, n0 + c, v);
-                }
+                for (int u = 0; u < 16; ++u) v[u] = sum[c + u];
+                store_any16(a, m, n0 + c, v);
             }
         }
         if (CG == 2 && lane == 0) tma_store_wait();
@@ -735,7 +742,7 @@ bool encode(CUtensorMap* tm, CUtensorMapDataType type, int elem, const void* bas
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool ONE, int CG>
+template <int BN, bool ONE, int CG, bool F32 = false>
 cudaError_t run(const Fp8LinearArgs& g, FlArgs a, int splits, int sm_count, cudaStream_t stream) {
     using Cfg = FlCfg<BN, ONE, CG>;
     a.m_tiles = static_cast<int>((g.m + CG * kTileM - 1) / (CG * kTileM));
@@ -764,12 +771,12 @@ cudaError_t run(const Fp8LinearArgs& g, FlArgs a, int splits, int sm_count, cuda
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevicesFl) return cudaErrorInvalidDevice;
     if (!attr_set[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(fp8_linear_kernel<BN, ONE, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+        e = cudaFuncSetAttribute(fp8_linear_kernel<BN, ONE, CG, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
         if (e != cudaSuccess) return e;
         if (Cfg::kSplitRegs) {
             // the shares are drawn from the launch's registers: never ask for more
             cudaFuncAttributes fa;
-            if ((e = cudaFuncGetAttributes(&fa, fp8_linear_kernel<BN, ONE, CG>)) != cudaSuccess) return e;
+            if ((e = cudaFuncGetAttributes(&fa, fp8_linear_kernel<BN, ONE, CG, F32>)) != cudaSuccess) return e;
             if (fa.numRegs != Cfg::kLaunchRegs) return cudaErrorInvalidConfiguration;
         }
         attr_set[dev].store(true, std::memory_order_relaxed);
@@ -786,7 +793,7 @@ cudaError_t run(const Fp8LinearArgs& g, FlArgs a, int splits, int sm_count, cuda
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = splits * CG > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fp8_linear_kernel<BN, ONE, CG>, tm_p, tm_q, tm_y, a);
+    return cudaLaunchKernelEx(&cfg, fp8_linear_kernel<BN, ONE, CG, F32>, tm_p, tm_q, tm_y, a);
 }
 
 }  // namespace
@@ -831,7 +838,10 @@ cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const S
         return cudaGetLastError();
     }
     if (wide)
-        return ws.shift ? run<256, true, 2>(g, a, 1, sm_count, stream) : run<256, false, 2>(g, a, 1, sm_count, stream);
+        return y_type == VNM_F32 ? ws.shift ? run<256, true, 2, true>(g, a, 1, sm_count, stream)
+                                            : run<256, false, 2, true>(g, a, 1, sm_count, stream)
+               : ws.shift        ? run<256, true, 2>(g, a, 1, sm_count, stream)
+                                 : run<256, false, 2>(g, a, 1, sm_count, stream);
     const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
     const int64_t tiles = ceil_div(R, kTileM) * ceil_div(T, bn);
     int splits = 1;
