@@ -23,6 +23,8 @@ constexpr int kMaxWarps = 32;
 // Warps of a row that keeps `cpt` groups a warp in registers: 64 registers a
 // thread hold two groups, 128 hold eight.
 constexpr int max_warps(int cpt) { return cpt <= 2 ? kMaxWarps : 16; }
+constexpr int min_ctas(int cpt) { return cpt == 4 ? 2 : 1; }
+constexpr int grad_min_ctas(int) { return 1; }
 
 // 4 elements of a lane as one vector access.
 template <typename T>
@@ -116,53 +118,67 @@ __device__ __forceinline__ void store_group(const RmsNormArgs& a, int64_t t, int
     }
 }
 
-// Forward. CPT > 0: the row's groups stay in registers. CPT = 0: rows longer
-// than the registers hold; h is formed twice from the inputs (or read back
-// where it was stored).
+// Forward. A CTA takes the rows blockIdx.x, + gridDim.x, ... CPT > 0: the row's
+// groups stay in registers, its weights too, and the next row's loads are issued
+// before this row's sum is waited for. CPT = 0: rows longer than the registers
+// hold; h is formed twice from the inputs (or read back where it was stored).
 template <typename T, bool VEC, int CPT>
-__global__ void __launch_bounds__(32 * max_warps(CPT)) rmsnorm_kernel(const RmsNormArgs a, int warps, int rows_per_cta) {
+__global__ void __launch_bounds__(32 * max_warps(CPT), min_ctas(CPT)) rmsnorm_kernel(const RmsNormArgs a, int warps, int rows_per_cta) {
     __shared__ float buf[2][kMaxWarps];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int warp = warps == 1 ? 0 : wid;
     const int64_t groups = (a.D + kGroup - 1) / kGroup;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * rows_per_cta;
     const T* w = static_cast<const T*>(a.w);
+    constexpr int N = CPT > 0 ? CPT : 1;
+    T xv[N][4], rv[N][4], hv[N][4], wv[N][4];
+    auto load_row = [&](int64_t t) {
+        const T* x = static_cast<const T*>(a.x) + t * a.ld_x;
+#pragma unroll
+        for (int i = 0; i < N; ++i) load4<T, VEC>(x, warp + static_cast<int64_t>(i) * warps, lane, a.D, xv[i]);
+        if (a.res) {
+            const T* r = static_cast<const T*>(a.res) + t * a.ld_res;
+#pragma unroll
+            for (int i = 0; i < N; ++i) load4<T, VEC>(r, warp + static_cast<int64_t>(i) * warps, lane, a.D, rv[i]);
+        }
+    };
+    // h of the loaded elements
+    auto add = [&](const T(&x4)[4], const T(&r4)[4], T(&h4)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h4[j] = a.res ? narrow<T>(widen(x4[j]) + widen(r4[j])) : x4[j];
+    };
     int slot = 0;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * rows_per_cta + (warps == 1 ? wid : 0); t < a.T;
-         t += static_cast<int64_t>(gridDim.x) * rows_per_cta) {
+    int64_t t = static_cast<int64_t>(blockIdx.x) * rows_per_cta + (warps == 1 ? wid : 0);
+    if (CPT > 0) {
+        if (t < a.T) load_row(t);
+        if (w) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) load4<T, VEC>(w, warp + static_cast<int64_t>(i) * warps, lane, a.D, wv[i]);
+        }
+    }
+    for (; t < a.T; t += step) {
         const T* x = static_cast<const T*>(a.x) + t * a.ld_x;
         const T* r = a.res ? static_cast<const T*>(a.res) + t * a.ld_res : nullptr;
         T* hrow = a.h ? static_cast<T*>(a.h) + t * a.ld_h : nullptr;
-        constexpr int N = CPT > 0 ? CPT : 1;
-        T hv[N][4];
         float sum = 0.f;
         if (CPT > 0) {
-            T rv[N][4];
 #pragma unroll
-            for (int i = 0; i < N; ++i) load4<T, VEC>(x, warp + static_cast<int64_t>(i) * warps, lane, a.D, hv[i]);
-            if (r) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) load4<T, VEC>(r, warp + static_cast<int64_t>(i) * warps, lane, a.D, rv[i]);
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) hv[i][j] = narrow<T>(widen(hv[i][j]) + widen(rv[i][j]));
-                    if (hrow) store4<T, VEC>(hrow, warp + static_cast<int64_t>(i) * warps, lane, a.D, hv[i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < N; ++i)
+            for (int i = 0; i < N; ++i) {
+                add(xv[i], rv[i], hv[i]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) sum = fmaf(widen(hv[i][j]), widen(hv[i][j]), sum);
+            }
+            if (t + step < a.T) load_row(t + step);
+            if (hrow) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) store4<T, VEC>(hrow, warp + static_cast<int64_t>(i) * warps, lane, a.D, hv[i]);
+            }
         } else {
             for (int64_t g = warp; g < groups; g += warps) {
-                load4<T, VEC>(x, g, lane, a.D, hv[0]);
-                if (r) {
-                    T rv[4];
-                    load4<T, VEC>(r, g, lane, a.D, rv);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) hv[0][j] = narrow<T>(widen(hv[0][j]) + widen(rv[j]));
-                    if (hrow) store4<T, VEC>(hrow, g, lane, a.D, hv[0]);
-                }
+                load4<T, VEC>(x, g, lane, a.D, xv[0]);
+                if (r) load4<T, VEC>(r, g, lane, a.D, rv[0]);
+                add(xv[0], rv[0], hv[0]);
+                if (hrow) store4<T, VEC>(hrow, g, lane, a.D, hv[0]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) sum = fmaf(widen(hv[0][j]), widen(hv[0][j]), sum);
             }
@@ -172,12 +188,10 @@ __global__ void __launch_bounds__(32 * max_warps(CPT)) rmsnorm_kernel(const RmsN
         const float rstd = 1.f / sqrtf(sum / static_cast<float>(a.D) + a.eps);
         if (a.rstd && warp == 0 && lane == 0) a.rstd[t] = rstd;
         T* yrow = a.y ? static_cast<T*>(a.y) + t * a.ld_y : nullptr;
-        auto out_group = [&](int64_t g, const T(&h4)[4]) {
-            T wv[4];
-            if (w) load4<T, VEC>(w, g, lane, a.D, wv);
+        auto out_group = [&](int64_t g, const T(&h4)[4], const T(&w4)[4]) {
             float y[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = widen(h4[j]) * rstd * (w ? widen(wv[j]) : 1.f);
+            for (int j = 0; j < 4; ++j) y[j] = widen(h4[j]) * rstd * (w ? widen(w4[j]) : 1.f);
             if (a.q) store_group<VEC>(a, t, g, lane, y);
             if (yrow) {
                 T yv[4];
@@ -190,19 +204,20 @@ __global__ void __launch_bounds__(32 * max_warps(CPT)) rmsnorm_kernel(const RmsN
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int64_t g = warp + static_cast<int64_t>(i) * warps;
-                if (g < groups) out_group(g, hv[i]);  // the same for the whole warp
+                if (g < groups) out_group(g, hv[i], wv[i]);  // the same for the whole warp
             }
         } else {
             for (int64_t g = warp; g < groups; g += warps) {
                 // the lane reads back what it wrote itself, or forms h again
-                load4<T, VEC>(hrow ? hrow : x, g, lane, a.D, hv[0]);
-                if (r && !hrow) {
-                    T rv[4];
-                    load4<T, VEC>(r, g, lane, a.D, rv);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) hv[0][j] = narrow<T>(widen(hv[0][j]) + widen(rv[j]));
+                if (hrow) {
+                    load4<T, VEC>(hrow, g, lane, a.D, hv[0]);
+                } else {
+                    load4<T, VEC>(x, g, lane, a.D, xv[0]);
+                    if (r) load4<T, VEC>(r, g, lane, a.D, rv[0]);
+                    add(xv[0], rv[0], hv[0]);
                 }
-                out_group(g, hv[0]);
+                if (w) load4<T, VEC>(w, g, lane, a.D, wv[0]);
+                out_group(g, hv[0], wv[0]);
             }
         }
     }
@@ -210,10 +225,11 @@ __global__ void __launch_bounds__(32 * max_warps(CPT)) rmsnorm_kernel(const RmsN
 
 // Backward. A CTA takes the rows t = blockIdx.x, + gridDim.x, ...; a thread owns
 // the same columns in all of them, so its share of dweight stays in registers
-// and is written once, to the CTA's row of `partial`. CPT = 0: no dweight here
-// (long rows, see rmsnorm_dw_kernel), dy and h read twice.
+// and is written once, to the CTA's row of `partial`. The next row's loads are
+// issued before this row's sum is waited for. CPT = 0: no dweight here (long
+// rows, see rmsnorm_dw_kernel), dy and h read twice.
 template <typename T, bool VEC, int CPT>
-__global__ void __launch_bounds__(32 * max_warps(CPT)) rmsnorm_grad_kernel(const RmsNormGradArgs a, int warps, bool with_dw) {
+__global__ void __launch_bounds__(32 * max_warps(CPT), grad_min_ctas(CPT)) rmsnorm_grad_kernel(const RmsNormGradArgs a, int warps, bool with_dw) {
     __shared__ float buf[2][kMaxWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t groups = (a.D + kGroup - 1) / kGroup;
@@ -224,66 +240,92 @@ __global__ void __launch_bounds__(32 * max_warps(CPT)) rmsnorm_grad_kernel(const
     for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    int slot = 0;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    T dyv[N][4], hv[N][4], rv[N][4], wv[N][4];
+    float rstd_next = 0.f;
+    auto load_row = [&](int64_t t) {
         const T* dy = static_cast<const T*>(a.dy) + t * a.ld_dy;
         const T* h = static_cast<const T*>(a.h) + t * a.ld_h;
-        const T* dr = a.dres ? static_cast<const T*>(a.dres) + t * a.ld_dres : nullptr;
-        T* dh = a.dh ? static_cast<T*>(a.dh) + t * a.ld_dh : nullptr;
-        const float rstd = a.rstd[t];
-        T dyv[N][4], hv[N][4];
-        float dot = 0.f;
-        auto add_dot = [&](int64_t g, const T(&d4)[4], const T(&h4)[4]) {
-            T wv[4];
-            if (w) load4<T, VEC>(w, g, lane, a.D, wv);
+        rstd_next = a.rstd[t];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dot = fmaf(widen(d4[j]) * (w ? widen(wv[j]) : 1.f), widen(h4[j]), dot);
+        for (int i = 0; i < N; ++i) {
+            load4<T, VEC>(dy, warp + static_cast<int64_t>(i) * warps, lane, a.D, dyv[i]);
+            load4<T, VEC>(h, warp + static_cast<int64_t>(i) * warps, lane, a.D, hv[i]);
+        }
+    };
+    int64_t t = blockIdx.x;
+    if (CPT > 0) {
+        if (t < a.T) load_row(t);
+        if (w) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) load4<T, VEC>(w, warp + static_cast<int64_t>(i) * warps, lane, a.D, wv[i]);
+        }
+    }
+    int slot = 0;
+    for (; t < a.T; t += gridDim.x) {
+        const T* dy = static_cast<const T*>(a.dy) + t * a.ld_dy;
+        const T* h = static_cast<const T*>(a.h) + t * a.ld_h;
+        const T* dr = a.dres && a.dh ? static_cast<const T*>(a.dres) + t * a.ld_dres : nullptr;
+        T* dh = a.dh ? static_cast<T*>(a.dh) + t * a.ld_dh : nullptr;
+        const float rstd = CPT > 0 ? rstd_next : a.rstd[t];
+        float g[N][4], hf[N][4];  // dy w and h of the row
+        float dot = 0.f;
+        auto take = [&](const T(&d4)[4], const T(&h4)[4], const T(&w4)[4], float(&g4)[4], float(&f4)[4]) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                g4[j] = widen(d4[j]) * (w ? widen(w4[j]) : 1.f);
+                f4[j] = widen(h4[j]);
+                dot = fmaf(g4[j], f4[j], dot);
+            }
         };
         if (CPT > 0) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                load4<T, VEC>(dy, warp + static_cast<int64_t>(i) * warps, lane, a.D, dyv[i]);
-                load4<T, VEC>(h, warp + static_cast<int64_t>(i) * warps, lane, a.D, hv[i]);
-            }
+                take(dyv[i], hv[i], wv[i], g[i], hf[i]);
+                if (with_dw) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) add_dot(warp + static_cast<int64_t>(i) * warps, dyv[i], hv[i]);
+                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(widen(dyv[i][j]), hf[i][j] * rstd, acc[i][j]);
+                }
+            }
+            if (dr) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) load4<T, VEC>(dr, warp + static_cast<int64_t>(i) * warps, lane, a.D, rv[i]);
+            }
+            if (t + gridDim.x < a.T) load_row(t + gridDim.x);
         } else {
-            for (int64_t g = warp; g < groups; g += warps) {
-                load4<T, VEC>(dy, g, lane, a.D, dyv[0]);
-                load4<T, VEC>(h, g, lane, a.D, hv[0]);
-                add_dot(g, dyv[0], hv[0]);
+            for (int64_t k = warp; k < groups; k += warps) {
+                load4<T, VEC>(dy, k, lane, a.D, dyv[0]);
+                load4<T, VEC>(h, k, lane, a.D, hv[0]);
+                if (w) load4<T, VEC>(w, k, lane, a.D, wv[0]);
+                take(dyv[0], hv[0], wv[0], g[0], hf[0]);
             }
         }
+        if (!dh) continue;  // dweight alone needs no row sum
         dot = row_sum(dot, warps, warp, lane, buf, slot);
         slot ^= 1;
         const float c = rstd * rstd * (dot / static_cast<float>(a.D));
-        auto out_group = [&](int64_t g, const T(&d4)[4], const T(&h4)[4]) {
-            T wv[4], rv[4], ov[4];
-            if (w) load4<T, VEC>(w, g, lane, a.D, wv);
-            if (dr) load4<T, VEC>(dr, g, lane, a.D, rv);
+        auto out_group = [&](int64_t k, const float(&g4)[4], const float(&f4)[4], const T(&r4)[4]) {
+            T ov[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float gj = widen(d4[j]) * (w ? widen(wv[j]) : 1.f);
-                const float v = rstd * (gj - widen(h4[j]) * c);
-                ov[j] = narrow<T>(dr ? v + widen(rv[j]) : v);
+                const float v = rstd * (g4[j] - f4[j] * c);
+                ov[j] = narrow<T>(dr ? v + widen(r4[j]) : v);
             }
-            store4<T, VEC>(dh, g, lane, a.D, ov);
+            store4<T, VEC>(dh, k, lane, a.D, ov);
         };
         if (CPT > 0) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int64_t g = warp + static_cast<int64_t>(i) * warps;
-                if (dh && g < groups) out_group(g, dyv[i], hv[i]);
-                if (with_dw) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(widen(dyv[i][j]), widen(hv[i][j]) * rstd, acc[i][j]);
-                }
+                const int64_t k = warp + static_cast<int64_t>(i) * warps;
+                if (k < groups) out_group(k, g[i], hf[i], rv[i]);
             }
-        } else if (dh) {
-            for (int64_t g = warp; g < groups; g += warps) {
-                load4<T, VEC>(dy, g, lane, a.D, dyv[0]);
-                load4<T, VEC>(h, g, lane, a.D, hv[0]);
-                out_group(g, dyv[0], hv[0]);
+        } else {
+            for (int64_t k = warp; k < groups; k += warps) {
+                load4<T, VEC>(dy, k, lane, a.D, dyv[0]);
+                load4<T, VEC>(h, k, lane, a.D, hv[0]);
+                if (w) load4<T, VEC>(w, k, lane, a.D, wv[0]);
+                if (dr) load4<T, VEC>(dr, k, lane, a.D, rv[0]);
+                take(dyv[0], hv[0], wv[0], g[0], hf[0]);
+                out_group(k, g[0], hf[0], rv[0]);
             }
         }
     }
@@ -350,7 +392,9 @@ cudaError_t run_forward(const RmsNormArgs& a, int sm_count, cudaStream_t stream)
     const int rows_per_cta = warps == 1 ? 4 : 1;
     const int threads = warps == 1 ? 128 : 32 * warps;
     const int64_t ctas = (a.T + rows_per_cta - 1) / rows_per_cta;
-    const unsigned grid = static_cast<unsigned>(ctas < (int64_t(1) << 30) ? ctas : (int64_t(1) << 30));
+    // persistent: as many CTAs as fit the SMs at 64 registers a thread
+    const int64_t fit = static_cast<int64_t>(sm_count) * (1024 / threads > 0 ? 1024 / threads : 1);
+    const unsigned grid = static_cast<unsigned>(ctas < fit ? ctas : fit);
     switch (cpt) {
         case 0: rmsnorm_kernel<T, VEC, 0><<<grid, threads, 0, stream>>>(a, warps, rows_per_cta); break;
         case 1: rmsnorm_kernel<T, VEC, 1><<<grid, threads, 0, stream>>>(a, warps, rows_per_cta); break;
