@@ -7,12 +7,16 @@
 //                        dw = sum over rows of dy h rstd
 //
 // Both are bound by memory traffic: a row is read once, kept in registers
-// while its sum is formed, and written once. The unit of work is a warp on a
-// group of 128 columns: 4 elements a lane, so that a group's largest magnitude
-// is one warp reduction and its 8-bit values one 128-byte store, whatever the
-// type. A row takes `warps` warps with CPT groups each; rows of one warp share
-// a CTA of four. The row's sum crosses warps through shared memory in a fixed
-// order, so results do not depend on timing.
+// while its sum is formed, and written once. The unit of work is a warp on two
+// groups of 128 columns, 8 elements a lane (16 bytes of a 16-bit type), so that a
+// group's largest magnitude is a reduction over half a warp whatever the type,
+// and the scale's arithmetic is shared by 8 elements. A row takes `warps` warps
+// with CPT units each; rows of one warp share a CTA of four. CTAs are persistent,
+// keep their weights, and load the next row before they wait for this one's sum.
+// The sum crosses warps through shared memory in a fixed order, so results do not
+// depend on timing.
+#include <algorithm>
+
 #include "vnm_dense.h"
 #include "vnm_fp8.cuh"
 
@@ -20,63 +24,54 @@ namespace vnm {
 namespace {
 
 constexpr int kMaxWarps = 32;
-// Warps of a row that keeps `cpt` groups a warp in registers: 64 registers a
-// thread hold two groups, 128 hold eight.
-constexpr int max_warps(int cpt) { return cpt <= 2 ? kMaxWarps : 16; }
-constexpr int min_ctas(int cpt) { return cpt == 4 ? 2 : 1; }
-constexpr int grad_min_ctas(int) { return 1; }
+constexpr int kUnit = 2 * kGroup;  // columns of a warp's unit of work
+// Warps of a row that keeps `cpt` units a warp in registers: 64 registers a
+// thread hold one, 128 hold two or four.
+constexpr int max_warps(int cpt) { return cpt <= 1 ? kMaxWarps : 16; }
 
-// 4 elements of a lane as one vector access.
-template <typename T>
-struct Vec4;
-template <>
-struct Vec4<float> {
-    using type = uint4;
-};
-template <>
-struct Vec4<__half> {
-    using type = uint2;
-};
-template <>
-struct Vec4<__nv_bfloat16> {
-    using type = uint2;
-};
-
-// Column of element j of a lane in group g: 4 neighbours for vector accesses,
-// 32 apart for scalar ones (each access of the warp is then contiguous).
+// A lane's elements of a unit: 8 neighbours for vector accesses, 16 apart for
+// scalar ones (each access of a half-warp is then contiguous). first_column is the
+// lane's first; element j is at first_column + j * kStep.
 template <bool VEC>
-__device__ __forceinline__ int64_t column(int64_t g, int lane, int j) {
-    return g * kGroup + (VEC ? 4 * lane + j : lane + 32 * j);
+constexpr int kStep = VEC ? 1 : 16;
+template <bool VEC>
+__device__ __forceinline__ int64_t first_column(int64_t u, int lane) {
+    return u * kUnit + (lane >> 4) * kGroup + (lane & 15) * (VEC ? 8 : 1);
 }
 
-// The lane's elements of group g of a row; columns from D on read as 0.
+// A lane's 8 elements of a unit, as they came.
+template <typename T>
+struct alignas(16) Elems {
+    T v[8];
+};
+
+// The lane's elements of a row, `left` = D less the lane's first column: past the
+// row's end they read as 0. p: the row's element at that column.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load4(const T* row, int64_t g, int lane, int64_t D, T (&v)[4]) {
-    if (VEC) {  // D % 4 == 0: the lane's 4 are inside or outside together
-        typename Vec4<T>::type raw{};
-        const int64_t c = column<VEC>(g, lane, 0);
-        if (c < D) raw = *reinterpret_cast<const typename Vec4<T>::type*>(row + c);
-        *reinterpret_cast<typename Vec4<T>::type*>(v) = raw;
+__device__ __forceinline__ void load8(const T* p, int64_t left, Elems<T>& e) {
+    if (VEC) {  // D % 8 == 0: the lane's 8 are inside or outside together
+        uint4* raw = reinterpret_cast<uint4*>(&e);
+#pragma unroll
+        for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k)
+            raw[k] = left > 0 ? reinterpret_cast<const uint4*>(p)[k] : make_uint4(0, 0, 0, 0);
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t c = column<VEC>(g, lane, j);
-            v[j] = c < D ? row[c] : narrow<T>(0.f);
-        }
+        for (int j = 0; j < 8; ++j) e.v[j] = left > j * kStep<VEC> ? p[j * kStep<VEC>] : narrow<T>(0.f);
     }
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store4(T* row, int64_t g, int lane, int64_t D, const T (&v)[4]) {
+__device__ __forceinline__ void store8(T* p, int64_t left, const Elems<T>& e) {
     if (VEC) {
-        const int64_t c = column<VEC>(g, lane, 0);
-        if (c < D) *reinterpret_cast<typename Vec4<T>::type*>(row + c) = *reinterpret_cast<const typename Vec4<T>::type*>(v);
+        const uint4* raw = reinterpret_cast<const uint4*>(&e);
+        if (left > 0) {
+#pragma unroll
+            for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k) reinterpret_cast<uint4*>(p)[k] = raw[k];
+        }
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t c = column<VEC>(g, lane, j);
-            if (c < D) row[c] = v[j];
-        }
+        for (int j = 0; j < 8; ++j)
+            if (left > j * kStep<VEC>) p[j * kStep<VEC>] = e.v[j];
     }
 }
 
@@ -96,248 +91,291 @@ __device__ __forceinline__ float row_sum(float v, int warps, int warp, int lane,
     return warp_sum(lane < warps ? buf[slot][lane] : 0.f);
 }
 
-// One 8-bit group: the scale and the lane's 4 values.
+// 1 / sqrt(v) to fp32 accuracy: the approximation and one Newton step.
+__device__ __forceinline__ float inverse_root(float v) {
+    const float r = rsqrtf(v);
+    const float e = fmaf(-v * r, r, 1.f);
+    const float n = fmaf(0.5f * r, e, r);
+    return isfinite(n) ? n : r;  // v = 0, Inf, or too small or large for the step
+}
+
+// The unit's two 8-bit groups: the scale of the half-warp's, and the lane's 8
+// values. q: the row's byte at the lane's first column, s: the group's scale.
 template <bool VEC>
-__device__ __forceinline__ void store_group(const RmsNormArgs& a, int64_t t, int64_t g, int lane, const float (&y)[4]) {
-    uint32_t m = max(max(magnitude_bits(y[0]), magnitude_bits(y[1])), max(magnitude_bits(y[2]), magnitude_bits(y[3])));
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
+__device__ __forceinline__ void store_groups(const float (&y)[8], bool e5m2, uint8_t* q, float* s, int64_t left, int lane) {
+    float m = max_magnitude(y[0], y[1]);
+#pragma unroll
+    for (int j = 2; j < 8; ++j) m = max_magnitude(m, y[j]);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max_magnitude(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     float inv;
-    const float s = group_scale(m, a.e5m2, inv);
-    if (lane == 0) a.s[t * a.s_rs + g * a.s_cs] = s;
-    const uint32_t q = to_fp8x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv, a.e5m2);
-    uint8_t* row = static_cast<uint8_t*>(a.q) + t * a.ld_q;
+    const float scale = group_scale(m, e5m2, inv);
+    if ((lane & 15) == 0 && left > 0) *s = scale;
+    const uint32_t lo = to_fp8x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv, e5m2);
+    const uint32_t hi = to_fp8x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv, e5m2);
     if (VEC) {
-        const int64_t c = column<VEC>(g, lane, 0);
-        if (c < a.D) *reinterpret_cast<uint32_t*>(row + c) = q;
+        if (left > 0) *reinterpret_cast<uint2*>(q) = make_uint2(lo, hi);
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t c = column<VEC>(g, lane, j);
-            if (c < a.D) row[c] = static_cast<uint8_t>(q >> (8 * j));
-        }
+        for (int j = 0; j < 8; ++j)
+            if (left > j * kStep<VEC>) q[j * kStep<VEC>] = static_cast<uint8_t>((j < 4 ? lo : hi) >> (8 * (j & 3)));
     }
 }
 
 // Forward. A CTA takes the rows blockIdx.x, + gridDim.x, ... CPT > 0: the row's
-// groups stay in registers, its weights too, and the next row's loads are issued
-// before this row's sum is waited for. CPT = 0: rows longer than the registers
-// hold; h is formed twice from the inputs (or read back where it was stored).
+// units stay in registers. CPT = 0: rows longer than the registers hold; h is
+// formed twice from the inputs (or read back where it was stored).
 template <typename T, bool VEC, int CPT>
-__global__ void __launch_bounds__(32 * max_warps(CPT), min_ctas(CPT)) rmsnorm_kernel(const RmsNormArgs a, int warps, int rows_per_cta) {
+__global__ void __launch_bounds__(32 * max_warps(CPT), 1) rmsnorm_kernel(const RmsNormArgs a, int warps, int rows_per_cta) {
     __shared__ float buf[2][kMaxWarps];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int warp = warps == 1 ? 0 : wid;
-    const int64_t groups = (a.D + kGroup - 1) / kGroup;
     const int64_t step = static_cast<int64_t>(gridDim.x) * rows_per_cta;
-    const T* w = static_cast<const T*>(a.w);
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * rows_per_cta + (warps == 1 ? wid : 0);
+    if (t0 >= a.T) return;
     constexpr int N = CPT > 0 ? CPT : 1;
-    T xv[N][4], rv[N][4], hv[N][4], wv[N][4];
-    auto load_row = [&](int64_t t) {
-        const T* x = static_cast<const T*>(a.x) + t * a.ld_x;
+    const int64_t c0 = first_column<VEC>(warp, lane);       // of the lane's first unit
+    const int64_t across = static_cast<int64_t>(warps) * kUnit;  // to the warp's next unit
+    // the lane's places in the row at hand; s: of its half-warp's group
+    const T* x = static_cast<const T*>(a.x) + t0 * a.ld_x + c0;
+    const T* r = a.res ? static_cast<const T*>(a.res) + t0 * a.ld_res + c0 : nullptr;
+    const T* w = a.w ? static_cast<const T*>(a.w) + c0 : nullptr;
+    T* h = a.h ? static_cast<T*>(a.h) + t0 * a.ld_h + c0 : nullptr;
+    T* y = a.y ? static_cast<T*>(a.y) + t0 * a.ld_y + c0 : nullptr;
+    uint8_t* q = a.q ? static_cast<uint8_t*>(a.q) + t0 * a.ld_q + c0 : nullptr;
+    float* s = a.s ? a.s + t0 * a.s_rs + (2 * static_cast<int64_t>(warp) + (lane >> 4)) * a.s_cs : nullptr;
+    const int64_t s_across = 2 * static_cast<int64_t>(warps) * a.s_cs;
+    const float inv_d = 1.f / static_cast<float>(a.D);
+
+    Elems<T> x8[N], r8[N];
+    float hf[N][8], wf[N][8];
+    auto load_row = [&](const T* px, const T* pr) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) load4<T, VEC>(x, warp + static_cast<int64_t>(i) * warps, lane, a.D, xv[i]);
-        if (a.res) {
-            const T* r = static_cast<const T*>(a.res) + t * a.ld_res;
+        for (int i = 0; i < N; ++i) load8<T, VEC>(px + i * across, a.D - c0 - i * across, x8[i]);
+        if (pr) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) load4<T, VEC>(r, warp + static_cast<int64_t>(i) * warps, lane, a.D, rv[i]);
+            for (int i = 0; i < N; ++i) load8<T, VEC>(pr + i * across, a.D - c0 - i * across, r8[i]);
         }
     };
-    // h of the loaded elements
-    auto add = [&](const T(&x4)[4], const T(&r4)[4], T(&h4)[4]) {
+    auto load_weight = [&](const T* pw, int64_t left, float(&f)[8]) {
+        Elems<T> e;
+        if (pw) load8<T, VEC>(pw, left, e);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h4[j] = a.res ? narrow<T>(widen(x4[j]) + widen(r4[j])) : x4[j];
+        for (int j = 0; j < 8; ++j) f[j] = pw ? widen(e.v[j]) : 1.f;
     };
-    int slot = 0;
-    int64_t t = static_cast<int64_t>(blockIdx.x) * rows_per_cta + (warps == 1 ? wid : 0);
+    float sum = 0.f;
+    // h of the loaded elements as it is stored, widened, and its squares
+    auto add = [&](const Elems<T>& xe, const Elems<T>& re, float(&f)[8], T* ph, int64_t left) {
+        if (r) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = widen(xe.v[j]) + widen(re.v[j]);
+            Elems<T> he;
+            narrow8(f, he.v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = widen(he.v[j]);
+            if (ph) store8<T, VEC>(ph, left, he);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = widen(xe.v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+    };
+    auto out_unit = [&](int64_t u, float rstd, const float(&f)[8], const float(&wt)[8]) {
+        const int64_t left = a.D - c0 - u * across;
+        float yf[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) yf[j] = f[j] * rstd * wt[j];
+        if (q) store_groups<VEC>(yf, a.e5m2, q + u * across, s + u * s_across, left, lane);
+        if (y) {
+            Elems<T> ye;
+            narrow8(yf, ye.v);
+            store8<T, VEC>(y + u * across, left, ye);
+        }
+    };
     if (CPT > 0) {
-        if (t < a.T) load_row(t);
-        if (w) {
+        load_row(x, r);
 #pragma unroll
-            for (int i = 0; i < N; ++i) load4<T, VEC>(w, warp + static_cast<int64_t>(i) * warps, lane, a.D, wv[i]);
-        }
+        for (int i = 0; i < N; ++i) load_weight(w ? w + i * across : nullptr, a.D - c0 - i * across, wf[i]);
     }
-    for (; t < a.T; t += step) {
-        const T* x = static_cast<const T*>(a.x) + t * a.ld_x;
-        const T* r = a.res ? static_cast<const T*>(a.res) + t * a.ld_res : nullptr;
-        T* hrow = a.h ? static_cast<T*>(a.h) + t * a.ld_h : nullptr;
-        float sum = 0.f;
+    int slot = 0;
+    for (int64_t t = t0; t < a.T; t += step) {
+        sum = 0.f;
+        const int64_t own = (a.D + across - 1 - warp * kUnit) / across;  // units of this warp
         if (CPT > 0) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                add(xv[i], rv[i], hv[i]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sum = fmaf(widen(hv[i][j]), widen(hv[i][j]), sum);
-            }
-            if (t + step < a.T) load_row(t + step);
-            if (hrow) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) store4<T, VEC>(hrow, warp + static_cast<int64_t>(i) * warps, lane, a.D, hv[i]);
-            }
+            for (int i = 0; i < N; ++i)
+                add(x8[i], r8[i], hf[i], h ? h + i * across : nullptr, a.D - c0 - i * across);
+            if (t + step < a.T) load_row(x + step * a.ld_x, r ? r + step * a.ld_res : nullptr);
         } else {
-            for (int64_t g = warp; g < groups; g += warps) {
-                load4<T, VEC>(x, g, lane, a.D, xv[0]);
-                if (r) load4<T, VEC>(r, g, lane, a.D, rv[0]);
-                add(xv[0], rv[0], hv[0]);
-                if (hrow) store4<T, VEC>(hrow, g, lane, a.D, hv[0]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sum = fmaf(widen(hv[0][j]), widen(hv[0][j]), sum);
+            for (int64_t u = 0; u < own; ++u) {
+                const int64_t left = a.D - c0 - u * across;
+                load8<T, VEC>(x + u * across, left, x8[0]);
+                if (r) load8<T, VEC>(r + u * across, left, r8[0]);
+                add(x8[0], r8[0], hf[0], h ? h + u * across : nullptr, left);
             }
         }
-        sum = row_sum(sum, warps, warp, lane, buf, slot);
+        const float total = row_sum(sum, warps, warp, lane, buf, slot);
         slot ^= 1;
-        const float rstd = 1.f / sqrtf(sum / static_cast<float>(a.D) + a.eps);
+        const float rstd = inverse_root(fmaf(total, inv_d, a.eps));
         if (a.rstd && warp == 0 && lane == 0) a.rstd[t] = rstd;
-        T* yrow = a.y ? static_cast<T*>(a.y) + t * a.ld_y : nullptr;
-        auto out_group = [&](int64_t g, const T(&h4)[4], const T(&w4)[4]) {
-            float y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = widen(h4[j]) * rstd * (w ? widen(w4[j]) : 1.f);
-            if (a.q) store_group<VEC>(a, t, g, lane, y);
-            if (yrow) {
-                T yv[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) yv[j] = narrow<T>(y[j]);
-                store4<T, VEC>(yrow, g, lane, a.D, yv);
-            }
-        };
         if (CPT > 0) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int64_t g = warp + static_cast<int64_t>(i) * warps;
-                if (g < groups) out_group(g, hv[i], wv[i]);  // the same for the whole warp
-            }
+            for (int i = 0; i < N; ++i)
+                if (i < own) out_unit(i, rstd, hf[i], wf[i]);  // the same for the whole warp
         } else {
-            for (int64_t g = warp; g < groups; g += warps) {
+            for (int64_t u = 0; u < own; ++u) {
+                const int64_t left = a.D - c0 - u * across;
                 // the lane reads back what it wrote itself, or forms h again
-                if (hrow) {
-                    load4<T, VEC>(hrow, g, lane, a.D, hv[0]);
+                load8<T, VEC>((h ? h : x) + u * across, left, x8[0]);
+                if (r && !h) {
+                    load8<T, VEC>(r + u * across, left, r8[0]);
+                    add(x8[0], r8[0], hf[0], nullptr, left);
                 } else {
-                    load4<T, VEC>(x, g, lane, a.D, xv[0]);
-                    if (r) load4<T, VEC>(r, g, lane, a.D, rv[0]);
-                    add(xv[0], rv[0], hv[0]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) hf[0][j] = widen(x8[0].v[j]);
                 }
-                if (w) load4<T, VEC>(w, g, lane, a.D, wv[0]);
-                out_group(g, hv[0], wv[0]);
+                load_weight(w ? w + u * across : nullptr, left, wf[0]);
+                out_unit(u, rstd, hf[0], wf[0]);
             }
         }
+        x += step * a.ld_x;
+        if (r) r += step * a.ld_res;
+        if (h) h += step * a.ld_h;
+        if (y) y += step * a.ld_y;
+        if (q) q += step * a.ld_q;
+        if (s) s += step * a.s_rs;
     }
 }
 
 // Backward. A CTA takes the rows t = blockIdx.x, + gridDim.x, ...; a thread owns
 // the same columns in all of them, so its share of dweight stays in registers
-// and is written once, to the CTA's row of `partial`. The next row's loads are
-// issued before this row's sum is waited for. CPT = 0: no dweight here (long
-// rows, see rmsnorm_dw_kernel), dy and h read twice.
+// and is written once, to the CTA's row of `partial`. CPT = 0: no dweight here
+// (long rows, see rmsnorm_dw_kernel), dy and h read twice.
 template <typename T, bool VEC, int CPT>
-__global__ void __launch_bounds__(32 * max_warps(CPT), grad_min_ctas(CPT)) rmsnorm_grad_kernel(const RmsNormGradArgs a, int warps, bool with_dw) {
+__global__ void __launch_bounds__(32 * max_warps(CPT), 1) rmsnorm_grad_kernel(const RmsNormGradArgs a, int warps, bool with_dw) {
     __shared__ float buf[2][kMaxWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t groups = (a.D + kGroup - 1) / kGroup;
-    const T* w = static_cast<const T*>(a.w);
+    const int64_t step = gridDim.x;
     constexpr int N = CPT > 0 ? CPT : 1;
-    float acc[N][4];
+    constexpr bool kAhead = CPT == 1 || CPT == 2;  // the next row's loads in flight: four units leave no registers for it
+    const int64_t c0 = first_column<VEC>(warp, lane);
+    const int64_t across = static_cast<int64_t>(warps) * kUnit;
+    const int64_t own = (a.D + across - 1 - warp * kUnit) / across;  // units of this warp
+    const T* dy = static_cast<const T*>(a.dy) + blockIdx.x * a.ld_dy + c0;
+    const T* h = static_cast<const T*>(a.h) + blockIdx.x * a.ld_h + c0;
+    const T* dr = a.dres && a.dh ? static_cast<const T*>(a.dres) + blockIdx.x * a.ld_dres + c0 : nullptr;
+    T* dh = a.dh ? static_cast<T*>(a.dh) + blockIdx.x * a.ld_dh + c0 : nullptr;
+    const T* w = a.w ? static_cast<const T*>(a.w) + c0 : nullptr;
+    const float inv_d = 1.f / static_cast<float>(a.D);
+    float acc[N][8];
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    T dyv[N][4], hv[N][4], rv[N][4], wv[N][4];
+        for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+    Elems<T> dn[kAhead ? N : 1], hn[kAhead ? N : 1], d8[N], h8[N], r8[N], w8[N];  // dn, hn: the next row's dy and h
     float rstd_next = 0.f;
-    auto load_row = [&](int64_t t) {
-        const T* dy = static_cast<const T*>(a.dy) + t * a.ld_dy;
-        const T* h = static_cast<const T*>(a.h) + t * a.ld_h;
+    auto load_row = [&](const T* pd, const T* ph, int64_t t, Elems<T>* de, Elems<T>* he) {
         rstd_next = a.rstd[t];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            load4<T, VEC>(dy, warp + static_cast<int64_t>(i) * warps, lane, a.D, dyv[i]);
-            load4<T, VEC>(h, warp + static_cast<int64_t>(i) * warps, lane, a.D, hv[i]);
+            load8<T, VEC>(pd + i * across, a.D - c0 - i * across, de[i]);
+            load8<T, VEC>(ph + i * across, a.D - c0 - i * across, he[i]);
         }
     };
-    int64_t t = blockIdx.x;
     if (CPT > 0) {
-        if (t < a.T) load_row(t);
+        if (kAhead) load_row(dy, h, blockIdx.x, dn, hn);
         if (w) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) load4<T, VEC>(w, warp + static_cast<int64_t>(i) * warps, lane, a.D, wv[i]);
+            for (int i = 0; i < N; ++i) load8<T, VEC>(w + i * across, a.D - c0 - i * across, w8[i]);
         }
     }
+    // dy w
+    auto scaled = [&](const Elems<T>& de, const Elems<T>& we, int j) {
+        return widen(de.v[j]) * (w ? widen(we.v[j]) : 1.f);
+    };
+    float rstd = 0.f, c = 0.f;
+    auto out_unit = [&](int64_t u, const Elems<T>& de, const Elems<T>& he, const Elems<T>& we, const Elems<T>& re) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float v = fmaf(-widen(he.v[j]), c, scaled(de, we, j));
+            f[j] = dr ? fmaf(rstd, v, widen(re.v[j])) : rstd * v;
+        }
+        Elems<T> oe;
+        narrow8(f, oe.v);
+        store8<T, VEC>(dh + u * across, a.D - c0 - u * across, oe);
+    };
     int slot = 0;
-    for (; t < a.T; t += gridDim.x) {
-        const T* dy = static_cast<const T*>(a.dy) + t * a.ld_dy;
-        const T* h = static_cast<const T*>(a.h) + t * a.ld_h;
-        const T* dr = a.dres && a.dh ? static_cast<const T*>(a.dres) + t * a.ld_dres : nullptr;
-        T* dh = a.dh ? static_cast<T*>(a.dh) + t * a.ld_dh : nullptr;
-        const float rstd = CPT > 0 ? rstd_next : a.rstd[t];
-        float g[N][4], hf[N][4];  // dy w and h of the row
+    for (int64_t t = blockIdx.x; t < a.T; t += step) {
         float dot = 0.f;
-        auto take = [&](const T(&d4)[4], const T(&h4)[4], const T(&w4)[4], float(&g4)[4], float(&f4)[4]) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                g4[j] = widen(d4[j]) * (w ? widen(w4[j]) : 1.f);
-                f4[j] = widen(h4[j]);
-                dot = fmaf(g4[j], f4[j], dot);
-            }
-        };
         if (CPT > 0) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                take(dyv[i], hv[i], wv[i], g[i], hf[i]);
-                if (with_dw) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(widen(dyv[i][j]), hf[i][j] * rstd, acc[i][j]);
-                }
-            }
             if (dr) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) load4<T, VEC>(dr, warp + static_cast<int64_t>(i) * warps, lane, a.D, rv[i]);
+                for (int i = 0; i < N; ++i) load8<T, VEC>(dr + i * across, a.D - c0 - i * across, r8[i]);
             }
-            if (t + gridDim.x < a.T) load_row(t + gridDim.x);
+            if (kAhead) {
+                rstd = rstd_next;
+#pragma unroll
+                for (int i = 0; i < (kAhead ? N : 1); ++i) {
+                    d8[i] = dn[i];
+                    h8[i] = hn[i];
+                }
+                if (t + step < a.T) load_row(dy + step * a.ld_dy, h + step * a.ld_h, t + step, dn, hn);
+            } else {
+                load_row(dy, h, t, d8, h8);
+                rstd = rstd_next;
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float hj = widen(h8[i].v[j]);
+                    dot = fmaf(scaled(d8[i], w8[i], j), hj, dot);
+                    acc[i][j] = fmaf(widen(d8[i].v[j]), hj * rstd, acc[i][j]);
+                }
         } else {
-            for (int64_t k = warp; k < groups; k += warps) {
-                load4<T, VEC>(dy, k, lane, a.D, dyv[0]);
-                load4<T, VEC>(h, k, lane, a.D, hv[0]);
-                if (w) load4<T, VEC>(w, k, lane, a.D, wv[0]);
-                take(dyv[0], hv[0], wv[0], g[0], hf[0]);
+            rstd = a.rstd[t];
+            for (int64_t u = 0; u < own; ++u) {
+                const int64_t left = a.D - c0 - u * across;
+                load8<T, VEC>(dy + u * across, left, d8[0]);
+                load8<T, VEC>(h + u * across, left, h8[0]);
+                if (w) load8<T, VEC>(w + u * across, left, w8[0]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dot = fmaf(scaled(d8[0], w8[0], j), widen(h8[0].v[j]), dot);
             }
         }
-        if (!dh) continue;  // dweight alone needs no row sum
-        dot = row_sum(dot, warps, warp, lane, buf, slot);
-        slot ^= 1;
-        const float c = rstd * rstd * (dot / static_cast<float>(a.D));
-        auto out_group = [&](int64_t k, const float(&g4)[4], const float(&f4)[4], const T(&r4)[4]) {
-            T ov[4];
+        if (dh) {  // dweight alone needs no row sum
+            const float total = row_sum(dot, warps, warp, lane, buf, slot);
+            slot ^= 1;
+            c = rstd * rstd * (total * inv_d);
+            if (CPT > 0) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float v = rstd * (g4[j] - f4[j] * c);
-                ov[j] = narrow<T>(dr ? v + widen(r4[j]) : v);
+                for (int i = 0; i < N; ++i)
+                    if (i < own) out_unit(i, d8[i], h8[i], w8[i], r8[i]);
+            } else {
+                for (int64_t u = 0; u < own; ++u) {
+                    const int64_t left = a.D - c0 - u * across;
+                    load8<T, VEC>(dy + u * across, left, d8[0]);
+                    load8<T, VEC>(h + u * across, left, h8[0]);
+                    if (w) load8<T, VEC>(w + u * across, left, w8[0]);
+                    if (dr) load8<T, VEC>(dr + u * across, left, r8[0]);
+                    out_unit(u, d8[0], h8[0], w8[0], r8[0]);
+                }
             }
-            store4<T, VEC>(dh, k, lane, a.D, ov);
-        };
-        if (CPT > 0) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int64_t k = warp + static_cast<int64_t>(i) * warps;
-                if (k < groups) out_group(k, g[i], hf[i], rv[i]);
-            }
-        } else {
-            for (int64_t k = warp; k < groups; k += warps) {
-                load4<T, VEC>(dy, k, lane, a.D, dyv[0]);
-                load4<T, VEC>(h, k, lane, a.D, hv[0]);
-                if (w) load4<T, VEC>(w, k, lane, a.D, wv[0]);
-                if (dr) load4<T, VEC>(dr, k, lane, a.D, rv[0]);
-                take(dyv[0], hv[0], wv[0], g[0], hf[0]);
-                out_group(k, g[0], hf[0], rv[0]);
-            }
+            dh += step * a.ld_dh;
         }
+        dy += step * a.ld_dy;
+        h += step * a.ld_h;
+        if (dr) dr += step * a.ld_dres;
     }
     if (CPT > 0 && with_dw) {
-        float* part = a.partial + static_cast<int64_t>(blockIdx.x) * a.D;
+        float* part = a.partial + static_cast<int64_t>(blockIdx.x) * a.D + c0;
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t c = column<VEC>(warp + static_cast<int64_t>(i) * warps, lane, j);
-                if (c < a.D) part[c] = acc[i][j];
-            }
+            for (int j = 0; j < 8; ++j)
+                if (a.D - c0 - i * across > j * kStep<VEC>) part[i * across + j * kStep<VEC>] = acc[i][j];
     }
 }
 
@@ -369,38 +407,39 @@ __global__ void rmsnorm_dw_reduce_kernel(const float* partial, int64_t parts, in
     }
 }
 
+// Rows of 8 elements on 8 * elem bytes (16 at most).
 bool vec_ok(const void* p, int64_t ld, int elem) {
-    return p == nullptr || (reinterpret_cast<uintptr_t>(p) % (4 * elem) == 0 && ld % 4 == 0);
+    return p == nullptr || (reinterpret_cast<uintptr_t>(p) % (elem == 1 ? 8 : 16) == 0 && ld % 8 == 0);
 }
 
-// Groups a warp keeps in registers, for a row of `groups` groups: the fewest that
-// cover it (0: none does, the row is read twice). With enough rows to fill the
-// GPU, fewer and busier warps a row.
-int groups_per_warp(int64_t groups, bool many_rows) {
-    int c = 1;
-    while (c <= 8 && groups > static_cast<int64_t>(c) * max_warps(c)) c *= 2;
-    if (c > 8) return 0;
-    while (many_rows && c < 4 && groups > c) c *= 2;
-    return c;
+// Units a warp keeps in registers for a row of `units` (0: too many, the row is
+// read twice), and the row's warps. Two units a warp where the rows fill the GPU:
+// the sum across warps and the row's scalars are then shared by 16 elements a
+// lane; with few rows one unit, for the shortest chain.
+int units_per_warp(int64_t units, bool many_rows, int& warps) {
+    const int cpt = units <= max_warps(1) && !(many_rows && units >= 4) ? 1
+                    : units <= 2 * max_warps(2)                        ? 2
+                    : units <= 4 * max_warps(4)                        ? 4
+                                                                       : 0;
+    warps = cpt == 0 ? kMaxWarps : static_cast<int>((units + cpt - 1) / cpt);
+    return cpt;
 }
 
 template <typename T, bool VEC>
 cudaError_t run_forward(const RmsNormArgs& a, int sm_count, cudaStream_t stream) {
-    const int64_t groups = (a.D + kGroup - 1) / kGroup;
-    const int cpt = groups_per_warp(groups, a.T > 2 * sm_count);
-    const int warps = cpt == 0 ? kMaxWarps : static_cast<int>((groups + cpt - 1) / cpt);
+    int warps;
+    const int cpt = units_per_warp((a.D + kUnit - 1) / kUnit, a.T >= 4 * sm_count, warps);
     const int rows_per_cta = warps == 1 ? 4 : 1;
     const int threads = warps == 1 ? 128 : 32 * warps;
     const int64_t ctas = (a.T + rows_per_cta - 1) / rows_per_cta;
-    // persistent: as many CTAs as fit the SMs at 64 registers a thread
-    const int64_t fit = static_cast<int64_t>(sm_count) * (1024 / threads > 0 ? 1024 / threads : 1);
-    const unsigned grid = static_cast<unsigned>(ctas < fit ? ctas : fit);
+    // persistent: the CTAs that fit at 64, 84 or 128 registers a thread
+    const int64_t fit = static_cast<int64_t>(sm_count) * std::max(1, (cpt == 1 ? 1024 : cpt == 2 ? 768 : 512) / threads);
+    const unsigned grid = static_cast<unsigned>(std::min(ctas, fit));
     switch (cpt) {
         case 0: rmsnorm_kernel<T, VEC, 0><<<grid, threads, 0, stream>>>(a, warps, rows_per_cta); break;
         case 1: rmsnorm_kernel<T, VEC, 1><<<grid, threads, 0, stream>>>(a, warps, rows_per_cta); break;
         case 2: rmsnorm_kernel<T, VEC, 2><<<grid, threads, 0, stream>>>(a, warps, rows_per_cta); break;
-        case 4: rmsnorm_kernel<T, VEC, 4><<<grid, threads, 0, stream>>>(a, warps, rows_per_cta); break;
-        default: rmsnorm_kernel<T, VEC, 8><<<grid, threads, 0, stream>>>(a, warps, rows_per_cta); break;
+        default: rmsnorm_kernel<T, VEC, 4><<<grid, threads, 0, stream>>>(a, warps, rows_per_cta); break;
     }
     return cudaGetLastError();
 }
@@ -408,18 +447,19 @@ cudaError_t run_forward(const RmsNormArgs& a, int sm_count, cudaStream_t stream)
 template <typename T>
 cudaError_t forward_of(const RmsNormArgs& a, int sm_count, cudaStream_t stream) {
     const int e = sizeof(T);
-    const bool vec = a.D % 4 == 0 && vec_ok(a.x, a.ld_x, e) && vec_ok(a.res, a.ld_res, e) && vec_ok(a.w, 0, e) &&
+    const bool vec = a.D % 8 == 0 && vec_ok(a.x, a.ld_x, e) && vec_ok(a.res, a.ld_res, e) && vec_ok(a.w, 0, e) &&
                      vec_ok(a.h, a.ld_h, e) && vec_ok(a.y, a.ld_y, e) && vec_ok(a.q, a.ld_q, 1);
     return vec ? run_forward<T, true>(a, sm_count, stream) : run_forward<T, false>(a, sm_count, stream);
 }
 
-constexpr int64_t kGradParts = 304;  // two CTAs for each of 152 SMs
+// Rows of partial sums of dweight, and CTAs, at most: four for each of 152 SMs
+// where a row's warps leave room for them, two (of 512 threads or more) elsewhere.
+int64_t grad_parts_of(int64_t D) { return D <= 8 * kUnit ? 608 : 304; }
 
 template <typename T, bool VEC>
 cudaError_t run_grad(const RmsNormGradArgs& a, cudaStream_t stream) {
-    const int64_t groups = (a.D + kGroup - 1) / kGroup;
-    const int cpt = groups_per_warp(groups, a.T > kGradParts);
-    const int warps = cpt == 0 ? kMaxWarps : static_cast<int>((groups + cpt - 1) / cpt);
+    int warps;
+    const int cpt = units_per_warp((a.D + kUnit - 1) / kUnit, a.T >= 608, warps);
     const int64_t parts = rmsnorm_grad_parts(a.T, a.D);
     const bool dw = a.dw != nullptr;
     if (a.T > 0) {
@@ -434,8 +474,7 @@ cudaError_t run_grad(const RmsNormGradArgs& a, cudaStream_t stream) {
             case 0: rmsnorm_grad_kernel<T, VEC, 0><<<grid, 32 * warps, 0, stream>>>(a, warps, false); break;
             case 1: rmsnorm_grad_kernel<T, VEC, 1><<<grid, 32 * warps, 0, stream>>>(a, warps, dw); break;
             case 2: rmsnorm_grad_kernel<T, VEC, 2><<<grid, 32 * warps, 0, stream>>>(a, warps, dw); break;
-            case 4: rmsnorm_grad_kernel<T, VEC, 4><<<grid, 32 * warps, 0, stream>>>(a, warps, dw); break;
-            default: rmsnorm_grad_kernel<T, VEC, 8><<<grid, 32 * warps, 0, stream>>>(a, warps, dw); break;
+            default: rmsnorm_grad_kernel<T, VEC, 4><<<grid, 32 * warps, 0, stream>>>(a, warps, dw); break;
         }
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
@@ -451,7 +490,7 @@ cudaError_t run_grad(const RmsNormGradArgs& a, cudaStream_t stream) {
 template <typename T>
 cudaError_t grad_of(const RmsNormGradArgs& a, cudaStream_t stream) {
     const int e = sizeof(T);
-    const bool vec = a.D % 4 == 0 && vec_ok(a.dy, a.ld_dy, e) && vec_ok(a.h, a.ld_h, e) && vec_ok(a.w, 0, e) &&
+    const bool vec = a.D % 8 == 0 && vec_ok(a.dy, a.ld_dy, e) && vec_ok(a.h, a.ld_h, e) && vec_ok(a.w, 0, e) &&
                      vec_ok(a.dres, a.ld_dres, e) && vec_ok(a.dh, a.ld_dh, e);
     return vec ? run_grad<T, true>(a, stream) : run_grad<T, false>(a, stream);
 }
@@ -466,7 +505,7 @@ cudaError_t launch_rmsnorm(const RmsNormArgs& a, vnm_dtype type, int sm_count, c
     }
 }
 
-int64_t rmsnorm_grad_parts(int64_t T, int64_t) { return T < kGradParts ? T : kGradParts; }
+int64_t rmsnorm_grad_parts(int64_t T, int64_t D) { return std::min(T, grad_parts_of(D)); }
 
 cudaError_t launch_rmsnorm_grad(const RmsNormGradArgs& a, vnm_dtype type, cudaStream_t stream) {
     switch (type) {

@@ -22,6 +22,20 @@ __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_
 template <>
 __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// 8 fp32 values rounded, in pairs.
+__device__ __forceinline__ void narrow8(const float (&f)[8], float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = f[j];
+}
+__device__ __forceinline__ void narrow8(const float (&f)[8], __half (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) *reinterpret_cast<__half2*>(&v[j]) = __floats2half2_rn(f[j], f[j + 1]);
+}
+__device__ __forceinline__ void narrow8(const float (&f)[8], __nv_bfloat16 (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) *reinterpret_cast<__nv_bfloat162*>(&v[j]) = __floats2bfloat162_rn(f[j], f[j + 1]);
+}
+
 // Largest finite values of the two formats.
 constexpr float kMaxE4m3 = 448.f;
 constexpr float kMaxE5m2 = 57344.f;
@@ -34,19 +48,28 @@ constexpr float kMinScale = 0x1p-100f;
 // of a group and whether it holds a non-finite value.
 __device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// Scale of a group whose largest magnitude has these bits, and its reciprocal
-// (both NaN for a group with a non-finite value, so that its q are NaN too).
-// Elements are multiplied by the rounded reciprocal rather than divided by the
-// scale: an element within 2^-23 of the middle between two fp8 values may round
-// to the other one, which is 2^-19 of its rounding error at most.
-__device__ __forceinline__ float group_scale(uint32_t bits, bool e5m2, float& inv) {
-    if (bits >= 0x7F800000u) {
-        inv = __uint_as_float(0x7FC00000u);
-        return inv;
-    }
-    const float s = fmaxf(__fdiv_rn(__uint_as_float(bits), e5m2 ? kMaxE5m2 : kMaxE4m3), kMinScale);
+// The larger magnitude, NaN if either is one.
+__device__ __forceinline__ float max_magnitude(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
+}
+
+// Scale of a group of largest magnitude m, m * (1 / F) but at least 2^-100, and
+// its reciprocal (both NaN for a group with a non-finite value, so that its q are
+// NaN too). Elements are multiplied by the rounded reciprocal rather than
+// divided by the scale: an element within 2^-23 of the middle between two fp8
+// values may round to the other one, which is 2^-19 of its rounding error at
+// most. A division in the norm's epilogue costs as much as the rest of a group.
+__device__ __forceinline__ float group_scale(float m, bool e5m2, float& inv) {
+    float s = m * (e5m2 ? 1.f / kMaxE5m2 : 1.f / kMaxE4m3);
+    s = s < kMinScale ? kMinScale : s;  // (false for NaN)
+    if (m == __uint_as_float(0x7F800000u)) s = __uint_as_float(0x7FC00000u);
     inv = __frcp_rn(s);
     return s;
+}
+__device__ __forceinline__ float group_scale(uint32_t bits, bool e5m2, float& inv) {
+    return group_scale(__uint_as_float(bits), e5m2, inv);
 }
 
 // Two fp32 values to fp8 (nearest even, saturating, NaN kept), `lo` in the low byte.
