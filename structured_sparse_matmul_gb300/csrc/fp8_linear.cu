@@ -52,12 +52,14 @@ struct FlCfg {
     static constexpr int kQRows = BN / CG;
     static constexpr int kQBytes = kQRows * 128;
     static constexpr int kStageBytes = kPBytes + kQBytes;
-    static constexpr int kStages = CG == 2 ? 5 : BN == 128 ? 6 : 8;
+    // narrow tiles: two CTAs an SM, whose waits overlap
+    static constexpr int kCtas = BN <= 64 ? 2 : 1;
+    static constexpr int kStages = CG == 2 ? 5 : BN == 128 ? 6 : BN == 64 ? 4 : BN == 32 ? 5 : 6;
     static constexpr int kAcc = BN == 256 ? 2 : 4;  // TMEM buffers
     static constexpr int kTmemCols = kAcc * BN;
     static constexpr int kAddWarps = BN >= 128 ? 8 : 4;
     static constexpr int kCols = BN * 4 / kAddWarps;  // columns a thread adds up
-    static constexpr int kLoad = kCols < 32 ? kCols : 32;  // columns of one TMEM load
+    static constexpr int kLoad = BN >= 128 ? 32 : 16;  // columns of one TMEM load
     static constexpr int kThreads = 32 * (kHelpers + kAddWarps);
     // Registers: 128 sums and two loads of 32 columns do not fit the 168 that 12
     // warps get; the adding warps take what the helper warps leave. The shares
@@ -70,10 +72,11 @@ struct FlCfg {
     static constexpr int kScaleSlots = ONE ? 0 : 8;
     // a pair's outputs leave by TMA stores, from 32 rows x 128 bytes for each adding warp
     static constexpr int kStoreBytes = CG == 2 ? kAddWarps * kStoreBox : 0;
-    // over half an SM's shared memory, so that a second CTA never waits for TMEM
-    // that the first one holds
+    // no CTA waits for TMEM that another of this kernel holds: either the CTAs that
+    // share an SM leave each other room, or the shared memory keeps a second one out
     static constexpr int kSmem = kStages * kStageBytes + kStoreBytes + kScaleSlots * BN * 4 + 1024;
-    static_assert(kSmem > 116 * 1024 && kSmem <= 226 * 1024, "one CTA an SM");
+    static_assert(kCtas * kTmemCols <= 512, "TMEM of the CTAs that share an SM");
+    static_assert(kCtas == 2 ? 2 * (kSmem + 2048) <= 228 * 1024 : kSmem > 116 * 1024 && kSmem <= 226 * 1024, "shared memory");
     static_assert(CG == 2 || kTileM * BN * 4 <= kStages * kStageBytes, "the split's sums fit the stage ring");
 };
 
@@ -239,25 +242,12 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, bool v
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
-__device__ __forceinline__ float load_any(const void* p, int type, int64_t i) {
-    if (type == VNM_F32) return static_cast<const float*>(p)[i];
-    if (type == VNM_F16) return __half2float(static_cast<const __half*>(p)[i]);
-    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-
-__device__ __forceinline__ void store_any(void* p, int type, int64_t i, float v) {
-    if (type == VNM_F32)
-        static_cast<float*>(p)[i] = v;
-    else if (type == VNM_F16)
-        static_cast<__half*>(p)[i] = __float2half_rn(v);
-    else
-        static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-}
-
-__device__ __forceinline__ float activate(int act, float v) {
-    // a comparison rather than fmaxf, which would turn NaN into 0
-    if (act == VNM_ACT_RELU) return v < 0.f ? 0.f : v;
-    if (act == VNM_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+__device__ __forceinline__ float4 dsmem_ld_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
@@ -334,9 +324,9 @@ __device__ __forceinline__ void tile_at(const FlArgs& a, int tile, int& mt, int&
 
 // F32: Y is fp32 (for a pair's staged output).
 template <int BN, bool ONE, int CG, bool F32>
-__global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, 1)
+__global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, CG>::kCtas)
     fp8_linear_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
-                      const __grid_constant__ CUtensorMap tm_y, const FlArgs a) {
+                      const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ FlArgs a) {
     using Cfg = FlCfg<BN, ONE, CG>;
     constexpr int ST = Cfg::kStages, ACC = Cfg::kAcc, SS = Cfg::kScaleSlots, COLS = Cfg::kCols, LD = Cfg::kLoad;
     constexpr int SSB = SS > 0 ? SS : 1;
@@ -354,7 +344,22 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, 1)
     float* const scales = reinterpret_cast<float*>(smem_gen + ST * Cfg::kStageBytes + Cfg::kStoreBytes);  // [SS][BN]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int pair_rank = CG == 2 ? static_cast<int>(blockIdx.x & 1) : 0;
+    // this CTA's tiles and K blocks: every role walks the same sequence
+    const int rank = CG == 1 && a.splits > 1 ? static_cast<int>(blockIdx.x) % a.splits : 0;
+    const int tile0 = static_cast<int>(blockIdx.x) / (CG == 2 ? 2 : a.splits);
+    const int tile_step = a.splits > 1 ? a.tiles : static_cast<int>(gridDim.x) / CG;
+    const int kb0 = rank * a.kb_per_split;
+    const int kb1 = min(a.num_kb, kb0 + a.kb_per_split);
 
+    const int early = CG == 1 ? min(ST, kb1 - kb0) : 0;  // stages loaded before the setup is over
+
+    // one stage's loads into its slot (a single CTA's)
+    auto load_stage = [&](int slot, int kb, int prow, int qrow) {
+        const uint32_t fb = smem_u32(&full_bar[slot]), sp = smem_base + slot * Cfg::kStageBytes;
+        mbar_arrive_expect_tx(fb, Cfg::kStageBytes);
+        tma_load_2d(sp, &tm_p, kb * 128, prow, fb);
+        tma_load_2d(sp + Cfg::kPBytes, &tm_q, kb * 128, qrow, fb);
+    };
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(smem_u32(&full_bar[s]), 1);
@@ -367,10 +372,11 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, 1)
         }
         abort_flag = 0;
         fence_barrier_init();
-    }
-    if (threadIdx.x == 64) {
-        tma_prefetch_desc(&tm_p);
-        tma_prefetch_desc(&tm_q);
+        // the first stages need no other thread: their latency covers the TMEM allocation
+        int mt, nt;
+        tile_at(a, tile0, mt, nt);
+        for (int k = 0; k < early; ++k)
+            if (k != a.skip_stage || blockIdx.x != 0) load_stage(k, kb0 + k, mt * kTileM, nt * BN);
     }
     if (warp == 1) tmem_alloc_group<CG>(smem_u32(&tmem_slot), Cfg::kTmemCols);
     tc_fence_before_sync();
@@ -379,13 +385,6 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem = tmem_slot;
     volatile int* abort = &abort_flag;
-
-    // this CTA's tiles and K blocks: every role walks the same sequence
-    const int rank = CG == 1 && a.splits > 1 ? static_cast<int>(blockIdx.x) % a.splits : 0;
-    const int tile0 = static_cast<int>(blockIdx.x) / (CG == 2 ? 2 : a.splits);
-    const int tile_step = a.splits > 1 ? a.tiles : static_cast<int>(gridDim.x) / CG;
-    const int kb0 = rank * a.kb_per_split;
-    const int kb1 = min(a.num_kb, kb0 + a.kb_per_split);
 
     if (Cfg::kSplitRegs && warp < kHelpers) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kHelperRegs));
     if (warp == 0) {
@@ -398,14 +397,14 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, 1)
             tile_at(a, tile, mt, nt);
             const int prow = (mt * CG + pair_rank) * kTileM, qrow = nt * BN + pair_rank * Cfg::kQRows;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                if (!mbar_wait_warp(smem_u32(&done_bar[slot]), phase, abort)) {
+                if (it >= early && !mbar_wait_warp(smem_u32(&done_bar[slot]), phase, abort)) {
                     run = false;
                     break;
                 }
-                if (elect_one() && (it != a.skip_stage || blockIdx.x != 0)) {
-                    const uint32_t fb = smem_u32(&full_bar[slot]);
-                    const uint32_t sp = smem_base + slot * Cfg::kStageBytes;
+                if (it >= early && elect_one() && (it != a.skip_stage || blockIdx.x != 0)) {
                     if (CG == 2) {
+                        const uint32_t fb = smem_u32(&full_bar[slot]);
+                        const uint32_t sp = smem_base + slot * Cfg::kStageBytes;
                         // the second CTA's bytes may arrive before the first CTA expects them: the
                         // phase cannot end before that CTA's own arrival
                         const uint32_t lead = dsmem_map(fb, 0);
@@ -413,9 +412,7 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, 1)
                         tma_load_2d_pair(sp, &tm_p, kb * 128, prow, lead);
                         tma_load_2d_pair(sp + Cfg::kPBytes, &tm_q, kb * 128, qrow, lead);
                     } else {
-                        mbar_arrive_expect_tx(fb, Cfg::kStageBytes);
-                        tma_load_2d(sp, &tm_p, kb * 128, prow, fb);
-                        tma_load_2d(sp + Cfg::kPBytes, &tm_q, kb * 128, qrow, fb);
+                        load_stage(slot, kb, prow, qrow);
                     }
                 }
                 __syncwarp();
@@ -683,19 +680,31 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, 1)
         cluster_sync_all();
         int mt, nt;
         tile_at(a, tile0, mt, nt);
-        const int share = BN / a.splits;
-        for (int i = threadIdx.x; i < share * kTileM; i += Cfg::kThreads) {
-            const int c = rank * share + i / kTileM, row = i % kTileM;
+        const int share = (BN + a.splits - 1) / a.splits, c0 = rank * share, c1 = min(BN, c0 + share);
+        const int64_t n0 = static_cast<int64_t>(nt) * BN;
+        // four rows of a column at a time
+        for (int i = threadIdx.x; i < (c1 - c0) * (kTileM / 4); i += Cfg::kThreads) {
+            const int c = c0 + i / (kTileM / 4), row = 4 * (i % (kTileM / 4));
+            const int64_t m = static_cast<int64_t>(mt) * kTileM + row, n = n0 + c;
+            if (m >= a.m || n >= a.n) continue;
             const uint32_t addr = smem_base + 4 * (c * kTileM + row);
-            float v[kMaxSplits];
+            float4 v[kMaxSplits];
 #pragma unroll
-            for (int s = 0; s < kMaxSplits; ++s) v[s] = s < a.splits ? dsmem_ld_f32(dsmem_map(addr, s)) : 0.f;
-            float sum = v[0];
+            for (int s = 0; s < kMaxSplits; ++s)
+                if (s < a.splits) v[s] = dsmem_ld_v4(dsmem_map(addr, s));
+            float4 sum = v[0];
 #pragma unroll
             for (int s = 1; s < kMaxSplits; ++s)
-                if (s < a.splits) sum += v[s];
-            const int64_t m = static_cast<int64_t>(mt) * kTileM + row, n = static_cast<int64_t>(nt) * BN + c;
-            if (m < a.m && n < a.n) store_one(a, m, n, sum);
+                if (s < a.splits) {
+                    sum.x += v[s].x;
+                    sum.y += v[s].y;
+                    sum.z += v[s].z;
+                    sum.w += v[s].w;
+                }
+            float out[4] = {sum.x, sum.y, sum.z, sum.w};
+            const int here = static_cast<int>(min(static_cast<int64_t>(4), a.m - m));
+#pragma unroll 1
+            for (int j = 0; j < here; ++j) store_one(a, m + j, n, out[j]);
         }
         cluster_sync_all();  // no CTA leaves while others read its sums
     }
@@ -782,7 +791,7 @@ cudaError_t run(const Fp8LinearArgs& g, FlArgs a, int splits, int sm_count, cuda
         attr_set[dev].store(true, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg = {};
-    const int64_t ctas = splits > 1 ? tiles * splits : CG * std::min<int64_t>(tiles, std::max(1, sm_count / CG));
+    const int64_t ctas = splits > 1 ? tiles * splits : CG * std::min<int64_t>(tiles, std::max(1, sm_count * Cfg::kCtas / CG));
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(Cfg::kThreads);
     cfg.dynamicSmemBytes = Cfg::kSmem;
@@ -796,6 +805,42 @@ cudaError_t run(const Fp8LinearArgs& g, FlArgs a, int splits, int sm_count, cuda
     return cudaLaunchKernelEx(&cfg, fp8_linear_kernel<BN, ONE, CG, F32>, tm_p, tm_q, tm_y, a);
 }
 
+// How a product of T tokens and R outputs over num_kb K blocks is tiled: pairs
+// of CTAs (bn = 0), X on the M side; or W on the M side, tiles of bn tokens, K over
+// `splits` CTAs of a cluster.
+struct TilePlan {
+    int bn, splits;
+};
+
+// The times the plan compares, in us, fitted to measurements over T = 1 .. 8192,
+// R = 300 .. 11008, K = 1024 .. 8192: a launch with its first loads and its last
+// stores; then the longer of a CTA's chain of K blocks and of its tiles' loads from
+// L2. At 4096 x 4096 (T, narrow, pairs): (64, 10.0, 20), (256, 19.3, 20.2), (512,
+// 32.7, 20.8); at 777 x 1000 x 1041: 13.1 and 9.9; at 100 x 300 x 8192: 8.3 and 36.
+TilePlan plan_tiles(int64_t T, int64_t R, int num_kb, bool one_scale, int sm_count) {
+    auto ceil_div = [](int64_t p, int64_t q) { return (p + q - 1) / q; };
+    TilePlan best{0, 1};
+    const int64_t pair_waves = ceil_div(ceil_div(T, 256) * ceil_div(R, 256), std::max(1, sm_count / 2));
+    double least = 4.0 + static_cast<double>(pair_waves) * num_kb * (one_scale ? 0.5 : 0.95);
+    for (int bn : {16, 32, 64, 128}) {
+        if (bn > 16 && bn / 2 >= T) break;  // the width below holds all tokens
+        const int64_t tiles = ceil_div(R, kTileM) * ceil_div(T, bn);
+        const int slots = sm_count * (bn <= 64 ? 2 : 1);
+        for (int splits : {1, 2, 4, 8}) {
+            if (splits > 1 && (splits > num_kb || tiles * splits > slots)) break;
+            const int64_t kbs = ceil_div(num_kb, splits), waves = ceil_div(tiles * splits, slots);
+            const double chain = static_cast<double>(waves * kbs) * (bn == 128 ? 0.45 : bn == 64 ? 0.30 : 0.25);
+            const double loads = static_cast<double>(tiles * num_kb) * (kTileM + bn) * 128 / 7e6;
+            const double t = 4.9 + std::max(chain, loads) + (splits == 8 ? 1.3 : splits > 1 ? 0.3 : 0.0);
+            if (t < least) {
+                least = t;
+                best = TilePlan{bn, splits};
+            }
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const ScaleView& xs, const void* wq,
@@ -803,10 +848,11 @@ cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const S
                               const void* bias, vnm_dtype bias_type, int act, void* y, int64_t ld_y, vnm_dtype y_type,
                               int* status, int skip_stage, int sm_count, cudaStream_t stream) {
     auto ceil_div = [](int64_t p, int64_t q) { return (p + q - 1) / q; };
-    // Many tiles of 256 tokens x 256 outputs: X on the M side, pairs of CTAs. Otherwise W on the
-    // M side, the narrowest tile that holds the tokens (128 at most), and K split
-    // while the tiles leave SMs idle.
-    const bool wide = 3 * ceil_div(T, 256) * ceil_div(R, 256) >= sm_count;
+    if (K > 0 && skip_stage < 0 && fp8_decode_serves(T))
+        return launch_fp8_decode(xq, ld_x, x_e5m2, xs, wq, ld_w, w_e5m2, ws, T, R, K, bias, bias_type, act, y, ld_y,
+                                 y_type, stream);
+    const TilePlan plan = plan_tiles(T, R, static_cast<int>(ceil_div(K, 128)), ws.shift != 0, sm_count);
+    const bool wide = plan.bn == 0;
     Fp8LinearArgs g{};
     if (wide)
         g = Fp8LinearArgs{xq, wq, ld_x, ld_w, x_e5m2, w_e5m2, xs, ws, T, R, K, y, ld_y, 1, y_type, bias, bias_type,
@@ -842,15 +888,11 @@ cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const S
                                             : run<256, false, 2, true>(g, a, 1, sm_count, stream)
                : ws.shift        ? run<256, true, 2>(g, a, 1, sm_count, stream)
                                  : run<256, false, 2>(g, a, 1, sm_count, stream);
-    const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
-    const int64_t tiles = ceil_div(R, kTileM) * ceil_div(T, bn);
-    int splits = 1;
-    while (splits < kMaxSplits && tiles * splits * 2 <= sm_count && a.num_kb >= 2 * splits) splits *= 2;
-    switch (bn) {
-        case 16: return run<16, false, 1>(g, a, splits, sm_count, stream);
-        case 32: return run<32, false, 1>(g, a, splits, sm_count, stream);
-        case 64: return run<64, false, 1>(g, a, splits, sm_count, stream);
-        default: return run<128, false, 1>(g, a, splits, sm_count, stream);
+    switch (plan.bn) {
+        case 16: return run<16, false, 1>(g, a, plan.splits, sm_count, stream);
+        case 32: return run<32, false, 1>(g, a, plan.splits, sm_count, stream);
+        case 64: return run<64, false, 1>(g, a, plan.splits, sm_count, stream);
+        default: return run<128, false, 1>(g, a, plan.splits, sm_count, stream);
     }
 }
 

@@ -77,4 +77,11 @@ cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const S
                               const void* bias, vnm_dtype bias_type, int act, void* y, int64_t ld_y, vnm_dtype y_type,
                               int* status, int skip_stage, int sm_count, cudaStream_t stream);
 
+// The same product for a few tokens (T >= 1, K >= 1).
+bool fp8_decode_serves(int64_t T);
+cudaError_t launch_fp8_decode(const void* xq, int64_t ld_x, bool x_e5m2, const ScaleView& xs, const void* wq,
+                              int64_t ld_w, bool w_e5m2, const ScaleView& ws, int64_t T, int64_t R, int64_t K,
+                              const void* bias, vnm_dtype bias_type, int act, void* y, int64_t ld_y, vnm_dtype y_type,
+                              cudaStream_t stream);
+
 }  // namespace vnm

@@ -7,6 +7,8 @@
 #include <cuda_fp8.h>
 #include <stdint.h>
 
+#include "../../include/vnm.h"
+
 namespace vnm {
 
 __device__ __forceinline__ float widen(float v) { return v; }
@@ -79,6 +81,29 @@ __device__ __forceinline__ uint32_t to_fp8x2(float lo, float hi, bool e5m2) {
 
 __device__ __forceinline__ uint32_t to_fp8x4(float a, float b, float c, float d, bool e5m2) {
     return to_fp8x2(a, b, e5m2) | (to_fp8x2(c, d, e5m2) << 16);
+}
+
+// An element of a vnm_dtype array.
+__device__ __forceinline__ float load_any(const void* p, int type, int64_t i) {
+    if (type == VNM_F32) return static_cast<const float*>(p)[i];
+    if (type == VNM_F16) return __half2float(static_cast<const __half*>(p)[i]);
+    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+__device__ __forceinline__ void store_any(void* p, int type, int64_t i, float v) {
+    if (type == VNM_F32)
+        static_cast<float*>(p)[i] = v;
+    else if (type == VNM_F16)
+        static_cast<__half*>(p)[i] = __float2half_rn(v);
+    else
+        static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+__device__ __forceinline__ float activate(int act, float v) {
+    // a comparison rather than fmaxf, which would turn NaN into 0
+    if (act == VNM_ACT_RELU) return v < 0.f ? 0.f : v;
+    if (act == VNM_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+    return v;
 }
 
 }  // namespace vnm
