@@ -266,23 +266,11 @@ __device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The bias and the activation of 16 neighbouring columns of row m. One copy of
-// this code: unrolled over a thread's columns, the activations' code alone is
-// tens of KB, and fetching it took 20 us a tile.
-__device__ __noinline__ void finish16(const FlArgs& a, int64_t m, int64_t n, float (&v)[16]) {
-    if (a.bias && a.bias_on_m) {
-        const float b = load_any(a.bias, a.bias_type, m);
+// One copy of this code: unrolled over a thread's columns, GELU's alone is tens of
+// KB, and fetching it took 20 us a tile.
+__device__ __noinline__ void gelu16(float (&v)[16]) {
 #pragma unroll
-        for (int u = 0; u < 16; ++u) v[u] += b;
-    } else if (a.bias) {
-#pragma unroll
-        for (int u = 0; u < 16; ++u)
-            if (n + u < a.n) v[u] += load_any(a.bias, a.bias_type, n + u);
-    }
-    if (a.act != VNM_ACT_NONE) {
-#pragma unroll
-        for (int u = 0; u < 16; ++u) v[u] = activate(a.act, v[u]);
-    }
+    for (int u = 0; u < 16; ++u) v[u] = activate(VNM_ACT_GELU, v[u]);
 }
 
 // 16 neighbouring outputs of row m from their finished sums: 16-byte stores where
@@ -618,14 +606,29 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
                 continue;
             }
             const int64_t m = static_cast<int64_t>(m0) + lane;
-            const bool finish = a.bias || a.act != VNM_ACT_NONE;
-            if (finish && m < a.m) {
+            if (a.bias) {
+                // the bias of the row, or of columns lane, lane + 32, ... (the sum over a
+                // cluster adds it by itself)
+                float bias[(COLS + 31) / 32];
+#pragma unroll
+                for (int i = 0; i < (COLS + 31) / 32; ++i) {
+                    const int64_t n = min(static_cast<int64_t>(n0) + 32 * i + lane, a.n - 1);
+                    bias[i] = load_any(a.bias, a.bias_type, a.bias_on_m ? min(m, a.m - 1) : n);
+                }
+#pragma unroll
+                for (int c = 0; c < COLS; ++c)
+                    sum[c] += a.bias_on_m ? bias[0] : __shfl_sync(0xFFFFFFFFu, bias[c / 32], c & 31);
+            }
+            if (a.act == VNM_ACT_RELU) {
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) sum[c] = activate(VNM_ACT_RELU, sum[c]);
+            } else if (a.act == VNM_ACT_GELU && m < a.m) {
 #pragma unroll
                 for (int c = 0; c < COLS; c += 16) {
                     float v[16];
 #pragma unroll
                     for (int u = 0; u < 16; ++u) v[u] = sum[c + u];
-                    finish16(a, m, n0 + c, v);
+                    gelu16(v);
 #pragma unroll
                     for (int u = 0; u < 16; ++u) sum[c + u] = v[u];
                 }
