@@ -2,13 +2,15 @@
 
 Each translation unit compiles in parallel; the link uses nvcc's static CUDA
 runtime, so the library needs only the driver at run time. Output:
-``structured_sparse_matmul_gb300/_build/libvnm.so`` (git-ignored).
+``structured_sparse_matmul_gb300/_build/libvnm.so`` (git-ignored), and beside it
+the Python binding's C part, ``_vnm_binding.so``.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from typing import List
 
@@ -17,6 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libvnm.so")
+BINDING_PATH = os.path.join(BUILD_DIR, "_vnm_binding.so")
 SOURCES = ["api.cu", "compress.cu", "spmm_simt.cu", "spmm_tc.cu", "spmm_noalloc.cu", "gemm_compress.cu", "energy.cu", "bitmap.cu",
            "rmsnorm.cu", "fp8_quantize.cu", "fp8_linear.cu", "fp8_decode.cu", "dense_api.cu"]
 HEADERS = ["vnm_internal.h", "vnm_ptx.cuh", "vnm_select.cuh", "vnm_dense.h", "vnm_fp8.cuh"]
@@ -31,16 +34,27 @@ def _nvcc() -> str:
 
 
 def _inputs() -> List[str]:
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
+    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS + ["binding.c"]]
     files += [os.path.join(ROOT, "include", h) for h in ("vnm.h", "vnm_testing.h")]
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return False
     t = os.path.getmtime(LIB_PATH)
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def build_binding() -> None:
+    """Compile the binding's C part with the host compiler for the running Python."""
+    tmp = BINDING_PATH + ".tmp"
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "binding.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on binding.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -65,6 +79,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
+    build_binding()  # before the library, whose time up_to_date() goes by
     tmp = LIB_PATH + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

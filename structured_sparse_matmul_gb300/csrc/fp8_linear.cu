@@ -63,9 +63,9 @@ struct FlCfg {
     static constexpr int kThreads = 32 * (kHelpers + kAddWarps);
     // Registers: 128 sums and two loads of 32 columns do not fit the 168 that 12
     // warps get; the adding warps take what the helper warps leave. The shares
-    // add up to the launch's (in warps: 4 x 72 + 8 x 216 = 12 x 168).
+    // add up to the launch's (in warps: 4 x 56 + 8 x 224 = 12 x 168).
     static constexpr bool kSplitRegs = kCols == 128;
-    static constexpr int kLaunchRegs = 168, kHelperRegs = 72, kAddRegs = 216;
+    static constexpr int kLaunchRegs = 168, kHelperRegs = 56, kAddRegs = 224;
     static_assert(!kSplitRegs || kHelpers * kHelperRegs + kAddWarps * kAddRegs == (kHelpers + kAddWarps) * kLaunchRegs,
                   "register shares");
     // Q's scales (ONE reads its one scale itself); they take about as long to arrive as an operand stage

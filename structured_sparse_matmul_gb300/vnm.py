@@ -7,6 +7,7 @@ or PyTorch fallback: if libvnm.so is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 from dataclasses import dataclass
@@ -453,89 +454,33 @@ def vnm_spmm_noalloc(R: int, K: int, V: int, M: int, values: torch.Tensor, meta:
 
 # ---- the dense neighbours of a pruned layer: norm, 8-bit form, 8-bit Linear layer ----
 
-_DTYPES = {torch.float16: VNM_F16, torch.float32: VNM_F32, torch.bfloat16: VNM_BF16}
-_FP8 = {torch.float8_e4m3fn: VNM_E4M3, torch.float8_e5m2: VNM_E5M2}
+# Marshalled in C (csrc/binding.c), which reads each tensor's description and
+# calls the library: they stand in decode loops, where a call's host time counts.
+
+_native_module = None
 
 
-def _dtype(t: torch.Tensor, name: str) -> int:
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name} must be fp16, bf16 or fp32")
-    return code
-
-
-def _fp8(t: torch.Tensor, name: str) -> int:
-    code = _FP8.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name} must be float8_e4m3fn or float8_e5m2")
-    return code
-
-
-# The checks below stand on every call of a decode loop, where the host's time is
-# the call's: each tensor attribute is read once (they cost 0.1 us and more).
-
-
-def _refuse(t: torch.Tensor, name: str, shape, dev: int, dtype) -> None:
-    want = f"{tuple(shape)}{f' and type {dtype}' if dtype is not None else ''} on cuda:{dev}"
-    raise ValueError(f"{name} must be a row-major tensor of shape {want}, got {tuple(t.shape)}, {t.dtype} on {t.device}")
-
-
-def _matrix(t: Optional[torch.Tensor], name: str, shape, dev: int, dtype=None):
-    """(pointer, leading dimension) of a row-major matrix of a given shape; (None, 1) for None."""
-    if t is None:
-        return None, 1
-    if t.shape != shape or t.get_device() != dev or (dtype is not None and t.dtype is not dtype):
-        _refuse(t, name, shape, dev, dtype)
-    ld, one = t.stride()
-    if one != 1 and shape[1] > 1:
-        _refuse(t, name, shape, dev, dtype)
-    # (a matrix of one row or column may carry any stride)
-    return t.data_ptr() or None, ld if ld >= shape[1] and ld > 0 else max(shape[1], 1)
-
-
-def _vector(t: Optional[torch.Tensor], name: str, n: int, dev: int, dtype=None):
-    """Pointer of a contiguous vector of n elements, None for None."""
-    if t is None:
-        return None
-    if t.shape != (n,) or t.get_device() != dev or (dtype is not None and t.dtype is not dtype) or \
-            (n > 1 and t.stride(0) != 1):
-        _refuse(t, name, (n,), dev, dtype)
-    return t.data_ptr() or None
-
-
-def _scales(t: Optional[torch.Tensor], name: str, shape, dev: int):
-    """(pointer, strides) of fp32 scales: any strides."""
-    if t is None:
-        return None, 0, 0
-    if t.shape != shape or t.dtype is not torch.float32 or t.get_device() != dev:
-        _refuse(t, name, shape, dev, torch.float32)
-    rs, cs = t.stride()
-    return t.data_ptr() or None, rs, cs
-
-
-def _on_current_device(t: torch.Tensor, name: str):
-    """(shape, device index) of a CUDA matrix on the current device."""
-    shape, dev = t.shape, t.get_device()
-    if dev < 0 or len(shape) != 2:
-        raise ValueError(f"{name} must be a CUDA matrix")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device")
-    return shape, dev
-
-
-def _stream_on(stream, dev: int) -> int:
-    """The stream's handle: of the given one, or of torch's current one on the device."""
-    if stream is not None:
-        return int(stream.cuda_stream)
-    return _current_stream(dev)
-
-
-def _current_stream_plain(dev: int) -> int:
-    return int(torch.cuda.current_stream(dev).cuda_stream)
-
-
-# 0.1 us where torch has it, 3 us through a stream object
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream_plain)
+def _native():
+    """The binding's C part, given the loaded library's functions."""
+    global _native_module
+    if _native_module is None:
+        L = lib()
+        if not os.path.exists(_build.BINDING_PATH):
+            raise RuntimeError(f"the binding is not built ({_build.BINDING_PATH} missing); run "
+                               "`python -c 'import __graft_entry__ as g; g.build()'` first")
+        spec = importlib.util.spec_from_file_location("_vnm_binding", _build.BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        functions = (L.vnm_rmsnorm, L.vnm_rmsnorm_backward, L.vnm_rmsnorm_backward_workspace_size, L.vnm_fp8_quantize,
+                     L.vnm_fp8_linear, L.vnm_testing_fp8_linear_skip_stage)
+        # torch's raw query of the current stream takes 0.1 us, a stream object 3
+        stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                         lambda device: int(torch.cuda.current_stream(device).cuda_stream))
+        module.setup(tuple(ctypes.cast(f, ctypes.c_void_p).value for f in functions),
+                     (torch.float16, torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.float8_e5m2, torch.int32),
+                     torch.cuda.current_device, stream)
+        _native_module = module
+    return _native_module
 
 
 def vnm_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float, residual: Optional[torch.Tensor] = None,
@@ -547,28 +492,17 @@ def vnm_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float, res
     x, residual, h, y: T x D of one type (fp16, bf16, fp32); weight (D,) or None;
     rstd fp32 (T,); q: T x D float8 and q_scale fp32 (T, ceil(D / 128)), the
     8-bit form of y. Outputs that are None are not written (y or q is needed)."""
-    shape, dev = _on_current_device(x, "x")
-    T, D = shape
-    dt, code = x.dtype, _dtype(x, "x")
-    xp, ld_x = _matrix(x, "x", shape, dev)
-    rp, ld_r = _matrix(residual, "residual", shape, dev, dt)
-    wp = _vector(weight, "weight", D, dev, dt)
-    hp, ld_h = _matrix(h, "h", shape, dev, dt)
-    yp, ld_y = _matrix(y, "y", shape, dev, dt)
-    sp = _vector(rstd, "rstd", T, dev, torch.float32)
-    qp, ld_q = _matrix(q, "q", shape, dev)
-    qt = _fp8(q, "q") if q is not None else VNM_E4M3
-    cp, c_rs, c_cs = _scales(q_scale, "q_scale", (T, (D + 127) >> 7), dev)
-    code = lib().vnm_rmsnorm(xp, ld_x, rp, ld_r, wp, eps, T, D, code, hp, ld_h, yp, ld_y, sp, qp, ld_q, qt, cp, c_rs,
-                             c_cs, _stream_on(stream, dev))
+    code = _native().rmsnorm(x, weight, eps, residual, h, y, rstd, q, q_scale, stream)
     if code:
         raise VnmError(code, "vnm_rmsnorm")
 
 
 def vnm_rmsnorm_backward_workspace_size(T: int, D: int) -> int:
-    n = ctypes.c_size_t(0)
-    _check(lib().vnm_rmsnorm_backward_workspace_size(T, D, ctypes.byref(n)), "vnm_rmsnorm_backward_workspace_size")
-    return int(n.value)
+    """Bytes of workspace that vnm_rmsnorm_backward needs for dweight."""
+    n = _native().rmsnorm_workspace(T, D)
+    if n < 0:
+        raise VnmError(-n, "vnm_rmsnorm_backward_workspace_size")
+    return n
 
 
 def vnm_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: Optional[torch.Tensor], rstd: torch.Tensor,
@@ -577,22 +511,10 @@ def vnm_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: Optional[tor
                          stream=None) -> None:
     """Gradients of vnm_rmsnorm: dh (T x D, of x and residual alike; dresidual
     added where given) and dweight (fp32 (D,)); either may be None."""
-    shape, dev = _on_current_device(dy, "dy")
-    T, D = shape
-    dt, code = dy.dtype, _dtype(dy, "dy")
-    yp, ld_dy = _matrix(dy, "dy", shape, dev)
-    hp, ld_h = _matrix(h, "h", shape, dev, dt)
-    wp = _vector(weight, "weight", D, dev, dt)
-    sp = _vector(rstd, "rstd", T, dev, torch.float32)
-    rp, ld_r = _matrix(dresidual, "dresidual", shape, dev, dt)
-    op, ld_o = _matrix(dh, "dh", shape, dev, dt)
-    gp = _vector(dweight, "dweight", D, dev, torch.float32)
     if workspace is None and dweight is not None:
-        workspace = torch.empty(vnm_rmsnorm_backward_workspace_size(T, D), dtype=torch.uint8, device=dy.device)
-    ws_ptr = (workspace.data_ptr() or None) if workspace is not None else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    code = lib().vnm_rmsnorm_backward(yp, ld_dy, hp, ld_h, wp, sp, rp, ld_r, T, D, code, op, ld_o, gp, ws_ptr, ws_bytes,
-                                      _stream_on(stream, dev))
+        workspace = torch.empty(vnm_rmsnorm_backward_workspace_size(*dy.shape), dtype=torch.uint8, device=dy.device)
+    ws_ptr, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    code = _native().rmsnorm_backward(dy, h, weight, rstd, dh, dweight, dresidual, ws_ptr, ws_bytes, stream)
     if code:
         raise VnmError(code, "vnm_rmsnorm_backward")
 
@@ -603,20 +525,7 @@ def vnm_fp8_quantize(X: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optio
     """The block-scaled 8-bit form of X (R x C; fp16, bf16, fp32): q (R x C
     float8) with s, and/or of X^T: qt (C x R) with st. Scales (fp32, any strides)
     are (rows / block_rows, ceil(columns / 128)); block_rows 1 or 128."""
-    shape, dev = _on_current_device(X, "X")
-    R, C = shape
-    code = _dtype(X, "X")
-    rows = max(int(block_rows), 1)
-    xp, ld_x = _matrix(X, "X", shape, dev)
-    qp, ld_q = _matrix(q, "q", (R, C), dev)
-    tp, ld_t = _matrix(qt, "qt", (C, R), dev)
-    kinds = {_fp8(t, n) for t, n in ((q, "q"), (qt, "qt")) if t is not None}
-    if len(kinds) > 1:
-        raise ValueError("q and qt must have the same type")
-    sp, s_rs, s_cs = _scales(s, "s", (-(-R // rows), (C + 127) >> 7), dev)
-    up, u_rs, u_cs = _scales(st, "st", (-(-C // rows), (R + 127) >> 7), dev)
-    code = lib().vnm_fp8_quantize(xp, ld_x, R, C, code, int(block_rows), kinds.pop() if kinds else VNM_E4M3, qp, ld_q,
-                                  sp, s_rs, s_cs, tp, ld_t, up, u_rs, u_cs, _stream_on(stream, dev))
+    code = _native().fp8_quantize(X, q, s, qt, st, block_rows, stream)
     if code:
         raise VnmError(code, "vnm_fp8_quantize")
 
@@ -629,8 +538,7 @@ def vnm_fp8_linear(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_
     (R or ceil(R / 128), ceil(K / 128)); Y T x R (fp16, bf16, fp32); bias (R,) of
     those types. ``status``: optional int32 CUDA tensor of 3 zeroed words that
     receives kernel errors."""
-    args, dev = _fp8_linear_args(xq, x_scale, wq, w_scale, Y, bias, act, status)
-    code = lib().vnm_fp8_linear(*args, _stream_on(stream, dev))
+    code = _native().fp8_linear(xq, x_scale, wq, w_scale, Y, bias, act, status, -1, stream)
     if code:
         raise VnmError(code, "vnm_fp8_linear")
 
@@ -639,30 +547,6 @@ def vnm_testing_fp8_linear_skip_stage(xq: torch.Tensor, x_scale: torch.Tensor, w
                                       Y: torch.Tensor, skip_stage: int, status: torch.Tensor, stream=None) -> None:
     """Test support: vnm_fp8_linear with the first CTA's loads of one pipeline
     stage never issued (include/vnm_testing.h)."""
-    args, dev = _fp8_linear_args(xq, x_scale, wq, w_scale, Y, None, VNM_ACT_NONE, status)
-    _check(lib().vnm_testing_fp8_linear_skip_stage(*args, int(skip_stage), _stream_on(stream, dev)),
-           "vnm_testing_fp8_linear_skip_stage")
-
-
-def _fp8_linear_args(xq, x_scale, wq, w_scale, Y, bias, act, status):
-    shape, dev = _on_current_device(xq, "xq")
-    T, K = shape
-    R = wq.shape[0]
-    groups = (K + 127) >> 7
-    xp, ld_x = _matrix(xq, "xq", shape, dev)
-    wp, ld_w = _matrix(wq, "wq", (R, K), dev)
-    yp, ld_y = _matrix(Y, "Y", (T, R), dev)
-    rows = w_scale.shape[0]
-    block = 1 if rows == R else 128
-    sp, s_rs, s_cs = _scales(x_scale, "x_scale", (T, groups), dev)
-    vp, v_rs, v_cs = _scales(w_scale, "w_scale", (R if block == 1 else (R + 127) >> 7, groups), dev)
-    bp, b_code = None, VNM_F32
-    if bias is not None:
-        bp, b_code = _vector(bias, "bias", R, dev), _dtype(bias, "bias")
-    stp = None
-    if status is not None:
-        if status.dtype != torch.int32 or not status.is_cuda or status.numel() < 3:
-            raise ValueError("status must be a CUDA int32 tensor of at least 3 words")
-        stp = status.data_ptr()
-    return (xp, ld_x, _fp8(xq, "xq"), sp, s_rs, s_cs, wp, ld_w, _fp8(wq, "wq"), vp, v_rs, v_cs, block, T, R, K, bp,
-            b_code, int(act), yp, ld_y, _dtype(Y, "Y"), stp), dev
+    code = _native().fp8_linear(xq, x_scale, wq, w_scale, Y, None, VNM_ACT_NONE, status, int(skip_stage), stream)
+    if code:
+        raise VnmError(code, "vnm_testing_fp8_linear_skip_stage")
