@@ -10,12 +10,13 @@
 // while its sum is formed, and written once. The unit of work is a warp on two
 // groups of 128 columns, 8 elements a lane (16 bytes of a 16-bit type), so that a
 // group's largest magnitude is a reduction over half a warp whatever the type,
-// and the scale's arithmetic is shared by 8 elements. A row takes `warps` warps
-// with CPT units each; rows of one warp share a CTA of four. CTAs are persistent,
-// keep their weights, and load the next row before they wait for this one's sum.
+// and the scale's arithmetic is shared by 8 elements. A CTA takes a row at a time,
+// its warps CPT units each. CTAs are persistent, keep their weights, and load the
+// next row before they wait for this one's sum.
 // The sum crosses warps through shared memory in a fixed order, so results do not
 // depend on timing.
 #include <algorithm>
+#include <type_traits>
 
 #include "vnm_dense.h"
 #include "vnm_fp8.cuh"
@@ -122,58 +123,52 @@ __device__ __forceinline__ void store_groups(const float (&y)[8], bool e5m2, uin
     }
 }
 
-// Forward. A CTA takes the rows blockIdx.x, + gridDim.x, ... CPT > 0: the row's
+// Forward. A CTA takes the rows t = blockIdx.x, + gridDim.x, ... CPT > 0: the row's
 // units stay in registers. CPT = 0: rows longer than the registers hold; h is
 // formed twice from the inputs (or read back where it was stored).
 template <typename T, bool VEC, int CPT>
-__global__ void __launch_bounds__(32 * max_warps(CPT), 1) rmsnorm_kernel(const RmsNormArgs a, int warps, int rows_per_cta) {
+__global__ void __launch_bounds__(32 * max_warps(CPT), 1) rmsnorm_kernel(const __grid_constant__ RmsNormArgs a) {
+    using Off = std::conditional_t<(CPT > 0), int, int64_t>;  // columns: rows in registers are short
     __shared__ float buf[2][kMaxWarps];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int warp = warps == 1 ? 0 : wid;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * rows_per_cta;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * rows_per_cta + (warps == 1 ? wid : 0);
-    if (t0 >= a.T) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     constexpr int N = CPT > 0 ? CPT : 1;
-    const int64_t c0 = first_column<VEC>(warp, lane);       // of the lane's first unit
-    const int64_t across = static_cast<int64_t>(warps) * kUnit;  // to the warp's next unit
-    // the lane's places in the row at hand; s: of its half-warp's group
-    const T* x = static_cast<const T*>(a.x) + t0 * a.ld_x + c0;
-    const T* r = a.res ? static_cast<const T*>(a.res) + t0 * a.ld_res + c0 : nullptr;
-    const T* w = a.w ? static_cast<const T*>(a.w) + c0 : nullptr;
-    T* h = a.h ? static_cast<T*>(a.h) + t0 * a.ld_h + c0 : nullptr;
-    T* y = a.y ? static_cast<T*>(a.y) + t0 * a.ld_y + c0 : nullptr;
-    uint8_t* q = a.q ? static_cast<uint8_t*>(a.q) + t0 * a.ld_q + c0 : nullptr;
-    float* s = a.s ? a.s + t0 * a.s_rs + (2 * static_cast<int64_t>(warp) + (lane >> 4)) * a.s_cs : nullptr;
-    const int64_t s_across = 2 * static_cast<int64_t>(warps) * a.s_cs;
+    const Off D = static_cast<Off>(a.D);
+    const Off c0 = static_cast<Off>(first_column<VEC>(warp, lane));  // of the lane's first unit
+    const Off across = static_cast<Off>(warps) * kUnit;              // to the warp's next unit
+    const Off own = (D + across - 1 - warp * kUnit) / across;        // units of this warp
+    const T* w = static_cast<const T*>(a.w);
     const float inv_d = 1.f / static_cast<float>(a.D);
 
     Elems<T> x8[N], r8[N];
     float hf[N][8], wf[N][8];
-    auto load_row = [&](const T* px, const T* pr) {
+    // (a row's address is the same for the whole CTA: only columns are a lane's own)
+    auto load_row = [&](int64_t t) {
+        const T* x = static_cast<const T*>(a.x) + t * a.ld_x;
 #pragma unroll
-        for (int i = 0; i < N; ++i) load8<T, VEC>(px + i * across, a.D - c0 - i * across, x8[i]);
-        if (pr) {
+        for (int i = 0; i < N; ++i) load8<T, VEC>(x + (c0 + i * across), D - c0 - i * across, x8[i]);
+        if (a.res) {
+            const T* r = static_cast<const T*>(a.res) + t * a.ld_res;
 #pragma unroll
-            for (int i = 0; i < N; ++i) load8<T, VEC>(pr + i * across, a.D - c0 - i * across, r8[i]);
+            for (int i = 0; i < N; ++i) load8<T, VEC>(r + (c0 + i * across), D - c0 - i * across, r8[i]);
         }
     };
-    auto load_weight = [&](const T* pw, int64_t left, float(&f)[8]) {
+    auto load_weight = [&](Off c, float(&f)[8]) {
         Elems<T> e;
-        if (pw) load8<T, VEC>(pw, left, e);
+        if (w) load8<T, VEC>(w + c, D - c, e);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = pw ? widen(e.v[j]) : 1.f;
+        for (int j = 0; j < 8; ++j) f[j] = w ? widen(e.v[j]) : 1.f;
     };
     float sum = 0.f;
     // h of the loaded elements as it is stored, widened, and its squares
-    auto add = [&](const Elems<T>& xe, const Elems<T>& re, float(&f)[8], T* ph, int64_t left) {
-        if (r) {
+    auto add = [&](const Elems<T>& xe, const Elems<T>& re, float(&f)[8], T* h, Off c) {
+        if (a.res) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = widen(xe.v[j]) + widen(re.v[j]);
             Elems<T> he;
             narrow8(f, he.v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = widen(he.v[j]);
-            if (ph) store8<T, VEC>(ph, left, he);
+            if (h) store8<T, VEC>(h + c, D - c, he);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = widen(xe.v[j]);
@@ -181,70 +176,69 @@ __global__ void __launch_bounds__(32 * max_warps(CPT), 1) rmsnorm_kernel(const R
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
     };
-    auto out_unit = [&](int64_t u, float rstd, const float(&f)[8], const float(&wt)[8]) {
-        const int64_t left = a.D - c0 - u * across;
+    auto out_unit = [&](int64_t t, Off u, float rstd, const float(&f)[8], const float(&wt)[8]) {
+        const Off c = c0 + u * across;
         float yf[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) yf[j] = f[j] * rstd * wt[j];
-        if (q) store_groups<VEC>(yf, a.e5m2, q + u * across, s + u * s_across, left, lane);
-        if (y) {
+        if (a.q)
+            store_groups<VEC>(yf, a.e5m2, static_cast<uint8_t*>(a.q) + t * a.ld_q + c,
+                              a.s + t * a.s_rs + (c / kGroup) * a.s_cs, D - c, lane);
+        if (a.y) {
             Elems<T> ye;
             narrow8(yf, ye.v);
-            store8<T, VEC>(y + u * across, left, ye);
+            store8<T, VEC>(static_cast<T*>(a.y) + t * a.ld_y + c, D - c, ye);
         }
     };
     if (CPT > 0) {
-        load_row(x, r);
+        load_row(blockIdx.x);
 #pragma unroll
-        for (int i = 0; i < N; ++i) load_weight(w ? w + i * across : nullptr, a.D - c0 - i * across, wf[i]);
+        for (int i = 0; i < N; ++i) load_weight(c0 + i * across, wf[i]);
     }
     int slot = 0;
-    for (int64_t t = t0; t < a.T; t += step) {
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        T* h = a.h ? static_cast<T*>(a.h) + t * a.ld_h : nullptr;
         sum = 0.f;
-        const int64_t own = (a.D + across - 1 - warp * kUnit) / across;  // units of this warp
         if (CPT > 0) {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                add(x8[i], r8[i], hf[i], h ? h + i * across : nullptr, a.D - c0 - i * across);
-            if (t + step < a.T) load_row(x + step * a.ld_x, r ? r + step * a.ld_res : nullptr);
+            for (int i = 0; i < N; ++i) add(x8[i], r8[i], hf[i], h, c0 + i * across);
+            if (t + gridDim.x < a.T) load_row(t + gridDim.x);
         } else {
-            for (int64_t u = 0; u < own; ++u) {
-                const int64_t left = a.D - c0 - u * across;
-                load8<T, VEC>(x + u * across, left, x8[0]);
-                if (r) load8<T, VEC>(r + u * across, left, r8[0]);
-                add(x8[0], r8[0], hf[0], h ? h + u * across : nullptr, left);
+            const T* x = static_cast<const T*>(a.x) + t * a.ld_x;
+            const T* r = a.res ? static_cast<const T*>(a.res) + t * a.ld_res : nullptr;
+            for (Off u = 0; u < own; ++u) {
+                const Off c = c0 + u * across;
+                load8<T, VEC>(x + c, D - c, x8[0]);
+                if (r) load8<T, VEC>(r + c, D - c, r8[0]);
+                add(x8[0], r8[0], hf[0], h, c);
             }
         }
         const float total = row_sum(sum, warps, warp, lane, buf, slot);
         slot ^= 1;
         const float rstd = inverse_root(fmaf(total, inv_d, a.eps));
-        if (a.rstd && warp == 0 && lane == 0) a.rstd[t] = rstd;
+        if (a.rstd && threadIdx.x == 0) a.rstd[t] = rstd;
         if (CPT > 0) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (i < own) out_unit(i, rstd, hf[i], wf[i]);  // the same for the whole warp
+                if (i < own) out_unit(t, i, rstd, hf[i], wf[i]);  // the same for the whole warp
         } else {
-            for (int64_t u = 0; u < own; ++u) {
-                const int64_t left = a.D - c0 - u * across;
+            const T* x = static_cast<const T*>(a.x) + t * a.ld_x;
+            const T* r = a.res ? static_cast<const T*>(a.res) + t * a.ld_res : nullptr;
+            for (Off u = 0; u < own; ++u) {
+                const Off c = c0 + u * across;
                 // the lane reads back what it wrote itself, or forms h again
-                load8<T, VEC>((h ? h : x) + u * across, left, x8[0]);
+                load8<T, VEC>((h ? h : x) + c, D - c, x8[0]);
                 if (r && !h) {
-                    load8<T, VEC>(r + u * across, left, r8[0]);
-                    add(x8[0], r8[0], hf[0], nullptr, left);
+                    load8<T, VEC>(r + c, D - c, r8[0]);
+                    add(x8[0], r8[0], hf[0], nullptr, c);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) hf[0][j] = widen(x8[0].v[j]);
                 }
-                load_weight(w ? w + u * across : nullptr, left, wf[0]);
-                out_unit(u, rstd, hf[0], wf[0]);
+                load_weight(c, wf[0]);
+                out_unit(t, u, rstd, hf[0], wf[0]);
             }
         }
-        x += step * a.ld_x;
-        if (r) r += step * a.ld_res;
-        if (h) h += step * a.ld_h;
-        if (y) y += step * a.ld_y;
-        if (q) q += step * a.ld_q;
-        if (s) s += step * a.s_rs;
     }
 }
 
@@ -253,20 +247,18 @@ __global__ void __launch_bounds__(32 * max_warps(CPT), 1) rmsnorm_kernel(const R
 // and is written once, to the CTA's row of `partial`. CPT = 0: no dweight here
 // (long rows, see rmsnorm_dw_kernel), dy and h read twice.
 template <typename T, bool VEC, int CPT>
-__global__ void __launch_bounds__(32 * max_warps(CPT), 1) rmsnorm_grad_kernel(const RmsNormGradArgs a, int warps, bool with_dw) {
+__global__ void __launch_bounds__(32 * max_warps(CPT), 1)
+    rmsnorm_grad_kernel(const __grid_constant__ RmsNormGradArgs a, bool with_dw) {
+    using Off = std::conditional_t<(CPT > 0), int, int64_t>;
     __shared__ float buf[2][kMaxWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t step = gridDim.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     constexpr int N = CPT > 0 ? CPT : 1;
     constexpr bool kAhead = CPT == 1 || CPT == 2;  // the next row's loads in flight: four units leave no registers for it
-    const int64_t c0 = first_column<VEC>(warp, lane);
-    const int64_t across = static_cast<int64_t>(warps) * kUnit;
-    const int64_t own = (a.D + across - 1 - warp * kUnit) / across;  // units of this warp
-    const T* dy = static_cast<const T*>(a.dy) + blockIdx.x * a.ld_dy + c0;
-    const T* h = static_cast<const T*>(a.h) + blockIdx.x * a.ld_h + c0;
-    const T* dr = a.dres && a.dh ? static_cast<const T*>(a.dres) + blockIdx.x * a.ld_dres + c0 : nullptr;
-    T* dh = a.dh ? static_cast<T*>(a.dh) + blockIdx.x * a.ld_dh + c0 : nullptr;
-    const T* w = a.w ? static_cast<const T*>(a.w) + c0 : nullptr;
+    const Off D = static_cast<Off>(a.D);
+    const Off c0 = static_cast<Off>(first_column<VEC>(warp, lane));
+    const Off across = static_cast<Off>(warps) * kUnit;
+    const Off own = (D + across - 1 - warp * kUnit) / across;  // units of this warp
+    const T* w = static_cast<const T*>(a.w);
     const float inv_d = 1.f / static_cast<float>(a.D);
     float acc[N][8];
 #pragma unroll
@@ -275,44 +267,49 @@ __global__ void __launch_bounds__(32 * max_warps(CPT), 1) rmsnorm_grad_kernel(co
         for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
     Elems<T> dn[kAhead ? N : 1], hn[kAhead ? N : 1], d8[N], h8[N], r8[N], w8[N];  // dn, hn: the next row's dy and h
     float rstd_next = 0.f;
-    auto load_row = [&](const T* pd, const T* ph, int64_t t, Elems<T>* de, Elems<T>* he) {
+    auto load_row = [&](int64_t t, Elems<T>* de, Elems<T>* he) {
+        const T* dy = static_cast<const T*>(a.dy) + t * a.ld_dy;
+        const T* h = static_cast<const T*>(a.h) + t * a.ld_h;
         rstd_next = a.rstd[t];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            load8<T, VEC>(pd + i * across, a.D - c0 - i * across, de[i]);
-            load8<T, VEC>(ph + i * across, a.D - c0 - i * across, he[i]);
+            load8<T, VEC>(dy + (c0 + i * across), D - c0 - i * across, de[i]);
+            load8<T, VEC>(h + (c0 + i * across), D - c0 - i * across, he[i]);
         }
     };
     if (CPT > 0) {
-        if (kAhead) load_row(dy, h, blockIdx.x, dn, hn);
+        if (kAhead) load_row(blockIdx.x, dn, hn);
         if (w) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) load8<T, VEC>(w + i * across, a.D - c0 - i * across, w8[i]);
+            for (int i = 0; i < N; ++i) load8<T, VEC>(w + (c0 + i * across), D - c0 - i * across, w8[i]);
         }
     }
     // dy w
     auto scaled = [&](const Elems<T>& de, const Elems<T>& we, int j) {
         return widen(de.v[j]) * (w ? widen(we.v[j]) : 1.f);
     };
-    float rstd = 0.f, c = 0.f;
-    auto out_unit = [&](int64_t u, const Elems<T>& de, const Elems<T>& he, const Elems<T>& we, const Elems<T>& re) {
+    const bool add_res = a.dres && a.dh;
+    float rstd = 0.f, k = 0.f;  // k = rstd^2 mean(g h)
+    auto out_unit = [&](T* dh, Off c, const Elems<T>& de, const Elems<T>& he, const Elems<T>& we, const Elems<T>& re) {
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float v = fmaf(-widen(he.v[j]), c, scaled(de, we, j));
-            f[j] = dr ? fmaf(rstd, v, widen(re.v[j])) : rstd * v;
+            const float v = fmaf(-widen(he.v[j]), k, scaled(de, we, j));
+            f[j] = add_res ? fmaf(rstd, v, widen(re.v[j])) : rstd * v;
         }
         Elems<T> oe;
         narrow8(f, oe.v);
-        store8<T, VEC>(dh + u * across, a.D - c0 - u * across, oe);
+        store8<T, VEC>(dh + c, D - c, oe);
     };
     int slot = 0;
-    for (int64_t t = blockIdx.x; t < a.T; t += step) {
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const T* dr = static_cast<const T*>(a.dres) + (add_res ? t * a.ld_dres : 0);
+        T* dh = static_cast<T*>(a.dh) + (a.dh ? t * a.ld_dh : 0);
         float dot = 0.f;
         if (CPT > 0) {
-            if (dr) {
+            if (add_res) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) load8<T, VEC>(dr + i * across, a.D - c0 - i * across, r8[i]);
+                for (int i = 0; i < N; ++i) load8<T, VEC>(dr + (c0 + i * across), D - c0 - i * across, r8[i]);
             }
             if (kAhead) {
                 rstd = rstd_next;
@@ -321,9 +318,9 @@ __global__ void __launch_bounds__(32 * max_warps(CPT), 1) rmsnorm_grad_kernel(co
                     d8[i] = dn[i];
                     h8[i] = hn[i];
                 }
-                if (t + step < a.T) load_row(dy + step * a.ld_dy, h + step * a.ld_h, t + step, dn, hn);
+                if (t + gridDim.x < a.T) load_row(t + gridDim.x, dn, hn);
             } else {
-                load_row(dy, h, t, d8, h8);
+                load_row(t, d8, h8);
                 rstd = rstd_next;
             }
 #pragma unroll
@@ -335,39 +332,38 @@ __global__ void __launch_bounds__(32 * max_warps(CPT), 1) rmsnorm_grad_kernel(co
                     acc[i][j] = fmaf(widen(d8[i].v[j]), hj * rstd, acc[i][j]);
                 }
         } else {
+            const T* dy = static_cast<const T*>(a.dy) + t * a.ld_dy;
+            const T* h = static_cast<const T*>(a.h) + t * a.ld_h;
             rstd = a.rstd[t];
-            for (int64_t u = 0; u < own; ++u) {
-                const int64_t left = a.D - c0 - u * across;
-                load8<T, VEC>(dy + u * across, left, d8[0]);
-                load8<T, VEC>(h + u * across, left, h8[0]);
-                if (w) load8<T, VEC>(w + u * across, left, w8[0]);
+            for (Off u = 0; u < own; ++u) {
+                const Off c = c0 + u * across;
+                load8<T, VEC>(dy + c, D - c, d8[0]);
+                load8<T, VEC>(h + c, D - c, h8[0]);
+                if (w) load8<T, VEC>(w + c, D - c, w8[0]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) dot = fmaf(scaled(d8[0], w8[0], j), widen(h8[0].v[j]), dot);
             }
         }
-        if (dh) {  // dweight alone needs no row sum
-            const float total = row_sum(dot, warps, warp, lane, buf, slot);
-            slot ^= 1;
-            c = rstd * rstd * (total * inv_d);
-            if (CPT > 0) {
+        if (!a.dh) continue;  // dweight alone needs no row sum
+        const float total = row_sum(dot, warps, warp, lane, buf, slot);
+        slot ^= 1;
+        k = rstd * rstd * (total * inv_d);
+        if (CPT > 0) {
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (i < own) out_unit(i, d8[i], h8[i], w8[i], r8[i]);
-            } else {
-                for (int64_t u = 0; u < own; ++u) {
-                    const int64_t left = a.D - c0 - u * across;
-                    load8<T, VEC>(dy + u * across, left, d8[0]);
-                    load8<T, VEC>(h + u * across, left, h8[0]);
-                    if (w) load8<T, VEC>(w + u * across, left, w8[0]);
-                    if (dr) load8<T, VEC>(dr + u * across, left, r8[0]);
-                    out_unit(u, d8[0], h8[0], w8[0], r8[0]);
-                }
+            for (int i = 0; i < N; ++i)
+                if (i < own) out_unit(dh, c0 + i * across, d8[i], h8[i], w8[i], r8[i]);
+        } else {
+            const T* dy = static_cast<const T*>(a.dy) + t * a.ld_dy;
+            const T* h = static_cast<const T*>(a.h) + t * a.ld_h;
+            for (Off u = 0; u < own; ++u) {
+                const Off c = c0 + u * across;
+                load8<T, VEC>(dy + c, D - c, d8[0]);
+                load8<T, VEC>(h + c, D - c, h8[0]);
+                if (w) load8<T, VEC>(w + c, D - c, w8[0]);
+                if (add_res) load8<T, VEC>(dr + c, D - c, r8[0]);
+                out_unit(dh, c, d8[0], h8[0], w8[0], r8[0]);
             }
-            dh += step * a.ld_dh;
         }
-        dy += step * a.ld_dy;
-        h += step * a.ld_h;
-        if (dr) dr += step * a.ld_dres;
     }
     if (CPT > 0 && with_dw) {
         float* part = a.partial + static_cast<int64_t>(blockIdx.x) * a.D + c0;
@@ -375,7 +371,7 @@ __global__ void __launch_bounds__(32 * max_warps(CPT), 1) rmsnorm_grad_kernel(co
         for (int i = 0; i < N; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (a.D - c0 - i * across > j * kStep<VEC>) part[i * across + j * kStep<VEC>] = acc[i][j];
+                if (D - c0 - i * across > j * kStep<VEC>) part[i * across + j * kStep<VEC>] = acc[i][j];
     }
 }
 
@@ -391,18 +387,20 @@ __global__ void rmsnorm_dw_kernel(const RmsNormGradArgs a) {
     a.partial[static_cast<int64_t>(blockIdx.y) * a.D + c] = acc;
 }
 
-// dw[c] = sum over the parts, in order within each of 8 slices, then the slices.
-__global__ void rmsnorm_dw_reduce_kernel(const float* partial, int64_t parts, int64_t D, float* dw) {
-    __shared__ float sum[8][33];
+// dw[c] = sum over the parts: in order within each of 32 slices, then the slices.
+__global__ void __launch_bounds__(1024) rmsnorm_dw_reduce_kernel(const float* partial, int64_t parts, int64_t D, float* dw) {
+    __shared__ float sum[32][33];
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
     float v = 0.f;
-    if (c < D)
-        for (int64_t p = threadIdx.y; p < parts; p += 8) v += partial[p * D + c];
+    if (c < D) {
+#pragma unroll 4
+        for (int64_t p = threadIdx.y; p < parts; p += 32) v += partial[p * D + c];
+    }
     sum[threadIdx.y][threadIdx.x] = v;
     __syncthreads();
     if (threadIdx.y == 0 && c < D) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) v += sum[i][threadIdx.x];
+        for (int i = 1; i < 32; ++i) v += sum[i][threadIdx.x];
         dw[c] = v;
     }
 }
@@ -429,17 +427,15 @@ template <typename T, bool VEC>
 cudaError_t run_forward(const RmsNormArgs& a, int sm_count, cudaStream_t stream) {
     int warps;
     const int cpt = units_per_warp((a.D + kUnit - 1) / kUnit, a.T >= 4 * sm_count, warps);
-    const int rows_per_cta = warps == 1 ? 4 : 1;
-    const int threads = warps == 1 ? 128 : 32 * warps;
-    const int64_t ctas = (a.T + rows_per_cta - 1) / rows_per_cta;
+    const int threads = 32 * warps;
     // persistent: the CTAs that fit at 64, 84 or 128 registers a thread
-    const int64_t fit = static_cast<int64_t>(sm_count) * std::max(1, (cpt == 1 ? 1024 : cpt == 2 ? 768 : 512) / threads);
-    const unsigned grid = static_cast<unsigned>(std::min(ctas, fit));
+    const int64_t fit = static_cast<int64_t>(sm_count) * std::max(1, std::min(32, (cpt == 1 ? 1024 : cpt == 2 ? 768 : 512) / threads));
+    const unsigned grid = static_cast<unsigned>(std::min(a.T, fit));
     switch (cpt) {
-        case 0: rmsnorm_kernel<T, VEC, 0><<<grid, threads, 0, stream>>>(a, warps, rows_per_cta); break;
-        case 1: rmsnorm_kernel<T, VEC, 1><<<grid, threads, 0, stream>>>(a, warps, rows_per_cta); break;
-        case 2: rmsnorm_kernel<T, VEC, 2><<<grid, threads, 0, stream>>>(a, warps, rows_per_cta); break;
-        default: rmsnorm_kernel<T, VEC, 4><<<grid, threads, 0, stream>>>(a, warps, rows_per_cta); break;
+        case 0: rmsnorm_kernel<T, VEC, 0><<<grid, threads, 0, stream>>>(a); break;
+        case 1: rmsnorm_kernel<T, VEC, 1><<<grid, threads, 0, stream>>>(a); break;
+        case 2: rmsnorm_kernel<T, VEC, 2><<<grid, threads, 0, stream>>>(a); break;
+        default: rmsnorm_kernel<T, VEC, 4><<<grid, threads, 0, stream>>>(a); break;
     }
     return cudaGetLastError();
 }
@@ -471,16 +467,16 @@ cudaError_t run_grad(const RmsNormGradArgs& a, cudaStream_t stream) {
             if (e != cudaSuccess) return e;
         }
         switch (cpt) {
-            case 0: rmsnorm_grad_kernel<T, VEC, 0><<<grid, 32 * warps, 0, stream>>>(a, warps, false); break;
-            case 1: rmsnorm_grad_kernel<T, VEC, 1><<<grid, 32 * warps, 0, stream>>>(a, warps, dw); break;
-            case 2: rmsnorm_grad_kernel<T, VEC, 2><<<grid, 32 * warps, 0, stream>>>(a, warps, dw); break;
-            default: rmsnorm_grad_kernel<T, VEC, 4><<<grid, 32 * warps, 0, stream>>>(a, warps, dw); break;
+            case 0: rmsnorm_grad_kernel<T, VEC, 0><<<grid, 32 * warps, 0, stream>>>(a, false); break;
+            case 1: rmsnorm_grad_kernel<T, VEC, 1><<<grid, 32 * warps, 0, stream>>>(a, dw); break;
+            case 2: rmsnorm_grad_kernel<T, VEC, 2><<<grid, 32 * warps, 0, stream>>>(a, dw); break;
+            default: rmsnorm_grad_kernel<T, VEC, 4><<<grid, 32 * warps, 0, stream>>>(a, dw); break;
         }
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     if (dw) {
-        rmsnorm_dw_reduce_kernel<<<static_cast<unsigned>((a.D + 31) / 32), dim3(32, 8), 0, stream>>>(
+        rmsnorm_dw_reduce_kernel<<<static_cast<unsigned>((a.D + 31) / 32), dim3(32, 32), 0, stream>>>(
             a.partial, a.T > 0 ? parts : 0, a.D, a.dw);
         return cudaGetLastError();
     }
