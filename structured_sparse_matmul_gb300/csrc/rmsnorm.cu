@@ -411,14 +411,16 @@ bool vec_ok(const void* p, int64_t ld, int elem) {
 }
 
 // Units a warp keeps in registers for a row of `units` (0: too many, the row is
-// read twice), and the row's warps. Two units a warp where the rows fill the GPU:
-// the sum across warps and the row's scalars are then shared by 16 elements a
-// lane; with few rows one unit, for the shortest chain.
-int units_per_warp(int64_t units, bool many_rows, int& warps) {
-    const int cpt = units <= max_warps(1) && !(many_rows && units >= 4) ? 1
-                    : units <= 2 * max_warps(2)                        ? 2
-                    : units <= 4 * max_warps(4)                        ? 4
-                                                                       : 0;
+// read twice), and the row's warps. Forward (pair = false): one unit a warp as long
+// as 32 warps reach (8192 x 4096 with 8-bit output: 42.9 us; two units a warp 54.4).
+// Backward: two units where there are rows enough to fill the GPU, so that the sum
+// across warps and the row's scalars are shared by 16 elements a lane (8192 x 4096:
+// 51.3 us; one unit 56.2).
+int units_per_warp(int64_t units, bool pair, int& warps) {
+    const int cpt = pair && units >= 4 && units <= 2 * max_warps(2) ? 2
+                    : units <= max_warps(1)                        ? 1
+                    : units <= 4 * max_warps(4)                    ? 4
+                                                                   : 0;
     warps = cpt == 0 ? kMaxWarps : static_cast<int>((units + cpt - 1) / cpt);
     return cpt;
 }
@@ -426,15 +428,14 @@ int units_per_warp(int64_t units, bool many_rows, int& warps) {
 template <typename T, bool VEC>
 cudaError_t run_forward(const RmsNormArgs& a, int sm_count, cudaStream_t stream) {
     int warps;
-    const int cpt = units_per_warp((a.D + kUnit - 1) / kUnit, a.T >= 4 * sm_count, warps);
+    const int cpt = units_per_warp((a.D + kUnit - 1) / kUnit, false, warps);
     const int threads = 32 * warps;
-    // persistent: the CTAs that fit at 64, 84 or 128 registers a thread
-    const int64_t fit = static_cast<int64_t>(sm_count) * std::max(1, std::min(32, (cpt == 1 ? 1024 : cpt == 2 ? 768 : 512) / threads));
+    // persistent: the CTAs that fit at 64 (one unit) or 128 registers a thread
+    const int64_t fit = static_cast<int64_t>(sm_count) * std::max(1, std::min(32, (cpt == 1 ? 1024 : 512) / threads));
     const unsigned grid = static_cast<unsigned>(std::min(a.T, fit));
     switch (cpt) {
         case 0: rmsnorm_kernel<T, VEC, 0><<<grid, threads, 0, stream>>>(a); break;
         case 1: rmsnorm_kernel<T, VEC, 1><<<grid, threads, 0, stream>>>(a); break;
-        case 2: rmsnorm_kernel<T, VEC, 2><<<grid, threads, 0, stream>>>(a); break;
         default: rmsnorm_kernel<T, VEC, 4><<<grid, threads, 0, stream>>>(a); break;
     }
     return cudaGetLastError();
