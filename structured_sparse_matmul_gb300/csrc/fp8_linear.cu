@@ -19,8 +19,9 @@
 //   warp 0     TMA producer: a stage is 128 rows of P and the CTA's rows of Q by
 //              128 bytes of K, 128B swizzle.
 //   warp 1     TMEM owner and MMA issuer (one thread; of a pair, the first CTA's).
-//   warp 2     the K block's scales of Q into a shared-memory ring by 4-byte
-//              cp.async (any strides), where the tile has more than one or two.
+//   warps 2, 3 the K blocks' scales of Q into a shared-memory ring, where the tile has
+//              more than one or two of them (any strides; four blocks at once where
+//              they are 16 aligned bytes).
 //   warps 4..  add up: thread = row of P, whose scale it loads two blocks ahead; 4
 //              warps, or 8 with half the columns each.
 // Every mbarrier wait is bounded.
@@ -40,7 +41,7 @@ namespace {
 
 constexpr int kTileM = 128;
 constexpr int kMaxSplits = 8;
-constexpr int kHelpers = 4;  // warps before the adding ones (the fourth is idle)
+constexpr int kHelpers = 4;  // warps before the adding ones
 constexpr int kMaxDevicesFl = 64;
 constexpr int kStoreBox = 32 * 128;  // bytes of a TMA store: 32 rows x 128 bytes
 
@@ -63,18 +64,25 @@ struct FlCfg {
     static constexpr int kThreads = 32 * (kHelpers + kAddWarps);
     // Registers: 128 sums and two loads of 32 columns do not fit the 168 that 12
     // warps get; the adding warps take what the helper warps leave. The shares
-    // add up to the launch's (in warps: 4 x 56 + 8 x 224 = 12 x 168).
+    // add up to the launch's (in warps: 4 x 56 + 8 x 224 = 4 x 104 + 8 x 200 = 12 x 168).
     static constexpr bool kSplitRegs = kCols == 128;
-    static constexpr int kLaunchRegs = 168, kHelperRegs = 56, kAddRegs = 224;
+    static constexpr int kLaunchRegs = 168, kHelperRegs = ONE ? 56 : 104, kAddRegs = ONE ? 224 : 200;
     static_assert(!kSplitRegs || kHelpers * kHelperRegs + kAddWarps * kAddRegs == (kHelpers + kAddWarps) * kLaunchRegs,
                   "register shares");
-    // Q's scales (ONE reads its one scale itself); they take about as long to arrive as an operand stage
+    // FRAG: a pair whose columns have a scale each. A thread then holds 4 rows x 32
+    // columns (two neighbours of every 8) instead of a row x 128, and reads 32 of Q's
+    // scales a K block instead of 128: as one row a thread, their broadcasts from
+    // shared memory took 1 us a K block.
+    static constexpr bool kFrag = CG == 2 && !ONE;
+    // Q's scales (ONE reads its one scale itself), FRAG: and P's; they take about as long to arrive
+    // as an operand stage
     static constexpr int kScaleSlots = ONE ? 0 : 8;
+    static constexpr int kScaleFloats = BN + (kFrag ? kTileM : 0);
     // a pair's outputs leave by TMA stores, from 32 rows x 128 bytes for each adding warp
     static constexpr int kStoreBytes = CG == 2 ? kAddWarps * kStoreBox : 0;
     // no CTA waits for TMEM that another of this kernel holds: either the CTAs that
     // share an SM leave each other room, or the shared memory keeps a second one out
-    static constexpr int kSmem = kStages * kStageBytes + kStoreBytes + kScaleSlots * BN * 4 + 1024;
+    static constexpr int kSmem = kStages * kStageBytes + kStoreBytes + kScaleSlots * kScaleFloats * 4 + 1024;
     static_assert(kCtas * kTmemCols <= 512, "TMEM of the CTAs that share an SM");
     static_assert(kCtas == 2 ? 2 * (kSmem + 2048) <= 228 * 1024 : kSmem > 116 * 1024 && kSmem <= 226 * 1024, "shared memory");
     static_assert(CG == 2 || kTileM * BN * 4 <= kStages * kStageBytes, "the split's sums fit the stage ring");
@@ -86,6 +94,7 @@ struct FlArgs {
     int m_tiles, n_tiles, tiles;
     uint32_t idesc;
     ScaleView ps, qs;
+    bool quad_scales;  // four blocks' scales of a row are 16 aligned bytes
     void* y;
     int64_t y_ms, y_ns;
     int y_type;
@@ -223,6 +232,18 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
         : "memory");
 }
 
+// 16 lanes x 32 columns as matrix fragments: of every 8 columns, thread (g, i) =
+// (lane / 4, lane % 4) gets columns 2i, 2i + 1 of rows g (r[0], r[1]) and g + 8.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 // One thread of a converged warp. Unlike a test of the lane number it keeps the
 // branch uniform for the compiler, which matters to the tcgen05 instructions:
 // their operands live in uniform registers.
@@ -299,6 +320,25 @@ __device__ __noinline__ void store_any16(const FlArgs& a, int64_t m, int64_t n, 
     }
 }
 
+// The bias of columns n, n + 1 (the last one's past the edge).
+__device__ __noinline__ float2 bias2(const FlArgs& a, int64_t n) {
+    return make_float2(load_any(a.bias, a.bias_type, min(n, a.n - 1)), load_any(a.bias, a.bias_type, min(n + 1, a.n - 1)));
+}
+
+// Outputs (m, n), (m, n + 1) from their finished sums, where they exist.
+__device__ __noinline__ void store_pair(const FlArgs& a, int64_t m, int64_t n, float v0, float v1) {
+    if (m >= a.m) return;
+    if (n < a.n) store_any(a.y, a.y_type, m * a.y_ms + n * a.y_ns, v0);
+    if (n + 1 < a.n) store_any(a.y, a.y_type, m * a.y_ms + (n + 1) * a.y_ns, v1);
+}
+
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, float x, float y) {
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // Tiles in groups of kGroupM row tiles, row tiles fastest: the CTAs that run
 // together share a few tiles of both operands in L2.
 constexpr int kGroupM = 8;
@@ -329,7 +369,7 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
 
     const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* const smem_gen = smem_raw + (smem_base - smem_u32(smem_raw));
-    float* const scales = reinterpret_cast<float*>(smem_gen + ST * Cfg::kStageBytes + Cfg::kStoreBytes);  // [SS][BN]
+    float* const scales = reinterpret_cast<float*>(smem_gen + ST * Cfg::kStageBytes + Cfg::kStoreBytes);  // [SS][kScaleFloats]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int pair_rank = CG == 2 ? static_cast<int>(blockIdx.x & 1) : 0;
     // this CTA's tiles and K blocks: every role walks the same sequence
@@ -355,7 +395,7 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
         }
         for (int s = 0; s < ACC; ++s) mbar_init(smem_u32(&acce_bar[s]), CG * Cfg::kAddWarps);
         for (int s = 0; s < SS; ++s) {
-            mbar_init(smem_u32(&scf_bar[s]), 32);
+            mbar_init(smem_u32(&scf_bar[s]), 64);
             mbar_init(smem_u32(&sce_bar[s]), Cfg::kAddWarps);
         }
         abort_flag = 0;
@@ -460,27 +500,59 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
         }
         // every MMA issued is done before TMEM goes back
         if (it > 0) mbar_drain(smem_u32(&done_bar[(it - 1) % ST]), static_cast<uint32_t>((it - 1) / ST) & 1u);
-    } else if (warp == 2 && !ONE) {
-        // ------------------------------------------------ scales of Q
+    } else if (warp < kHelpers && !ONE) {
+        // ------------------------------------------------ scales, by warps 2 and 3
+        constexpr int F = Cfg::kScaleFloats, kPer = (F + 63) / 64;  // scales of a slot, and a lane's share
+        const int first = 32 * (warp - 2) + lane;                   // the lane's: first, first + 64, ...
         int it = 0;
         bool run = true;
         for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
             int mt, nt;
             tile_at(a, tile, mt, nt);
-            const int64_t n0 = static_cast<int64_t>(nt) * BN;
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int slot = it % SSB;
-                if (!mbar_wait_warp(smem_u32(&sce_bar[slot]), (static_cast<uint32_t>(it / SSB) & 1u) ^ 1u, abort)) {
-                    run = false;
-                    break;
+            const int64_t n0 = static_cast<int64_t>(nt) * BN, m0 = static_cast<int64_t>(mt * CG + pair_rank) * kTileM;
+            // scale i of a slot at block 0; null past the operand's edge
+            auto place = [&](int i) -> const float* {
+                const bool q = i < BN;
+                const int64_t r = q ? n0 + i : m0 + (i - BN);
+                if (i >= F || r >= (q ? a.n : a.m)) return nullptr;
+                return q ? a.qs.p + (r >> a.qs.shift) * a.qs.rs : a.ps.p + (r >> a.ps.shift) * a.ps.rs;
+            };
+            for (int kb = kb0; kb < kb1 && run;) {
+                // four blocks of a row in one load where the scales' layout allows it: one by one,
+                // a weight gradient's 384 scales a block cost a third of its time
+                const int many = a.quad_scales && (kb & 3) == 0 && kb + 4 <= kb1 ? 4 : 1;
+                for (int u = 0; u < many && run; ++u)
+                    run = mbar_wait_warp(smem_u32(&sce_bar[(it + u) % SSB]), (static_cast<uint32_t>((it + u) / SSB) & 1u) ^ 1u,
+                                         abort);
+                if (!run) break;
+                if (many == 4) {
+                    float4 v[kPer];
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) {
+                        const float* p = place(first + 64 * j);
+                        v[j] = p ? *reinterpret_cast<const float4*>(p + kb) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        float* dst = scales + (it + u) % SSB * F;
+#pragma unroll
+                        for (int j = 0; j < kPer; ++j)
+                            if (first + 64 * j < F)
+                                dst[first + 64 * j] = u == 0 ? v[j].x : u == 1 ? v[j].y : u == 2 ? v[j].z : v[j].w;
+                        mbar_arrive(smem_u32(&scf_bar[(it + u) % SSB]));
+                    }
+                } else {
+                    const uint32_t dst = smem_u32(scales + it % SSB * F);
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) {
+                        const int i = first + 64 * j;
+                        const float* p = place(i);
+                        if (i < F) cp_async_4(dst + 4 * i, p ? p + kb * (i < BN ? a.qs.cs : a.ps.cs) : a.qs.p, p != nullptr);
+                    }
+                    cp_async_arrive_noinc(smem_u32(&scf_bar[it % SSB]));
                 }
-                const uint32_t dst = smem_u32(scales + slot * BN);
-                for (int i = lane; i < BN; i += 32) {
-                    const int64_t r = n0 + i;
-                    const bool in = r < a.n;
-                    cp_async_4(dst + 4 * i, a.qs.p + (in ? (r >> a.qs.shift) * a.qs.rs + kb * a.qs.cs : 0), in);
-                }
-                cp_async_arrive_noinc(smem_u32(&scf_bar[slot]));
+                kb += many;
+                it += many;
             }
         }
         cp_async_wait_all();
@@ -510,11 +582,11 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
         cur_p = next_p;
         cur_q = next_q;
         const bool two = kb1 - kb0 >= 2;
-        if (kb0 < kb1) {
+        if (!Cfg::kFrag && kb0 < kb1) {
             p1 = *cur_p;
             if (ONE) q1 = *cur_q;
         }
-        if (two) {
+        if (!Cfg::kFrag && two) {
             p2 = *(cur_p += a.ps.cs);
             if (ONE) q2 = *(cur_q += a.qs.cs);
         }
@@ -531,20 +603,22 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int acc = it % ACC, slot = it % SSB;
                 const float sp = p1, sq1 = q1;
-                p1 = p2;
-                q1 = q2;
-                if (kb + 2 == kb1 || !two) {
-                    cur_p = next_p;
-                    cur_q = next_q;
-                } else {
-                    cur_p += a.ps.cs;
-                    cur_q += a.qs.cs;
-                }
-                p2 = *cur_p;
-                if (ONE) q2 = *cur_q;
-                if (!two) {  // one block a tile: the next tile's is the next one
+                if (!Cfg::kFrag) {
                     p1 = p2;
                     q1 = q2;
+                    if (kb + 2 == kb1 || !two) {
+                        cur_p = next_p;
+                        cur_q = next_q;
+                    } else {
+                        cur_p += a.ps.cs;
+                        cur_q += a.qs.cs;
+                    }
+                    p2 = *cur_p;
+                    if (ONE) q2 = *cur_q;
+                    if (!two) {  // one block a tile: the next tile's is the next one
+                        p1 = p2;
+                        q1 = q2;
+                    }
                 }
                 const uint32_t done = smem_u32(&done_bar[stage]);
                 const bool ok = ONE ? mbar_wait(done, phase, abort)
@@ -559,37 +633,68 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
                     break;
                 }
                 tc_fence_after_sync();
-                const float* sq = scales + slot * BN + col0;
+                const float* sq = scales + slot * Cfg::kScaleFloats + col0;
                 const float s1 = ONE ? sp * sq1 : sp;
                 const uint32_t taddr = tmem + lane_addr + acc * BN + col0;
+                // all read: the MMAs may have the buffer back
+                auto release = [&] {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (elect_one()) {
+                        if (CG == 2)
+                            mbar_arrive_cluster(acce_lead + 8 * acc);
+                        else
+                            mbar_arrive(smem_u32(&acce_bar[acc]));
+                    }
+                };
                 // the next columns are on their way while these are added
-                uint32_t v[2][LD];
-                tmem_ld(taddr, v[0]);
+                if constexpr (Cfg::kFrag) {
+                    // chunk x: rows 16 (x & 1) of the warp's 32, columns 32 (x / 2)
+                    const float *fp = scales + slot * Cfg::kScaleFloats + BN + 32 * quarter + (lane >> 2),
+                                *fq = sq + 2 * (lane & 3);
+                    const float rows[4] = {fp[0], fp[8], fp[16], fp[24]};
+                    auto at = [&](int x) { return taddr + (static_cast<uint32_t>(16 * (x & 1)) << 16) + 32 * (x / 2); };
+                    uint32_t v[2][16];
+                    tmem_ld_frag(at(0), v[0]);
 #pragma unroll
-                for (int c = 0; c < COLS; c += LD) {
-                    uint32_t(&cur)[LD] = v[(c / LD) & 1];
-                    tmem_wait_ld(cur);
-                    if (c + LD < COLS) {
-                        tmem_ld(taddr + c + LD, v[(c / LD + 1) & 1]);
-                    } else {
-                        // all read: the MMAs may have the buffer back
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (elect_one()) {
-                            if (CG == 2)
-                                mbar_arrive_cluster(acce_lead + 8 * acc);
-                            else
-                                mbar_arrive(smem_u32(&acce_bar[acc]));
+                    for (int x = 0; x < 8; ++x) {
+                        uint32_t(&cur)[16] = v[x & 1];
+                        tmem_wait_ld(cur);
+                        if (x + 1 < 8)
+                            tmem_ld_frag(at(x + 1), v[(x + 1) & 1]);
+                        else
+                            release();
+                        const float top = rows[2 * (x & 1)], low = rows[2 * (x & 1) + 1];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 q = *reinterpret_cast<const float2*>(fq + 32 * (x / 2) + 8 * j);
+                            float* d = sum + 16 * x + 4 * j;
+                            d[0] = fmaf(__uint_as_float(cur[4 * j]), top * q.x, d[0]);
+                            d[1] = fmaf(__uint_as_float(cur[4 * j + 1]), top * q.y, d[1]);
+                            d[2] = fmaf(__uint_as_float(cur[4 * j + 2]), low * q.x, d[2]);
+                            d[3] = fmaf(__uint_as_float(cur[4 * j + 3]), low * q.y, d[3]);
                         }
                     }
+                } else {
+                    uint32_t v[2][LD];
+                    tmem_ld(taddr, v[0]);
 #pragma unroll
-                    for (int u = 0; u < LD; u += 4) {
-                        float4 q4 = make_float4(1.f, 1.f, 1.f, 1.f);
-                        if (!ONE) q4 = *reinterpret_cast<const float4*>(sq + c + u);
-                        sum[c + u] = fmaf(__uint_as_float(cur[u]), ONE ? s1 : s1 * q4.x, sum[c + u]);
-                        sum[c + u + 1] = fmaf(__uint_as_float(cur[u + 1]), ONE ? s1 : s1 * q4.y, sum[c + u + 1]);
-                        sum[c + u + 2] = fmaf(__uint_as_float(cur[u + 2]), ONE ? s1 : s1 * q4.z, sum[c + u + 2]);
-                        sum[c + u + 3] = fmaf(__uint_as_float(cur[u + 3]), ONE ? s1 : s1 * q4.w, sum[c + u + 3]);
+                    for (int c = 0; c < COLS; c += LD) {
+                        uint32_t(&cur)[LD] = v[(c / LD) & 1];
+                        tmem_wait_ld(cur);
+                        if (c + LD < COLS)
+                            tmem_ld(taddr + c + LD, v[(c / LD + 1) & 1]);
+                        else
+                            release();
+#pragma unroll
+                        for (int u = 0; u < LD; u += 4) {
+                            float4 q4 = make_float4(1.f, 1.f, 1.f, 1.f);
+                            if (!ONE) q4 = *reinterpret_cast<const float4*>(sq + c + u);
+                            sum[c + u] = fmaf(__uint_as_float(cur[u]), ONE ? s1 : s1 * q4.x, sum[c + u]);
+                            sum[c + u + 1] = fmaf(__uint_as_float(cur[u + 1]), ONE ? s1 : s1 * q4.y, sum[c + u + 1]);
+                            sum[c + u + 2] = fmaf(__uint_as_float(cur[u + 2]), ONE ? s1 : s1 * q4.z, sum[c + u + 2]);
+                            sum[c + u + 3] = fmaf(__uint_as_float(cur[u + 3]), ONE ? s1 : s1 * q4.w, sum[c + u + 3]);
+                        }
                     }
                 }
                 if (!ONE) {
@@ -606,7 +711,20 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
                 continue;
             }
             const int64_t m = static_cast<int64_t>(m0) + lane;
-            if (a.bias) {
+            if (Cfg::kFrag && a.bias) {
+#pragma unroll
+                for (int x = 0; x < COLS / 16; x += 2) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 b = bias2(a, static_cast<int64_t>(n0) + 16 * x + 8 * j + 2 * (lane & 3));
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            sum[16 * x + 16 * (h / 2) + 4 * j + 2 * (h & 1)] += b.x;
+                            sum[16 * x + 16 * (h / 2) + 4 * j + 2 * (h & 1) + 1] += b.y;
+                        }
+                    }
+                }
+            } else if (a.bias) {
                 // the bias of the row, or of columns lane, lane + 32, ... (the sum over a
                 // cluster adds it by itself)
                 float bias[(COLS + 31) / 32];
@@ -622,7 +740,7 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
             if (a.act == VNM_ACT_RELU) {
 #pragma unroll
                 for (int c = 0; c < COLS; ++c) sum[c] = activate(VNM_ACT_RELU, sum[c]);
-            } else if (a.act == VNM_ACT_GELU && m < a.m) {
+            } else if (a.act == VNM_ACT_GELU && (Cfg::kFrag || m < a.m)) {
 #pragma unroll
                 for (int c = 0; c < COLS; c += 16) {
                     float v[16];
@@ -644,22 +762,51 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
                 for (int c = 0; c < COLS; c += kBoxCols) {
                     if (lane == 0) tma_store_wait_read();
                     __syncwarp();
+                    if (Cfg::kFrag) {
+                        const int g = lane >> 2, i = lane & 3;  // (rows g, g + 8, ...: all of the swizzle's row g)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {  // 16 bytes each
-                        uint32_t w[4];
+                        for (int x = c / 16; x < (c + kBoxCols) / 16; ++x)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int e = c + j * kBoxCols / 8 + (F32 ? i : 2 * i);
-                            w[i] = F32    ? __float_as_uint(sum[e])
-                                   : bf16 ? to_bf16x2(sum[e], sum[e + 1])
-                                          : to_f16x2(sum[e], sum[e + 1]);
+                            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                for (int low = 0; low < 2; ++low) {
+                                    const float *d = sum + 16 * x + 4 * j + 2 * low;
+                                    const uint32_t to = buf + 128 * (16 * (x & 1) + g + 8 * low);
+                                    const int col = 32 * (x / 2) + 8 * j - c;  // of the box
+                                    if (F32)
+                                        st_shared_v2(to + 16 * ((col / 4 + (i >> 1)) ^ g) + 8 * (i & 1), d[0], d[1]);
+                                    else
+                                        st_shared_u32(to + 16 * ((col / 8) ^ g) + 4 * i,
+                                                      bf16 ? to_bf16x2(d[0], d[1]) : to_f16x2(d[0], d[1]));
+                                }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {  // 16 bytes each
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int e = c + j * kBoxCols / 8 + (F32 ? i : 2 * i);
+                                w[i] = F32    ? __float_as_uint(sum[e])
+                                       : bf16 ? to_bf16x2(sum[e], sum[e + 1])
+                                              : to_f16x2(sum[e], sum[e + 1]);
+                            }
+                            st_shared_v4(dst + 16 * (j ^ flip), w[0], w[1], w[2], w[3]);
                         }
-                        st_shared_v4(dst + 16 * (j ^ flip), w[0], w[1], w[2], w[3]);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0 && m0 < a.m && n0 + c < a.n) tma_store_2d(&tm_y, n0 + c, m0, buf);
                 }
+                continue;
+            }
+            if (Cfg::kFrag) {
+#pragma unroll
+                for (int x = 0; x < COLS / 16; ++x)
+#pragma unroll
+                    for (int h = 0; h < 8; ++h)
+                        store_pair(a, static_cast<int64_t>(m0) + 16 * (x & 1) + (lane >> 2) + 8 * (h & 1),
+                                   static_cast<int64_t>(n0) + 32 * (x / 2) + 8 * (h / 2) + 2 * (lane & 3),
+                                   sum[16 * x + 4 * (h / 2) + 2 * (h & 1)], sum[16 * x + 4 * (h / 2) + 2 * (h & 1) + 1]);
                 continue;
             }
             if (m >= a.m) continue;
@@ -869,6 +1016,8 @@ cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const S
     a.num_kb = static_cast<int>(ceil_div(K, 128));
     a.ps = g.ps;
     a.qs = g.qs;
+    auto quad = [](const ScaleView& v) { return v.cs == 1 && v.rs % 4 == 0 && reinterpret_cast<uintptr_t>(v.p) % 16 == 0; };
+    a.quad_scales = quad(g.qs) && (!wide || quad(g.ps));  // (narrow tiles' P is not read through the ring)
     a.y = y;
     a.y_ms = g.y_ms;
     a.y_ns = g.y_ns;
