@@ -55,7 +55,7 @@ struct FlCfg {
     static constexpr int kStageBytes = kPBytes + kQBytes;
     // narrow tiles: two CTAs an SM, whose waits overlap
     static constexpr int kCtas = BN <= 64 ? 2 : 1;
-    static constexpr int kStages = CG == 2 ? 5 : BN == 128 ? 6 : BN == 64 ? 4 : BN == 32 ? 5 : 6;
+    static constexpr int kStages = CG == 2 ? 4 : BN == 128 ? 6 : BN == 64 ? 4 : BN == 32 ? 5 : 6;
     static constexpr int kAcc = BN == 256 ? 2 : 4;  // TMEM buffers
     static constexpr int kTmemCols = kAcc * BN;
     static constexpr int kAddWarps = BN >= 128 ? 8 : 4;
@@ -78,8 +78,8 @@ struct FlCfg {
     // as an operand stage
     static constexpr int kScaleSlots = ONE ? 0 : 8;
     static constexpr int kScaleFloats = BN + (kFrag ? kTileM : 0);
-    // a pair's outputs leave by TMA stores, from 32 rows x 128 bytes for each adding warp
-    static constexpr int kStoreBytes = CG == 2 ? kAddWarps * kStoreBox : 0;
+    // a pair's outputs leave by TMA stores, from two boxes of 32 rows x 128 bytes for each adding warp
+    static constexpr int kStoreBytes = CG == 2 ? kAddWarps * 2 * kStoreBox : 0;
     // no CTA waits for TMEM that another of this kernel holds: either the CTAs that
     // share an SM leave each other room, or the shared memory keeps a second one out
     static constexpr int kSmem = kStages * kStageBytes + kStoreBytes + kScaleSlots * kScaleFloats * 4 + 1024;
@@ -179,17 +179,18 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
-// Store of a box from shared memory; it belongs to the thread's bulk group.
+// Store of a box from shared memory, in the thread's open bulk group.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, int32_t x, int32_t y, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                      reinterpret_cast<uint64_t>(tm)),
                  "r"(x), "r"(y), "r"(src)
                  : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// The thread's stores have read their shared memory / are complete.
-__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+
+// All but the thread's last group have read their shared memory / all are complete.
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Arrive on a barrier of any CTA of the cluster (address from dsmem_map). The
@@ -756,10 +757,11 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
                 // leaves out what lies past Y's edges)
                 constexpr int kBoxCols = F32 ? 32 : 64;
                 const bool bf16 = a.y_type == VNM_BF16;
-                const uint32_t buf = smem_base + ST * Cfg::kStageBytes + (warp - kHelpers) * kStoreBox;
-                const uint32_t dst = buf + 128 * lane, flip = lane & 7;
+                const uint32_t bufs = smem_base + ST * Cfg::kStageBytes + (warp - kHelpers) * 2 * kStoreBox;
+                const uint32_t flip = lane & 7;
 #pragma unroll
                 for (int c = 0; c < COLS; c += kBoxCols) {
+                    const uint32_t buf = bufs + (c / kBoxCols & 1) * kStoreBox, dst = buf + 128 * lane;
                     if (lane == 0) tma_store_wait_read();
                     __syncwarp();
                     if (Cfg::kFrag) {
@@ -795,7 +797,11 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0 && m0 < a.m && n0 + c < a.n) tma_store_2d(&tm_y, n0 + c, m0, buf);
+                    if (lane == 0) {
+                        // a box past Y's edges is an empty group: the waits count groups
+                        if (m0 < a.m && n0 + c < a.n) tma_store_2d(&tm_y, n0 + c, m0, buf);
+                        tma_store_commit();
+                    }
                 }
                 continue;
             }
@@ -971,7 +977,7 @@ TilePlan plan_tiles(int64_t T, int64_t R, int num_kb, bool one_scale, int sm_cou
     auto ceil_div = [](int64_t p, int64_t q) { return (p + q - 1) / q; };
     TilePlan best{0, 1};
     const int64_t pair_waves = ceil_div(ceil_div(T, 256) * ceil_div(R, 256), std::max(1, sm_count / 2));
-    double least = 4.0 + static_cast<double>(pair_waves) * num_kb * (one_scale ? 0.5 : 0.95);
+    double least = 4.0 + static_cast<double>(pair_waves) * num_kb * (one_scale ? 0.5 : 0.7);
     for (int bn : {16, 32, 64, 128}) {
         if (bn > 16 && bn / 2 >= T) break;  // the width below holds all tokens
         const int64_t tiles = ceil_div(R, kTileM) * ceil_div(T, bn);

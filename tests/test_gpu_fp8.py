@@ -347,3 +347,17 @@ def test_bounded_wait_reports_timeout_and_device_stays_usable(T, R, K, skip):
     vnm.vnm_fp8_linear(xq, xs, wq, ws, Y, status=status)
     assert status.tolist() == [0, 0, 0]
     check_linear(Y, linear64(xq, xs, wq, ws, None, 0), K, 0)
+
+
+@pytest.mark.parametrize("y_type", [F32, F16])
+@pytest.mark.parametrize("T,R,K", [(200, 300, 260), (300, 2200, 130), (1100, 1060, 100)])
+def test_outputs_that_end_inside_a_tile(T, R, K, y_type):
+    """Tiles of which only some of the output boxes exist, many times: a box past the
+    edge must not reuse memory that a box before it is still being stored from."""
+    xq, xs, wq, ws = _operands(T, R, K, 128, E4M3, E4M3, 14)
+    ref = linear64(xq, xs, wq, ws, None, 0)
+    Y = [torch.full((T, R), float("nan"), dtype=y_type, device=DEV) for _ in range(24)]
+    for y in Y:
+        vnm.vnm_fp8_linear(xq, xs, wq, ws, y)
+    for y in Y:
+        check_linear(y, ref, K, 0)
