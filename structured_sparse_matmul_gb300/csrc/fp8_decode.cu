@@ -47,13 +47,29 @@ __device__ __forceinline__ uint4 load_once(const uint8_t* p) {
 }
 
 // 16 bytes of a row from column k on, 0 from column K on (the last, shorter block).
-__device__ __noinline__ uint4 load_edge(const uint8_t* row, int64_t k, int64_t K) {
+// Rows are 16-byte aligned, so the 16 bytes lie within the row's pitch; the last
+// row's pitch may not be all there, and its last bytes are read one by one.
+__device__ __noinline__ uint4 load_edge(const uint8_t* row, int64_t k, int64_t K, bool last_row) {
+    const int n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(16), K - k)));  // bytes that exist
     uint32_t u[4] = {0u, 0u, 0u, 0u};
-#pragma unroll 1
-    for (int i = 0; i < 16; ++i) {
-        const uint32_t byte = k + i < K ? row[k + i] : 0u;
+    if (n == 16 || (n > 0 && !last_row)) {
+        const uint4 v = load_once(row + k);
+        u[0] = v.x;
+        u[1] = v.y;
+        u[2] = v.z;
+        u[3] = v.w;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] |= j == i / 4 ? byte << (8 * (i & 3)) : 0u;
+        for (int j = 0; j < 4; ++j) {
+            const int left = n - 4 * j;
+            u[j] = left >= 4 ? u[j] : left <= 0 ? 0u : u[j] & (0xFFFFFFFFu >> (8 * (4 - left)));
+        }
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const uint32_t byte = row[k + i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] |= j == i / 4 ? byte << (8 * (i & 3)) : 0u;
+        }
     }
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
@@ -155,9 +171,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) fp8_decode_kernel(const Decode
         const int64_t k = static_cast<int64_t>(full) * kGroup + 16 * i;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            ring[0].v[0][h] = load_edge(w0 - 16 * i, k + 64 * h, a.K);
-            ring[0].v[1][h] = load_edge(w1 - 16 * i, k + 64 * h, a.K);
-            cur.x[h] = load_edge(x0 - 16 * i, k + 64 * h, a.K);
+            ring[0].v[0][h] = load_edge(w0 - 16 * i, k + 64 * h, a.K, row0 == a.R - 1);
+            ring[0].v[1][h] = load_edge(w1 - 16 * i, k + 64 * h, a.K, row1 == a.R - 1);
+            cur.x[h] = load_edge(x0 - 16 * i, k + 64 * h, a.K, g >= last);
         }
         load_scales(cur, full);
         multiply(ring[0], cur);

@@ -326,11 +326,29 @@ __device__ __noinline__ float2 bias2(const FlArgs& a, int64_t n) {
     return make_float2(load_any(a.bias, a.bias_type, min(n, a.n - 1)), load_any(a.bias, a.bias_type, min(n + 1, a.n - 1)));
 }
 
-// Outputs (m, n), (m, n + 1) from their finished sums, where they exist.
-__device__ __noinline__ void store_pair(const FlArgs& a, int64_t m, int64_t n, float v0, float v1) {
-    if (m >= a.m) return;
-    if (n < a.n) store_any(a.y, a.y_type, m * a.y_ms + n * a.y_ns, v0);
-    if (n + 1 < a.n) store_any(a.y, a.y_type, m * a.y_ms + (n + 1) * a.y_ns, v1);
+// A staged box (32 rows x 128 bytes, 128B-swizzled) to Y's rows m0 .. and columns
+// n0 .., by a warp, 4 bytes a lane: whole words where the row's address allows them.
+template <bool F32>
+__device__ __noinline__ void copy_box(const FlArgs& a, uint32_t buf, int m0, int n0, int lane) {
+    const int rows = static_cast<int>(min(static_cast<int64_t>(32), a.m - m0));
+    const int64_t n = n0 + (F32 ? lane : 2 * lane);
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+        uint32_t v;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(buf + 128 * r + 16 * ((lane >> 2) ^ (r & 7)) + 4 * (lane & 3)));
+        const int64_t at = static_cast<int64_t>(m0 + r) * a.y_ms + n;
+        if (F32) {
+            if (n < a.n) static_cast<uint32_t*>(a.y)[at] = v;
+        } else {
+            uint16_t* p = static_cast<uint16_t*>(a.y) + at;
+            if (n + 1 < a.n && (reinterpret_cast<uintptr_t>(p) & 3) == 0) {
+                *reinterpret_cast<uint32_t*>(p) = v;
+            } else {
+                if (n < a.n) p[0] = static_cast<uint16_t>(v);
+                if (n + 1 < a.n) p[1] = static_cast<uint16_t>(v >> 16);
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ void st_shared_v2(uint32_t addr, float x, float y) {
@@ -752,9 +770,10 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
                     for (int u = 0; u < 16; ++u) sum[c + u] = v[u];
                 }
             }
-            if (CG == 2 && a.y_tma) {
+            if (CG == 2) {
                 // 128 bytes of 32 rows at a time, 128B-swizzled, then one TMA store (which
-                // leaves out what lies past Y's edges)
+                // leaves out what lies past Y's edges), or, where Y's rows are not 16-byte
+                // aligned, a copy row by row
                 constexpr int kBoxCols = F32 ? 32 : 64;
                 const bool bf16 = a.y_type == VNM_BF16;
                 const uint32_t bufs = smem_base + ST * Cfg::kStageBytes + (warp - kHelpers) * 2 * kStoreBox;
@@ -795,6 +814,12 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
                             st_shared_v4(dst + 16 * (j ^ flip), w[0], w[1], w[2], w[3]);
                         }
                     }
+                    if (!a.y_tma) {
+                        __syncwarp();
+                        copy_box<F32>(a, buf, m0, n0 + c, lane);
+                        __syncwarp();
+                        continue;
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -803,16 +828,6 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
                         tma_store_commit();
                     }
                 }
-                continue;
-            }
-            if (Cfg::kFrag) {
-#pragma unroll
-                for (int x = 0; x < COLS / 16; ++x)
-#pragma unroll
-                    for (int h = 0; h < 8; ++h)
-                        store_pair(a, static_cast<int64_t>(m0) + 16 * (x & 1) + (lane >> 2) + 8 * (h & 1),
-                                   static_cast<int64_t>(n0) + 32 * (x / 2) + 8 * (h / 2) + 2 * (lane & 3),
-                                   sum[16 * x + 4 * (h / 2) + 2 * (h & 1)], sum[16 * x + 4 * (h / 2) + 2 * (h & 1) + 1]);
                 continue;
             }
             if (m >= a.m) continue;

@@ -361,3 +361,32 @@ def test_outputs_that_end_inside_a_tile(T, R, K, y_type):
         vnm.vnm_fp8_linear(xq, xs, wq, ws, y)
     for y in Y:
         check_linear(y, ref, K, 0)
+
+
+@pytest.mark.parametrize("T,R,K,off", [(300, 301, 100, 0), (2500, 1999, 130, 0), (2500, 2003, 130, 1), (600, 2050, 70, 3)])
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("y_type", [F16, F32])
+def test_outputs_of_any_alignment(T, R, K, off, rows, y_type):
+    """Rows of Y that TMA cannot write: odd widths, and a start off every alignment but the type's."""
+    xq, xs, wq, ws = _operands(T, R, K, rows, E4M3, E4M3, 15)
+    buf = torch.full((T + 2, R + off), 7.0, dtype=y_type, device=DEV)
+    Y = buf[1:T + 1, off:]
+    vnm.vnm_fp8_linear(xq, xs, wq, ws, Y)
+    check_linear(Y, linear64(xq, xs, wq, ws, None, 0), K, 0)
+    buf[1:T + 1, off:] = 7.0
+    assert (buf == 7.0).all()
+
+
+@pytest.mark.parametrize("T,R,K", [(1, 33, 1259), (3, 16, 127), (8, 40, 129), (5, 17, 1)])
+def test_last_rows_end_with_their_storage(T, R, K):
+    """Operands whose storage ends with the last row's last element: nothing past it is read
+    into the sums (the storage is cut from buffers of NaN bytes)."""
+    xq, xs, wq, ws = _operands(T, R, K, 1, E4M3, E4M3, 16)
+    ld = -(-K // 16) * 16
+    flat = [torch.full(((n - 1) * ld + K + 64,), 0x7F, dtype=torch.uint8, device=DEV) for n in (T, R)]
+    cut = [f[: (n - 1) * ld + K].as_strided((n, K), (ld, 1)) for f, n in zip(flat, (T, R))]
+    cut[0].copy_(xq.view(torch.uint8))
+    cut[1].copy_(wq.view(torch.uint8))
+    Y = torch.empty((T, R), device=DEV)
+    vnm.vnm_fp8_linear(cut[0].view(E4M3), xs, cut[1].view(E4M3), ws, Y)
+    check_linear(Y, linear64(xq, xs, wq, ws, None, 0), K, 0)
