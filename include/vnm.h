@@ -39,7 +39,8 @@
  *     time. The library's global state is limited to: per-process caches
  *     filled on first use (the driver's tensor-map encoder and context
  *     queries; per kernel instance and device, the shared-memory attribute
- *     and the co-resident CTA count), all guarded for concurrent callers; and
+ *     and the co-resident CTA count; per device, the SM count), all guarded
+ *     for concurrent callers; and
  *     the static 8 MiB (+ 256-byte) device array of vnm_spmm_noalloc, held by
  *     every GPU that loads the library, with its address resolved once per
  *     CUDA context.
@@ -404,8 +405,9 @@ vnm_status vnm_spmm_noalloc(int64_t R, int64_t K, int32_t V, int32_t M, const vo
  * of a row (1 x 128, activations and gradients) or for each 128 x 128 block
  * (weights); the last group or block of an edge is shorter. An element stands
  * for q * s. For a group with largest magnitude m:
- *   s = max(m / F, 2^-100), F = 448 (e4m3) or 57344 (e5m2),
- *   q = the nearest fp8 value to y * (1 / s) (ties to even, saturating);
+ *   s = max(m * (1 / F), 2^-100), F = 448 (e4m3) or 57344 (e5m2),
+ *   q = the nearest fp8 value to y * (1 / s) (ties to even, saturating),
+ * each reciprocal and product rounded to fp32;
  * a group that holds an Inf or a NaN gets s = NaN and q = NaN throughout.
  * Scales are addressed with two strides in elements: the scale of row (or row
  * block) i and column group g is s[i * s_rs + g * s_cs].
@@ -428,7 +430,8 @@ vnm_status vnm_spmm_noalloc(int64_t R, int64_t K, int32_t V, int32_t M, const vo
  * ignored. Any alignment of the type; 16-byte aligned rows run faster.
  * h may be x or residual themselves, and so may y where h is not (same pointer
  * and leading dimension); no other overlap.
- * A NaN in a row makes its y, rstd and groups NaN. eps >= 0.
+ * A NaN in a row makes its y, rstd and groups NaN; an Inf (or squares whose sum
+ * overflows fp32) makes rstd 0. eps >= 0.
  * Errors: VNM_ERR_INVALID_ARG (pointers, alignment, leading dimensions, types,
  * eps, h without residual, neither y nor q), VNM_ERR_CUDA.
  */
@@ -483,7 +486,8 @@ vnm_status vnm_fp8_quantize(const void* X, int64_t ld_x, int64_t R, int64_t C, v
  * with r' = r for w_block_rows = 1 and r / 128 for 128. X: T x K with 1 x 128
  * scales; W: R x K. All sums are fp32; Y (T x R, ld_y >= R; VNM_F16, VNM_BF16 or
  * VNM_F32) is rounded once, bias ([R], bias_type, or NULL) and act are
- * applied in fp32 before that. The gradients are products of the same form:
+ * applied in fp32 before that (GELU to 1e-7 |z| of its argument z). The gradients
+ * are products of the same form:
  *   dX = dY . W:   X := dY (1 x 128 along R), W := W^T (vnm_fp8_quantize's qt, st);
  *   dW = dY^T . X: X := dY^T, W := X^T (both qt, st with block_rows = 1).
  * xq and wq: 16-byte aligned with ld % 16 == 0 (elements past K in the

@@ -14,6 +14,11 @@
 // K blocks among themselves and meet once in shared memory, in a fixed order. The
 // loads of W run kRing blocks ahead, those of x and the scales (from L2) one. The
 // code is kept short: a launch this small pays for every line that it fetches.
+//
+// Measured, one token: 4096 x 4096 4.6 us, 3.7 TB/s, of which about 2 us are the launch
+// and the first round trip (the tiled kernel 7.2); 11008 x 4096 13.0 us (12.6); 1024 x
+// 1024 2.4 us (5.0). Up to 8 tokens cost the same; 16 as two groups of 8 took 8.0 and
+// 18.5 us against the tiled kernel's 7.7 and 13.2, so they go there.
 #include "vnm_dense.h"
 #include "vnm_fp8.cuh"
 

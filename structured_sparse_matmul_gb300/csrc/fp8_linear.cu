@@ -25,6 +25,13 @@
 //   warps 4..  add up: thread = row of P, whose scale it loads two blocks ahead; 4
 //              warps, or 8 with half the columns each.
 // Every mbarrier wait is bounded.
+//
+// Measured: 8192 tokens, 11008 x 4096, bf16 out: 287-302 us, 2.45-2.57 PFLOP/s, 1.3-1.4 of
+// the dense bf16 product's rate. The loads and MMAs alone run in 196 us, the sums alone
+// (TMEM loads, 32768 fp32 FMAs a K block and SM, barriers) in 250: with two TMEM buffers
+// a K block's MMAs wait for the sums of the block before last (tensor pipe 43 % busy).
+// Scales on both sides (4096 x 1024 outputs over 8192 tokens, fp32): 47.7 us. 16 tokens,
+// 11008 x 4096: 13.7 us, 3.3 TB/s, a chain of 16 K blocks a CTA and 5 us of start and end.
 #include <cudaTypedefs.h>
 
 #include <algorithm>

@@ -15,6 +15,9 @@
 // transposed bytes cross one 16 KB tile in shared memory, in 8-byte units whose
 // index is XORed with the column group so that writing 16 columns and reading
 // 16 rows both touch every bank once.
+//
+// Measured: 8192 x 4096 bf16 to both forms 28.0 us, 4.9 TB/s, 0.72 of a copy's rate;
+// 11008 x 4096 fp16 in blocks 32.3 us, 5.6 TB/s, 0.82 (issue 63 and 55 % active).
 #include <type_traits>
 
 #include "vnm_dense.h"
