@@ -5,12 +5,13 @@
  * These calls stand in decode loops, where one takes a few microseconds on the
  * GPU. Reading a tensor's shape, type, device, strides and address from Python
  * and passing two dozen arguments through ctypes costs 7 us a call; the same reads
- * from C cost 2. Nothing is computed here: every check is of a tensor's description,
+ * from C cost 2, each attribute read once. Nothing is computed here: every check is of a tensor's description,
  * and the functions called are the library's exported ones, whose addresses
  * setup() is given.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <string.h>
 
 #include "../../include/vnm.h"
 
@@ -27,15 +28,18 @@ static testing_linear_t fn_linear_skip;
 
 static PyObject *py_f16, *py_f32, *py_bf16, *py_e4m3, *py_e5m2, *py_i32; /* torch dtypes */
 static PyObject *py_current_device, *py_current_stream;
-static PyObject *s_shape, *s_dtype, *s_get_device, *s_stride, *s_data_ptr, *s_cuda_stream;
+static PyObject *s_shape, *s_dtype, *s_get_device, *s_stride, *s_data_ptr, *s_cuda_stream, *s_nbytes;
 
-/* A tensor's description. */
+/* A tensor's description, each attribute read once; dims = -1 for None. */
 typedef struct {
-    int64_t rows, cols; /* a vector: cols = its length, rows = -1 */
+    PyObject* object;   /* borrowed from the call's arguments */
     PyObject* dtype;    /* borrowed: torch's dtype objects live for good */
-} Desc;
+    Py_ssize_t dims;
+    int64_t size[2], stride[2], device;
+    void* p;
+} Tensor;
 
-static int long_of(PyObject* o, int64_t* out) {
+static int long_of(PyObject* o, int64_t* out) { /* steals o */
     if (o == NULL) return -1;
     *out = PyLong_AsLongLong(o);
     Py_DECREF(o);
@@ -61,88 +65,83 @@ static int ints_of(PyObject* t, int64_t* v, Py_ssize_t* n) { /* up to two whole 
     return 0;
 }
 
-static int describe(PyObject* t, Desc* d, int64_t* device) {
-    int64_t v[2] = {0, 0};
-    Py_ssize_t n = 0;
-    if (ints_of(PyObject_GetAttr(t, s_shape), v, &n) < 0) return -1;
-    d->rows = n == 2 ? v[0] : -1;
-    d->cols = n == 2 ? v[1] : n == 1 ? v[0] : -1;
-    if (n != 1 && n != 2) d->rows = -2;
-    d->dtype = PyObject_GetAttr(t, s_dtype);
-    if (d->dtype == NULL) return -1;
-    Py_DECREF(d->dtype);
-    return long_of(PyObject_CallMethodNoArgs(t, s_get_device), device);
+static int read_tensor(PyObject* o, Tensor* t) {
+    memset(t, 0, sizeof(*t));
+    t->object = o;
+    t->dims = -1;
+    t->device = -1;
+    if (o == Py_None) return 0;
+    Py_ssize_t strides;
+    int64_t address;
+    if (ints_of(PyObject_GetAttr(o, s_shape), t->size, &t->dims) < 0 ||
+        ints_of(PyObject_CallMethodNoArgs(o, s_stride), t->stride, &strides) < 0 ||
+        long_of(PyObject_CallMethodNoArgs(o, s_get_device), &t->device) < 0 ||
+        long_of(PyObject_CallMethodNoArgs(o, s_data_ptr), &address) < 0)
+        return -1;
+    t->dtype = PyObject_GetAttr(o, s_dtype);
+    if (t->dtype == NULL) return -1;
+    Py_DECREF(t->dtype);
+    t->p = (void*)(intptr_t)address;
+    return 0;
 }
 
-static int refuse(PyObject* t, const char* name, int64_t rows, int64_t cols, PyObject* dtype, int64_t device) {
-    PyObject* shape = PyObject_GetAttr(t, s_shape);
-    PyObject* got = PyObject_GetAttr(t, s_dtype);
+static int read_all(PyObject* const* o, const int* which, int n, Tensor* t) {
+    for (int i = 0; i < n; ++i)
+        if (read_tensor(o[which[i]], &t[i]) < 0) return -1;
+    return 0;
+}
+
+static int refuse(const Tensor* t, const char* name, int64_t rows, int64_t cols, PyObject* dtype, int64_t device) {
+    PyObject* shape = PyObject_GetAttr(t->object, s_shape);
     PyObject* want = dtype ? PyObject_Str(dtype) : PyUnicode_FromString("any type served");
-    if (shape && got && want) {
+    if (shape && want) {
         if (rows >= 0)
             PyErr_Format(PyExc_ValueError, "%s must be a row-major tensor of shape (%lld, %lld), %U, on cuda:%lld; got %S, %S", name,
-                         (long long)rows, (long long)cols, want, (long long)device, shape, got);
+                         (long long)rows, (long long)cols, want, (long long)device, shape, t->dtype);
         else
             PyErr_Format(PyExc_ValueError, "%s must be a contiguous tensor of shape (%lld,), %U, on cuda:%lld; got %S, %S", name,
-                         (long long)cols, want, (long long)device, shape, got);
+                         (long long)cols, want, (long long)device, shape, t->dtype);
     }
     Py_XDECREF(shape);
-    Py_XDECREF(got);
     Py_XDECREF(want);
     return -1;
 }
 
-static int address(PyObject* t, void** p) {
-    int64_t v;
-    if (long_of(PyObject_CallMethodNoArgs(t, s_data_ptr), &v) < 0) return -1;
-    *p = (void*)(intptr_t)v;
+/* Row-major rows x cols, of a type or (dtype NULL) any; *ld its leading dimension (1 for None). */
+static int matrix(const Tensor* t, const char* name, int64_t rows, int64_t cols, PyObject* dtype, int64_t device, int64_t* ld) {
+    *ld = 1;
+    if (t->dims < 0) return 0;
+    if (t->dims != 2 || t->size[0] != rows || t->size[1] != cols || t->device != device ||
+        (dtype != NULL && t->dtype != dtype) || (cols > 1 && t->stride[1] != 1))
+        return refuse(t, name, rows, cols, dtype, device);
+    /* (a matrix of one row may carry any stride) */
+    *ld = t->stride[0] >= cols && t->stride[0] > 0 ? t->stride[0] : cols > 0 ? cols : 1;
     return 0;
 }
 
-/* Row-major rows x cols (rows = -1: a contiguous vector), of a type or (dtype NULL) any. */
-static int tensor(PyObject* t, const char* name, int64_t rows, int64_t cols, PyObject* dtype, int64_t device, void** p,
-                  int64_t* ld) {
-    *p = NULL;
-    *ld = 1;
-    if (t == Py_None) return 0;
-    Desc d;
-    int64_t dev, st[2] = {1, 1};
-    Py_ssize_t n;
-    if (describe(t, &d, &dev) < 0 || ints_of(PyObject_CallMethodNoArgs(t, s_stride), st, &n) < 0) return -1;
-    if (d.rows != rows || d.cols != cols || dev != device || (dtype != NULL && d.dtype != dtype) ||
-        (cols > 1 && st[n - 1] != 1))
-        return refuse(t, name, rows, cols, dtype, device);
-    /* (a matrix of one row may carry any stride) */
-    if (rows >= 0) *ld = st[0] >= cols && st[0] > 0 ? st[0] : cols > 0 ? cols : 1;
-    return address(t, p);
+/* A contiguous vector. */
+static int vector(const Tensor* t, const char* name, int64_t n, PyObject* dtype, int64_t device) {
+    if (t->dims < 0) return 0;
+    if (t->dims != 1 || t->size[0] != n || t->device != device || (dtype != NULL && t->dtype != dtype) ||
+        (n > 1 && t->stride[0] != 1))
+        return refuse(t, name, -1, n, dtype, device);
+    return 0;
 }
 
 /* fp32 scales of any strides. */
-static int scales(PyObject* t, const char* name, int64_t rows, int64_t cols, int64_t device, float** p, int64_t* rs,
-                  int64_t* cs) {
-    *p = NULL;
-    *rs = *cs = 0;
-    if (t == Py_None) return 0;
-    Desc d;
-    int64_t dev, st[2] = {0, 0};
-    Py_ssize_t n;
-    if (describe(t, &d, &dev) < 0 || ints_of(PyObject_CallMethodNoArgs(t, s_stride), st, &n) < 0) return -1;
-    if (d.rows != rows || d.cols != cols || dev != device || d.dtype != py_f32)
+static int scales(const Tensor* t, const char* name, int64_t rows, int64_t cols, int64_t device) {
+    if (t->dims < 0) return 0;
+    if (t->dims != 2 || t->size[0] != rows || t->size[1] != cols || t->device != device || t->dtype != py_f32)
         return refuse(t, name, rows, cols, py_f32, device);
-    *rs = st[0];
-    *cs = st[1];
-    void* v;
-    if (address(t, &v) < 0) return -1;
-    *p = v;
     return 0;
 }
 
-static int dtype_of(PyObject* dtype, const char* name, vnm_dtype* out) {
-    if (dtype == py_f16)
+static int dtype_of(const Tensor* t, const char* name, vnm_dtype* out) {
+    if (t->dims >= 0 && t->dtype == py_f16)
         *out = VNM_F16;
-    else if (dtype == py_bf16)
+    else if (t->dims >= 0 && t->dtype == py_bf16)
         *out = VNM_BF16;
-    else if (dtype == py_f32)
+    else if (t->dims >= 0 && t->dtype == py_f32)
         *out = VNM_F32;
     else {
         PyErr_Format(PyExc_ValueError, "%s must be fp16, bf16 or fp32", name);
@@ -151,10 +150,10 @@ static int dtype_of(PyObject* dtype, const char* name, vnm_dtype* out) {
     return 0;
 }
 
-static int fp8_of(PyObject* dtype, const char* name, vnm_fp8* out) {
-    if (dtype == py_e4m3)
+static int fp8_of(const Tensor* t, const char* name, vnm_fp8* out) {
+    if (t->dims >= 0 && t->dtype == py_e4m3)
         *out = VNM_E4M3;
-    else if (dtype == py_e5m2)
+    else if (t->dims >= 0 && t->dtype == py_e5m2)
         *out = VNM_E5M2;
     else {
         PyErr_Format(PyExc_ValueError, "%s must be float8_e4m3fn or float8_e5m2", name);
@@ -163,23 +162,15 @@ static int fp8_of(PyObject* dtype, const char* name, vnm_fp8* out) {
     return 0;
 }
 
-/* The type of a tensor argument that may be None (then `none`). */
-static PyObject* type_of(PyObject* t) {
-    PyObject* d = PyObject_GetAttr(t, s_dtype);
-    Py_XDECREF(d);
-    return d;
-}
-
 /* The call's first tensor: a matrix on the current CUDA device. */
-static int first(PyObject* t, const char* name, Desc* d, int64_t* device) {
+static int first(const Tensor* t, const char* name) {
     int64_t cur;
-    if (describe(t, d, device) < 0) return -1;
-    if (d->rows < 0 || *device < 0) {
+    if (t->dims != 2 || t->device < 0) {
         PyErr_Format(PyExc_ValueError, "%s must be a CUDA matrix", name);
         return -1;
     }
     if (long_of(PyObject_CallNoArgs(py_current_device), &cur) < 0) return -1;
-    if (cur != *device) {
+    if (cur != t->device) {
         PyErr_Format(PyExc_ValueError, "%s must be on the current CUDA device", name);
         return -1;
     }
@@ -212,51 +203,57 @@ static int count(Py_ssize_t n, Py_ssize_t want) {
 
 /* x, weight, eps, residual, h, y, rstd, q, q_scale, stream -> status */
 static PyObject* rmsnorm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-    Desc x, dq;
-    int64_t dev, ld_x, ld_r, ld_h, ld_y, ld_q, one, rs, cs, q_dev;
-    void *xp, *rp, *wp, *hp, *yp, *sp, *qp;
-    float* cp;
+    static const int which[8] = {0, 1, 3, 4, 5, 6, 7, 8};
+    Tensor t[8];
+    const Tensor *x = &t[0], *w = &t[1], *r = &t[2], *h = &t[3], *y = &t[4], *rstd = &t[5], *q = &t[6], *s = &t[7];
+    int64_t ld_x, ld_r, ld_h, ld_y, ld_q;
     vnm_dtype type;
     vnm_fp8 q_type = VNM_E4M3;
     vnm_stream_t stream;
-    if (count(n, 10) < 0 || first(a[0], "x", &x, &dev) < 0 || dtype_of(x.dtype, "x", &type) < 0) return NULL;
+    if (count(n, 10) < 0 || read_all(a, which, 8, t) < 0 || first(x, "x") < 0 || dtype_of(x, "x", &type) < 0) return NULL;
     const double eps = PyFloat_AsDouble(a[2]);
     if (eps == -1.0 && PyErr_Occurred()) return NULL;
-    const int64_t T = x.rows, D = x.cols;
-    if (tensor(a[0], "x", T, D, NULL, dev, &xp, &ld_x) < 0 || tensor(a[1], "weight", -1, D, x.dtype, dev, &wp, &one) < 0 ||
-        tensor(a[3], "residual", T, D, x.dtype, dev, &rp, &ld_r) < 0 || tensor(a[4], "h", T, D, x.dtype, dev, &hp, &ld_h) < 0 ||
-        tensor(a[5], "y", T, D, x.dtype, dev, &yp, &ld_y) < 0 || tensor(a[6], "rstd", -1, T, py_f32, dev, &sp, &one) < 0 ||
-        tensor(a[7], "q", T, D, NULL, dev, &qp, &ld_q) < 0 || scales(a[8], "q_scale", T, groups(D), dev, &cp, &rs, &cs) < 0)
+    const int64_t T = x->size[0], D = x->size[1], dev = x->device;
+    if (matrix(x, "x", T, D, NULL, dev, &ld_x) < 0 || vector(w, "weight", D, x->dtype, dev) < 0 ||
+        matrix(r, "residual", T, D, x->dtype, dev, &ld_r) < 0 || matrix(h, "h", T, D, x->dtype, dev, &ld_h) < 0 ||
+        matrix(y, "y", T, D, x->dtype, dev, &ld_y) < 0 || vector(rstd, "rstd", T, py_f32, dev) < 0 ||
+        matrix(q, "q", T, D, NULL, dev, &ld_q) < 0 || scales(s, "q_scale", T, groups(D), dev) < 0 ||
+        (q->dims >= 0 && fp8_of(q, "q", &q_type) < 0) || stream_of(a[9], dev, &stream) < 0)
         return NULL;
-    if (a[7] != Py_None && (describe(a[7], &dq, &q_dev) < 0 || fp8_of(dq.dtype, "q", &q_type) < 0)) return NULL;
-    if (stream_of(a[9], dev, &stream) < 0) return NULL;
     vnm_status st;
     Py_BEGIN_ALLOW_THREADS
-    st = fn_rmsnorm(xp, ld_x, rp, ld_r, wp, (float)eps, T, D, type, hp, ld_h, yp, ld_y, sp, qp, ld_q, q_type, cp, rs, cs, stream);
+    st = fn_rmsnorm(x->p, ld_x, r->p, ld_r, w->p, (float)eps, T, D, type, h->p, ld_h, y->p, ld_y, rstd->p, q->p, ld_q, q_type,
+                    s->p, s->stride[0], s->stride[1], stream);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(st);
 }
 
-/* dy, h, weight, rstd, dh, dweight, dresidual, workspace address, workspace bytes, stream -> status */
+/* dy, h, weight, rstd, dh, dweight, dresidual, workspace, stream -> status */
 static PyObject* rmsnorm_backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-    Desc x;
-    int64_t dev, ld_dy, ld_h, ld_r, ld_o, one, ws, bytes;
-    void *yp, *hp, *wp, *sp, *rp, *op, *gp;
+    static const int which[8] = {0, 1, 2, 3, 4, 5, 6, 7};
+    Tensor t[8];
+    const Tensor *dy = &t[0], *h = &t[1], *w = &t[2], *rstd = &t[3], *dh = &t[4], *dw = &t[5], *dr = &t[6], *ws = &t[7];
+    int64_t ld_dy, ld_h, ld_r, ld_o, bytes = 0;
     vnm_dtype type;
     vnm_stream_t stream;
-    if (count(n, 10) < 0 || first(a[0], "dy", &x, &dev) < 0 || dtype_of(x.dtype, "dy", &type) < 0) return NULL;
-    const int64_t T = x.rows, D = x.cols;
-    if (tensor(a[0], "dy", T, D, NULL, dev, &yp, &ld_dy) < 0 || tensor(a[1], "h", T, D, x.dtype, dev, &hp, &ld_h) < 0 ||
-        tensor(a[2], "weight", -1, D, x.dtype, dev, &wp, &one) < 0 || tensor(a[3], "rstd", -1, T, py_f32, dev, &sp, &one) < 0 ||
-        tensor(a[4], "dh", T, D, x.dtype, dev, &op, &ld_o) < 0 || tensor(a[5], "dweight", -1, D, py_f32, dev, &gp, &one) < 0 ||
-        tensor(a[6], "dresidual", T, D, x.dtype, dev, &rp, &ld_r) < 0)
+    if (count(n, 9) < 0 || read_all(a, which, 8, t) < 0 || first(dy, "dy") < 0 || dtype_of(dy, "dy", &type) < 0) return NULL;
+    const int64_t T = dy->size[0], D = dy->size[1], dev = dy->device;
+    if (matrix(dy, "dy", T, D, NULL, dev, &ld_dy) < 0 || matrix(h, "h", T, D, dy->dtype, dev, &ld_h) < 0 ||
+        vector(w, "weight", D, dy->dtype, dev) < 0 || vector(rstd, "rstd", T, py_f32, dev) < 0 ||
+        matrix(dh, "dh", T, D, dy->dtype, dev, &ld_o) < 0 || vector(dw, "dweight", D, py_f32, dev) < 0 ||
+        matrix(dr, "dresidual", T, D, dy->dtype, dev, &ld_r) < 0)
         return NULL;
-    ws = PyLong_AsLongLong(a[7]);
-    bytes = PyLong_AsLongLong(a[8]);
-    if (PyErr_Occurred() || stream_of(a[9], dev, &stream) < 0) return NULL;
+    if (ws->dims >= 0) {
+        if (ws->device != dev) {
+            PyErr_SetString(PyExc_ValueError, "workspace must be on dy's device");
+            return NULL;
+        }
+        if (long_of(PyObject_GetAttr(ws->object, s_nbytes), &bytes) < 0) return NULL;
+    }
+    if (stream_of(a[8], dev, &stream) < 0) return NULL;
     vnm_status st;
     Py_BEGIN_ALLOW_THREADS
-    st = fn_rmsnorm_backward(yp, ld_dy, hp, ld_h, wp, sp, rp, ld_r, T, D, type, op, ld_o, gp, (void*)(intptr_t)ws,
+    st = fn_rmsnorm_backward(dy->p, ld_dy, h->p, ld_h, w->p, rstd->p, dr->p, ld_r, T, D, type, dh->p, ld_o, dw->p, ws->p,
                              (size_t)bytes, stream);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(st);
@@ -264,81 +261,71 @@ static PyObject* rmsnorm_backward(PyObject* self, PyObject* const* a, Py_ssize_t
 
 /* X, q, s, qt, st, block_rows, stream -> status */
 static PyObject* fp8_quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-    Desc x;
-    int64_t dev, ld_x, ld_q, ld_t, rs, cs, trs, tcs;
-    void *xp, *qp, *tp;
-    float *sp, *up;
+    static const int which[5] = {0, 1, 2, 3, 4};
+    Tensor t[5];
+    const Tensor *x = &t[0], *q = &t[1], *s = &t[2], *qt = &t[3], *u = &t[4];
+    int64_t ld_x, ld_q, ld_t;
     vnm_dtype type;
     vnm_fp8 q_type = VNM_E4M3, t_type = VNM_E4M3;
     vnm_stream_t stream;
-    PyObject* d;
-    if (count(n, 7) < 0 || first(a[0], "X", &x, &dev) < 0 || dtype_of(x.dtype, "X", &type) < 0) return NULL;
+    if (count(n, 7) < 0 || read_all(a, which, 5, t) < 0 || first(x, "X") < 0 || dtype_of(x, "X", &type) < 0) return NULL;
     const long block = PyLong_AsLong(a[5]);
     if (block == -1 && PyErr_Occurred()) return NULL;
-    const int64_t R = x.rows, C = x.cols, per = block > 0 ? block : 1;
-    if (a[1] != Py_None && ((d = type_of(a[1])) == NULL || fp8_of(d, "q", &q_type) < 0)) return NULL;
-    if (a[3] != Py_None && ((d = type_of(a[3])) == NULL || fp8_of(d, "qt", &t_type) < 0)) return NULL;
-    if (a[1] != Py_None && a[3] != Py_None && q_type != t_type) {
+    const int64_t R = x->size[0], C = x->size[1], dev = x->device, per = block > 0 ? block : 1;
+    if ((q->dims >= 0 && fp8_of(q, "q", &q_type) < 0) || (qt->dims >= 0 && fp8_of(qt, "qt", &t_type) < 0)) return NULL;
+    if (q->dims >= 0 && qt->dims >= 0 && q_type != t_type) {
         PyErr_SetString(PyExc_ValueError, "q and qt must have the same type");
         return NULL;
     }
-    if (tensor(a[0], "X", R, C, NULL, dev, &xp, &ld_x) < 0 || tensor(a[1], "q", R, C, NULL, dev, &qp, &ld_q) < 0 ||
-        scales(a[2], "s", (R + per - 1) / per, groups(C), dev, &sp, &rs, &cs) < 0 ||
-        tensor(a[3], "qt", C, R, NULL, dev, &tp, &ld_t) < 0 ||
-        scales(a[4], "st", (C + per - 1) / per, groups(R), dev, &up, &trs, &tcs) < 0 || stream_of(a[6], dev, &stream) < 0)
+    if (matrix(x, "X", R, C, NULL, dev, &ld_x) < 0 || matrix(q, "q", R, C, NULL, dev, &ld_q) < 0 ||
+        scales(s, "s", (R + per - 1) / per, groups(C), dev) < 0 || matrix(qt, "qt", C, R, NULL, dev, &ld_t) < 0 ||
+        scales(u, "st", (C + per - 1) / per, groups(R), dev) < 0 || stream_of(a[6], dev, &stream) < 0)
         return NULL;
     vnm_status st;
     Py_BEGIN_ALLOW_THREADS
-    st = fn_quantize(xp, ld_x, R, C, type, (int32_t)block, a[1] != Py_None ? q_type : t_type, qp, ld_q, sp, rs, cs, tp,
-                     ld_t, up, trs, tcs, stream);
+    st = fn_quantize(x->p, ld_x, R, C, type, (int32_t)block, q->dims >= 0 ? q_type : t_type, q->p, ld_q, s->p, s->stride[0],
+                     s->stride[1], qt->p, ld_t, u->p, u->stride[0], u->stride[1], stream);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(st);
 }
 
 /* xq, x_scale, wq, w_scale, Y, bias, act, status, skip_stage (-1: none), stream -> status */
 static PyObject* fp8_linear(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-    Desc x, w, ws, y, b;
-    int64_t dev, d2, ld_x, ld_w, ld_y, one, xrs, xcs, wrs, wcs;
-    void *xp, *wp, *yp, *bp, *sp;
-    float *xs, *wsp;
+    static const int which[7] = {0, 1, 2, 3, 4, 5, 7};
+    Tensor t[7];
+    const Tensor *x = &t[0], *xs = &t[1], *w = &t[2], *ws = &t[3], *y = &t[4], *b = &t[5], *status = &t[6];
+    int64_t ld_x, ld_w, ld_y;
     vnm_fp8 x_type, w_type;
     vnm_dtype y_type, b_type = VNM_F32;
     vnm_stream_t stream;
-    if (count(n, 10) < 0 || first(a[0], "xq", &x, &dev) < 0 || fp8_of(x.dtype, "xq", &x_type) < 0 ||
-        describe(a[2], &w, &d2) < 0 || fp8_of(w.dtype, "wq", &w_type) < 0 || describe(a[3], &ws, &d2) < 0 ||
-        describe(a[4], &y, &d2) < 0 || dtype_of(y.dtype, "Y", &y_type) < 0)
+    if (count(n, 10) < 0 || read_all(a, which, 7, t) < 0 || first(x, "xq") < 0 || fp8_of(x, "xq", &x_type) < 0 ||
+        fp8_of(w, "wq", &w_type) < 0 || dtype_of(y, "Y", &y_type) < 0)
         return NULL;
     const long act = PyLong_AsLong(a[6]), skip = PyLong_AsLong(a[8]);
     if (PyErr_Occurred()) return NULL;
-    const int64_t T = x.rows, K = x.cols, R = w.rows >= 0 ? w.rows : 0;
+    const int64_t T = x->size[0], K = x->size[1], R = w->size[0], dev = x->device;
     /* the scales tell a scale a row from one for 128 rows (the same thing for one row) */
-    const int32_t block = ws.rows == R ? 1 : 128;
-    if (tensor(a[0], "xq", T, K, NULL, dev, &xp, &ld_x) < 0 || tensor(a[2], "wq", R, K, NULL, dev, &wp, &ld_w) < 0 ||
-        tensor(a[4], "Y", T, R, NULL, dev, &yp, &ld_y) < 0 ||
-        scales(a[1], "x_scale", T, groups(K), dev, &xs, &xrs, &xcs) < 0 ||
-        scales(a[3], "w_scale", block == 1 ? R : groups(R), groups(K), dev, &wsp, &wrs, &wcs) < 0 ||
-        tensor(a[5], "bias", -1, R, NULL, dev, &bp, &one) < 0)
+    const int32_t block = ws->dims == 2 && ws->size[0] == R ? 1 : 128;
+    if (matrix(x, "xq", T, K, NULL, dev, &ld_x) < 0 || matrix(w, "wq", R, K, NULL, dev, &ld_w) < 0 ||
+        matrix(y, "Y", T, R, NULL, dev, &ld_y) < 0 || scales(xs, "x_scale", T, groups(K), dev) < 0 ||
+        scales(ws, "w_scale", block == 1 ? R : groups(R), groups(K), dev) < 0 || vector(b, "bias", R, NULL, dev) < 0 ||
+        (b->dims >= 0 && dtype_of(b, "bias", &b_type) < 0))
         return NULL;
-    if (a[5] != Py_None && (describe(a[5], &b, &d2) < 0 || dtype_of(b.dtype, "bias", &b_type) < 0)) return NULL;
-    sp = NULL;
-    if (a[7] != Py_None) {
-        Desc s;
-        if (describe(a[7], &s, &d2) < 0) return NULL;
-        if (s.dtype != py_i32 || d2 != dev || s.rows != -1 || s.cols < 3) {
-            PyErr_SetString(PyExc_ValueError, "status must be a CUDA int32 tensor of at least 3 words");
-            return NULL;
-        }
-        if (address(a[7], &sp) < 0) return NULL;
+    if (status->dims >= 0 && (status->dtype != py_i32 || status->device != dev || status->dims != 1 || status->size[0] < 3 ||
+                              status->stride[0] != 1)) {
+        PyErr_SetString(PyExc_ValueError, "status must be a CUDA int32 tensor of at least 3 words");
+        return NULL;
     }
     if (stream_of(a[9], dev, &stream) < 0) return NULL;
     vnm_status st;
     Py_BEGIN_ALLOW_THREADS
     if (skip >= 0)
-        st = fn_linear_skip(xp, ld_x, x_type, xs, xrs, xcs, wp, ld_w, w_type, wsp, wrs, wcs, block, T, R, K, bp, b_type,
-                            (vnm_activation)act, yp, ld_y, y_type, sp, (int32_t)skip, stream);
+        st = fn_linear_skip(x->p, ld_x, x_type, xs->p, xs->stride[0], xs->stride[1], w->p, ld_w, w_type, ws->p, ws->stride[0],
+                            ws->stride[1], block, T, R, K, b->p, b_type, (vnm_activation)act, y->p, ld_y, y_type, status->p,
+                            (int32_t)skip, stream);
     else
-        st = fn_linear(xp, ld_x, x_type, xs, xrs, xcs, wp, ld_w, w_type, wsp, wrs, wcs, block, T, R, K, bp, b_type,
-                       (vnm_activation)act, yp, ld_y, y_type, sp, stream);
+        st = fn_linear(x->p, ld_x, x_type, xs->p, xs->stride[0], xs->stride[1], w->p, ld_w, w_type, ws->p, ws->stride[0],
+                       ws->stride[1], block, T, R, K, b->p, b_type, (vnm_activation)act, y->p, ld_y, y_type, status->p, stream);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(st);
 }
@@ -394,6 +381,7 @@ PyMODINIT_FUNC PyInit__vnm_binding(void) {
     s_stride = PyUnicode_InternFromString("stride");
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
     s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
-    if (!s_shape || !s_dtype || !s_get_device || !s_stride || !s_data_ptr || !s_cuda_stream) return NULL;
+    s_nbytes = PyUnicode_InternFromString("nbytes");
+    if (!s_shape || !s_dtype || !s_get_device || !s_stride || !s_data_ptr || !s_cuda_stream || !s_nbytes) return NULL;
     return PyModule_Create(&module);
 }

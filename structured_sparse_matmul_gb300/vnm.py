@@ -513,10 +513,7 @@ def vnm_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: Optional[tor
     added where given) and dweight (fp32 (D,)); either may be None."""
     if workspace is None and dweight is not None:
         workspace = torch.empty(vnm_rmsnorm_backward_workspace_size(*dy.shape), dtype=torch.uint8, device=dy.device)
-    ws_ptr, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    if workspace is not None and workspace.get_device() != dy.get_device():
-        raise ValueError("workspace must be on dy's device")
-    code = _native().rmsnorm_backward(dy, h, weight, rstd, dh, dweight, dresidual, ws_ptr, ws_bytes, stream)
+    code = _native().rmsnorm_backward(dy, h, weight, rstd, dh, dweight, dresidual, workspace, stream)
     if code:
         raise VnmError(code, "vnm_rmsnorm_backward")
 
