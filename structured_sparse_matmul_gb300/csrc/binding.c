@@ -5,9 +5,9 @@
  * These calls stand in decode loops, where one takes a few microseconds on the
  * GPU. Reading a tensor's shape, type, device, strides and address from Python
  * and passing two dozen arguments through ctypes costs 7 us a call; the same reads
- * from C cost 2, each attribute read once. Nothing is computed here: every check is of a tensor's description,
- * and the functions called are the library's exported ones, whose addresses
- * setup() is given.
+ * from C cost 2, each attribute read once. Nothing is computed here: every check
+ * is of a tensor's description, and the functions called are the library's
+ * exported ones, whose addresses setup() is given.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -114,8 +114,10 @@ static int matrix(const Tensor* t, const char* name, int64_t rows, int64_t cols,
     if (t->dims != 2 || t->size[0] != rows || t->size[1] != cols || t->device != device ||
         (dtype != NULL && t->dtype != dtype) || (cols > 1 && t->stride[1] != 1))
         return refuse(t, name, rows, cols, dtype, device);
-    /* (a matrix of one row may carry any stride) */
-    *ld = t->stride[0] >= cols && t->stride[0] > 0 ? t->stride[0] : cols > 0 ? cols : 1;
+    /* Rows that overlap (an expanded tensor's) have no leading dimension; one row may carry any stride. */
+    const int64_t least = cols > 0 ? cols : 1;
+    if (rows > 1 && cols > 0 && t->stride[0] < least) return refuse(t, name, rows, cols, dtype, device);
+    *ld = t->stride[0] >= least ? t->stride[0] : least;
     return 0;
 }
 
@@ -244,8 +246,8 @@ static PyObject* rmsnorm_backward(PyObject* self, PyObject* const* a, Py_ssize_t
         matrix(dr, "dresidual", T, D, dy->dtype, dev, &ld_r) < 0)
         return NULL;
     if (ws->dims >= 0) {
-        if (ws->device != dev) {
-            PyErr_SetString(PyExc_ValueError, "workspace must be on dy's device");
+        if (ws->device != dev || ws->dims != 1 || (ws->size[0] > 1 && ws->stride[0] != 1)) {
+            PyErr_SetString(PyExc_ValueError, "workspace must be a contiguous vector on dy's device");
             return NULL;
         }
         if (long_of(PyObject_GetAttr(ws->object, s_nbytes), &bytes) < 0) return NULL;

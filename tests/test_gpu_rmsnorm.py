@@ -282,3 +282,24 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         vnm.vnm_rmsnorm_backward(x, x, w, torch.ones(4, device=DEV), None, torch.empty(64, device=DEV),
                                  workspace=torch.empty(1 << 20, dtype=torch.uint8))
+
+
+def test_overlapping_rows_are_refused():
+    """An expanded tensor's rows have stride 0: no leading dimension describes them."""
+    T, D = 4, 64
+    w = torch.ones(D, dtype=F16, device=DEV)
+    x, y, rstd, dw = torch.zeros((T, D), dtype=F16, device=DEV), torch.empty((T, D), dtype=F16, device=DEV), \
+        torch.ones(T, device=DEV), torch.empty(D, device=DEV)
+    wide, one = w.expand(T, D), torch.zeros((1, 1), dtype=F16, device=DEV).expand(T, 1)
+    for kw in (dict(x=wide, y=y), dict(x=x, residual=wide, y=y), dict(x=x, y=wide)):
+        with pytest.raises(ValueError):
+            vnm.vnm_rmsnorm(kw.pop("x"), w, EPS, **kw)
+    with pytest.raises(ValueError):
+        vnm.vnm_rmsnorm(one, w[:1], EPS, y=torch.empty_like(one.contiguous()))
+    with pytest.raises(ValueError):
+        vnm.vnm_rmsnorm_backward(wide, x, w, rstd, y, dw)
+    with pytest.raises(ValueError):
+        vnm.vnm_rmsnorm_backward(x, x, w, rstd, y, dw,
+                                 workspace=torch.empty(1, dtype=torch.uint8, device=DEV).expand(1 << 20))
+    vnm.vnm_rmsnorm(wide[:1], w, EPS, y=y[:1])  # one row: any stride
+    assert (y[0].double() - 1).abs().max() < 2e-3
