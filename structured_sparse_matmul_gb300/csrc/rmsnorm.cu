@@ -258,7 +258,12 @@ __global__ void __launch_bounds__(32 * max_warps(CPT), 1)
     __shared__ float buf[2][kMaxWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     constexpr int N = CPT > 0 ? CPT : 1;
-    constexpr bool kAhead = CPT == 1 || CPT == 2;  // the next row's loads in flight: four units leave no registers for it
+    // The next row's loads are in flight (four units leave no registers for it) and a
+    // row's elements stay in registers until dh. Four units of a 32-bit type, or by
+    // scalar accesses, read dy and h again from the caches instead of spilling (2048 x
+    // 16383 bf16: 123 us, 148 with them kept; 2048 x 8704 fp16, vectors: 73.6, kept 48.1).
+    constexpr bool kAhead = CPT == 1 || CPT == 2, kKeep = kAhead || (CPT == 4 && VEC && sizeof(T) == 2);
+    constexpr int M = kKeep ? N : 1;
     const Off D = static_cast<Off>(a.D);
     const Off c0 = static_cast<Off>(first_column<VEC>(warp, lane));
     const Off across = static_cast<Off>(warps) * kUnit;
@@ -270,23 +275,28 @@ __global__ void __launch_bounds__(32 * max_warps(CPT), 1)
     for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
-    Elems<T> dn[kAhead ? N : 1], hn[kAhead ? N : 1], d8[N], h8[N], r8[N], w8[N];  // dn, hn: the next row's dy and h
+    Elems<T> dn[kAhead ? N : 1], hn[kAhead ? N : 1], d8[M], h8[M], r8[M], w8[M];  // dn, hn: the next row's dy and h
     float rstd_next = 0.f;
     auto load_row = [&](int64_t t, Elems<T>* de, Elems<T>* he) {
         const T* dy = static_cast<const T*>(a.dy) + t * a.ld_dy;
         const T* h = static_cast<const T*>(a.h) + t * a.ld_h;
         rstd_next = a.rstd[t];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < M; ++i) {
             load8<T, VEC>(dy + (c0 + i * across), D - c0 - i * across, de[i]);
             load8<T, VEC>(h + (c0 + i * across), D - c0 - i * across, he[i]);
         }
     };
+    auto load_unit = [&](int64_t t, Off c) {
+        load8<T, VEC>(static_cast<const T*>(a.dy) + t * a.ld_dy + c, D - c, d8[0]);
+        load8<T, VEC>(static_cast<const T*>(a.h) + t * a.ld_h + c, D - c, h8[0]);
+        if (w) load8<T, VEC>(w + c, D - c, w8[0]);
+    };
     if (CPT > 0) {
         if (kAhead) load_row(blockIdx.x, dn, hn);
-        if (w) {
+        if (kKeep && w) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) load8<T, VEC>(w + (c0 + i * across), D - c0 - i * across, w8[i]);
+            for (int i = 0; i < M; ++i) load8<T, VEC>(w + (c0 + i * across), D - c0 - i * across, w8[i]);
         }
     }
     // dy w
@@ -312,9 +322,9 @@ __global__ void __launch_bounds__(32 * max_warps(CPT), 1)
         T* dh = static_cast<T*>(a.dh) + (a.dh ? t * a.ld_dh : 0);
         float dot = 0.f;
         if (CPT > 0) {
-            if (add_res) {
+            if (kKeep && add_res) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) load8<T, VEC>(dr + (c0 + i * across), D - c0 - i * across, r8[i]);
+                for (int i = 0; i < M; ++i) load8<T, VEC>(dr + (c0 + i * across), D - c0 - i * across, r8[i]);
             }
             if (kAhead) {
                 rstd = rstd_next;
@@ -325,17 +335,20 @@ __global__ void __launch_bounds__(32 * max_warps(CPT), 1)
                 }
                 if (t + gridDim.x < a.T) load_row(t + gridDim.x, dn, hn);
             } else {
-                load_row(t, d8, h8);
-                rstd = rstd_next;
+                if (kKeep) load_row(t, d8, h8);
+                rstd = a.rstd[t];
             }
 #pragma unroll
-            for (int i = 0; i < N; ++i)
+            for (int i = 0; i < N; ++i) {
+                const int m = kKeep ? i : 0;
+                if (!kKeep) load_unit(t, c0 + i * across);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float hj = widen(h8[i].v[j]);
-                    dot = fmaf(scaled(d8[i], w8[i], j), hj, dot);
-                    acc[i][j] = fmaf(widen(d8[i].v[j]), hj * rstd, acc[i][j]);
+                    const float hj = widen(h8[m].v[j]);
+                    dot = fmaf(scaled(d8[m], w8[m], j), hj, dot);
+                    acc[i][j] = fmaf(widen(d8[m].v[j]), hj * rstd, acc[i][j]);
                 }
+            }
         } else {
             const T* dy = static_cast<const T*>(a.dy) + t * a.ld_dy;
             const T* h = static_cast<const T*>(a.h) + t * a.ld_h;
@@ -355,8 +368,15 @@ __global__ void __launch_bounds__(32 * max_warps(CPT), 1)
         k = rstd * rstd * (total * inv_d);
         if (CPT > 0) {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (i < own) out_unit(dh, c0 + i * across, d8[i], h8[i], w8[i], r8[i]);
+            for (int i = 0; i < N; ++i) {
+                const int m = kKeep ? i : 0;
+                if (i >= own) continue;  // the same for the whole warp
+                if (!kKeep) {
+                    load_unit(t, c0 + i * across);
+                    if (add_res) load8<T, VEC>(dr + (c0 + i * across), D - c0 - i * across, r8[0]);
+                }
+                out_unit(dh, c0 + i * across, d8[m], h8[m], w8[m], r8[m]);
+            }
         } else {
             const T* dy = static_cast<const T*>(a.dy) + t * a.ld_dy;
             const T* h = static_cast<const T*>(a.h) + t * a.ld_h;
@@ -455,8 +475,13 @@ cudaError_t forward_of(const RmsNormArgs& a, int sm_count, cudaStream_t stream) 
 }
 
 // Rows of partial sums of dweight, and CTAs, at most: four for each of 152 SMs
-// where a row's warps leave room for them, two (of 512 threads or more) elsewhere.
-int64_t grad_parts_of(int64_t D) { return D <= 8 * kUnit ? 608 : 304; }
+// where a row's warps leave room for them, two (of 512 threads or more)
+// elsewhere, one for rows of four units a warp, whose partial sums cost more traffic
+// than a second CTA in turn gains (300 x 12000 bf16: 24.7 us, with two 34.0; 2048 x
+// 16384: 90.6 and 98.7).
+int64_t grad_parts_of(int64_t D) {
+    return D <= 8 * kUnit ? 608 : D > kMaxWarps * kUnit && D <= 4 * max_warps(4) * kUnit ? 152 : 304;
+}
 
 template <typename T, bool VEC>
 cudaError_t run_grad(const RmsNormGradArgs& a, cudaStream_t stream) {
