@@ -406,8 +406,8 @@ vnm_status vnm_spmm_noalloc(int64_t R, int64_t K, int32_t V, int32_t M, const vo
  * (weights); the last group or block of an edge is shorter. An element stands
  * for q * s. For a group with largest magnitude m:
  *   s = max(m * (1 / F), 2^-100), F = 448 (e4m3) or 57344 (e5m2),
- *   q = the nearest fp8 value to y * (1 / s) (ties to even, saturating),
- * each reciprocal and product rounded to fp32;
+ *   q = the nearest fp8 value to y / s (ties to even, saturating),
+ * 1 / F, its product with m and the quotient each correctly rounded to fp32;
  * a group that holds an Inf or a NaN gets s = NaN and q = NaN throughout.
  * Scales are addressed with two strides in elements: the scale of row (or row
  * block) i and column group g is s[i * s_rs + g * s_cs].

@@ -1,7 +1,7 @@
 // The block-scaled 8-bit form of a matrix, plain and transposed, in one pass.
 //
 //   s = max(max |x| / F, 2^-100) over a group of 128 (or a 128 x 128 block),
-//   q = fp8(x * (1 / s))
+//   q = fp8(x / s)
 //
 // Bound by memory traffic (2 or 4 bytes read, 1 or 2 written for an element)
 // as long as the instructions for an element stay few. A CTA takes a 128 x 128
@@ -16,8 +16,8 @@
 // index is XORed with the column group so that writing 16 columns and reading
 // 16 rows both touch every bank once.
 //
-// Measured: 8192 x 4096 bf16 to both forms 28.0 us, 4.9 TB/s, 0.72 of a copy's rate;
-// 11008 x 4096 fp16 in blocks 32.3 us, 5.6 TB/s, 0.82 (issue 63 and 55 % active).
+// Measured: 8192 x 4096 bf16 to both forms 31.4 us, 4.3 TB/s, 0.64 of a copy's rate;
+// 11008 x 4096 fp16 in blocks 35.0 us, 5.2 TB/s, 0.76: instruction issue.
 #include <type_traits>
 
 #include "vnm_dense.h"
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
     using P = Part<T>;
     constexpr int kColWords = kGroup * P::kWords / 8;  // words of the tile's 128 columns
     __shared__ __align__(16) uint32_t colmax[8][kColWords];
-    __shared__ __align__(16) float colinv[kGroup];
+    __shared__ __align__(16) float2 colscale[kGroup];  // a column's scale and its reciprocal
     __shared__ uint2 turned[kGroup][16];
     const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
     const int64_t r0 = tr * kGroup, c0 = tc * kGroup;
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
         for (int k = 1; k < P::kWords; ++k) m = P::larger(m, P::mag(x.w[i][k]));
         rmax[i] = m;
     }
-    float rinv;  // of row lane & 7 of the lane's 8 rows (of the block: of all)
+    float rscale, rinv;  // of row lane & 7 of the lane's 8 rows (of the block: of all)
     if (a.block) {
         uint32_t m = rmax[0];
 #pragma unroll
@@ -138,10 +138,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = max(m, colmax[i][0]);
-        const float s = group_scale(m, a.e5m2, rinv);
+        rscale = group_scale(m, a.e5m2, rinv);
         if (threadIdx.x == 0) {
-            if (a.s) a.s[tr * a.s_rs + tc * a.s_cs] = s;
-            if (a.st) a.st[tc * a.st_rs + tr * a.st_cs] = s;
+            if (a.s) a.s[tr * a.s_rs + tc * a.s_cs] = rscale;
+            if (a.st) a.st[tc * a.st_rs + tr * a.st_cs] = rscale;
         }
     } else {
         // rows 0..7 over lanes of the same half-warp: bits 2, 1, 0 of the lane number
@@ -159,27 +159,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
         }
         uint32_t m = P::larger(lane & 1 ? u[1] : u[0], __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? u[0] : u[1], 1));
         m = P::larger(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
-        const float s = group_scale(P::widened(m), a.e5m2, rinv);
-        if (a.s && !(lane & 8) && (lane & 7) < nrow) a.s[(row + (lane & 7)) * a.s_rs + tc * a.s_cs] = s;
+        rscale = group_scale(P::widened(m), a.e5m2, rinv);
+        if (a.s && !(lane & 8) && (lane & 7) < nrow) a.s[(row + (lane & 7)) * a.s_rs + tc * a.s_cs] = rscale;
     }
     if (a.q) {
         uint8_t* q = a.q + row * a.ld_q + col;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+            const float s = a.block ? rscale : __shfl_sync(0xFFFFFFFFu, rscale, (lane & 16) | i);
             const float inv = a.block ? rinv : __shfl_sync(0xFFFFFFFFu, rinv, (lane & 16) | i);
             float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = x.get(i, j) * inv;
+            for (int j = 0; j < 8; ++j) v[j] = quotient(x.get(i, j), s, inv);
             if (i < nrow) store8(q + i * a.ld_q, pack8(v, a.e5m2), ncol, vec_q);
         }
     }
     if (!a.qt) return;
 
-    float inv[8];
-    if (a.block) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) inv[j] = rinv;
-    } else {
+    if (!a.block) {
         // columns: the thread's 8 rows, the warp's two row groups, then the 8 warps, a
         // thread a column
 #pragma unroll
@@ -204,19 +201,23 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
             if (P::kPacked) m = c & 1 ? m >> 16 : m & 0xFFFFu;
             float ci;
             const float s = group_scale(P::widened(m), a.e5m2, ci);
-            colinv[c] = ci;
+            colscale[c] = make_float2(s, ci);
             if (c0 + c < a.C) a.st[(c0 + c) * a.st_rs + tr * a.st_cs] = s;
         }
         __syncthreads();
-        *reinterpret_cast<float4*>(&inv[0]) = *reinterpret_cast<const float4*>(&colinv[8 * cg]);
-        *reinterpret_cast<float4*>(&inv[4]) = *reinterpret_cast<const float4*>(&colinv[8 * cg + 4]);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        float v[8];
+    for (int j = 0; j < 8; j += 2) {
+        float4 c = make_float4(rscale, rinv, rscale, rinv);
+        if (!a.block) c = *reinterpret_cast<const float4*>(&colscale[8 * cg + j]);
+        float v[2][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = x.get(i, j) * inv[j];
-        turned[8 * cg + j][rg ^ cg] = pack8(v, a.e5m2);
+        for (int i = 0; i < 8; ++i) {
+            v[0][i] = quotient(x.get(i, j), c.x, c.y);
+            v[1][i] = quotient(x.get(i, j + 1), c.z, c.w);
+        }
+        turned[8 * cg + j][rg ^ cg] = pack8(v[0], a.e5m2);
+        turned[8 * cg + j + 1][rg ^ cg] = pack8(v[1], a.e5m2);
     }
     __syncthreads();
     // rows of qt: 16 lanes a column, 8 bytes each
