@@ -128,6 +128,16 @@ def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> int:
     return int(s.cuda_stream)
 
 
+def _scratch(nbytes: int, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A call's default workspace, allocated on the stream that the call runs on:
+    torch hands a freed block on in the order of the stream it was allocated on,
+    whatever other streams still do with it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _rowmajor(t: torch.Tensor, name: str) -> int:
     """Leading dimension (elements) of a row-major 2-D tensor."""
     if t.dim() != 2 or t.stride(1) != 1:
@@ -510,9 +520,10 @@ def vnm_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: Optional[tor
                          dresidual: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                          stream=None) -> None:
     """Gradients of vnm_rmsnorm: dh (T x D, of x and residual alike; dresidual
-    added where given) and dweight (fp32 (D,)); either may be None."""
+    added where given) and dweight (fp32 (D,)); either may be None. A workspace
+    of one's own is used in the order of ``stream``, as the other tensors are."""
     if workspace is None and dweight is not None:
-        workspace = torch.empty(vnm_rmsnorm_backward_workspace_size(*dy.shape), dtype=torch.uint8, device=dy.device)
+        workspace = _scratch(vnm_rmsnorm_backward_workspace_size(*dy.shape), dy.device, stream)
     code = _native().rmsnorm_backward(dy, h, weight, rstd, dh, dweight, dresidual, workspace, stream)
     if code:
         raise VnmError(code, "vnm_rmsnorm_backward")

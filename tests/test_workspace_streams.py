@@ -1,0 +1,101 @@
+"""The workspace that a call allocates by itself belongs to the stream that the call runs
+on. Which stream is current when it is allocated is seen without a GPU; with one, the
+current stream reuses memory of the same sizes meanwhile."""
+import contextlib
+
+import pytest
+import torch
+
+from structured_sparse_matmul_gb300 import vnm
+
+
+class _Native:
+    """Stands for the binding's C part: sizes, and calls that do nothing."""
+
+    def __init__(self):
+        self.given = []
+
+    def rmsnorm_workspace(self, T, D):
+        return 4 * T * D
+
+    def rmsnorm_backward(self, *args):
+        self.given.append(args[7])
+        return 0
+
+
+class _Side:
+    cuda_stream = 64
+
+
+@pytest.fixture
+def allocations(monkeypatch):
+    """(stream current at the time, size) of each torch.empty."""
+    current, seen = [None], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        current.append(s)
+        yield
+        current.pop()
+
+    empty = torch.empty
+
+    def recorded(*a, **k):
+        seen.append((current[-1], a[0]))
+        return empty(*a, **k)
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch, "empty", recorded)
+    return seen
+
+
+@pytest.mark.parametrize("side", [None, _Side()])
+def test_norm_backward_allocates_on_its_stream(monkeypatch, allocations, side):
+    native = _Native()
+    monkeypatch.setattr(vnm, "_native", lambda: native)
+    x, rstd, dw = torch.zeros(3, 5), torch.zeros(3), torch.zeros(5)
+    vnm.vnm_rmsnorm_backward(x, x, None, rstd, None, dw, stream=side)
+    assert allocations == [(side, 60)] and native.given[0].nbytes == 60
+    own = torch.zeros(60, dtype=torch.uint8)
+    vnm.vnm_rmsnorm_backward(x, x, None, rstd, None, dw, workspace=own, stream=side)
+    vnm.vnm_rmsnorm_backward(x, x, None, rstd, x, None, stream=side)
+    assert len(allocations) == 1 and native.given[1] is own and native.given[2] is None
+
+
+def _busy(stream, a, b):
+    """A few milliseconds of copies."""
+    with torch.cuda.stream(stream):
+        for _ in range(12):
+            a.copy_(b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D", [(2000, 1024), (600, 6000), (300, 20000)])
+def test_norm_backward_on_a_side_stream(T, D):
+    g = torch.Generator(device="cuda").manual_seed(T)
+    h, dy = (torch.randn(T, D, generator=g, device="cuda").half() for _ in range(2))
+    rstd = torch.rsqrt(h.float().square().mean(1))
+    dh, want = torch.empty_like(h), torch.empty(D, device="cuda")
+    vnm.vnm_rmsnorm_backward(dy, h, None, rstd, dh, want)
+    n = vnm.vnm_rmsnorm_backward_workspace_size(T, D)
+    big = [torch.zeros(1 << 28, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    # blocks that the current stream takes after the call's return must not be the call's
+    dw = torch.empty(D, device="cuda")
+    torch.cuda.synchronize()
+    _busy(side, *big)
+    vnm.vnm_rmsnorm_backward(dy, h, None, rstd, dh, dw, stream=side)
+    later = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(dw, want)
+    del later
+    # a block that the current stream has given back but not yet read must not be the call's
+    kept, out = torch.full((n,), 7, dtype=torch.uint8, device="cuda"), torch.empty(n, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    _busy(torch.cuda.current_stream(), *big)
+    out.copy_(kept)
+    del kept
+    vnm.vnm_rmsnorm_backward(dy, h, None, rstd, dh, dw, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(dw, want) and (out == 7).all()
