@@ -321,7 +321,7 @@ def vnm_linear(A: VnmMatrix, X: torch.Tensor, Y: torch.Tensor, bias: Optional[to
         raise ValueError("bias must be a contiguous CUDA fp16 tensor of shape (R,)")
     if workspace is None:
         n = vnm_linear_workspace_size(A, T)
-        workspace = torch.empty(n, dtype=torch.uint8, device=X.device) if n else None
+        workspace = _scratch(n, X.device, stream) if n else None
     ws_ptr = workspace.data_ptr() if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     ld_x = _rowmajor(X, "X") if A.K > 0 else 1
@@ -347,7 +347,7 @@ def vnm_energy(A: VnmMatrix, W: torch.Tensor, pattern: int, workspace: Optional[
     if W.dtype != torch.float16 or not W.is_cuda or tuple(W.shape) != (A.R, A.K):
         raise ValueError("W must be a CUDA fp16 tensor of shape (R, K)")
     if workspace is None:
-        workspace = torch.empty(vnm_energy_workspace_size(A), dtype=torch.uint8, device=W.device)
+        workspace = _scratch(vnm_energy_workspace_size(A), W.device, stream)
     kept = (ctypes.c_uint64 * 2)()
     total = (ctypes.c_uint64 * 2)()
     e = ctypes.c_double(0.0)

@@ -62,6 +62,40 @@ def test_norm_backward_allocates_on_its_stream(monkeypatch, allocations, side):
     assert len(allocations) == 1 and native.given[1] is own and native.given[2] is None
 
 
+class _OnGpu:
+    """A CPU tensor that says it is on a GPU."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self._t = t
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+
+class _Library:
+    """Stands for libvnm: every call succeeds."""
+
+    def __getattr__(self, name):
+        return lambda *a: 0
+
+
+@pytest.mark.parametrize("side", [None, _Side()])
+@pytest.mark.parametrize("call", ["vnm_linear", "vnm_energy"])
+def test_the_pruned_calls_allocate_on_their_stream(monkeypatch, allocations, call, side):
+    monkeypatch.setattr(vnm, "lib", _Library)
+    monkeypatch.setattr(vnm, "_stream_ptr", lambda stream: 0)
+    monkeypatch.setattr(vnm, "vnm_linear_workspace_size", lambda A, T: 48)
+    monkeypatch.setattr(vnm, "vnm_energy_workspace_size", lambda A: 48)
+    A = vnm.VnmMatrix(0, 4, 8, 4, 4, None, None, None)
+    X = _OnGpu(torch.zeros(4, 8, dtype=torch.float16))
+    if call == "vnm_linear":
+        vnm.vnm_linear(A, X, _OnGpu(torch.zeros(4, 4)), stream=side)
+    else:
+        vnm.vnm_energy(A, X, vnm.VNM_PATTERN_UNSTRUCTURED, stream=side)
+    assert allocations == [(side, 48)]
+
+
 def _busy(stream, a, b):
     """A few milliseconds of copies."""
     with torch.cuda.stream(stream):
@@ -99,3 +133,34 @@ def test_norm_backward_on_a_side_stream(T, D):
     vnm.vnm_rmsnorm_backward(dy, h, None, rstd, dh, dw, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(dw, want) and (out == 7).all()
+
+
+@pytest.mark.gpu
+def test_linear_on_a_side_stream():
+    g = torch.Generator(device="cuda").manual_seed(1)
+    R, K, T = 1024, 4096, 64
+    A = vnm.vnm_matrix_alloc(R, K, 64, 8)
+    vnm.vnm_compress(A, (0.02 * torch.randn(R, K, generator=g, device="cuda")).half())
+    X = torch.randn(T, K, generator=g, device="cuda").half()
+    want, Y = torch.empty((T, R), device="cuda"), torch.empty((T, R), device="cuda")
+    n = vnm.vnm_linear_workspace_size(A, T)
+    assert n > 0
+    vnm.vnm_linear(A, X, want)
+    big = [torch.zeros(1 << 28, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _busy(side, *big)
+    vnm.vnm_linear(A, X, Y, stream=side)
+    later = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want)
+    del later
+    kept, out = torch.full((n,), 7, dtype=torch.uint8, device="cuda"), torch.empty(n, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    _busy(torch.cuda.current_stream(), *big)
+    out.copy_(kept)
+    del kept
+    vnm.vnm_linear(A, X, Y, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want) and (out == 7).all()
+    assert vnm.vnm_get_status(A) == vnm.VNM_OK
