@@ -138,6 +138,15 @@ def _scratch(nbytes: int, device, stream: Optional[torch.cuda.Stream]) -> torch.
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def _written_on(stream: Optional[torch.cuda.Stream], *tensors: torch.Tensor) -> None:
+    """New tensors of the current stream's that a call on ``stream`` writes: work queued
+    before them may still use their memory, and that call theirs when they are freed."""
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream(tensors[0].device))
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def _rowmajor(t: torch.Tensor, name: str) -> int:
     """Leading dimension (elements) of a row-major 2-D tensor."""
     if t.dim() != 2 or t.stride(1) != 1:
@@ -265,11 +274,13 @@ def bitmap_encode(W: torch.Tensor, stream=None) -> BitmapMatrix:
     offsets = torch.empty(max(1, no.value // 4), dtype=torch.int32, device=dev)
     bases = torch.empty(nbase.value // 8, dtype=torch.int64, device=dev)
     ld = _rowmajor(W, "W") if K > 0 else 1
+    _written_on(stream, bitmaps, offsets, bases)
     need = ctypes.c_int64(0)
     code = lib().vnm_bitmap_encode(W.data_ptr() or None, ld, R, K, bitmaps.data_ptr(), offsets.data_ptr(),
                                    bases.data_ptr(), None, 0, ctypes.byref(need), _stream_ptr(stream))
     values = torch.empty(max(8, int(need.value)), dtype=torch.float16, device=dev)
     if code == VNM_ERR_INVALID_ARG and need.value > 0:
+        _written_on(stream, values)
         code = lib().vnm_bitmap_encode(W.data_ptr() or None, ld, R, K, bitmaps.data_ptr(), offsets.data_ptr(),
                                        bases.data_ptr(), values.data_ptr(), values.numel(), ctypes.byref(need),
                                        _stream_ptr(stream))

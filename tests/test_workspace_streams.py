@@ -164,3 +164,53 @@ def test_linear_on_a_side_stream():
     torch.cuda.synchronize()
     assert torch.equal(Y, want) and (out == 7).all()
     assert vnm.vnm_get_status(A) == vnm.VNM_OK
+
+
+@pytest.mark.gpu
+def test_bitmap_encode_on_a_side_stream():
+    g = torch.Generator(device="cuda").manual_seed(2)
+    W = torch.randn(1024, 4096, generator=g, device="cuda").half()
+    W *= torch.rand(1024, 4096, generator=g, device="cuda") < 0.5
+    want = vnm.bitmap_encode(W)
+    big = [torch.zeros(1 << 28, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    parts = (want.bitmaps, want.offsets, want.bases, want._values_storage)
+    # blocks of the arrays' sizes that the current stream has given back but not yet read
+    kept = [torch.full((t.nbytes,), 7, dtype=torch.uint8, device="cuda") for t in parts]
+    out = [torch.empty_like(t) for t in kept]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _busy(torch.cuda.current_stream(), *big)
+    for o, k in zip(out, kept):
+        o.copy_(k)
+    del kept, k
+    got = vnm.bitmap_encode(W, stream=side)
+    torch.cuda.synchronize()
+    for a, b in zip(parts, (got.bitmaps, got.offsets, got.bases, got._values_storage)):
+        assert torch.equal(a, b)
+    assert all((o == 7).all() for o in out)
+
+
+class _Waiting(_Side):
+    def __init__(self):
+        self.waits = []
+
+    def wait_stream(self, other):
+        self.waits.append(other)
+
+
+class _Recorded:
+    def __init__(self):
+        self.streams = []
+        self.device = None
+
+    def record_stream(self, s):
+        self.streams.append(s)
+
+
+def test_tensors_that_another_stream_writes(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
+    side, t = _Waiting(), _Recorded()
+    vnm._written_on(None, t)
+    assert not side.waits and not t.streams
+    vnm._written_on(side, t)
+    assert side.waits == ["current"] and t.streams == [side]
