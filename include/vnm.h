@@ -486,7 +486,7 @@ vnm_status vnm_fp8_quantize(const void* X, int64_t ld_x, int64_t R, int64_t C, v
  * with r' = r for w_block_rows = 1 and r / 128 for 128. X: T x K with 1 x 128
  * scales; W: R x K. All sums are fp32; Y (T x R, ld_y >= R; VNM_F16, VNM_BF16 or
  * VNM_F32) is rounded once, bias ([R], bias_type, or NULL) and act are
- * applied in fp32 before that (GELU to 1e-7 |z| of its argument z). The gradients
+ * applied in fp32 before that (GELU within 1.5 * 2^-23 |z| of its argument z). The gradients
  * are products of the same form:
  *   dX = dY . W:   X := dY (1 x 128 along R), W := W^T (vnm_fp8_quantize's qt, st);
  *   dW = dY^T . X: X := dY^T, W := X^T (both qt, st with block_rows = 1).

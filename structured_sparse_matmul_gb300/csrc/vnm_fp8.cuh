@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "../../include/vnm.h"
+#include "vnm_internal.h"
 
 namespace vnm {
 
@@ -106,19 +107,6 @@ __device__ __forceinline__ void store_any(void* p, int type, int64_t i, float v)
         static_cast<__half*>(p)[i] = __float2half_rn(v);
     else
         static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-}
-
-// GELU, v Phi(v), from erfc(z) = (a1 t + ... + a5 t^5) exp(-z^2), t = 1 / (1 + p z),
-// z = |v| / sqrt 2 (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26: off by
-// at most 1.5e-7, so GELU by 0.75e-7 |v|). Half the instructions of erff, which took
-// a third of a 256 x 256 tile's time; no cancellation for negative v.
-__device__ __forceinline__ float gelu(float v) {
-    const float z = fabsf(v) * 0.70710678118654752f;
-    const float t = __fdividef(1.f, fmaf(0.3275911f, z, 1.f));
-    const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
-                                0.254829592f);
-    const float tail = 0.5f * poly * exp2f(-1.44269504088896341f * z * z);  // of the nearer side
-    return v * (v < 0.f ? tail : 1.f - tail);
 }
 
 __device__ __forceinline__ float activate(int act, float v) {
