@@ -101,7 +101,7 @@ def main():
     b = ffn.buffers(T)
     y, h = ffn.forward(x, residual, b)
     grads = ffn.train_step(x, residual, dz, dh)
-    assert vnm.vnm_get_status(ffn.down) == vnm.VNM_OK
+    assert vnm.vnm_get_status(ffn.down) == vnm.VNM_OK and vnm.vnm_fp8_linear_get_status() == vnm.VNM_OK
     print(f"{T} tokens, D = {D}, F = {F}: |y| = {y.float().norm().item():.4f}, "
           f"|dh| = {grads[0].float().norm().item():.4f}, |dw| = {grads[1].norm().item():.4f}, |dWu| = {grads[2].norm().item():.4f}")
 

@@ -43,7 +43,7 @@
  *     for concurrent callers; and
  *     the static 8 MiB (+ 256-byte) device array of vnm_spmm_noalloc, held by
  *     every GPU that loads the library, with its address resolved once per
- *     CUDA context.
+ *     CUDA context, and the three status words of vnm_fp8_linear.
  */
 #ifndef VNM_H
 #define VNM_H
@@ -495,7 +495,8 @@ vnm_status vnm_fp8_quantize(const void* X, int64_t ld_x, int64_t R, int64_t C, v
  * be a finite fp32 number. The result does not depend on timing: no atomics.
  * status: optional device pointer to 3 zeroed int32 words (first error code,
  * detail, count): a bounded wait that runs out records VNM_ERR_TIMEOUT there
- * (Y is then undefined); NULL: not recorded.
+ * (Y is then undefined). NULL: in words that all such calls on the device share,
+ * read by vnm_fp8_linear_get_status.
  * T = 0 or R = 0 is a no-op; K = 0 gives act(bias).
  * Errors: VNM_ERR_INVALID_ARG (pointers, alignment, leading dimensions, types,
  * w_block_rows), VNM_ERR_CUDA.
@@ -505,6 +506,14 @@ vnm_status vnm_fp8_linear(const void* xq, int64_t ld_x, vnm_fp8 x_type, const fl
                           int64_t ws_rs, int64_t ws_cs, int32_t w_block_rows, int64_t T, int64_t R, int64_t K,
                           const void* bias, vnm_dtype bias_type, vnm_activation act, void* Y, int64_t ld_y,
                           vnm_dtype y_type, int32_t* status, vnm_stream_t stream);
+
+/*
+ * Synchronise `stream`, then return and clear the first error that a
+ * vnm_fp8_linear without status words recorded on the current device since the
+ * last call (VNM_OK if none).
+ * Errors: VNM_ERR_CUDA if the synchronisation itself failed.
+ */
+vnm_status vnm_fp8_linear_get_status(vnm_stream_t stream);
 
 /*
  * Synchronise `stream`, then return and clear the first error any kernel

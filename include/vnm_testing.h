@@ -41,6 +41,15 @@ vnm_status vnm_testing_fp8_linear_skip_stage(const void* xq, int64_t ld_x, vnm_f
                                              vnm_dtype y_type, int32_t* status, int32_t skip_stage,
                                              vnm_stream_t stream);
 
+/* The same without status words, bias and activation (vnm_fp8_linear_get_status reads what it records). */
+vnm_status vnm_testing_fp8_linear_skip_stage_no_status(const void* xq, int64_t ld_x, vnm_fp8 x_type,
+                                                       const float* x_scale, int64_t xs_rs, int64_t xs_cs,
+                                                       const void* wq, int64_t ld_w, vnm_fp8 w_type,
+                                                       const float* w_scale, int64_t ws_rs, int64_t ws_cs,
+                                                       int32_t w_block_rows, int64_t T, int64_t R, int64_t K, void* Y,
+                                                       int64_t ld_y, vnm_dtype y_type, int32_t skip_stage,
+                                                       vnm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

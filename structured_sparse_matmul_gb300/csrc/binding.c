@@ -25,6 +25,10 @@ typedef vnm_status (*testing_linear_t)(const void*, int64_t, vnm_fp8, const floa
                                        const void*, vnm_dtype, vnm_activation, void*, int64_t, vnm_dtype, int32_t*, int32_t,
                                        vnm_stream_t);
 static testing_linear_t fn_linear_skip;
+typedef vnm_status (*testing_linear_no_status_t)(const void*, int64_t, vnm_fp8, const float*, int64_t, int64_t, const void*,
+                                                 int64_t, vnm_fp8, const float*, int64_t, int64_t, int32_t, int64_t, int64_t,
+                                                 int64_t, void*, int64_t, vnm_dtype, int32_t, vnm_stream_t);
+static testing_linear_no_status_t fn_linear_skip_no_status;
 
 static PyObject *py_f16, *py_f32, *py_bf16, *py_e4m3, *py_e5m2, *py_i32; /* torch dtypes */
 static PyObject *py_current_device, *py_current_stream;
@@ -321,7 +325,10 @@ static PyObject* fp8_linear(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     if (stream_of(a[9], dev, &stream) < 0) return NULL;
     vnm_status st;
     Py_BEGIN_ALLOW_THREADS
-    if (skip >= 0)
+    if (skip >= 0 && status->dims < 0)
+        st = fn_linear_skip_no_status(x->p, ld_x, x_type, xs->p, xs->stride[0], xs->stride[1], w->p, ld_w, w_type, ws->p,
+                                      ws->stride[0], ws->stride[1], block, T, R, K, y->p, ld_y, y_type, (int32_t)skip, stream);
+    else if (skip >= 0)
         st = fn_linear_skip(x->p, ld_x, x_type, xs->p, xs->stride[0], xs->stride[1], w->p, ld_w, w_type, ws->p, ws->stride[0],
                             ws->stride[1], block, T, R, K, b->p, b_type, (vnm_activation)act, y->p, ld_y, y_type, status->p,
                             (int32_t)skip, stream);
@@ -342,11 +349,11 @@ static PyObject* rmsnorm_workspace(PyObject* self, PyObject* const* a, Py_ssize_
     return PyLong_FromLongLong(st == VNM_OK ? (int64_t)bytes : -(int64_t)st);
 }
 
-/* The six functions' addresses, torch's six types, current device and current stream. */
+/* The seven functions' addresses, torch's six types, current device and current stream. */
 static PyObject* setup(PyObject* self, PyObject* args) {
-    unsigned long long f[6];
+    unsigned long long f[7];
     PyObject *t[6], *device, *stream;
-    if (!PyArg_ParseTuple(args, "(KKKKKK)(OOOOOO)OO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &t[0], &t[1], &t[2], &t[3],
+    if (!PyArg_ParseTuple(args, "(KKKKKKK)(OOOOOO)OO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &t[0], &t[1], &t[2], &t[3],
                           &t[4], &t[5], &device, &stream))
         return NULL;
     fn_rmsnorm = (__typeof__(fn_rmsnorm))(uintptr_t)f[0];
@@ -355,6 +362,7 @@ static PyObject* setup(PyObject* self, PyObject* args) {
     fn_quantize = (__typeof__(fn_quantize))(uintptr_t)f[3];
     fn_linear = (__typeof__(fn_linear))(uintptr_t)f[4];
     fn_linear_skip = (testing_linear_t)(uintptr_t)f[5];
+    fn_linear_skip_no_status = (testing_linear_no_status_t)(uintptr_t)f[6];
     PyObject** to[8] = {&py_f16, &py_bf16, &py_f32, &py_e4m3, &py_e5m2, &py_i32, &py_current_device, &py_current_stream};
     PyObject* from[8] = {t[0], t[1], t[2], t[3], t[4], t[5], device, stream};
     for (int i = 0; i < 8; ++i) {

@@ -214,4 +214,22 @@ vnm_status vnm_testing_fp8_linear_skip_stage(const void* xq, int64_t ld_x, vnm_f
                       T, R, K, bias, bias_type, act, Y, ld_y, y_type, status, skip_stage, stream);
 }
 
+vnm_status vnm_testing_fp8_linear_skip_stage_no_status(const void* xq, int64_t ld_x, vnm_fp8 x_type,
+                                                       const float* x_scale, int64_t xs_rs, int64_t xs_cs,
+                                                       const void* wq, int64_t ld_w, vnm_fp8 w_type,
+                                                       const float* w_scale, int64_t ws_rs, int64_t ws_cs,
+                                                       int32_t w_block_rows, int64_t T, int64_t R, int64_t K, void* Y,
+                                                       int64_t ld_y, vnm_dtype y_type, int32_t skip_stage,
+                                                       vnm_stream_t stream) {
+    if (skip_stage < 0) return VNM_ERR_INVALID_ARG;
+    return fp8_linear(xq, ld_x, x_type, x_scale, xs_rs, xs_cs, wq, ld_w, w_type, w_scale, ws_rs, ws_cs, w_block_rows,
+                      T, R, K, nullptr, VNM_F32, VNM_ACT_NONE, Y, ld_y, y_type, nullptr, skip_stage, stream);
+}
+
+vnm_status vnm_fp8_linear_get_status(vnm_stream_t stream) {
+    int code = 0;
+    if (vnm::take_fp8_linear_status(&code, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return VNM_ERR_CUDA;
+    return static_cast<vnm_status>(code);
+}
+
 }  // extern "C"

@@ -376,6 +376,9 @@ __device__ __forceinline__ void tile_at(const FlArgs& a, int tile, int& mt, int&
     mt = g * kGroupM + (r - nt * rows);
 }
 
+// Status words of the calls that were given none (of the device's all).
+__device__ int g_status[3];
+
 // F32: Y is fp32 (for a pair's staged output).
 template <int BN, bool ONE, int CG, bool F32>
 __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, CG>::kCtas)
@@ -886,7 +889,7 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
         }
         cluster_sync_all();  // no CTA leaves while others read its sums
     }
-    if (threadIdx.x == 0 && abort_flag && a.status) record_error(a.status, VNM_ERR_TIMEOUT, 12);
+    if (threadIdx.x == 0 && abort_flag) record_error(a.status ? a.status : g_status, VNM_ERR_TIMEOUT, 12);
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc_group<CG>(tmem, Cfg::kTmemCols);
@@ -1020,6 +1023,18 @@ TilePlan plan_tiles(int64_t T, int64_t R, int num_kb, bool one_scale, int sm_cou
 }
 
 }  // namespace
+
+cudaError_t take_fp8_linear_status(int* code, cudaStream_t stream) {
+    int words[3] = {0, 0, 0};
+    cudaError_t e = cudaStreamSynchronize(stream);
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(words, g_status, sizeof(words));
+    *code = words[kStatusCode];
+    if (e == cudaSuccess && *code != 0) {
+        const int clear[3] = {0, 0, 0};
+        e = cudaMemcpyToSymbol(g_status, clear, sizeof(clear));
+    }
+    return e;
+}
 
 cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const ScaleView& xs, const void* wq,
                               int64_t ld_w, bool w_e5m2, const ScaleView& ws, int64_t T, int64_t R, int64_t K,

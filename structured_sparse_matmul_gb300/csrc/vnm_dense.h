@@ -77,6 +77,9 @@ cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const S
                               const void* bias, vnm_dtype bias_type, int act, void* y, int64_t ld_y, vnm_dtype y_type,
                               int* status, int skip_stage, int sm_count, cudaStream_t stream);
 
+// The first error that calls without status words recorded on the current device, and clears it.
+cudaError_t take_fp8_linear_status(int* code, cudaStream_t stream);
+
 // The same product for a few tokens (T >= 1, K >= 1).
 bool fp8_decode_serves(int64_t T);
 cudaError_t launch_fp8_decode(const void* xq, int64_t ld_x, bool x_e5m2, const ScaleView& xs, const void* wq,

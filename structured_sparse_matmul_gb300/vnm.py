@@ -90,6 +90,8 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.vnm_fp8_linear.argtypes = [p, i64, dt, p, i64, i64, p, i64, dt, p, i64, i64, i32, i64, i64, i64, p, dt, dt, p, i64,
                                  dt, p, p]
     L.vnm_testing_fp8_linear_skip_stage.argtypes = L.vnm_fp8_linear.argtypes[:-1] + [i32, p]
+    L.vnm_testing_fp8_linear_skip_stage_no_status.argtypes = L.vnm_fp8_linear.argtypes[:16] + [p, i64, dt, i32, p]
+    L.vnm_fp8_linear_get_status.argtypes = [p]
     for name in ("vnm_sizes", "vnm_matrix_create", "vnm_matrix_destroy", "vnm_compress", "vnm_decompress",
                  "vnm_spmm", "vnm_spmm_workspace_size", "vnm_spmm_plan_query", "vnm_spmm_with_plan",
                  "vnm_get_status", "vnm_spmm_noalloc", "vnm_testing_spmm_skip_stage"):
@@ -493,7 +495,7 @@ def _native():
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         functions = (L.vnm_rmsnorm, L.vnm_rmsnorm_backward, L.vnm_rmsnorm_backward_workspace_size, L.vnm_fp8_quantize,
-                     L.vnm_fp8_linear, L.vnm_testing_fp8_linear_skip_stage)
+                     L.vnm_fp8_linear, L.vnm_testing_fp8_linear_skip_stage, L.vnm_testing_fp8_linear_skip_stage_no_status)
         # torch's raw query of the current stream takes 0.1 us, a stream object 3
         stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                          lambda device: int(torch.cuda.current_stream(device).cuda_stream))
@@ -558,14 +560,21 @@ def vnm_fp8_linear(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_
     float8) with x_scale (T, ceil(K / 128)); wq (R x K float8) with w_scale of
     (R or ceil(R / 128), ceil(K / 128)); Y T x R (fp16, bf16, fp32); bias (R,) of
     those types. ``status``: optional int32 CUDA tensor of 3 zeroed words that
-    receives kernel errors."""
+    receives kernel errors (without it: vnm_fp8_linear_get_status)."""
     code = _native().fp8_linear(xq, x_scale, wq, w_scale, Y, bias, act, status, -1, stream)
     if code:
         raise VnmError(code, "vnm_fp8_linear")
 
 
+def vnm_fp8_linear_get_status(stream=None) -> int:
+    """Synchronise the stream and return (and clear) the first error code that a
+    vnm_fp8_linear without ``status`` recorded on the current device."""
+    return int(lib().vnm_fp8_linear_get_status(_stream_ptr(stream)))
+
+
 def vnm_testing_fp8_linear_skip_stage(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
-                                      Y: torch.Tensor, skip_stage: int, status: torch.Tensor, stream=None) -> None:
+                                      Y: torch.Tensor, skip_stage: int, status: Optional[torch.Tensor],
+                                      stream=None) -> None:
     """Test support: vnm_fp8_linear with the first CTA's loads of one pipeline
     stage never issued (include/vnm_testing.h)."""
     code = _native().fp8_linear(xq, x_scale, wq, w_scale, Y, None, VNM_ACT_NONE, status, int(skip_stage), stream)
