@@ -490,8 +490,8 @@ vnm_status vnm_fp8_quantize(const void* X, int64_t ld_x, int64_t R, int64_t C, v
  * are products of the same form:
  *   dX = dY . W:   X := dY (1 x 128 along R), W := W^T (vnm_fp8_quantize's qt, st);
  *   dW = dY^T . X: X := dY^T, W := X^T (both qt, st with block_rows = 1).
- * xq and wq: 16-byte aligned with ld % 16 == 0 (elements past K in the
- * rows' padding are not used). The product of an x_scale and a w_scale has to
+ * xq and wq: 16-byte aligned with ld % 16 == 0 (any ld >= K for a single row;
+ * elements past K in the rows' padding are not used). The product of an x_scale and a w_scale has to
  * be a finite fp32 number. The result does not depend on timing: no atomics.
  * status: optional device pointer to 3 zeroed int32 words (first error code,
  * detail, count): a bounded wait that runs out records VNM_ERR_TIMEOUT there

@@ -60,6 +60,9 @@ vnm_status fp8_linear(const void* xq, int64_t ld_x, vnm_fp8 x_type, const float*
     if (!aligned(status, 4)) return VNM_ERR_INVALID_ARG;
     if (T == 0 || R == 0) return VNM_OK;
     if (!matrix_ok(Y, ld_y, R, e)) return VNM_ERR_INVALID_ARG;
+    // one row has no pitch
+    if (T == 1 && ld_x >= K) ld_x = (K + 15) / 16 * 16;
+    if (R == 1 && ld_w >= K) ld_w = (K + 15) / 16 * 16;
     if (K > 0 && (!matrix_ok(xq, ld_x, K, 16) || !matrix_ok(wq, ld_w, K, 16) || ld_x % 16 != 0 || ld_w % 16 != 0 ||
                   x_scale == nullptr || w_scale == nullptr || !aligned(x_scale, 4) || !aligned(w_scale, 4)))
         return VNM_ERR_INVALID_ARG;
