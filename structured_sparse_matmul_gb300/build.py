@@ -3,7 +3,7 @@
 Each translation unit compiles in parallel; the link uses nvcc's static CUDA
 runtime, so the library needs only the driver at run time. Output:
 ``structured_sparse_matmul_gb300/_build/libvnm.so`` (git-ignored), and beside it
-the Python binding's C part, ``_vnm_binding.so``.
+the Python binding's C part, ``_vnm_binding.*.so``, named after the Python it is for.
 """
 from __future__ import annotations
 
@@ -19,7 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libvnm.so")
-BINDING_PATH = os.path.join(BUILD_DIR, "_vnm_binding.so")
+BINDING_PATH = os.path.join(BUILD_DIR, "_vnm_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["api.cu", "compress.cu", "spmm_simt.cu", "spmm_tc.cu", "spmm_noalloc.cu", "gemm_compress.cu", "energy.cu", "bitmap.cu",
            "rmsnorm.cu", "fp8_quantize.cu", "fp8_linear.cu", "fp8_decode.cu", "dense_api.cu"]
 HEADERS = ["vnm_internal.h", "vnm_ptx.cuh", "vnm_select.cuh", "vnm_dense.h", "vnm_fp8.cuh"]
@@ -33,23 +33,37 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _inputs() -> List[str]:
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS + ["binding.c"]]
+def _newer_than(path: str, names: List[str]) -> bool:
+    """Whether `path` exists and is no older than these files of csrc and the public headers."""
+    if not os.path.exists(path):
+        return False
+    files = [os.path.join(CSRC, s) for s in names]
     files += [os.path.join(ROOT, "include", h) for h in ("vnm.h", "vnm_testing.h")]
-    return files
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(f) <= t for f in files)
+
+
+def _library_up_to_date() -> bool:
+    return _newer_than(LIB_PATH, SOURCES + HEADERS)
+
+
+def _binding_up_to_date() -> bool:
+    return _newer_than(BINDING_PATH, ["binding.c"])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
-        return False
-    t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return _library_up_to_date() and _binding_up_to_date()
 
 
 def build_binding() -> None:
-    """Compile the binding's C part with the host compiler for the running Python."""
+    """Compile the binding's C part with the host compiler for the running Python. Without
+    Python's headers it is left out: the library and the pruned calls do not need it."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        sys.stderr.write(f"no Python.h in {include}: the norm and 8-bit calls will not be available from Python\n")
+        return
     tmp = BINDING_PATH + ".tmp"
-    cmd = [os.environ.get("CC", "gcc"), "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-Wall", "-shared", "-fPIC", "-I", include,
            os.path.join(CSRC, "binding.c"), "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -58,10 +72,17 @@ def build_binding() -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libvnm.so if any input is newer; return its path."""
-    if not force and up_to_date():
-        return LIB_PATH
+    """Compile and link libvnm.so, then the binding, where any input is newer; return the library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
+    if force or not _library_up_to_date():
+        build_library(verbose)
+    if force or not _binding_up_to_date():
+        build_binding()
+    return LIB_PATH
+
+
+def build_library(verbose: bool = False) -> None:
+    """Compile and link libvnm.so."""
     nvcc = _nvcc()
 
     def compile_one(src: str) -> str:
@@ -79,14 +100,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-    build_binding()  # before the library, whose time up_to_date() goes by
     tmp = LIB_PATH + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":

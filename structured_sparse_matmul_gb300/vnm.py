@@ -490,7 +490,7 @@ def _native():
         L = lib()
         if not os.path.exists(_build.BINDING_PATH):
             raise RuntimeError(f"the binding is not built ({_build.BINDING_PATH} missing); run "
-                               "`python -c 'import __graft_entry__ as g; g.build()'` first")
+                               "`python -c 'import __graft_entry__ as g; g.build()'` first (it needs Python's headers)")
         spec = importlib.util.spec_from_file_location("_vnm_binding", _build.BINDING_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
