@@ -199,6 +199,9 @@ static int stream_of(PyObject* stream, int64_t device, vnm_stream_t* out) {
     return 0;
 }
 
+/* A number of the C ABI's 32 bits; -1, which every such argument refuses, for one that does not fit. */
+static int32_t narrow(long v) { return v >= INT32_MIN && v <= INT32_MAX ? (int32_t)v : -1; }
+
 static int64_t groups(int64_t n) { return (n + 127) / 128; }
 
 static int count(Py_ssize_t n, Py_ssize_t want) {
@@ -289,7 +292,7 @@ static PyObject* fp8_quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) 
         return NULL;
     vnm_status st;
     Py_BEGIN_ALLOW_THREADS
-    st = fn_quantize(x->p, ld_x, R, C, type, (int32_t)block, q->dims >= 0 ? q_type : t_type, q->p, ld_q, s->p, s->stride[0],
+    st = fn_quantize(x->p, ld_x, R, C, type, narrow(block), q->dims >= 0 ? q_type : t_type, q->p, ld_q, s->p, s->stride[0],
                      s->stride[1], qt->p, ld_t, u->p, u->stride[0], u->stride[1], stream);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(st);
@@ -327,14 +330,14 @@ static PyObject* fp8_linear(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     Py_BEGIN_ALLOW_THREADS
     if (skip >= 0 && status->dims < 0)
         st = fn_linear_skip_no_status(x->p, ld_x, x_type, xs->p, xs->stride[0], xs->stride[1], w->p, ld_w, w_type, ws->p,
-                                      ws->stride[0], ws->stride[1], block, T, R, K, y->p, ld_y, y_type, (int32_t)skip, stream);
+                                      ws->stride[0], ws->stride[1], block, T, R, K, y->p, ld_y, y_type, narrow(skip), stream);
     else if (skip >= 0)
         st = fn_linear_skip(x->p, ld_x, x_type, xs->p, xs->stride[0], xs->stride[1], w->p, ld_w, w_type, ws->p, ws->stride[0],
-                            ws->stride[1], block, T, R, K, b->p, b_type, (vnm_activation)act, y->p, ld_y, y_type, status->p,
-                            (int32_t)skip, stream);
+                            ws->stride[1], block, T, R, K, b->p, b_type, (vnm_activation)narrow(act), y->p, ld_y, y_type, status->p,
+                            narrow(skip), stream);
     else
         st = fn_linear(x->p, ld_x, x_type, xs->p, xs->stride[0], xs->stride[1], w->p, ld_w, w_type, ws->p, ws->stride[0],
-                       ws->stride[1], block, T, R, K, b->p, b_type, (vnm_activation)act, y->p, ld_y, y_type, status->p, stream);
+                       ws->stride[1], block, T, R, K, b->p, b_type, (vnm_activation)narrow(act), y->p, ld_y, y_type, status->p, stream);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(st);
 }
