@@ -50,6 +50,15 @@ vnm_status vnm_testing_fp8_linear_skip_stage_no_status(const void* xq, int64_t l
                                                        int64_t ld_y, vnm_dtype y_type, int32_t skip_stage,
                                                        vnm_stream_t stream);
 
+/*
+ * How vnm_fp8_linear takes a product on a GPU of sm_count SMs (host only): tiles of
+ * *tile_tokens = 16, 32, 64 or 128 tokens with K over *splits CTAs of a cluster; 0: pairs of
+ * CTAs, 256 x 256 outputs; 8: the few-token kernel.
+ * Errors: VNM_ERR_INVALID_ARG (sizes below 1, w_block_rows, null pointers).
+ */
+vnm_status vnm_testing_fp8_linear_plan(int64_t T, int64_t R, int64_t K, int32_t w_block_rows, int32_t sm_count,
+                                       int32_t* tile_tokens, int32_t* splits);
+
 #ifdef __cplusplus
 }
 #endif

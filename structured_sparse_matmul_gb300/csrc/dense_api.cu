@@ -229,6 +229,15 @@ vnm_status vnm_testing_fp8_linear_skip_stage_no_status(const void* xq, int64_t l
                       T, R, K, nullptr, VNM_F32, VNM_ACT_NONE, Y, ld_y, y_type, nullptr, skip_stage, stream);
 }
 
+vnm_status vnm_testing_fp8_linear_plan(int64_t T, int64_t R, int64_t K, int32_t w_block_rows, int32_t sm_count,
+                                       int32_t* tile_tokens, int32_t* splits) {
+    if (!size_ok(T) || !size_ok(R) || !size_ok(K) || T == 0 || R == 0 || K == 0 || sm_count < 1 ||
+        (w_block_rows != 1 && w_block_rows != vnm::kGroup) || tile_tokens == nullptr || splits == nullptr)
+        return VNM_ERR_INVALID_ARG;
+    vnm::fp8_linear_plan(T, R, K, w_block_rows != 1, sm_count, tile_tokens, splits);
+    return VNM_OK;
+}
+
 vnm_status vnm_fp8_linear_get_status(vnm_stream_t stream) {
     int code = 0;
     if (vnm::take_fp8_linear_status(&code, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return VNM_ERR_CUDA;

@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kRows = 16;                // rows of W of a CTA
 constexpr int kWarps = 8;
-constexpr int kMaxTokens = 8;
+constexpr int kMaxTokens = kMaxDecodeTokens;
 constexpr int kRing = 4;
 
 struct DecodeArgs {

@@ -1024,6 +1024,13 @@ TilePlan plan_tiles(int64_t T, int64_t R, int num_kb, bool one_scale, int sm_cou
 
 }  // namespace
 
+void fp8_linear_plan(int64_t T, int64_t R, int64_t K, bool one_scale, int sm_count, int* tile_tokens, int* splits) {
+    TilePlan plan{kMaxDecodeTokens, 1};
+    if (!fp8_decode_serves(T)) plan = plan_tiles(T, R, static_cast<int>((K + 127) / 128), one_scale, sm_count);
+    *tile_tokens = plan.bn;
+    *splits = plan.splits;
+}
+
 cudaError_t take_fp8_linear_status(int* code, cudaStream_t stream) {
     int words[3] = {0, 0, 0};
     cudaError_t e = cudaStreamSynchronize(stream);

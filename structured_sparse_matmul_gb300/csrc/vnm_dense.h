@@ -77,6 +77,11 @@ cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const S
                               const void* bias, vnm_dtype bias_type, int act, void* y, int64_t ld_y, vnm_dtype y_type,
                               int* status, int skip_stage, int sm_count, cudaStream_t stream);
 
+// Which kernel takes a product (K >= 1), by the rule that launch_fp8_linear goes by: tiles of 16, 32,
+// 64 or 128 tokens with K over `splits` CTAs; pairs of CTAs (0); the few-token kernel (kMaxDecodeTokens).
+constexpr int kMaxDecodeTokens = 8;
+void fp8_linear_plan(int64_t T, int64_t R, int64_t K, bool one_scale, int sm_count, int* tile_tokens, int* splits);
+
 // The first error that calls without status words recorded on the current device, and clears it.
 cudaError_t take_fp8_linear_status(int* code, cudaStream_t stream);
 

@@ -92,6 +92,7 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.vnm_testing_fp8_linear_skip_stage.argtypes = L.vnm_fp8_linear.argtypes[:-1] + [i32, p]
     L.vnm_testing_fp8_linear_skip_stage_no_status.argtypes = L.vnm_fp8_linear.argtypes[:16] + [p, i64, dt, i32, p]
     L.vnm_fp8_linear_get_status.argtypes = [p]
+    L.vnm_testing_fp8_linear_plan.argtypes = [i64, i64, i64, i32, i32, p, p]
     for name in ("vnm_sizes", "vnm_matrix_create", "vnm_matrix_destroy", "vnm_compress", "vnm_decompress",
                  "vnm_spmm", "vnm_spmm_workspace_size", "vnm_spmm_plan_query", "vnm_spmm_with_plan",
                  "vnm_get_status", "vnm_spmm_noalloc", "vnm_testing_spmm_skip_stage"):
@@ -580,3 +581,12 @@ def vnm_testing_fp8_linear_skip_stage(xq: torch.Tensor, x_scale: torch.Tensor, w
     code = _native().fp8_linear(xq, x_scale, wq, w_scale, Y, None, VNM_ACT_NONE, status, int(skip_stage), stream)
     if code:
         raise VnmError(code, "vnm_testing_fp8_linear_skip_stage")
+
+
+def vnm_testing_fp8_linear_plan(T: int, R: int, K: int, w_block_rows: int, sm_count: int) -> Tuple[int, int]:
+    """Test support: (tokens of a tile, splits of K) that vnm_fp8_linear takes; 0 tokens: pairs of
+    CTAs, 8: the few-token kernel (include/vnm_testing.h)."""
+    tile, splits = ctypes.c_int32(), ctypes.c_int32()
+    _check(lib().vnm_testing_fp8_linear_plan(T, R, K, w_block_rows, sm_count, ctypes.byref(tile), ctypes.byref(splits)),
+           "vnm_testing_fp8_linear_plan")
+    return tile.value, splits.value
