@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(32 * max_warps(CPT), 1) rmsnorm_kernel(const _
 // Backward. A CTA takes the rows t = blockIdx.x, + gridDim.x, ...; a thread owns
 // the same columns in all of them, so its share of dweight stays in registers
 // and is written once, to the CTA's row of `partial`. CPT = 0: no dweight here
-// (long rows, see rmsnorm_dw_kernel), dy and h read twice.
+// (long rows, see rmsnorm_dw_kernel; launched for dh only), dy and h read twice.
 template <typename T, bool VEC, int CPT>
 __global__ void __launch_bounds__(32 * max_warps(CPT), 1)
     rmsnorm_grad_kernel(const __grid_constant__ RmsNormGradArgs a, bool with_dw) {
@@ -500,7 +500,9 @@ cudaError_t run_grad(const RmsNormGradArgs& a, cudaStream_t stream) {
             if (e != cudaSuccess) return e;
         }
         switch (cpt) {
-            case 0: rmsnorm_grad_kernel<T, VEC, 0><<<grid, 32 * warps, 0, stream>>>(a, false); break;
+            case 0:
+                if (a.dh != nullptr) rmsnorm_grad_kernel<T, VEC, 0><<<grid, 32 * warps, 0, stream>>>(a, false);
+                break;
             case 1: rmsnorm_grad_kernel<T, VEC, 1><<<grid, 32 * warps, 0, stream>>>(a, dw); break;
             case 2: rmsnorm_grad_kernel<T, VEC, 2><<<grid, 32 * warps, 0, stream>>>(a, dw); break;
             default: rmsnorm_grad_kernel<T, VEC, 4><<<grid, 32 * warps, 0, stream>>>(a, dw); break;
