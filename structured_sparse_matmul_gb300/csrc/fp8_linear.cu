@@ -105,8 +105,7 @@ struct FlArgs {
     void* y;
     int64_t y_ms, y_ns;
     int y_type;
-    int y_align;   // bytes by which rows of 16 outputs are aligned (y_ns == 1)
-    bool y_tma;    // Y is written by TMA stores (pairs)
+    bool y_tma;    // Y's rows start on 16 bytes: pairs write it by TMA stores
     const void* bias;
     int bias_type;
     bool bias_on_m;
@@ -302,30 +301,12 @@ __device__ __noinline__ void gelu16(float (&v)[16]) {
     for (int u = 0; u < 16; ++u) v[u] = activate(VNM_ACT_GELU, v[u]);
 }
 
-// 16 neighbouring outputs of row m from their finished sums: 16-byte stores where
-// Y's rows allow them.
+// 16 outputs of row m from their finished sums (narrow tiles: neighbouring lanes' rows are
+// neighbours in Y).
 __device__ __noinline__ void store_any16(const FlArgs& a, int64_t m, int64_t n, float (&v)[16]) {
-    if (a.y_ns == 1 && a.y_align >= 16 && n + 16 <= a.n) {
-        uint4* d = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.y) + (m * a.y_ms + n) * (a.y_type == VNM_F32 ? 4 : 2));
-        if (a.y_type == VNM_F32) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                d[u] = make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]), __float_as_uint(v[4 * u + 2]),
-                                  __float_as_uint(v[4 * u + 3]));
-        } else {
-            const bool bf16 = a.y_type == VNM_BF16;
-            uint32_t w[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                w[u] = bf16 ? to_bf16x2(v[2 * u], v[2 * u + 1]) : to_f16x2(v[2 * u], v[2 * u + 1]);
-            d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            d[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-    } else {
-#pragma unroll
-        for (int u = 0; u < 16; ++u)
-            if (n + u < a.n) store_any(a.y, a.y_type, m * a.y_ms + (n + u) * a.y_ns, v[u]);
-    }
+    for (int u = 0; u < 16; ++u)
+        if (n + u < a.n) store_any(a.y, a.y_type, m * a.y_ms + (n + u) * a.y_ns, v[u]);
 }
 
 // The bias of columns n, n + 1 (the last one's past the edge).
@@ -948,8 +929,7 @@ cudaError_t run(const Fp8LinearArgs& g, FlArgs a, int splits, int sm_count, cuda
         !encode(&tm_q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.q, g.k, g.n, g.ld_q, Cfg::kQRows))
         return cudaErrorInvalidValue;
     tm_y = tm_p;  // not used, unless:
-    a.y_tma = CG == 2 && a.y_ns == 1 && a.y_align >= 16;
-    if (a.y_tma) {
+    if (CG == 2 && a.y_tma) {
         const CUtensorMapDataType t = a.y_type == VNM_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                       : a.y_type == VNM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -1055,11 +1035,9 @@ cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const S
     const bool wide = plan.bn == 0;
     Fp8LinearArgs g{};
     if (wide)
-        g = Fp8LinearArgs{xq, wq, ld_x, ld_w, x_e5m2, w_e5m2, xs, ws, T, R, K, y, ld_y, 1, y_type, bias, bias_type,
-                          false, act, status};
+        g = Fp8LinearArgs{xq, wq, ld_x, ld_w, x_e5m2, w_e5m2, xs, ws, T, R, K, ld_y, 1, false};
     else
-        g = Fp8LinearArgs{wq, xq, ld_w, ld_x, w_e5m2, x_e5m2, ws, xs, R, T, K, y, 1, ld_y, y_type, bias, bias_type,
-                          true, act, status};
+        g = Fp8LinearArgs{wq, xq, ld_w, ld_x, w_e5m2, x_e5m2, ws, xs, R, T, K, 1, ld_y, true};
     FlArgs a{};
     a.m = g.m;
     a.n = g.n;
@@ -1073,7 +1051,7 @@ cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const S
     a.y_ns = g.y_ns;
     a.y_type = y_type;
     const uintptr_t align = reinterpret_cast<uintptr_t>(y) | (static_cast<uintptr_t>(ld_y) * (y_type == VNM_F32 ? 4 : 2));
-    a.y_align = align % 32 == 0 ? 32 : align % 16 == 0 ? 16 : 1;
+    a.y_tma = align % 16 == 0;
     a.bias = bias;
     a.bias_type = bias_type;
     a.bias_on_m = g.bias_on_m;

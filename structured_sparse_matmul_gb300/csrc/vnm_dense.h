@@ -63,14 +63,8 @@ struct Fp8LinearArgs {
     bool p_e5m2, q_e5m2;
     ScaleView ps, qs;
     int64_t m, n, k;
-    void* y;
     int64_t y_ms, y_ns;
-    vnm_dtype y_type;
-    const void* bias;
-    vnm_dtype bias_type;
     bool bias_on_m;
-    int act;
-    int* status;
 };
 cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const ScaleView& xs, const void* wq,
                               int64_t ld_w, bool w_e5m2, const ScaleView& ws, int64_t T, int64_t R, int64_t K,
