@@ -16,6 +16,41 @@
 
 namespace {
 
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+}  // namespace
+
+namespace vnm {
+
+bool encode_2d(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, uint64_t dim0, uint64_t dim1,
+               uint64_t row_bytes, uint32_t box0, uint32_t box1, CUtensorMapSwizzle sw) {
+    auto enc = tensor_map_encoder();
+    if (enc == nullptr) return false;
+    const cuuint64_t gdim[2] = {dim0, dim1};
+    const cuuint64_t gstride[1] = {row_bytes};
+    const cuuint32_t box[2] = {box0, box1};
+    const cuuint32_t estride[2] = {1, 1};
+    return enc(tm, dt, 2, const_cast<void*>(base), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace vnm
+
+namespace {
+
+using vnm::encode_2d;
 using vnm::meta_pitch;
 using vnm::values_per_row;
 
@@ -40,34 +75,6 @@ vnm_status check_device(vnm_matrix A) {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) return VNM_ERR_CUDA;
     return dev == A->device ? VNM_OK : VNM_ERR_INVALID_ARG;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-// 2-D row-major tensor: dim0 contiguous elements per row, dim1 rows,
-// row_bytes apart; box0 x box1 box.
-bool encode_2d(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, uint64_t dim0, uint64_t dim1,
-               uint64_t row_bytes, uint32_t box0, uint32_t box1, CUtensorMapSwizzle sw) {
-    auto enc = tensor_map_encoder();
-    if (enc == nullptr) return false;
-    const cuuint64_t gdim[2] = {dim0, dim1};
-    const cuuint64_t gstride[1] = {row_bytes};
-    const cuuint32_t box[2] = {box0, box1};
-    const cuuint32_t estride[2] = {1, 1};
-    return enc(tm, dt, 2, const_cast<void*>(base), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The tensor-core path serves: condensed K a whole number of 128-column

@@ -32,11 +32,8 @@
 // a K block's MMAs wait for the sums of the block before last (tensor pipe 43 % busy).
 // Scales on both sides (4096 x 1024 outputs over 8192 tokens, fp32): 47.7 us. 16 tokens,
 // 11008 x 4096: 13.7 us, 3.3 TB/s, a chain of 16 K blocks a CTA and 5 us of start and end.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <atomic>
-#include <mutex>
 
 #include "vnm_dense.h"
 #include "vnm_fp8.cuh"
@@ -884,33 +881,11 @@ __global__ void fp8_linear_empty_kernel(const FlArgs a) {
         store_one(a, i / a.n, i % a.n, 0.f);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
 // A row-major matrix as boxes of 128 bytes x `box_rows` rows, 128B swizzle; past
 // its edges it reads as 0.
 bool encode(CUtensorMap* tm, CUtensorMapDataType type, int elem, const void* base, int64_t cols, int64_t rows, int64_t ld,
             int box_rows) {
-    auto enc = encoder();
-    if (enc == nullptr) return false;
-    const cuuint64_t dim[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(ld * elem)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), static_cast<cuuint32_t>(box_rows)};
-    const cuuint32_t step[2] = {1, 1};
-    return enc(tm, type, 2, const_cast<void*>(base), dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_2d(tm, type, base, cols, rows, ld * elem, 128 / elem, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int BN, bool ONE, int CG, bool F32 = false>

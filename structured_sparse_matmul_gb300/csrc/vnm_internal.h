@@ -81,6 +81,11 @@ __device__ __forceinline__ void out_store(const OutSpec& o, int64_t r, int64_t n
 }
 #endif
 
+// Tensor map of a 2-D row-major tensor: dim0 contiguous elements per row, dim1 rows,
+// row_bytes apart; box0 x box1 box, zeros past the edges. False where it cannot be encoded.
+bool encode_2d(CUtensorMap* tm, CUtensorMapDataType dt, const void* base, uint64_t dim0, uint64_t dim1,
+               uint64_t row_bytes, uint32_t box0, uint32_t box1, CUtensorMapSwizzle sw);
+
 // ---- launchers (each returns the launch's cudaError_t) ----
 
 cudaError_t launch_compress(const vnm_matrix_s& A, const void* W, int64_t ld_w, cudaStream_t stream);
