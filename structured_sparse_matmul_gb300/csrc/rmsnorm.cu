@@ -17,8 +17,9 @@
 // depend on timing.
 //
 // Measured: forward 8192 x 4096 bf16 with residual and 8-bit output 45.5 us, 5.2 TB/s,
-// 0.76 of a copy's rate; what is left is instruction issue. Backward 8192 x 4096 bf16 51.9 us, 5.2 TB/s, 0.76 (53 % issue active, loads
-// of one row ahead in flight). One row of 4096: 2.4 us, the launch and one round trip.
+// 0.76 of a copy's rate; what is left is instruction issue (72 % active, 39 for an
+// element). Backward 8192 x 4096 bf16 52.1 us, 5.2 TB/s, 0.76 (53 % issue active, loads
+// of one row ahead in flight). One row of 4096: 2.5 us, the launch and one round trip.
 #include <algorithm>
 #include <type_traits>
 
@@ -439,7 +440,8 @@ bool vec_ok(const void* p, int64_t ld, int elem) {
 
 // Units a warp keeps in registers for a row of `units` (0: too many, the row is
 // read twice), and the row's warps. Forward (pair = false): one unit a warp as long
-// as 32 warps reach (8192 x 4096 with 8-bit output: 42.9 us; two units a warp 54.4).
+// as 32 warps reach (8192 x 4096 with 8-bit output, by a product with the reciprocal in place
+// of the quotient: 42.9 us; two units a warp 54.4).
 // Backward: two units where there are rows enough to fill the GPU, so that the sum
 // across warps and the row's scalars are shared by 16 elements a lane (8192 x 4096:
 // 51.3 us; one unit 56.2).
