@@ -12,7 +12,8 @@ L2 before it is used again. The K timed steps are captured once in a CUDA
 graph and replayed between two events; each kernel's own launch duration
 comes from graphs of K launches of that kernel alone over the same sets.
 
-Output: one JSON line (rank 0). ``value`` is the dense-equivalent TFLOP/s of
+Output: one JSON line on stdout (rank 0), and the table of workloads as
+another on stderr. ``value`` is the dense-equivalent TFLOP/s of
 the whole step (2*R*N*K per step over the step time); ``e2e`` is the same
 metric through the public API with host buffers, copies included; the
 ``roofline`` object covers the kernel that takes most of the step.
@@ -404,6 +405,24 @@ def profiled_traffic(kernel: str, workload: str):
 
 def workload_tag(case) -> str:
     return f"{case.R}x{case.K}x{case.N}_v{case.V}m{case.M}"
+
+
+def print_line(line: dict) -> None:
+    """The result as one JSON line on stdout, of 3 KB at most, so that a caller who keeps only the end of
+    the output has all of it: numbers to 7 digits, and the table of workloads, ten times as long,
+    as a JSON line of its own on stderr."""
+    def short(v):
+        if isinstance(v, float):
+            return float(f"{v:.7g}") if math.isfinite(v) else v
+        if isinstance(v, dict):
+            return {k: short(x) for k, x in v.items()}
+        return [short(x) for x in v] if isinstance(v, (list, tuple)) else v
+
+    line = dict(line)
+    table = line.pop("per_config", None)
+    if table is not None:
+        print(json.dumps({"per_config": table}), file=sys.stderr, flush=True)
+    print(json.dumps(short(line)), flush=True)
 
 
 def config_of(case, l2_note):
@@ -1168,7 +1187,7 @@ def main():
             "gpu_launches": steps * kernels_per_step, "context": ctx,
             "gpu": props.name, "sm_count": props.multi_processor_count,
         }
-        print(json.dumps(line), flush=True)
+        print_line(line)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
