@@ -43,7 +43,8 @@
  *     for concurrent callers; and
  *     the static 8 MiB (+ 256-byte) device array of vnm_spmm_noalloc, held by
  *     every GPU that loads the library, with its address resolved once per
- *     CUDA context, and the three status words of vnm_fp8_linear.
+ *     CUDA context, and three status words each of vnm_fp8_linear and of the
+ *     dense 16-bit layers.
  */
 #ifndef VNM_H
 #define VNM_H
@@ -67,8 +68,8 @@ typedef enum vnm_status {
     VNM_ERR_INTERNAL = 6     /* a kernel found an inconsistent internal state */
 } vnm_status;
 
-/* VNM_BF16 is a type of the norm, the 8-bit quantiser and the 8-bit Linear
- * layer only; the V:N:M and bitmap entry points take VNM_F16 and VNM_F32. */
+/* VNM_BF16 is a type of the norm, the 8-bit quantiser, the 8-bit Linear layer and
+ * the dense 16-bit layers only; the V:N:M and bitmap entry points take VNM_F16 and VNM_F32. */
 typedef enum vnm_dtype { VNM_F16 = 0, VNM_F32 = 1, VNM_BF16 = 2 } vnm_dtype;
 
 /* 8-bit floating-point formats: e4m3 (no infinities, largest value 448) and
@@ -84,11 +85,13 @@ typedef enum vnm_path {
                           distributed shared memory); larger N, one warp per row */
 } vnm_path;
 
-/* Activations of the Linear-layer form (vnm_linear). */
+/* Activations of the Linear-layer forms. VNM_ACT_SILU is one of the dense 16-bit
+ * layers only (vnm_dense_linear, vnm_gated_linear and its backward pass); the others refuse it. */
 typedef enum vnm_activation {
     VNM_ACT_NONE = 0,
     VNM_ACT_RELU = 1, /* max(x, 0) */
-    VNM_ACT_GELU = 2  /* x * (1 + erf(x / sqrt 2)) / 2 */
+    VNM_ACT_GELU = 2, /* x * (1 + erf(x / sqrt 2)) / 2 */
+    VNM_ACT_SILU = 3  /* x / (1 + e^-x) */
 } vnm_activation;
 
 /* Selection policies of vnm_energy (all at the V:N:M density 2/M). */
@@ -514,6 +517,96 @@ vnm_status vnm_fp8_linear(const void* xq, int64_t ld_x, vnm_fp8 x_type, const fl
  * Errors: VNM_ERR_CUDA if the synchronisation itself failed.
  */
 vnm_status vnm_fp8_linear_get_status(vnm_stream_t stream);
+
+/* ---- dense 16-bit layers: product with epilogue, gated pair of projections ----
+ *
+ * Operands are fp16 or bf16 (all of a call the same, `type`) matrices whose rows start on 16
+ * bytes: base 16-byte aligned, leading dimension a multiple of 8 (any for a matrix of a single
+ * row); what lies past the last column in the rows' padding is not used. A transposed
+ * operand (`*_transposed` = 1) is stored with K along its columns: K x T for X, K x R for W.
+ * Outputs, residuals and checkpoints may have any alignment of their type; 16-byte aligned
+ * rows run faster. All sums are fp32, added in an order that the sizes alone fix (no
+ * atomics), and rounded once; the tensor cores' sums truncate, so for fp32 outputs they are
+ * taken out and added up every 2048 elements of K.
+ * status: optional device pointer to 3 zeroed int32 words (first error code, detail,
+ * count): a bounded wait that runs out records VNM_ERR_TIMEOUT there (the outputs are then
+ * undefined). NULL: in words that all such calls on the device share, read by
+ * vnm_dense_get_status. These entry points run on the current device and take no handle.
+ */
+
+/*
+ * Y = act(X . W^T + bias) + residual
+ * X: T x K, W: R x K; bias: [R] of bias_type, or NULL; residual: T x R of y_type, or NULL; Y: T x
+ * R, of y_type: the operands' type or VNM_F32. Everything after the sum is fp32.
+ * The gradients of Y = X . W^T are products of the same form:
+ *   dX = dY . W:            X := dY, W := W with w_transposed = 1;
+ *   dW = dW0 + dY^T . X:    X := dY, W := X, both transposed, residual := dW0.
+ * residual may be Y itself (same pointer and leading dimension): Y is then added to. No other overlap.
+ * T = 0 or R = 0 is a no-op; K = 0 gives act(bias) + residual.
+ * Errors: VNM_ERR_INVALID_ARG (pointers, alignment, leading dimensions, types, act), VNM_ERR_CUDA.
+ */
+vnm_status vnm_dense_linear(const void* X, int64_t ld_x, int32_t x_transposed, const void* W, int64_t ld_w,
+                            int32_t w_transposed, vnm_dtype type, int64_t T, int64_t R, int64_t K, const void* bias,
+                            vnm_dtype bias_type, vnm_activation act, const void* residual, int64_t ld_residual, void* Y,
+                            int64_t ld_y, vnm_dtype y_type, int32_t* status, vnm_stream_t stream);
+
+/* How vnm_gated_linear keeps the two products for the backward pass. */
+typedef enum vnm_keep {
+    VNM_KEEP_NONE = 0, /* not at all */
+    VNM_KEEP_16 = 1,   /* in the operands' type */
+    VNM_KEEP_E4M3 = 2, /* in the block-scaled 8-bit form, a scale for each 1 x 128 group */
+    VNM_KEEP_E5M2 = 3
+} vnm_keep;
+
+/*
+ * The gated pair of projections of a feed-forward block, in one kernel:
+ *   G = X . Wg^T, U = X . Wu^T, Y = act(G) * U
+ * X: T x K; Wg, Wu: F x K, row-major; Y: T x F, of type. act is any
+ * activation, applied to the unrounded G. g and u (T x F) are checkpoints of G and U for
+ * vnm_gated_linear_backward, as `keep` says (not read for VNM_KEEP_NONE), each rounded on its
+ * own; in 8 bits with g_scale and u_scale (T x ceil(F / 128), any strides), by the rule of the
+ * block-scaled form.
+ * T = 0 or F = 0 is a no-op.
+ * Errors: VNM_ERR_INVALID_ARG, VNM_ERR_CUDA.
+ */
+vnm_status vnm_gated_linear(const void* X, int64_t ld_x, const void* Wg, int64_t ld_wg, const void* Wu, int64_t ld_wu,
+                            vnm_dtype type, int64_t T, int64_t F, int64_t K, vnm_activation act, void* Y, int64_t ld_y,
+                            vnm_keep keep, void* g, int64_t ld_g, float* g_scale, int64_t gs_rs, int64_t gs_cs, void* u,
+                            int64_t ld_u, float* u_scale, int64_t us_rs, int64_t us_cs, int32_t* status,
+                            vnm_stream_t stream);
+
+/*
+ * Backward pass of vnm_gated_linear. dY: gradient of Y (T x F, any alignment; not needed for H alone); X, Wg, Wu as
+ * there; g, u and their scales as it kept them (keep: not VNM_KEEP_NONE). With G and U as kept:
+ *   dG = dY * U * act'(G), dU = dY * act(G)   (each rounded once to type: they are operands)
+ *   dX = dG . Wg + dU . Wu                    (T x K, type)
+ *   dWg = dG^T . X, dWu = dU^T . X            (F x K, of w_type: type or VNM_F32, one leading
+ *                                             dimension; with accumulate = 1 added to what is there)
+ *   H = act(G) * U                            (T x F, type: Y again, from the checkpoint)
+ * Outputs are NULL where not wanted (dWg and dWu together); X is needed for dWg and dWu, Wg and
+ * Wu for dX. relu'(0) = 0. H may be dY (same pointer and leading dimension); no other overlap.
+ * workspace: vnm_gated_linear_backward_workspace_size bytes, 16-byte aligned, for dG and dU (not
+ * needed for H alone). T = 0 gives dWg = dWu = 0.
+ * Errors: VNM_ERR_INVALID_ARG, VNM_ERR_CUDA.
+ */
+vnm_status vnm_gated_linear_backward(const void* dY, int64_t ld_dy, const void* X, int64_t ld_x, const void* Wg,
+                                     int64_t ld_wg, const void* Wu, int64_t ld_wu, vnm_dtype type, int64_t T, int64_t F,
+                                     int64_t K, vnm_activation act, vnm_keep keep, const void* g, int64_t ld_g,
+                                     const float* g_scale, int64_t gs_rs, int64_t gs_cs, const void* u, int64_t ld_u,
+                                     const float* u_scale, int64_t us_rs, int64_t us_cs, void* dX, int64_t ld_dx, void* dWg,
+                                     void* dWu, int64_t ld_dw, vnm_dtype w_type, int32_t accumulate, void* H, int64_t ld_h,
+                                     void* workspace, size_t workspace_bytes, int32_t* status, vnm_stream_t stream);
+
+/* Bytes of workspace vnm_gated_linear_backward needs (host only). */
+vnm_status vnm_gated_linear_backward_workspace_size(int64_t T, int64_t F, size_t* bytes);
+
+/*
+ * Synchronise `stream`, then return and clear the first error that one of the dense 16-bit
+ * layers without status words recorded on the current device since the last call
+ * (VNM_OK if none).
+ * Errors: VNM_ERR_CUDA if the synchronisation itself failed.
+ */
+vnm_status vnm_dense_get_status(vnm_stream_t stream);
 
 /*
  * Synchronise `stream`, then return and clear the first error any kernel

@@ -59,6 +59,24 @@ vnm_status vnm_testing_fp8_linear_skip_stage_no_status(const void* xq, int64_t l
 vnm_status vnm_testing_fp8_linear_plan(int64_t T, int64_t R, int64_t K, int32_t w_block_rows, int32_t sm_count,
                                        int32_t* tile_tokens, int32_t* splits);
 
+/*
+ * vnm_dense_linear without bias, activation and residual, except that the first CTA never issues
+ * the TMA loads of its pipeline stage number `skip_stage`: as vnm_testing_fp8_linear_skip_stage;
+ * the few-token kernel is not taken. status: as in vnm_dense_linear.
+ */
+vnm_status vnm_testing_dense_linear_skip_stage(const void* X, int64_t ld_x, const void* W, int64_t ld_w, vnm_dtype type,
+                                               int64_t T, int64_t R, int64_t K, void* Y, int64_t ld_y, vnm_dtype y_type,
+                                               int32_t* status, int32_t skip_stage, vnm_stream_t stream);
+
+/*
+ * How the dense 16-bit layers take a product on a GPU of sm_count SMs (host only), as
+ * vnm_testing_fp8_linear_plan. kind: 0 one product (T x R over K), 1 the sum of two, 2 two
+ * side by side in rows (T each), 3 a gated pair (R features; keep = 1: with checkpoints).
+ * Errors: VNM_ERR_INVALID_ARG.
+ */
+vnm_status vnm_testing_dense_plan(int32_t kind, int64_t T, int64_t R, int64_t K, int32_t x_transposed, int32_t w_transposed,
+                                  int32_t keep, int32_t sm_count, int32_t* tile_tokens, int32_t* splits);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,6 +1,6 @@
 /*
- * Argument marshalling of the norm, 8-bit quantiser and 8-bit Linear layer for
- * Python: torch tensors to the C ABI of include/vnm.h.
+ * Argument marshalling of the norm, 8-bit quantiser, 8-bit Linear layer and dense
+ * 16-bit layers for Python: torch tensors to the C ABI of include/vnm.h.
  *
  * These calls stand in decode loops, where one takes a few microseconds on the
  * GPU. Reading a tensor's shape, type, device, strides and address from Python
@@ -29,6 +29,10 @@ typedef vnm_status (*testing_linear_no_status_t)(const void*, int64_t, vnm_fp8, 
                                                  int64_t, vnm_fp8, const float*, int64_t, int64_t, int32_t, int64_t, int64_t,
                                                  int64_t, void*, int64_t, vnm_dtype, int32_t, vnm_stream_t);
 static testing_linear_no_status_t fn_linear_skip_no_status;
+static __typeof__(&vnm_dense_linear) fn_dense;
+static __typeof__(&vnm_gated_linear) fn_gated;
+static __typeof__(&vnm_gated_linear_backward) fn_gated_backward;
+static __typeof__(&vnm_gated_linear_backward_workspace_size) fn_gated_workspace;
 
 static PyObject *py_f16, *py_f32, *py_bf16, *py_e4m3, *py_e5m2, *py_i32; /* torch dtypes */
 static PyObject *py_current_device, *py_current_stream;
@@ -352,12 +356,212 @@ static PyObject* rmsnorm_workspace(PyObject* self, PyObject* const* a, Py_ssize_
     return PyLong_FromLongLong(st == VNM_OK ? (int64_t)bytes : -(int64_t)st);
 }
 
-/* The seven functions' addresses, torch's six types, current device and current stream. */
+/* Rows start 8 elements (16 bytes) apart or a multiple of it; one row has no pitch. */
+static int pitched(int64_t rows, int64_t cols, int64_t stride) { return rows <= 1 || (stride >= cols && stride % 8 == 0); }
+
+/* A 16-bit operand, rows x cols: row-major, or the transposed view of a row-major matrix. A view that is
+ * both (one row or one column) is taken as what its strides allow. */
+static int operand(const Tensor* t, const char* name, int64_t rows, int64_t cols, PyObject* dtype, int64_t device, int64_t* ld,
+                   int32_t* transposed) {
+    *ld = 1;
+    *transposed = 0;
+    if (t->dims < 0) return 0;
+    if (t->dims != 2 || t->size[0] != rows || t->size[1] != cols || t->device != device || t->dtype != dtype)
+        return refuse(t, name, rows, cols, dtype, device);
+    const int plain = cols <= 1 || t->stride[1] == 1, turned = rows <= 1 || t->stride[0] == 1;
+    if (rows == 0 || cols == 0) return 0; /* nothing is read */
+    *transposed = !(plain && pitched(rows, cols, t->stride[0])) && turned && (!plain || pitched(cols, rows, t->stride[1]));
+    if (!plain && !turned) return refuse(t, name, rows, cols, dtype, device);
+    const int64_t n = *transposed ? cols : rows, width = *transposed ? rows : cols, stride = t->stride[*transposed];
+    /* rows that overlap (an expanded tensor's) have no leading dimension; one row may carry any stride */
+    if (n > 1 && stride < width) return refuse(t, name, rows, cols, dtype, device);
+    *ld = stride >= width ? stride : width;
+    return 0;
+}
+
+static int status_words(const Tensor* t, int64_t device) {
+    if (t->dims >= 0 && (t->dtype != py_i32 || t->device != device || t->dims != 1 || t->size[0] < 3 || t->stride[0] != 1)) {
+        PyErr_SetString(PyExc_ValueError, "status must be a CUDA int32 tensor of at least 3 words");
+        return -1;
+    }
+    return 0;
+}
+
+/* X, W, Y, bias, act, residual, status, stream -> status */
+static PyObject* dense_linear(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    static const int which[6] = {0, 1, 2, 3, 5, 6};
+    Tensor t[6];
+    const Tensor *x = &t[0], *w = &t[1], *y = &t[2], *b = &t[3], *r = &t[4], *status = &t[5];
+    int64_t ld_x, ld_w, ld_y, ld_r;
+    int32_t tx, tw;
+    vnm_dtype type, y_type, b_type = VNM_F32;
+    vnm_stream_t stream;
+    if (count(n, 8) < 0 || read_all(a, which, 6, t) < 0 || first(x, "X") < 0 || dtype_of(x, "X", &type) < 0 ||
+        dtype_of(y, "Y", &y_type) < 0)
+        return NULL;
+    const long act = PyLong_AsLong(a[4]);
+    if (act == -1 && PyErr_Occurred()) return NULL;
+    if (w->dims != 2) {
+        PyErr_SetString(PyExc_ValueError, "W must be a CUDA matrix");
+        return NULL;
+    }
+    const int64_t T = x->size[0], K = x->size[1], R = w->size[0], dev = x->device;
+    if (operand(x, "X", T, K, x->dtype, dev, &ld_x, &tx) < 0 || operand(w, "W", R, K, x->dtype, dev, &ld_w, &tw) < 0 ||
+        matrix(y, "Y", T, R, NULL, dev, &ld_y) < 0 || vector(b, "bias", R, NULL, dev) < 0 ||
+        (b->dims >= 0 && dtype_of(b, "bias", &b_type) < 0) || matrix(r, "residual", T, R, y->dtype, dev, &ld_r) < 0 ||
+        status_words(status, dev) < 0 || stream_of(a[7], dev, &stream) < 0)
+        return NULL;
+    vnm_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = fn_dense(x->p, ld_x, tx, w->p, ld_w, tw, type, T, R, K, b->p, b_type, (vnm_activation)narrow(act), r->p, ld_r, y->p, ld_y,
+                  y_type, status->p, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* The checkpoints g and u with their scales (T x F each): how they are kept. */
+static int kept(const Tensor* g, const Tensor* u, const Tensor* gs, const Tensor* us, int64_t T, int64_t F, PyObject* dtype,
+                int64_t device, vnm_keep* keep, int64_t* ld_g, int64_t* ld_u) {
+    vnm_fp8 type;
+    *keep = VNM_KEEP_NONE;
+    *ld_g = *ld_u = 1;
+    if ((g->dims < 0) != (u->dims < 0)) {
+        PyErr_SetString(PyExc_ValueError, "g and u must be given together");
+        return -1;
+    }
+    if (g->dims < 0) return 0;
+    if (g->dtype == dtype) {
+        *keep = VNM_KEEP_16;
+    } else {
+        if (fp8_of(g, "g (of another type than X)", &type) < 0) return -1;
+        if (gs->dims < 0 || us->dims < 0) {
+            PyErr_SetString(PyExc_ValueError, "float8 checkpoints need g_scale and u_scale");
+            return -1;
+        }
+        *keep = type == VNM_E4M3 ? VNM_KEEP_E4M3 : VNM_KEEP_E5M2;
+    }
+    return matrix(g, "g", T, F, NULL, device, ld_g) < 0 || matrix(u, "u", T, F, g->dtype, device, ld_u) < 0 ||
+                   (*keep != VNM_KEEP_16 && (scales(gs, "g_scale", T, groups(F), device) < 0 ||
+                                             scales(us, "u_scale", T, groups(F), device) < 0))
+               ? -1
+               : 0;
+}
+
+/* X, Wg, Wu, Y, act, g, u, g_scale, u_scale, status, stream -> status */
+static PyObject* gated_linear(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    static const int which[9] = {0, 1, 2, 3, 5, 6, 7, 8, 9};
+    Tensor t[9];
+    const Tensor *x = &t[0], *wg = &t[1], *wu = &t[2], *y = &t[3], *g = &t[4], *u = &t[5], *gs = &t[6], *us = &t[7], *status = &t[8];
+    int64_t ld_x, ld_wg, ld_wu, ld_y, ld_g, ld_u;
+    vnm_dtype type;
+    vnm_keep keep;
+    vnm_stream_t stream;
+    if (count(n, 11) < 0 || read_all(a, which, 9, t) < 0 || first(x, "X") < 0 || dtype_of(x, "X", &type) < 0) return NULL;
+    const long act = PyLong_AsLong(a[4]);
+    if (act == -1 && PyErr_Occurred()) return NULL;
+    if (wg->dims != 2 || wu->dims != 2 || y->dims != 2) {
+        PyErr_SetString(PyExc_ValueError, "Wg, Wu and Y must be CUDA matrices");
+        return NULL;
+    }
+    const int64_t T = x->size[0], K = x->size[1], F = wg->size[0], dev = x->device;
+    if (matrix(x, "X", T, K, NULL, dev, &ld_x) < 0 || matrix(wg, "Wg", F, K, x->dtype, dev, &ld_wg) < 0 ||
+        matrix(wu, "Wu", F, K, x->dtype, dev, &ld_wu) < 0 || matrix(y, "Y", T, F, x->dtype, dev, &ld_y) < 0 ||
+        kept(g, u, gs, us, T, F, x->dtype, dev, &keep, &ld_g, &ld_u) < 0 || status_words(status, dev) < 0 ||
+        stream_of(a[10], dev, &stream) < 0)
+        return NULL;
+    vnm_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = fn_gated(x->p, ld_x, wg->p, ld_wg, wu->p, ld_wu, type, T, F, K, (vnm_activation)narrow(act), y->p, ld_y, keep, g->p, ld_g,
+                  gs->p, gs->stride[0], gs->stride[1], u->p, ld_u, us->p, us->stride[0], us->stride[1], status->p, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* dY, X, Wg, Wu, g, u, g_scale, u_scale, act, dx, dwg, dwu, h, accumulate, workspace, status, stream -> status */
+static PyObject* gated_linear_backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    static const int which[14] = {0, 1, 2, 3, 4, 5, 6, 7, 9, 10, 11, 12, 14, 15};
+    Tensor t[14];
+    const Tensor *dy = &t[0], *x = &t[1], *wg = &t[2], *wu = &t[3], *g = &t[4], *u = &t[5], *gs = &t[6], *us = &t[7], *dx = &t[8],
+                 *dwg = &t[9], *dwu = &t[10], *h = &t[11], *ws = &t[12], *status = &t[13];
+    int64_t ld_dy, ld_x, ld_wg, ld_wu, ld_g, ld_u, ld_dx, ld_dw, ld_du, ld_h, bytes = 0, K = 0;
+    vnm_dtype type, w_type;
+    vnm_keep keep;
+    vnm_stream_t stream;
+    if (count(n, 17) < 0 || read_all(a, which, 14, t) < 0 || first(g, "g") < 0) return NULL;
+    const long act = PyLong_AsLong(a[8]);
+    if (act == -1 && PyErr_Occurred()) return NULL;
+    const int accumulate = PyObject_IsTrue(a[13]);
+    if (accumulate < 0) return NULL;
+    /* the layer's type: of the first tensor given that has it */
+    const Tensor* typed = dy->dims >= 0 ? dy : h->dims >= 0 ? h : NULL;
+    const Tensor* wide = x->dims >= 0 ? x : wg->dims >= 0 ? wg : dx->dims >= 0 ? dx : NULL; /* has K columns */
+    if (typed == NULL) {
+        PyErr_SetString(PyExc_ValueError, "dY must be a CUDA matrix");
+        return NULL;
+    }
+    if (dtype_of(typed, "dY and h", &type) < 0) return NULL;
+    PyObject* const dt = typed->dtype;
+    if (wide != NULL && wide->dims == 2) K = wide->size[1];
+    const int64_t T = g->size[0], F = g->size[1], dev = g->device;
+    w_type = type;
+    if ((dx->dims >= 0 || dwg->dims >= 0 || dwu->dims >= 0) && dy->dims < 0) {
+        PyErr_SetString(PyExc_ValueError, "dx, dwg and dwu need dY");
+        return NULL;
+    }
+    if ((dwg->dims < 0) != (dwu->dims < 0) || (dwg->dims >= 0 && x->dims < 0) ||
+        (dx->dims >= 0 && (wg->dims < 0 || wu->dims < 0))) {
+        PyErr_SetString(PyExc_ValueError, "dwg and dwu are computed together and need X; dx needs Wg and Wu");
+        return NULL;
+    }
+    if (matrix(dy, "dY", T, F, dt, dev, &ld_dy) < 0 || matrix(x, "X", T, K, dt, dev, &ld_x) < 0 ||
+        matrix(wg, "Wg", F, K, dt, dev, &ld_wg) < 0 || matrix(wu, "Wu", F, K, dt, dev, &ld_wu) < 0 ||
+        kept(g, u, gs, us, T, F, dt, dev, &keep, &ld_g, &ld_u) < 0 || matrix(dx, "dx", T, K, dt, dev, &ld_dx) < 0 ||
+        matrix(h, "h", T, F, dt, dev, &ld_h) < 0)
+        return NULL;
+    if (dwg->dims >= 0) {
+        if (dtype_of(dwg, "dwg", &w_type) < 0 || matrix(dwg, "dwg", F, K, NULL, dev, &ld_dw) < 0 ||
+            matrix(dwu, "dwu", F, K, dwg->dtype, dev, &ld_du) < 0)
+            return NULL;
+        if (F > 1 && ld_dw != ld_du) {
+            PyErr_SetString(PyExc_ValueError, "dwg and dwu must have the same row stride");
+            return NULL;
+        }
+    } else {
+        ld_dw = 1;
+    }
+    if (ws->dims >= 0) {
+        if (ws->device != dev || ws->dims != 1 || (ws->size[0] > 1 && ws->stride[0] != 1)) {
+            PyErr_SetString(PyExc_ValueError, "workspace must be a contiguous vector on g's device");
+            return NULL;
+        }
+        if (long_of(PyObject_GetAttr(ws->object, s_nbytes), &bytes) < 0) return NULL;
+    }
+    if (status_words(status, dev) < 0 || stream_of(a[16], dev, &stream) < 0) return NULL;
+    vnm_status st;
+    Py_BEGIN_ALLOW_THREADS
+    st = fn_gated_backward(dy->p, ld_dy, x->p, ld_x, wg->p, ld_wg, wu->p, ld_wu, type, T, F, K, (vnm_activation)narrow(act), keep,
+                           g->p, ld_g, gs->p, gs->stride[0], gs->stride[1], u->p, ld_u, us->p, us->stride[0], us->stride[1], dx->p,
+                           ld_dx, dwg->p, dwu->p, ld_dw, w_type, accumulate, h->p, ld_h, ws->p, (size_t)bytes, status->p, stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* T, F -> bytes of workspace of gated_linear_backward, or minus the status */
+static PyObject* gated_workspace(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    if (count(n, 2) < 0) return NULL;
+    const int64_t T = PyLong_AsLongLong(a[0]), F = PyLong_AsLongLong(a[1]);
+    if (PyErr_Occurred()) return NULL;
+    size_t bytes = 0;
+    const vnm_status st = fn_gated_workspace(T, F, &bytes);
+    return PyLong_FromLongLong(st == VNM_OK ? (int64_t)bytes : -(int64_t)st);
+}
+
+/* The eleven functions' addresses, torch's six types, current device and current stream. */
 static PyObject* setup(PyObject* self, PyObject* args) {
-    unsigned long long f[7];
+    unsigned long long f[11];
     PyObject *t[6], *device, *stream;
-    if (!PyArg_ParseTuple(args, "(KKKKKKK)(OOOOOO)OO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &t[0], &t[1], &t[2], &t[3],
-                          &t[4], &t[5], &device, &stream))
+    if (!PyArg_ParseTuple(args, "(KKKKKKKKKKK)(OOOOOO)OO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9],
+                          &f[10], &t[0], &t[1], &t[2], &t[3], &t[4], &t[5], &device, &stream))
         return NULL;
     fn_rmsnorm = (__typeof__(fn_rmsnorm))(uintptr_t)f[0];
     fn_rmsnorm_backward = (__typeof__(fn_rmsnorm_backward))(uintptr_t)f[1];
@@ -366,6 +570,10 @@ static PyObject* setup(PyObject* self, PyObject* args) {
     fn_linear = (__typeof__(fn_linear))(uintptr_t)f[4];
     fn_linear_skip = (testing_linear_t)(uintptr_t)f[5];
     fn_linear_skip_no_status = (testing_linear_no_status_t)(uintptr_t)f[6];
+    fn_dense = (__typeof__(fn_dense))(uintptr_t)f[7];
+    fn_gated = (__typeof__(fn_gated))(uintptr_t)f[8];
+    fn_gated_backward = (__typeof__(fn_gated_backward))(uintptr_t)f[9];
+    fn_gated_workspace = (__typeof__(fn_gated_workspace))(uintptr_t)f[10];
     PyObject** to[8] = {&py_f16, &py_bf16, &py_f32, &py_e4m3, &py_e5m2, &py_i32, &py_current_device, &py_current_stream};
     PyObject* from[8] = {t[0], t[1], t[2], t[3], t[4], t[5], device, stream};
     for (int i = 0; i < 8; ++i) {
@@ -382,6 +590,10 @@ static PyMethodDef methods[] = {
     {"rmsnorm_workspace", (PyCFunction)(void (*)(void))rmsnorm_workspace, METH_FASTCALL, "vnm_rmsnorm_backward_workspace_size"},
     {"fp8_quantize", (PyCFunction)(void (*)(void))fp8_quantize, METH_FASTCALL, "vnm_fp8_quantize"},
     {"fp8_linear", (PyCFunction)(void (*)(void))fp8_linear, METH_FASTCALL, "vnm_fp8_linear"},
+    {"dense_linear", (PyCFunction)(void (*)(void))dense_linear, METH_FASTCALL, "vnm_dense_linear"},
+    {"gated_linear", (PyCFunction)(void (*)(void))gated_linear, METH_FASTCALL, "vnm_gated_linear"},
+    {"gated_linear_backward", (PyCFunction)(void (*)(void))gated_linear_backward, METH_FASTCALL, "vnm_gated_linear_backward"},
+    {"gated_workspace", (PyCFunction)(void (*)(void))gated_workspace, METH_FASTCALL, "vnm_gated_linear_backward_workspace_size"},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_vnm_binding", "Argument marshalling for libvnm.", -1, methods,

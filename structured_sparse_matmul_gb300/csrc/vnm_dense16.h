@@ -1,0 +1,91 @@
+// Internal declarations of the dense 16-bit layers: the product with bias,
+// activation and residual, the gated pair of projections and its backward pass
+// (kernels in dense_linear.cu, dense_decode.cu and gated_grad.cu, argument checks in
+// dense16_api.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/vnm.h"
+
+namespace vnm {
+
+// A 16-bit operand of a product, rows x K: stored row-major (a row's K elements
+// are neighbours), or transposed (an element of K is a row of the storage).
+struct Operand16 {
+    const void* p;
+    int64_t ld;
+    bool transposed;
+};
+
+// What the two halves of a product of two operands are.
+enum ProductKind {
+    kOneProduct,   // y[0] = x[0] . w[0]^T
+    kSumOfTwo,     // y[0] = x[0] . w[0]^T + x[1] . w[1]^T
+    kTwoByRows,    // y[i] = x[i] . w[0]^T
+    kGatedPair     // y[0] = act(x[0] . w[0]^T) * (x[0] . w[1]^T)
+};
+
+// How a gated pair's two products are kept for the backward pass.
+enum KeepKind { kKeepNone, kKeep16, kKeep8 };
+
+struct Kept {
+    void* p;        // T x R: the inputs' type, or fp8
+    int64_t ld;
+    float* s;       // kKeep8: a scale for each 128 columns of a row
+    int64_t s_rs, s_cs;
+};
+
+struct ProductArgs {
+    ProductKind kind;
+    int64_t T, R, K;  // of one product
+    bool bf16;
+    Operand16 x[2], w[2];
+    void* y[2];
+    int64_t ld_y;
+    vnm_dtype y_type;
+    const void* bias;
+    vnm_dtype bias_type;
+    int act;
+    const void* residual[2];
+    int64_t ld_residual;
+    KeepKind keep;
+    bool e5m2;
+    Kept g, u;
+    int* status;
+    int skip_stage;  // tests of the bounded waits only (-1: none)
+};
+
+cudaError_t launch_product(const ProductArgs& a, int sm_count, cudaStream_t stream);
+
+// Which kernel takes a product (K >= 1), by the rule that launch_product goes by: tiles of 16, 32, 64
+// or 128 tokens with K over `splits` CTAs; pairs of CTAs (0); the few-token kernel (kFewTokens).
+constexpr int kFewTokens = 8;
+void product_plan(const ProductArgs& a, int sm_count, int* tile_tokens, int* splits);
+
+// The first error that products without status words recorded on the current device, and clears it.
+cudaError_t take_product_status(int* code, cudaStream_t stream);
+
+// The same product for up to kFewTokens tokens: kOneProduct or kGatedPair without
+// checkpoints, both operands row-major.
+cudaError_t launch_few_tokens(const ProductArgs& a, cudaStream_t stream);
+
+// dg = dy * u * act'(g), du = dy * act(g), h = act(g) * u, element by element.
+struct GatedGradArgs {
+    int64_t T, F;
+    bool bf16;
+    int act;
+    const void* dy;
+    int64_t ld_dy;
+    KeepKind keep;
+    bool e5m2;
+    Kept g, u;  // (read)
+    void *dg, *du;
+    int64_t ld_d;  // of both
+    void* h;
+    int64_t ld_h;
+};
+cudaError_t launch_gated_grad(const GatedGradArgs& a, int sm_count, cudaStream_t stream);
+
+}  // namespace vnm

@@ -93,6 +93,15 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.vnm_testing_fp8_linear_skip_stage_no_status.argtypes = L.vnm_fp8_linear.argtypes[:16] + [p, i64, dt, i32, p]
     L.vnm_fp8_linear_get_status.argtypes = [p]
     L.vnm_testing_fp8_linear_plan.argtypes = [i64, i64, i64, i32, i32, p, p]
+    L.vnm_dense_linear.argtypes = [p, i64, i32, p, i64, i32, dt, i64, i64, i64, p, dt, dt, p, i64, p, i64, dt, p, p]
+    L.vnm_gated_linear.argtypes = [p, i64, p, i64, p, i64, dt, i64, i64, i64, dt, p, i64, dt, p, i64, p, i64, i64, p, i64, p,
+                                   i64, i64, p, p]
+    L.vnm_gated_linear_backward.argtypes = [p, i64, p, i64, p, i64, p, i64, dt, i64, i64, i64, dt, dt, p, i64, p, i64, i64, p,
+                                            i64, p, i64, i64, p, i64, p, p, i64, dt, i32, p, i64, p, sz, p, p]
+    L.vnm_gated_linear_backward_workspace_size.argtypes = [i64, i64, p]
+    L.vnm_dense_get_status.argtypes = [p]
+    L.vnm_testing_dense_linear_skip_stage.argtypes = [p, i64, p, i64, dt, i64, i64, i64, p, i64, dt, p, i32, p]
+    L.vnm_testing_dense_plan.argtypes = [i32, i64, i64, i64, i32, i32, i32, i32, p, p]
     for name in ("vnm_sizes", "vnm_matrix_create", "vnm_matrix_destroy", "vnm_compress", "vnm_decompress",
                  "vnm_spmm", "vnm_spmm_workspace_size", "vnm_spmm_plan_query", "vnm_spmm_with_plan",
                  "vnm_get_status", "vnm_spmm_noalloc", "vnm_testing_spmm_skip_stage"):
@@ -314,6 +323,7 @@ def bitmap_spmm(A: BitmapMatrix, B: torch.Tensor, C: torch.Tensor, workspace: Op
 
 
 VNM_ACT_NONE, VNM_ACT_RELU, VNM_ACT_GELU = 0, 1, 2
+VNM_ACT_SILU = 3  # the dense 16-bit layers only
 
 
 def vnm_linear_workspace_size(A: VnmMatrix, T: int) -> int:
@@ -496,7 +506,9 @@ def _native():
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         functions = (L.vnm_rmsnorm, L.vnm_rmsnorm_backward, L.vnm_rmsnorm_backward_workspace_size, L.vnm_fp8_quantize,
-                     L.vnm_fp8_linear, L.vnm_testing_fp8_linear_skip_stage, L.vnm_testing_fp8_linear_skip_stage_no_status)
+                     L.vnm_fp8_linear, L.vnm_testing_fp8_linear_skip_stage, L.vnm_testing_fp8_linear_skip_stage_no_status,
+                     L.vnm_dense_linear, L.vnm_gated_linear, L.vnm_gated_linear_backward,
+                     L.vnm_gated_linear_backward_workspace_size)
         # torch's raw query of the current stream takes 0.1 us, a stream object 3
         stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                          lambda device: int(torch.cuda.current_stream(device).cuda_stream))
@@ -589,4 +601,90 @@ def vnm_testing_fp8_linear_plan(T: int, R: int, K: int, w_block_rows: int, sm_co
     tile, splits = ctypes.c_int32(), ctypes.c_int32()
     _check(lib().vnm_testing_fp8_linear_plan(T, R, K, w_block_rows, sm_count, ctypes.byref(tile), ctypes.byref(splits)),
            "vnm_testing_fp8_linear_plan")
+    return tile.value, splits.value
+
+
+# ---- dense 16-bit layers: product with epilogue, gated pair of projections ----
+
+
+def vnm_dense_linear(X: torch.Tensor, W: torch.Tensor, Y: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                     act: int = VNM_ACT_NONE, residual: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Y = act(X . W^T + bias) + residual: X (T x K) and W (R x K) fp16 or bf16, either of them
+    a matrix or the transposed view of one, the stored rows starting on 16 bytes; Y (T x R)
+    of that type or fp32; residual like Y, or Y itself; bias (R,) fp16, bf16 or fp32. The
+    gradients are calls of the same form: dX of (dY, W.t()), dW of (dY.t(), X.t()).
+    ``status``: optional int32 CUDA tensor of 3 zeroed words that receives kernel errors
+    (without it: vnm_dense_get_status)."""
+    code = _native().dense_linear(X, W, Y, bias, act, residual, status, stream)
+    if code:
+        raise VnmError(code, "vnm_dense_linear")
+
+
+def vnm_gated_linear(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Y: torch.Tensor, act: int = VNM_ACT_SILU,
+                     g: Optional[torch.Tensor] = None, u: Optional[torch.Tensor] = None,
+                     g_scale: Optional[torch.Tensor] = None, u_scale: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Y = act(G) * U with G = X . Wg^T and U = X . Wu^T: X (T x K), Wg and Wu (F x K), Y (T x F),
+    fp16 or bf16, rows of X, Wg and Wu starting on 16 bytes. g and u (T x F), where given, keep G
+    and U for vnm_gated_linear_backward: in the inputs' type, or in float8 with fp32
+    g_scale and u_scale (T, ceil(F / 128))."""
+    code = _native().gated_linear(X, Wg, Wu, Y, act, g, u, g_scale, u_scale, status, stream)
+    if code:
+        raise VnmError(code, "vnm_gated_linear")
+
+
+def vnm_gated_linear_backward_workspace_size(T: int, F: int) -> int:
+    """Bytes of workspace that vnm_gated_linear_backward needs for dG and dU."""
+    n = _native().gated_workspace(T, F)
+    if n < 0:
+        raise VnmError(-n, "vnm_gated_linear_backward_workspace_size")
+    return n
+
+
+def vnm_gated_linear_backward(dY: Optional[torch.Tensor], X: Optional[torch.Tensor], Wg: Optional[torch.Tensor],
+                              Wu: Optional[torch.Tensor], g: torch.Tensor, u: torch.Tensor,
+                              g_scale: Optional[torch.Tensor] = None, u_scale: Optional[torch.Tensor] = None,
+                              act: int = VNM_ACT_SILU, dx: Optional[torch.Tensor] = None,
+                              dwg: Optional[torch.Tensor] = None, dwu: Optional[torch.Tensor] = None,
+                              h: Optional[torch.Tensor] = None, accumulate: bool = False,
+                              workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                              stream=None) -> None:
+    """Gradients of vnm_gated_linear from dY (T x F) and its checkpoints g and u (with their scales):
+    dx (T x K), dwg and dwu (F x K, of X's type or fp32; ``accumulate``: added to), and
+    h (T x F), which is Y again; those that are None are not computed, nor the inputs needed
+    that only they use (X for dwg and dwu, Wg and Wu for dx, dY for all three). A workspace of
+    one's own is used in the order of ``stream``, as the other tensors are."""
+    if workspace is None and (dx is not None or dwg is not None):
+        workspace = _scratch(vnm_gated_linear_backward_workspace_size(*g.shape), g.device, stream)
+    code = _native().gated_linear_backward(dY, X, Wg, Wu, g, u, g_scale, u_scale, act, dx, dwg, dwu, h, bool(accumulate),
+                                           workspace, status, stream)
+    if code:
+        raise VnmError(code, "vnm_gated_linear_backward")
+
+
+def vnm_dense_get_status(stream=None) -> int:
+    """Synchronise the stream and return (and clear) the first error code that one of the dense
+    16-bit layers without ``status`` recorded on the current device."""
+    return int(lib().vnm_dense_get_status(_stream_ptr(stream)))
+
+
+def vnm_testing_dense_linear_skip_stage(X: torch.Tensor, W: torch.Tensor, Y: torch.Tensor, skip_stage: int,
+                                        status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Test support: vnm_dense_linear (row-major operands, no epilogue) with the first CTA's loads
+    of one pipeline stage never issued (include/vnm_testing.h)."""
+    dt = {torch.float16: VNM_F16, torch.bfloat16: VNM_BF16, torch.float32: VNM_F32}
+    _check(lib().vnm_testing_dense_linear_skip_stage(
+        X.data_ptr(), _rowmajor(X, "X"), W.data_ptr(), _rowmajor(W, "W"), dt[X.dtype], X.shape[0], W.shape[0], X.shape[1],
+        Y.data_ptr(), _rowmajor(Y, "Y"), dt[Y.dtype], status.data_ptr() if status is not None else None, int(skip_stage),
+        _stream_ptr(stream)), "vnm_testing_dense_linear_skip_stage")
+
+
+def vnm_testing_dense_plan(kind: int, T: int, R: int, K: int, sm_count: int, x_transposed: bool = False,
+                           w_transposed: bool = False, keep: bool = False) -> Tuple[int, int]:
+    """Test support: (tokens of a tile, splits of K) that the dense 16-bit layers take; 0 tokens:
+    pairs of CTAs, 8: the few-token kernel (include/vnm_testing.h)."""
+    tile, splits = ctypes.c_int32(), ctypes.c_int32()
+    _check(lib().vnm_testing_dense_plan(kind, T, R, K, int(x_transposed), int(w_transposed), int(keep), sm_count,
+                                        ctypes.byref(tile), ctypes.byref(splits)), "vnm_testing_dense_plan")
     return tile.value, splits.value
