@@ -117,6 +117,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) dense_decode_kernel(const FewA
     };
     Weights<NW> ring[kRing];
     Tokens cur, next;
+    let_next_grid_start();
+    after_previous_grid();
 #pragma unroll
     for (int u = 0; u < kRing; ++u)
         if (warp + u * kWarps < full) load_w(ring[u], warp + u * kWarps);
@@ -170,8 +172,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) dense_decode_kernel(const FewA
 }
 
 template <bool BF16, bool GATED>
-void launch(const FewArgs& a, cudaStream_t stream) {
-    dense_decode_kernel<BF16, GATED><<<static_cast<unsigned>((a.R + kRows - 1) / kRows), 32 * kWarps, 0, stream>>>(a);
+cudaError_t launch(const FewArgs& a, cudaStream_t stream) {
+    return launch_early(dense_decode_kernel<BF16, GATED>, (a.R + kRows - 1) / kRows, 32 * kWarps, 0, 1, stream, a);
 }
 
 }  // namespace
@@ -196,11 +198,8 @@ cudaError_t launch_few_tokens(const ProductArgs& p, cudaStream_t stream) {
     a.y = p.y[0];
     a.ld_y = p.ld_y;
     a.y_type = p.y_type;
-    if (gated)
-        p.bf16 ? launch<true, true>(a, stream) : launch<false, true>(a, stream);
-    else
-        p.bf16 ? launch<true, false>(a, stream) : launch<false, false>(a, stream);
-    return cudaGetLastError();
+    if (gated) return p.bf16 ? launch<true, true>(a, stream) : launch<false, true>(a, stream);
+    return p.bf16 ? launch<true, false>(a, stream) : launch<false, false>(a, stream);
 }
 
 }  // namespace vnm

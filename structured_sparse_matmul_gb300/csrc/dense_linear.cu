@@ -42,13 +42,18 @@ namespace {
 constexpr int kTile = 128;        // rows of an operand in a CTA's stage
 constexpr int kBlockK = 64;       // elements of K in a stage: 128 bytes
 constexpr int kOperandBytes = kTile * 128;
-constexpr int kChunk = 2048 / kBlockK;
-constexpr int kMaxSplits = 8;
+constexpr int kChunk = 1024 / kBlockK;
+constexpr int kMaxSplits = 8, kMaxPairSplits = 4;
 constexpr int kMaxDevicesDl = 64;
 constexpr int kGroupM = 8;
 
 struct Maps {
     CUtensorMap x[2], w[2];
+};
+
+// Of pairs' outputs and residuals, where their rows start on 16 bytes.
+struct OutMaps {
+    CUtensorMap y[2], g, u, res[2];
 };
 
 struct GemmArgs {
@@ -59,6 +64,8 @@ struct GemmArgs {
     int chunk_kb;     // K blocks of one TMEM sum
     int x_tiles;      // tiles of X's rows, of one product
     int m_tiles, n_tiles, tiles;
+    int stages, stage_bytes;  // of pairs
+    int tile_n;       // of pairs: rows of W of a tile (of a gated pair, half of them Wg's and half Wu's)
     int splits, kb_per_split;
     bool x_t, w_t;
     uint32_t idesc;
@@ -83,6 +90,20 @@ __device__ __forceinline__ void tc_mma_f16_pair(uint32_t d_tmem, uint64_t adesc,
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// Arrive on `bar` of both CTAs of the pair whose first CTA has rank `lead` in the cluster, when the
+// MMAs issued so far are done.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar, int lead) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3 << lead))
+        : "memory");
+}
+
+// Brings `bytes` (a multiple of 16) from `p` (16-byte aligned) into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // An operand's 128 x 64 part of a stage in shared memory, 128B swizzle. K along the rows: 128-byte
@@ -112,92 +133,131 @@ __device__ __forceinline__ float4 ld_shared_v4(uint32_t addr) {
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, float x, float y) {
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
 __device__ __forceinline__ void st_shared_f4(uint32_t addr, float a, float b, float c, float d) {
     st_shared_v4(addr, __float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
 }
 
 // ------------------------------------------------------------------ pairs of CTAs
 
-constexpr int kPairStages = 5;
-constexpr int kPairStageBytes = 2 * kOperandBytes;
+constexpr int kPairRing = 160 * 1024;  // 5 stages of 128 rows of X and 128 of W, or more of less
+constexpr int kPairMaxStages = 6;
 constexpr int kPairHelpers = 4, kPairEpilogue = 8;
 constexpr int kPairThreads = 32 * (kPairHelpers + kPairEpilogue);
-constexpr int kBoxBytes = 8192;  // a warp's staged sums: 32 rows x 64 columns (gated: 32 of each)
-constexpr int kPairSmem = kPairStages * kPairStageBytes + kPairEpilogue * kBoxBytes + 1024;
+// A warp's staged outputs: two boxes of 32 rows x 128 bytes. Of a gated pair a box holds 32 rows x 32 features
+// of Y and of the checkpoints: 2 KB, or 4 with 8-bit ones (two boxes), or 6 with 16-bit ones (one).
+constexpr int kStageOut = 8192;
+constexpr int kPairSmem = kPairRing + kPairEpilogue * kStageOut + 1024;
 static_assert(kPairSmem > 116 * 1024 && kPairSmem <= 226 * 1024, "one CTA an SM: each holds all of its TMEM");
-// Registers of the variant that adds chunks up (128 sums a thread), in warps:
-// 4 x 56 + 8 x 224 = 12 x 168 of the launch.
+// Registers of the variant that adds chunks up: 128 sums and a load of 32 columns do not fit the 168 that
+// 12 warps get; the epilogue takes what the helper warps leave (in warps: 4 x 56 + 8 x 224 = 12 x 168).
+// Where K is split, the code after the sums runs on all warps, and the loads are of 16 columns instead.
 constexpr int kSumLaunchRegs = 168, kSumHelperRegs = 56, kSumAddRegs = 224;
 static_assert(kPairHelpers * kSumHelperRegs + kPairEpilogue * kSumAddRegs == (kPairHelpers + kPairEpilogue) * kSumLaunchRegs,
               "register shares");
 
-// 16-byte piece j of row `row` of a staged box of `pitch` bytes a row.
-__device__ __forceinline__ uint32_t piece(uint32_t buf, int pitch, int row, int j) {
-    return buf + row * pitch + 16 * (j ^ (row & 7));
+// 16-byte piece j of row `row` of a box of RB-byte rows in shared memory, in the order of the tensor memory copies'
+// swizzle for that width (a warp's lanes, a row each, then write to all banks alike).
+template <int RB>
+__device__ __forceinline__ uint32_t box_piece(uint32_t buf, int row, int j) {
+    const int flip = RB == 128 ? row & 7 : RB == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
+    return buf + RB * row + 16 * (j ^ flip);
 }
 
-// Rows m0 .. m0 + 31, columns n0 .. n0 + 63 of Y from their staged sums.
-__device__ __forceinline__ void finish_rows(const OutArgs& o, int seg, uint32_t buf, int64_t m0, int64_t n0, int lane) {
-    const int c = lane & 7, top = lane >> 3;  // columns 8c .., rows top, top + 4, ...
-    const int64_t n = n0 + 8 * c, left = o.R - n;
-    if (o.bias != nullptr || o.act != VNM_ACT_NONE) {
-        float b[8];
+// Piece j and column c of row `row` of a split's fp32 sums, 256 columns a row.
+__device__ __forceinline__ uint32_t sum_piece(uint32_t base, int row, int j) { return base + 1024 * row + 16 * (j ^ (row & 7)); }
+__device__ __forceinline__ uint32_t sum_at(uint32_t base, int row, int c) { return sum_piece(base, row, c >> 2) + 4 * (c & 3); }
+
+// A staged box (the first `rows` rows, `bytes` bytes of each) to memory of any alignment of its elements (G bytes; row 0
+// at `to`), by a warp, a 4-byte word a lane: whole where the rows all start on 4 bytes, else element by element (putting
+// a word of memory together from two staged ones took twice as long). Apart from the epilogue's loop: its
+// code there, fetched for every tile, made the tiles that do not need it 40 % slower.
+template <int RB, int G>
+__device__ __noinline__ void copy_box(uint8_t* to, int64_t pitch, int rows, int bytes, uint32_t buf, int lane) {
+    constexpr int kPer = RB / 4, kRows = 32 / kPer;  // lanes of a row, rows at a time
+    const int w = lane % kPer, r = lane / kPer;
+    const bool words = ((reinterpret_cast<uintptr_t>(to) | static_cast<uintptr_t>(pitch)) & 3) == 0;
+    to += r * pitch + 4 * w;
+    const int left = bytes - 4 * w;
+#pragma unroll 4
+    for (int row0 = 0; row0 < 32; row0 += kRows) {
+        uint32_t x;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(box_piece<RB>(buf, row0 + r, w >> 2) + 4 * (w & 3)) : "memory");
+        const bool here = row0 + r < rows;
+        if (G == 4 || (words && left >= 4)) {
+            if (here && left >= 4) *reinterpret_cast<uint32_t*>(to) = x;
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] = o.bias != nullptr && j < left ? load_any(o.bias, o.bias_type, n + j) : 0.f;
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t p0 = piece(buf, 256, 4 * i + top, 2 * c), p1 = piece(buf, 256, 4 * i + top, 2 * c + 1);
-            const float4 x = ld_shared_v4(p0), y = ld_shared_v4(p1);
-            float v[8] = {x.x + b[0], x.y + b[1], x.z + b[2], x.w + b[3], y.x + b[4], y.y + b[5], y.z + b[6], y.w + b[7]};
-            activate8(o.act, v);
-            st_shared_f4(p0, v[0], v[1], v[2], v[3]);  // (read again by this lane alone)
-            st_shared_f4(p1, v[4], v[5], v[6], v[7]);
-        }
-    }
-    if (left <= 0) return;
-    void* const y = o.y[seg];
-    const void* const res = o.res[seg];
-#pragma unroll 1
-    for (int i = 0; i < 8; i += 4) {
-        float r[4][8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int64_t m = m0 + 4 * (i + k) + top;
-            if (res != nullptr && m < o.T) load8(res, o.y_type, m * o.ld_res + n, o.res_vec, left, r[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int row = 4 * (i + k) + top;
-            const int64_t m = m0 + row;
-            if (m >= o.T) break;
-            const float4 p = ld_shared_v4(piece(buf, 256, row, 2 * c)), q = ld_shared_v4(piece(buf, 256, row, 2 * c + 1));
-            float v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-            if (res != nullptr) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] += r[k][j];
+            for (int e = 0; e < 4; e += G) {
+                if (!here || e >= left) continue;
+                if (G == 2)
+                    *reinterpret_cast<uint16_t*>(to + e) = static_cast<uint16_t>(x >> (8 * e));
+                else
+                    to[e] = static_cast<uint8_t>(x >> (8 * e));
             }
-            store8(y, o.y_type, m * o.ld_y + n, o.y_vec, left, v);
         }
+        to += kRows * pitch;
     }
 }
 
-template <bool GATED, bool SUM>
+// A staged box of elements of G bytes to rows m0 .., columns n0 .. n0 + RB / G - 1 (below `end`) of a matrix. All lanes have
+// written their rows.
+template <int RB, int G, bool ALIGNED>
+__device__ __forceinline__ void emit_box(const CUtensorMap* tm, bool tma, void* p, int64_t ld, int64_t m0, int64_t n0, int64_t T,
+                                         int64_t end, uint32_t buf, int lane) {
+    if (m0 >= T || n0 >= end) return;
+    if (ALIGNED || tma) {
+        if (lane == 0) tma_store_2d(tm, static_cast<int32_t>(n0), static_cast<int32_t>(m0), buf);
+    } else {
+        copy_box<RB, G>(static_cast<uint8_t*>(p) + (m0 * ld + n0) * G, ld * G, static_cast<int>(min(static_cast<int64_t>(32), T - m0)),
+                        static_cast<int>(min(static_cast<int64_t>(RB), (end - n0) * G)), buf, lane);
+    }
+}
+
+__device__ __forceinline__ bool all_vec(const OutArgs& o) { return o.y_vec && o.res_vec && o.keep_vec; }
+
+// A row's 16 columns of the residual as they are stored.
+struct Raw16 {
+    Raw8 h[2];
+};
+
+// SUM: the sums are taken out every chunk_kb K blocks and added up in registers; SPLIT: K is split over
+// the pairs of a cluster, one tile a cluster; ALIGNED: the outputs' and the residual's rows start on 16 bytes (the
+// code for others, in the same loop, costs the aligned ones a third of their epilogue).
+template <bool GATED, bool SUM, bool SPLIT, bool ALIGNED>
 __global__ void __launch_bounds__(kPairThreads, 1)
-    dense_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmArgs a) {
-    constexpr int ST = kPairStages;
+    dense_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ OutMaps outs, const __grid_constant__ GemmArgs a) {
+    static_assert(SUM || !SPLIT, "a split's sums are held in registers until the ring is free");
+    constexpr int LD = SPLIT ? 16 : 32;
+    constexpr bool kSplitRegs = SUM && !SPLIT;
     constexpr int kTileN = GATED ? 128 : 256;  // columns of Y of a tile
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full_bar[ST];   // the stage has landed in both CTAs (the first CTA's)
-    __shared__ __align__(8) uint64_t empty_bar[ST];  // its MMAs are done
+    __shared__ __align__(8) uint64_t full_bar[kPairMaxStages];   // the stage has landed in both CTAs (the first CTA's)
+    __shared__ __align__(8) uint64_t empty_bar[kPairMaxStages];  // its MMAs are done
     __shared__ __align__(8) uint64_t accf_bar[2];    // the TMEM sum is complete
     __shared__ __align__(8) uint64_t acce_bar[2];    // and has been read by both CTAs (the first CTA's)
+    // of each epilogue warp's two output boxes: the residual's box has landed in it
+    __shared__ __align__(8) uint64_t res_bar[GATED ? 1 : kPairEpilogue][2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
 
     const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int ST = a.stages, stage_bytes = a.stage_bytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(blockIdx.x & 1);
-    const int tile0 = static_cast<int>(blockIdx.x >> 1), tile_step = static_cast<int>(gridDim.x >> 1);
+    const int rank = static_cast<int>(blockIdx.x & 1);  // of the pair
+    const int cluster = SPLIT ? 2 * a.splits : 2;       // CTAs of the cluster
+    const int pair = SPLIT ? (static_cast<int>(blockIdx.x) % cluster) >> 1 : 0, lead_rank = 2 * pair;
+    const int tile0 = static_cast<int>(blockIdx.x) / cluster;
+    const int tile_step = SPLIT ? a.tiles : static_cast<int>(gridDim.x >> 1);
+    const int kb_first = SPLIT ? min(a.total_kb, pair * a.kb_per_split) : 0;
+    const int kb_last = SPLIT ? min(a.total_kb, kb_first + a.kb_per_split) : a.total_kb;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
@@ -207,6 +267,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&accf_bar[s]), 1);
             mbar_init(smem_u32(&acce_bar[s]), 2 * kPairEpilogue);
+            for (int w = 0; !GATED && w < kPairEpilogue; ++w) mbar_init(smem_u32(&res_bar[w][s]), 1);
         }
         abort_flag = 0;
         fence_barrier_init();
@@ -214,12 +275,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (warp == 1) tmem_alloc_group<2>(smem_u32(&tmem_slot), 512);
     tc_fence_before_sync();
     __syncthreads();
-    cluster_sync_all();  // both CTAs' barriers and TMEM exist
+    cluster_sync_all();  // the CTAs' barriers and TMEM exist
     tc_fence_after_sync();
+    let_next_grid_start();
+    after_previous_grid();
     const uint32_t tmem = tmem_slot;
     volatile int* abort = &abort_flag;
 
-    if (SUM && warp < kPairHelpers) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSumHelperRegs));
+    if (kSplitRegs && warp < kPairHelpers) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSumHelperRegs));
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
         int it = 0, slot = 0;
@@ -230,8 +293,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             tile_at(a, tile, mt, nt);
             const int seg = a.kind == kTwoByRows && mt >= a.x_tiles ? 1 : 0;
             const int xrow = ((mt - seg * a.x_tiles) * 2 + rank) * kTile;
-            const int wrow = GATED ? nt * kTile : nt * 256 + rank * kTile;
-            for (int kb = 0; kb < a.total_kb; ++kb, ++it) {
+            const int wrows = a.tile_n / 2, wrow = GATED ? nt * wrows : nt * a.tile_n + rank * wrows;
+            const uint32_t wbytes = a.w_t ? (wrows > 64 ? 16384 : 8192) : wrows * 128;
+            for (int kb = kb_first; kb < kb_last; ++kb, ++it) {
                 if (!mbar_wait_warp(smem_u32(&empty_bar[slot]), phase, abort)) {
                     run = false;
                     break;
@@ -241,11 +305,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     const CUtensorMap* tx = &maps.x[second || seg];
                     const CUtensorMap* tw = &maps.w[GATED ? rank : second];
                     const int k = (second ? kb - a.num_kb : kb) * kBlockK;
-                    const uint32_t sx = smem_base + slot * kPairStageBytes, sw = sx + kOperandBytes;
-                    const uint32_t fb = smem_u32(&full_bar[slot]), lead = dsmem_map(fb, 0);
+                    const uint32_t sx = smem_base + slot * stage_bytes, sw = sx + kOperandBytes;
+                    const uint32_t fb = smem_u32(&full_bar[slot]), lead = dsmem_map(fb, lead_rank);
                     // the second CTA's bytes may arrive before the first CTA expects them: the
                     // phase cannot end before that CTA's own arrival
-                    if (rank == 0) mbar_arrive_expect_tx(fb, 2 * kPairStageBytes);
+                    if (rank == 0) mbar_arrive_expect_tx(fb, 2 * (kOperandBytes + wbytes));
                     if (a.x_t) {
                         tma_load_2d_pair(sx, tx, xrow, k, lead);
                         tma_load_2d_pair(sx + 8192, tx, xrow + 64, k, lead);
@@ -254,7 +318,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                     if (a.w_t) {
                         tma_load_2d_pair(sw, tw, wrow, k, lead);
-                        tma_load_2d_pair(sw + 8192, tw, wrow + 64, k, lead);
+                        if (wrows > 64) tma_load_2d_pair(sw + 8192, tw, wrow + 64, k, lead);
                     } else {
                         tma_load_2d_pair(sw, tw, k, wrow, lead);
                     }
@@ -286,8 +350,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         uint32_t phase = 0, acc_phase = 1;
         bool run = rank == 0;
         for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
-            for (int kb0 = 0; kb0 < a.total_kb && run; kb0 += a.chunk_kb) {
-                const int kb1 = min(a.total_kb, kb0 + a.chunk_kb);
+            for (int kb0 = kb_first; kb0 < kb_last && run; kb0 += a.chunk_kb) {
+                const int kb1 = min(kb_last, kb0 + a.chunk_kb);
                 if (!mbar_wait_warp(smem_u32(&acce_bar[acc]), acc_phase, abort)) {
                     run = false;
                     break;
@@ -299,13 +363,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                     tc_fence_after_sync();
                     if (elect_one()) {
-                        const uint64_t off = static_cast<uint64_t>((slot * kPairStageBytes) >> 4);
+                        const uint64_t off = static_cast<uint64_t>((slot * stage_bytes) >> 4);
 #pragma unroll
                         for (uint32_t s = 0; s < 4; ++s)
                             tc_mma_f16_pair(tmem + acc * 256, xdesc + off + s * xstep, wdesc + off + s * wstep, a.idesc,
                                             kb > kb0 || s > 0 ? 1u : 0u);
-                        tc_commit_group<2>(smem_u32(&empty_bar[slot]));
-                        if (kb + 1 == kb1) tc_commit_group<2>(smem_u32(&accf_bar[acc]));
+                        tc_commit_pair(smem_u32(&empty_bar[slot]), lead_rank);
+                        if (kb + 1 == kb1) tc_commit_pair(smem_u32(&accf_bar[acc]), lead_rank);
                     }
                     __syncwarp();
                     if (++slot == ST) {
@@ -323,13 +387,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (it > 0) mbar_drain(smem_u32(&empty_bar[(it - 1) % ST]), static_cast<uint32_t>((it - 1) / ST) & 1u);
     } else if (warp >= kPairHelpers) {
         // ------------------------------------------------ epilogue
-        if (SUM) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumAddRegs));
+        if (kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumAddRegs));
+        const OutArgs& o = a.o;
         const int quarter = warp & 3, half = (warp - kPairHelpers) >> 2;  // TMEM lanes 32 quarter ..; columns
         const uint32_t lane_addr = static_cast<uint32_t>(32 * quarter) << 16;
-        const uint32_t acce_lead = dsmem_map(smem_u32(&acce_bar[0]), 0);
-        const uint32_t buf = smem_base + ST * kPairStageBytes + (warp - kPairHelpers) * kBoxBytes;
-        int acc = 0;
-        uint32_t acc_phase = 0;
+        const uint32_t acce_lead = dsmem_map(smem_u32(&acce_bar[0]), lead_rank);
+        const uint32_t stage = smem_base + kPairRing + (warp - kPairHelpers) * kStageOut;
+        int acc = 0, box = 0;
+        uint32_t acc_phase = 0, res_phase = 0, res_pending = 0;
         bool run = true;
         auto wait_sum = [&] {
             run = mbar_wait_warp(smem_u32(&accf_bar[acc]), acc_phase, abort);
@@ -345,187 +410,426 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 acc_phase ^= 1;
             }
         };
-        // 32 of the lane's sums from column j of a staged row of 256 bytes on
-        auto stage32 = [&](const uint32_t (&v)[32], int j) {
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                st_shared_v4(piece(buf, 256, lane, j + u), v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-        };
         for (int tile = tile0; tile < a.tiles && run; tile += tile_step) {
             int mt, nt;
             tile_at(a, tile, mt, nt);
             const int seg = a.kind == kTwoByRows && mt >= a.x_tiles ? 1 : 0;
-            const int64_t m0 = static_cast<int64_t>((mt - seg * a.x_tiles) * 2 + rank) * kTile + 32 * quarter;
-            const int64_t n0 = static_cast<int64_t>(nt) * kTileN + half * (kTileN / 2);
+            const int64_t m0 = static_cast<int64_t>((mt - seg * a.x_tiles) * 2 + rank) * kTile + 32 * quarter, m = m0 + lane;
+            // this warp's columns of the tile (a gated pair's features): first .. last - 1
+            const int cols = GATED ? a.tile_n / 2 : a.tile_n, first = half * (kTileN / 2), last = min(cols, first + kTileN / 2);
+            const int64_t n_tile = static_cast<int64_t>(nt) * cols, end = min(o.R, n_tile + cols);
+            const void* const res = GATED || SPLIT ? nullptr : o.res[seg];
+            if (!GATED && res != nullptr && o.res_vec && m < o.T && n_tile + first < end) {
+                // the residual's row is on its way to L2 while the MMAs run
+                const int size = o.y_type == VNM_F32 ? 4 : 2;
+                const uint32_t bytes =
+                    static_cast<uint32_t>(min(static_cast<int64_t>(kTileN / 2), end - n_tile - first) * size) & ~15u;
+                if (bytes > 0) prefetch_l2(static_cast<const uint8_t*>(res) + (m * o.ld_res + n_tile + first) * size, bytes);
+            }
+            auto fetch = [&](int c) {  // columns c .. c + 15 of the tile
+                Raw16 r;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const Cols at{n_tile + c + 8 * h, end, 1, o.res_vec};
+                    if (res != nullptr && m < o.T && !at.none())
+                        r.h[h] = load_raw8(res, o.y_type, m * o.ld_res, at);
+                    else
+                        r.h[h] = Raw8{};
+                }
+                return r;
+            };
+            const bool f32 = o.y_type == VNM_F32, bf16 = o.y_type == VNM_BF16, res_tma = res != nullptr && (ALIGNED || o.res_vec);
+            const int box_cols = f32 ? 32 : 64;
+            // the residual's box from column c on, into output box `at`, whose last store has read it; the outputs then
+            // take its place
+            auto request = [&](int c, int at) {
+                if (!res_tma || m0 >= o.T || n_tile + c >= end) return;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_wait_all_read();
+                    const uint32_t bar = smem_u32(&res_bar[GATED ? 0 : warp - kPairHelpers][at & 1]);
+                    mbar_arrive_expect_tx(bar, 4096);
+                    tma_load_2d(stage + 4096 * (at & 1), &outs.res[seg], static_cast<int32_t>(n_tile + c), static_cast<int32_t>(m0), bar);
+                }
+                __syncwarp();
+                res_pending |= 1u << (at & 1);
+            };
+            if (!GATED && first < last) request(first, box);
+            Scales scale{1.f, 1.f, 1.f, 1.f};
             if constexpr (SUM) {
+                // half 0 the first 128 columns of the accumulator, half 1 the others; of a gated pair that is not
+                // split, 64 of G's and the same of U's
                 float sum[128];
 #pragma unroll
                 for (int c = 0; c < 128; ++c) sum[c] = 0.f;
-                for (int kb0 = 0; kb0 < a.total_kb; kb0 += a.chunk_kb) {
+                const auto column = [&](int c) { return half * (GATED && !SPLIT ? 64 : 128) + c + (GATED && !SPLIT && c >= 64 ? 64 : 0); };
+                for (int kb0 = kb_first; kb0 < kb_last; kb0 += a.chunk_kb) {
                     if (!wait_sum()) break;
+                    const uint32_t taddr = tmem + lane_addr + acc * 256;
+#pragma unroll
+                    for (int c = 0; c < 128; c += LD) {
+                        uint32_t v[LD];
+                        tmem_ld(taddr + column(c), v);
+                        tmem_wait_ld(v);
+#pragma unroll
+                        for (int j = 0; j < LD; ++j) sum[c + j] += __uint_as_float(v[j]);
+                    }
+                    if (SPLIT || kb0 + a.chunk_kb < kb_last) release();
+                }
+                if (!run) break;
+                if constexpr (SPLIT) {
+                    // the ring is free: this cluster's MMAs are done with it
+                    const int row = 32 * quarter + lane;
+#pragma unroll
+                    for (int u = 0; u < 32; ++u)
+                        st_shared_f4(sum_piece(smem_base, row, 32 * half + u), sum[4 * u], sum[4 * u + 1], sum[4 * u + 2],
+                                     sum[4 * u + 3]);
+                } else {
+                    if constexpr (GATED) {
+                        if (o.keep == kKeep8) {
+                            // the row's largest magnitudes over the tile's 128 features, a group of the 8-bit
+                            // form (features past the edge are zeros): this warp's half and the other's
+                            float g = 0.f, u = 0.f;
+#pragma unroll
+                            for (int c = 0; c < 64; ++c) {
+                                g = max_magnitude(g, sum[c]);
+                                u = max_magnitude(u, sum[64 + c]);
+                            }
+                            const uint32_t other = smem_base + kPairRing + ((warp - kPairHelpers) ^ 4) * kStageOut;
+                            if (lane == 0) tma_store_wait_all_read();
+                            __syncwarp();
+                            st_shared_v2(stage + 8 * lane, g, u);
+                            named_barrier(1 + quarter, 64);
+                            g = max_magnitude(g, ld_shared_f32(other + 8 * lane));
+                            u = max_magnitude(u, ld_shared_f32(other + 8 * lane + 4));
+                            named_barrier(1 + quarter, 64);  // (read before the boxes are written)
+                            scale = scales_of(o, make_float2(g, u), m, nt, half == 0 && m < o.T);
+                        }
+                    }
+                    // back to where the last chunk's sums were, from which the outputs are made as without chunks
+                    const uint32_t taddr = tmem + lane_addr + acc * 256;
 #pragma unroll
                     for (int c = 0; c < 128; c += 32) {
                         uint32_t v[32];
-                        tmem_ld(tmem + lane_addr + acc * 256 + half * 128 + c, v);
-                        tmem_wait_ld(v);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) sum[c + j] += __uint_as_float(v[j]);
+                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(sum[c + j]);
+                        tmem_st(taddr + column(c), v);
                     }
-                    release();
-                }
-                if (!run) break;
-#pragma unroll
-                for (int c = 0; c < 128; c += 64) {
-#pragma unroll
-                    for (int u = 0; u < 16; ++u)
-                        st_shared_f4(piece(buf, 256, lane, u), sum[c + 4 * u], sum[c + 4 * u + 1], sum[c + 4 * u + 2],
-                                     sum[c + 4 * u + 3]);
-                    __syncwarp();
-                    finish_rows(a.o, seg, buf, m0, n0 + c, lane);
-                    __syncwarp();
-                }
-            } else if constexpr (GATED) {
-                if (!wait_sum()) break;
-                const uint32_t taddr = tmem + lane_addr + acc * 256;
-                const int64_t m = m0 + lane;
-                float gs = 1.f, ginv = 1.f, us = 1.f, uinv = 1.f;
-                if (a.o.keep == kKeep8) {
-                    // the row's largest magnitudes over the tile's 128 columns, a group of the 8-bit
-                    // form (columns past the edge are zeros); both halves read them all
-                    float top[2] = {0.f, 0.f};
-#pragma unroll 1
-                    for (int c = 0; c < 256; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld(taddr + c, v);
-                        tmem_wait_ld(v);
-                        float t = c < 128 ? top[0] : top[1];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) t = max_magnitude(t, __uint_as_float(v[j]));
-                        if (c < 128)
-                            top[0] = t;
-                        else
-                            top[1] = t;
-                    }
-                    gs = group_scale(top[0], a.o.e5m2, ginv);
-                    us = group_scale(top[1], a.o.e5m2, uinv);
-                    if (half == 0 && m < a.o.T) {
-                        a.o.g.s[m * a.o.g.s_rs + nt * a.o.g.s_cs] = gs;
-                        a.o.u.s[m * a.o.u.s_rs + nt * a.o.u.s_cs] = us;
-                    }
-                }
-#pragma unroll 1
-                for (int c = 0; c < 64; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld(taddr + half * 64 + c, v);
-                    tmem_wait_ld(v);
-                    stage32(v, 0);
-                    tmem_ld(taddr + 128 + half * 64 + c, v);
-                    tmem_wait_ld(v);
-                    stage32(v, 8);
-                    if (c + 32 == 64) release();
-                    __syncwarp();
-                    const int q = lane & 3, first = lane >> 2;  // features 8q .., rows first, first + 8, ...
-#pragma unroll 1
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = 8 * i + first;
-                        const float4 p0 = ld_shared_v4(piece(buf, 256, row, 2 * q)), p1 = ld_shared_v4(piece(buf, 256, row, 2 * q + 1));
-                        const float4 q0 = ld_shared_v4(piece(buf, 256, row, 8 + 2 * q)),
-                                     q1 = ld_shared_v4(piece(buf, 256, row, 9 + 2 * q));
-                        float g[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-                        const float u[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-                        const float rgs = __shfl_sync(0xFFFFFFFFu, gs, row), rgi = __shfl_sync(0xFFFFFFFFu, ginv, row);
-                        const float rus = __shfl_sync(0xFFFFFFFFu, us, row), rui = __shfl_sync(0xFFFFFFFFu, uinv, row);
-                        if (m0 + row < a.o.T) finish_gated8(a.o, m0 + row, n0 + c + 8 * q, g, u, rgs, rgi, rus, rui);
-                    }
-                    __syncwarp();
-                }
-            } else {
-                if (!wait_sum()) break;
-                const uint32_t taddr = tmem + lane_addr + acc * 256 + half * 128;
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 64) {
-                    uint32_t v[32];
-                    tmem_ld(taddr + c, v);
-                    tmem_wait_ld(v);
-                    stage32(v, 0);
-                    tmem_ld(taddr + c + 32, v);
-                    tmem_wait_ld(v);
-                    stage32(v, 8);
-                    if (c + 64 == 128) release();
-                    __syncwarp();
-                    finish_rows(a.o, seg, buf, m0, n0 + c, lane);
-                    __syncwarp();
+                    tmem_wait_st();
                 }
             }
+            if constexpr (SPLIT) continue;
+            uint32_t next[16], next_u[16];
+            if constexpr (!GATED) {
+                float b[4];  // the bias of columns first + lane, + 32, ...
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t n = n_tile + first + 32 * j + lane;
+                    b[j] = o.bias != nullptr && n < end ? load_any(o.bias, o.bias_type, n) : 0.f;
+                }
+                if (!SUM && !wait_sum()) break;
+                const uint32_t taddr = tmem + lane_addr + acc * 256;
+                if (first < last) tmem_ld(taddr + first, next);
+#pragma unroll 1
+                for (int c = first; c < last; c += 16) {
+                    float v[16];
+                    Raw16 r;  // (a residual of another alignment: by the lanes themselves)
+                    if constexpr (!ALIGNED) {
+                        if (res != nullptr && !res_tma) r = fetch(c);
+                    }
+                    tmem_wait_ld(next);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(next[j]);
+                    if (c + 16 < last)
+                        tmem_ld(taddr + c + 16, next);
+                    else
+                        release();
+                    const int in = c & (box_cols - 1);  // the columns' place in their box
+                    const uint32_t buf = stage + 4096 * (box & 1);
+                    const bool landed = res_tma && m0 < o.T && n_tile + c - in < end;
+                    if (in == 0) {
+                        if (landed) {
+                            if (!mbar_wait_warp(smem_u32(&res_bar[GATED ? 0 : warp - kPairHelpers][box & 1]), res_phase >> (box & 1) & 1u, abort)) {
+                                run = false;
+                                break;
+                            }
+                            res_phase ^= 1u << (box & 1);
+                            res_pending &= ~(1u << (box & 1));
+                        } else if (lane == 0) {
+                            tma_store_wait_read();
+                        }
+                        __syncwarp();
+                    }
+                    if (o.bias != nullptr) {
+                        const int k = (c - first) >> 5;
+                        const float mine = k == 0 ? b[0] : k == 1 ? b[1] : k == 2 ? b[2] : b[3];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] += __shfl_sync(0xFFFFFFFFu, mine, ((c - first) & 16) + j);
+                    }
+                    activate_all(o.act, v);
+                    if (landed && f32) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const float4 w = ld_shared_v4(box_piece<128>(buf, lane, in / 4 + u));
+                            v[4 * u] += w.x, v[4 * u + 1] += w.y, v[4 * u + 2] += w.z, v[4 * u + 3] += w.w;
+                        }
+                    } else if (landed || (!ALIGNED && res != nullptr && !res_tma)) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float w[8];
+                            if (ALIGNED || landed) {
+                                const float4 q = ld_shared_v4(box_piece<128>(buf, lane, in / 8 + h));
+                                widen8(make_uint4(__float_as_uint(q.x), __float_as_uint(q.y), __float_as_uint(q.z), __float_as_uint(q.w)),
+                                       bf16, w);
+                            } else {
+                                widen_raw8(r.h[h], o.y_type, w);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) v[8 * h + j] += w[j];
+                        }
+                    }
+                    if (f32) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            st_shared_f4(box_piece<128>(buf, lane, in / 4 + u), v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+                    } else {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) w[u] = bf16 ? to_bf16x2(v[2 * u], v[2 * u + 1]) : to_f16x2(v[2 * u], v[2 * u + 1]);
+                        st_shared_v4(box_piece<128>(buf, lane, in / 8), w[0], w[1], w[2], w[3]);
+                        st_shared_v4(box_piece<128>(buf, lane, in / 8 + 1), w[4], w[5], w[6], w[7]);
+                    }
+                    // (half way, so that the last box's store has read the other one)
+                    if (in == box_cols / 2 && c - in + box_cols < last) request(c - in + box_cols, box + 1);
+                    if (in + 16 < box_cols) continue;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (f32)
+                        emit_box<128, 4, ALIGNED>(&outs.y[seg], o.y_tma, o.y[seg], o.ld_y, m0, n_tile + c - 16, o.T, end, buf, lane);
+                    else
+                        emit_box<128, 2, ALIGNED>(&outs.y[seg], o.y_tma, o.y[seg], o.ld_y, m0, n_tile + c - 48, o.T, end, buf, lane);
+                    if (lane == 0) tma_store_commit();
+                    ++box;
+                }
+            } else {
+                if (!SUM && !wait_sum()) break;
+                const uint32_t taddr = tmem + lane_addr + acc * 256;
+                if (first < last) {
+                    tmem_ld(taddr + first, next);
+                    tmem_ld(taddr + cols + first, next_u);
+                }
+                const bool twice = o.keep != kKeep16;
+#pragma unroll 1
+                for (int c = first; c < last; c += 16) {
+                    float g[16], u[16];
+                    tmem_wait_ld(next);
+                    tmem_wait_ld(next_u);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        g[j] = __uint_as_float(next[j]);
+                        u[j] = __uint_as_float(next_u[j]);
+                    }
+                    if (c + 16 < last) {
+                        tmem_ld(taddr + c + 16, next);
+                        tmem_ld(taddr + cols + c + 16, next_u);
+                    } else {
+                        release();
+                    }
+                    const int in = c & 16;
+                    const uint32_t buf = stage + (twice ? 4096 * (box & 1) : 0);
+                    if (in == 0) {
+                        if (lane == 0) {
+                            if (twice)
+                                tma_store_wait_read();
+                            else
+                                tma_store_wait_all_read();
+                        }
+                        __syncwarp();
+                    }
+                    auto stage16 = [&](uint32_t to, const float (&v)[16]) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) w[j] = bf16 ? to_bf16x2(v[2 * j], v[2 * j + 1]) : to_f16x2(v[2 * j], v[2 * j + 1]);
+                        st_shared_v4(box_piece<64>(to, lane, in / 8), w[0], w[1], w[2], w[3]);
+                        st_shared_v4(box_piece<64>(to, lane, in / 8 + 1), w[4], w[5], w[6], w[7]);
+                    };
+                    auto stage8 = [&](uint32_t to, const float (&v)[16], float s, float inv) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = to_fp8x4(quotient(v[4 * j], s, inv), quotient(v[4 * j + 1], s, inv),
+                                            quotient(v[4 * j + 2], s, inv), quotient(v[4 * j + 3], s, inv), o.e5m2);
+                        st_shared_v4(box_piece<32>(to, lane, in / 16), w[0], w[1], w[2], w[3]);
+                    };
+                    if (o.keep == kKeep16) {
+                        stage16(buf + 2048, g);
+                        stage16(buf + 4096, u);
+                    } else if (o.keep == kKeep8) {
+                        stage8(buf + 2048, g, scale.g, scale.g_inv);
+                        stage8(buf + 3072, u, scale.u, scale.u_inv);
+                    }
+                    activate_all(o.act, g);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) g[j] *= u[j];
+                    stage16(buf, g);
+                    if (in == 0) continue;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    const int64_t n0 = n_tile + c - 16;
+                    emit_box<64, 2, ALIGNED>(&outs.y[0], o.y_tma, o.y[0], o.ld_y, m0, n0, o.T, end, buf, lane);
+                    if (o.keep == kKeep16) {
+                        emit_box<64, 2, ALIGNED>(&outs.g, o.keep_tma, o.g.p, o.g.ld, m0, n0, o.T, end, buf + 2048, lane);
+                        emit_box<64, 2, ALIGNED>(&outs.u, o.keep_tma, o.u.p, o.u.ld, m0, n0, o.T, end, buf + 4096, lane);
+                    } else if (o.keep == kKeep8) {
+                        emit_box<32, 1, ALIGNED>(&outs.g, o.keep_tma, o.g.p, o.g.ld, m0, n0, o.T, end, buf + 2048, lane);
+                        emit_box<32, 1, ALIGNED>(&outs.u, o.keep_tma, o.u.p, o.u.ld, m0, n0, o.T, end, buf + 3072, lane);
+                    }
+                    if (lane == 0) tma_store_commit();
+                    ++box;
+                }
+            }
+            if (first >= last) release();
         }
+        if (lane == 0) tma_store_wait();
+        for (int at = 0; at < 2; ++at)  // (after a wait that ran out) copies in flight must land before the CTA exits
+            if (res_pending >> at & 1u) mbar_drain(smem_u32(&res_bar[GATED ? 0 : warp - kPairHelpers][at]), res_phase >> at & 1u);
     }
 
     tc_fence_before_sync();
     __syncthreads();
-    cluster_sync_all();  // neither CTA leaves while the other's arrivals or MMAs may reach it
-    if (threadIdx.x == 0 && abort_flag) record_error(a.status ? a.status : g_status, VNM_ERR_TIMEOUT, 13);
+    cluster_sync_all();  // no CTA leaves while the others' arrivals, MMAs or reads may reach it
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc_group<2>(tmem, 512);
     }
+    if constexpr (SPLIT) {
+        // add the pairs' sums, in their order, each pair a share of the rows
+        const OutArgs& o = a.o;
+        const bool vec = all_vec(o);
+        int mt, nt;
+        tile_at(a, tile0, mt, nt);
+        const int seg = a.kind == kTwoByRows && mt >= a.x_tiles ? 1 : 0;
+        const int64_t m0 = static_cast<int64_t>((mt - seg * a.x_tiles) * 2 + rank) * kTile;
+        const int share = (kTile + a.splits - 1) / a.splits, row0 = pair * share, row1 = min(kTile, row0 + share);
+        constexpr int kLanes = GATED ? 16 : 32, kRowsAtOnce = 32 / kLanes;  // of a row
+        const int q = lane & (kLanes - 1);
+        const int local = vec ? 8 * q : q, step = vec ? 1 : kLanes;
+        const Cols c{static_cast<int64_t>(nt) * kTileN + local, o.R, step, vec};
+        float b[8];
+        bias8(o, c, b);
+#pragma unroll 1
+        for (int base = row0 + kRowsAtOnce * warp; base < row1; base += kRowsAtOnce * (kPairThreads / 32)) {
+            const int row = base + lane / kLanes;
+            const int64_t t = m0 + row;
+            const bool here = row < row1 && t < o.T;
+            float v[GATED ? 2 : 1][8];
+            Raw8 r;
+            if (!GATED && here && o.res[seg] != nullptr && !c.none()) r = load_raw8(o.res[seg], o.y_type, t * o.ld_res, c);
+#pragma unroll
+            for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+                const int at = min(row, kTile - 1), col = 128 * h + local;
+                float w[kMaxPairSplits][8];  // all in flight at once
+#pragma unroll
+                for (int s = 0; s < kMaxPairSplits; ++s) {
+                    if (s >= a.splits) break;
+                    const uint32_t from = dsmem_map(smem_base, 2 * s + rank);
+                    if (vec) {
+                        const float4 x = dsmem_ld_v4(sum_piece(from, at, col >> 2)), y = dsmem_ld_v4(sum_piece(from, at, (col >> 2) + 1));
+                        w[s][0] = x.x, w[s][1] = x.y, w[s][2] = x.z, w[s][3] = x.w;
+                        w[s][4] = y.x, w[s][5] = y.y, w[s][6] = y.z, w[s][7] = y.w;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) w[s][j] = dsmem_ld_f32(sum_at(from, at, col + step * j));
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[h][j] = w[0][j];
+#pragma unroll
+                    for (int s = 1; s < kMaxPairSplits; ++s)
+                        if (s < a.splits) v[h][j] += w[s][j];
+                }
+            }
+            if constexpr (GATED) {
+                Scales s{1.f, 1.f, 1.f, 1.f};
+                if (o.keep == kKeep8) s = scales_of(o, largest_of<16>(v[0], v[1]), t, nt, here && q == 0);
+                if (here && !c.none()) {
+                    keep_gated8(o, t, c, v[0], v[1], s);
+                    finish_gated8(o, t, c, v[0], v[1]);
+                }
+            } else if (here) {
+                finish8(o, seg, t, c, v[0], b, r);
+            }
+        }
+        cluster_sync_all();  // no CTA leaves while others read its sums
+    }
+    if (threadIdx.x == 0 && abort_flag) record_error(a.status ? a.status : g_status, VNM_ERR_TIMEOUT, 13);
 }
 
 // ------------------------------------------------------------------ narrow tiles
 
-template <int BN, bool GATED>
+// Of a gated pair a tile's 128 rows are 64 of Wg's and the same 64 of Wu's.
+template <int BN>
 struct NarrowCfg {
-    static constexpr int kWBytes = (GATED ? 2 : 1) * kOperandBytes;
-    static constexpr int kStageBytes = kWBytes + BN * 128;
-    // two CTAs an SM, whose waits overlap, where their rings are deep enough
-    static constexpr int kCtas = GATED && BN >= 64 ? 1 : 2;
-    static constexpr int kStages = GATED ? (BN >= 128 ? 4 : BN == 64 ? 5 : 3) : BN == 128 ? 3 : BN == 64 ? 4 : 5;
-    static constexpr int kTmemCols = 2 * BN;  // two sums: of g and of u, or of two chunks
+    static constexpr int kStageBytes = kOperandBytes + BN * 128;
+    static constexpr int kStages = BN == 128 ? 3 : BN == 64 ? 4 : 5;
+    static constexpr int kTmemCols = 2 * BN;  // two chunks' sums
     static constexpr int kThreads = 192;
     static constexpr int kSmem = kStages * kStageBytes + 1024;
-    static constexpr int kPartBytes = (GATED ? 2 : 1) * kTile * BN * 4;
-    static_assert(kPartBytes <= kStages * kStageBytes, "the CTA's sums fit the stage ring");
-    static_assert(kCtas == 2 ? 2 * (kSmem + 2048) <= 228 * 1024 : kSmem > 116 * 1024 && kSmem <= 226 * 1024, "shared memory");
-    static_assert(kCtas * kTmemCols <= 512 && kTmemCols >= 32, "TMEM of the CTAs that share an SM");
+    static_assert(kTile * BN * 4 <= kStages * kStageBytes, "the CTA's sums fit the stage ring");
+    // two CTAs an SM, whose waits overlap
+    static_assert(2 * (kSmem + 4096) <= 228 * 1024 && 2 * kTmemCols <= 512 && kTmemCols >= 32, "shared memory and TMEM of two CTAs");
 };
 
 template <int BN, bool GATED>
-__global__ void __launch_bounds__(NarrowCfg<BN, GATED>::kThreads, NarrowCfg<BN, GATED>::kCtas)
+__global__ void __launch_bounds__(NarrowCfg<BN>::kThreads, 2)
     dense_narrow_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmArgs a) {
-    using Cfg = NarrowCfg<BN, GATED>;
+    using Cfg = NarrowCfg<BN>;
     constexpr int ST = Cfg::kStages;
+    constexpr int kFeatures = GATED ? 64 : 128;  // columns of Y of a tile
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[ST], empty_bar[ST];
     __shared__ __align__(8) uint64_t accf_bar[2], acce_bar[2];
+    __shared__ float2 tops[GATED ? BN : 1];  // of each token: G's and U's largest magnitudes over the tile
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
 
     const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    float* const part = reinterpret_cast<float*>(smem_raw + (smem_base - smem_u32(smem_raw)));  // [g, u][BN][kTile], over the ring
+    float* const part = reinterpret_cast<float*>(smem_raw + (smem_base - smem_u32(smem_raw)));  // [BN][kTile], over the ring
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(blockIdx.x) % a.splits, tile = static_cast<int>(blockIdx.x) / a.splits;
-    // tiles of tokens fastest: the CTAs that run together share W's tiles
-    const int mt = tile / a.n_tiles, nt = tile - mt * a.n_tiles;
+    // CTAs of a cluster: the splits of a tile, or (8-bit checkpoints) of two tiles, which share a group's 128 features
+    const bool twin = GATED && a.o.keep == kKeep8;
+    const int rank = static_cast<int>(blockIdx.x) % a.splits;
+    int mt, nt;  // tiles of W's rows and of tokens; those fastest: the CTAs that run together share W's tiles
+    if (twin) {
+        const int two = static_cast<int>(blockIdx.x) / (2 * a.splits);
+        mt = 2 * (two / a.n_tiles) + static_cast<int>(blockIdx.x) / a.splits % 2;
+        nt = two % a.n_tiles;
+    } else {
+        const int tile = static_cast<int>(blockIdx.x) / a.splits;
+        mt = tile / a.n_tiles;
+        nt = tile % a.n_tiles;
+    }
     const int seg = a.kind == kTwoByRows && nt >= a.x_tiles ? 1 : 0;
-    const int xrow = (nt - seg * a.x_tiles) * BN, wrow = mt * kTile;
-    const int kb0 = rank * a.kb_per_split, kb1 = max(kb0, min(a.total_kb, kb0 + a.kb_per_split));
+    const int xrow = (nt - seg * a.x_tiles) * BN, wrow = mt * kFeatures;
+    const int kb0 = min(a.total_kb, rank * a.kb_per_split), kb1 = min(a.total_kb, kb0 + a.kb_per_split);
 
     // one stage's loads into its slot
     auto load_stage = [&](int slot, int kb) {
-        const uint32_t fb = smem_u32(&full_bar[slot]), sw = smem_base + slot * Cfg::kStageBytes, sx = sw + Cfg::kWBytes;
+        const uint32_t fb = smem_u32(&full_bar[slot]), sw = smem_base + slot * Cfg::kStageBytes, sx = sw + kOperandBytes;
         const bool second = kb >= a.num_kb;  // of a sum of two
-        const CUtensorMap* tx = &maps.x[second || seg];
+        const CUtensorMap *tx = &maps.x[second || seg], *tw = &maps.w[second];
         const int k = (second ? kb - a.num_kb : kb) * kBlockK;
         mbar_arrive_expect_tx(fb, Cfg::kStageBytes);
-#pragma unroll
-        for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-            const CUtensorMap* tw = &maps.w[GATED ? h : second];
-            const uint32_t to = sw + h * kOperandBytes;
-            if (a.w_t) {
-                tma_load_2d(to, tw, wrow, k, fb);
-                tma_load_2d(to + 8192, tw, wrow + 64, k, fb);
-            } else {
-                tma_load_2d(to, tw, k, wrow, fb);
-            }
+        if (GATED) {
+            tma_load_2d(sw, &maps.w[0], k, wrow, fb);
+            tma_load_2d(sw + 8192, &maps.w[1], k, wrow, fb);
+        } else if (a.w_t) {
+            tma_load_2d(sw, tw, wrow, k, fb);
+            tma_load_2d(sw + 8192, tw, wrow + 64, k, fb);
+        } else {
+            tma_load_2d(sw, tw, k, wrow, fb);
         }
         if (a.x_t) {  // (tiles of 64 or 128 tokens only)
             tma_load_2d(sx, tx, xrow, k, fb);
@@ -547,6 +851,7 @@ __global__ void __launch_bounds__(NarrowCfg<BN, GATED>::kThreads, NarrowCfg<BN, 
         abort_flag = 0;
         fence_barrier_init();
         // the first stages need no other thread: their latency covers the TMEM allocation
+        after_previous_grid();
         for (int k = 0; k < early; ++k)
             if (k != a.skip_stage || blockIdx.x != 0) load_stage(k, kb0 + k);
     }
@@ -554,6 +859,7 @@ __global__ void __launch_bounds__(NarrowCfg<BN, GATED>::kThreads, NarrowCfg<BN, 
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    after_previous_grid();
     const uint32_t tmem = tmem_slot;
     volatile int* abort = &abort_flag;
 
@@ -572,13 +878,13 @@ __global__ void __launch_bounds__(NarrowCfg<BN, GATED>::kThreads, NarrowCfg<BN, 
                     mbar_drain(smem_u32(&full_bar[k % ST]), static_cast<uint32_t>(k / ST) & 1u);
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        const uint64_t wdesc = operand_desc(smem_base, a.w_t), xdesc = operand_desc(smem_base + Cfg::kWBytes, a.x_t);
+        const uint64_t wdesc = operand_desc(smem_base, a.w_t), xdesc = operand_desc(smem_base + kOperandBytes, a.x_t);
         const uint32_t wstep = operand_step(a.w_t), xstep = operand_step(a.x_t);
         int it = 0, slot = 0, chunk = 0;
         uint32_t phase = 0;
         bool run = true;
         for (int c0 = kb0; c0 < kb1 && run; c0 += a.chunk_kb, ++chunk) {
-            const int c1 = min(kb1, c0 + a.chunk_kb), acc = GATED ? 0 : chunk & 1;
+            const int c1 = min(kb1, c0 + a.chunk_kb), acc = chunk & 1;
             if (chunk >= 2 && !mbar_wait_warp(smem_u32(&acce_bar[acc]), (static_cast<uint32_t>(chunk >> 1) & 1u) ^ 1u, abort)) break;
             for (int kb = c0; kb < c1; ++kb, ++it) {
                 if (!mbar_wait_warp(smem_u32(&full_bar[slot]), phase, abort)) {
@@ -589,13 +895,9 @@ __global__ void __launch_bounds__(NarrowCfg<BN, GATED>::kThreads, NarrowCfg<BN, 
                 if (elect_one()) {
                     const uint64_t off = static_cast<uint64_t>((slot * Cfg::kStageBytes) >> 4);
 #pragma unroll
-                    for (uint32_t s = 0; s < 4; ++s) {
-                        const uint32_t more = kb > c0 || s > 0 ? 1u : 0u;
-                        tc_mma_f16(tmem + acc * BN, wdesc + off + s * wstep, xdesc + off + s * xstep, a.idesc, more);
-                        if (GATED)
-                            tc_mma_f16(tmem + BN, wdesc + off + (kOperandBytes >> 4) + s * wstep, xdesc + off + s * xstep, a.idesc,
-                                       more);
-                    }
+                    for (uint32_t s = 0; s < 4; ++s)
+                        tc_mma_f16(tmem + acc * BN, wdesc + off + s * wstep, xdesc + off + s * xstep, a.idesc,
+                                   kb > c0 || s > 0 ? 1u : 0u);
                     tc_commit(smem_u32(&empty_bar[slot]));
                     if (kb + 1 == c1) tc_commit(smem_u32(&accf_bar[acc]));
                 }
@@ -613,148 +915,144 @@ __global__ void __launch_bounds__(NarrowCfg<BN, GATED>::kThreads, NarrowCfg<BN, 
         const int quarter = warp & 3, row = 32 * quarter + lane;
         const uint32_t lane_addr = static_cast<uint32_t>(32 * quarter) << 16;
         constexpr int LD = BN >= 32 ? 32 : 16;
-        if constexpr (GATED) {
-            const bool any = kb0 < kb1;
-            if (!any || mbar_wait_warp(smem_u32(&accf_bar[0]), 0, abort)) {
-                tc_fence_after_sync();
-#pragma unroll 1
-                for (int c = 0; c < 2 * BN; c += LD) {
-                    uint32_t v[LD];
-                    if (any) {
-                        tmem_ld(tmem + lane_addr + c, v);
-                        tmem_wait_ld(v);
-                    }
+        float sum[BN];
 #pragma unroll
-                    for (int j = 0; j < LD; ++j) part[(c + j) * kTile + row] = any ? __uint_as_float(v[j]) : 0.f;
-                }
+        for (int c = 0; c < BN; ++c) sum[c] = 0.f;
+        bool run = true;
+        int chunk = 0;
+        for (int c0 = kb0; c0 < kb1; c0 += a.chunk_kb, ++chunk) {
+            const int acc = chunk & 1;
+            if (!(run = mbar_wait_warp(smem_u32(&accf_bar[acc]), static_cast<uint32_t>(chunk >> 1) & 1u, abort))) break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < BN; c += LD) {
+                uint32_t v[LD];
+                tmem_ld(tmem + lane_addr + acc * BN + c, v);
+                tmem_wait_ld(v);
+#pragma unroll
+                for (int j = 0; j < LD; ++j) sum[c + j] += __uint_as_float(v[j]);
             }
-        } else {
-            float sum[BN];
+            tc_fence_before_sync();
+            __syncwarp();
+            if (elect_one()) mbar_arrive(smem_u32(&acce_bar[acc]));
+        }
+        // the ring is free: the MMAs of the last chunk are done with it
+        if (run) {
 #pragma unroll
-            for (int c = 0; c < BN; ++c) sum[c] = 0.f;
-            bool run = true;
-            int chunk = 0;
-            for (int c0 = kb0; c0 < kb1; c0 += a.chunk_kb, ++chunk) {
-                const int acc = chunk & 1;
-                if (!(run = mbar_wait_warp(smem_u32(&accf_bar[acc]), static_cast<uint32_t>(chunk >> 1) & 1u, abort))) break;
-                tc_fence_after_sync();
-#pragma unroll
-                for (int c = 0; c < BN; c += LD) {
-                    uint32_t v[LD];
-                    tmem_ld(tmem + lane_addr + acc * BN + c, v);
-                    tmem_wait_ld(v);
-#pragma unroll
-                    for (int j = 0; j < LD; ++j) sum[c + j] += __uint_as_float(v[j]);
-                }
-                tc_fence_before_sync();
-                __syncwarp();
-                if (elect_one()) mbar_arrive(smem_u32(&acce_bar[acc]));
-            }
-            // the ring is free: the MMAs of the last chunk are done with it
-            if (run) {
-#pragma unroll
-                for (int c = 0; c < BN; ++c) part[c * kTile + row] = sum[c];
-            }
+            for (int c = 0; c < BN; ++c) part[c * kTile + row] = sum[c];
         }
     }
 
     tc_fence_before_sync();
     __syncthreads();
+    let_next_grid_start();
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc_group<1>(tmem, Cfg::kTmemCols);
     }
     if (a.splits > 1) cluster_sync_all();
-    // add the cluster's sums, in rank order, each CTA a share of the tokens; 16 lanes x 8 features a token
-    const int share = (BN + a.splits - 1) / a.splits, c0 = rank * share, c1 = min(BN, c0 + share);
+    // add the cluster's sums, in rank order, each CTA a share of the tokens; kLanes lanes x 8 columns a token
+    constexpr int kLanes = kFeatures / 8, kAtOnce = 32 / kLanes, kStep = kAtOnce * (Cfg::kThreads / 32);
+    const int share = (BN + a.splits - 1) / a.splits, first = rank * share, last = min(BN, first + share);
+    const int tile_rank = (twin && (mt & 1) ? a.splits : 0);  // the tile's first CTA in the cluster
     const OutArgs& o = a.o;
-    const int64_t r = static_cast<int64_t>(wrow) + 8 * (lane & 15), left = o.R - r;
+    const bool vec = all_vec(o);
+    const int q = lane & (kLanes - 1), local = vec ? 8 * q : q, step = vec ? 1 : kLanes;
+    const Cols cols{static_cast<int64_t>(wrow) + local, o.R, step, vec};
     float bias[8];
+    bias8(o, cols, bias);
+    // the sums of token c of the tile at the lane's columns, from row `row0` of the tile on
+    auto gather = [&](int c, int row0, float (&v)[8]) {
+        const uint32_t addr = smem_base + 4 * (min(c, BN - 1) * kTile + row0 + local);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) bias[j] = !GATED && o.bias != nullptr && j < left ? load_any(o.bias, o.bias_type, r + j) : 0.f;
-#pragma unroll 1
-    for (int base = c0 + 2 * warp; base < c1; base += 2 * (Cfg::kThreads / 32)) {
-        const int c = base + (lane >> 4);
-        const int64_t t = static_cast<int64_t>(xrow) + c;
-        const bool here = c < c1 && t < o.T;
-        float v[GATED ? 2 : 1][8];
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
 #pragma unroll
-        for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-            const uint32_t addr = smem_base + 4 * ((h * BN + min(c, BN - 1)) * kTile + 8 * (lane & 15));
+        for (int s = 0; s < kMaxSplits; ++s) {
+            if (s >= a.splits) break;
+            const uint32_t from = dsmem_map(addr, tile_rank + s);
+            if (vec) {
+                const float4 x = dsmem_ld_v4(from), y = dsmem_ld_v4(from + 16);
+                v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+                v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[h][j] = 0.f;
-#pragma unroll
-            for (int s = 0; s < kMaxSplits; ++s) {
-                if (s >= a.splits) break;
-                const uint32_t from = a.splits > 1 ? dsmem_map(addr, s) : addr;
-                const float4 p = a.splits > 1 ? dsmem_ld_v4(from) : ld_shared_v4(from);
-                const float4 q = a.splits > 1 ? dsmem_ld_v4(from + 16) : ld_shared_v4(from + 16);
-                v[h][0] += p.x, v[h][1] += p.y, v[h][2] += p.z, v[h][3] += p.w;
-                v[h][4] += q.x, v[h][5] += q.y, v[h][6] += q.z, v[h][7] += q.w;
+                for (int j = 0; j < 8; ++j) v[j] += dsmem_ld_f32(from + 4 * kLanes * j);
             }
         }
-        if constexpr (GATED) {
-            float scale[2] = {1.f, 1.f}, inv[2] = {1.f, 1.f};
-            if (o.keep == kKeep8) {
-                // the tile's 128 features are a group of the 8-bit form (past the edge they are zeros)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float top = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) top = max_magnitude(top, v[h][j]);
-#pragma unroll
-                    for (int d = 8; d > 0; d >>= 1) top = max_magnitude(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                    scale[h] = group_scale(top, o.e5m2, inv[h]);
-                }
-                if (here && (lane & 15) == 0) {
-                    o.g.s[t * o.g.s_rs + mt * o.g.s_cs] = scale[0];
-                    o.u.s[t * o.u.s_rs + mt * o.u.s_cs] = scale[1];
-                }
+    };
+    if constexpr (GATED) {
+        if (twin) {
+            // (features past the edge are zeros)
+#pragma unroll 1
+            for (int base = first + kAtOnce * warp; base < last; base += kStep) {
+                const int c = base + lane / kLanes;
+                float g[8], u[8];
+                gather(c, 0, g);
+                gather(c, 64, u);
+                const float2 m = largest_of<kLanes>(g, u);
+                if (c < last && q == 0) tops[c] = m;
             }
-            if (here) finish_gated8(o, t, r, v[0], v[1], scale[0], inv[0], scale[1], inv[1]);
-        } else if (here && left > 0) {
-            float res[8];
-            if (o.res[seg] != nullptr) load8(o.res[seg], o.y_type, t * o.ld_res + r, o.res_vec, left, res);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[0][j] += bias[j];
-            activate8(o.act, v[0]);
-            if (o.res[seg] != nullptr) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[0][j] += res[j];
-            }
-            store8(o.y[seg], o.y_type, t * o.ld_y + r, o.y_vec, left, v[0]);
+            cluster_sync_all();
         }
     }
-    if (a.splits > 1) cluster_sync_all();  // no CTA leaves while others read its sums
+#pragma unroll 1
+    for (int base = first + kAtOnce * warp; base < last; base += kStep) {
+        const int c = base + lane / kLanes;
+        const int64_t t = static_cast<int64_t>(xrow) + c;
+        const bool here = c < last && t < o.T;
+        float v[8];
+        if constexpr (GATED) {
+            float u[8];
+            gather(c, 0, v);
+            gather(c, 64, u);
+            Scales s{1.f, 1.f, 1.f, 1.f};
+            if (twin) {
+                const int at = min(c, BN - 1);
+                // the other tile's CTA of the same rank
+                const uint32_t other = dsmem_map(smem_u32(&tops[at]), (mt & 1 ? 0 : a.splits) + rank);
+                const float2 m = make_float2(max_magnitude(tops[at].x, dsmem_ld_f32(other)),
+                                             max_magnitude(tops[at].y, dsmem_ld_f32(other + 4)));
+                s = scales_of(o, m, t, mt >> 1, here && q == 0 && (mt & 1) == 0);
+            }
+            if (here && !cols.none()) {
+                keep_gated8(o, t, cols, v, u, s);
+                finish_gated8(o, t, cols, v, u);
+            }
+        } else {
+            Raw8 r;
+            if (here && o.res[seg] != nullptr && !cols.none()) r = load_raw8(o.res[seg], o.y_type, t * o.ld_res, cols);
+            gather(c, 0, v);
+            if (here) finish8(o, seg, t, cols, v, bias, r);
+        }
+    }
+    if (a.splits > 1 || twin) cluster_sync_all();  // no CTA leaves while others read its sums
     if (threadIdx.x == 0 && abort_flag) record_error(a.status ? a.status : g_status, VNM_ERR_TIMEOUT, 14);
 }
 
 // K = 0: the sums are 0.
 __global__ void dense_empty_kernel(const OutArgs o, int kind) {
+    after_previous_grid();
     const int64_t per_row = (o.R + 7) / 8;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < o.T * per_row;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t t = i / per_row, r = 8 * (i - t * per_row), left = o.R - r;
+        const int64_t t = i / per_row;
+        const Cols c{8 * (i - t * per_row), o.R, 1, all_vec(o)};
+        float v[8] = {}, u[8] = {}, b[8];
         if (kind == kGatedPair) {
-            float g[8] = {}, u[8] = {};
-            if (o.keep == kKeep8 && r % 128 == 0) {
-                o.g.s[t * o.g.s_rs + (r / 128) * o.g.s_cs] = kMinScale;
-                o.u.s[t * o.u.s_rs + (r / 128) * o.u.s_cs] = kMinScale;
+            if (o.keep == kKeep8 && c.first % 128 == 0) {
+                o.g.s[t * o.g.s_rs + (c.first / 128) * o.g.s_cs] = kMinScale;
+                o.u.s[t * o.u.s_rs + (c.first / 128) * o.u.s_cs] = kMinScale;
             }
-            finish_gated8(o, t, r, g, u, kMinScale, 1.f / kMinScale, kMinScale, 1.f / kMinScale);
+            keep_gated8(o, t, c, v, u, Scales{kMinScale, 1.f / kMinScale, kMinScale, 1.f / kMinScale});
+            finish_gated8(o, t, c, v, u);
             continue;
         }
+        bias8(o, c, b);
         for (int seg = 0; seg < (kind == kTwoByRows ? 2 : 1); ++seg) {
-            float v[8], res[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = o.bias != nullptr && j < left ? load_any(o.bias, o.bias_type, r + j) : 0.f;
-            activate8(o.act, v);
-            if (o.res[seg] != nullptr) {
-                load8(o.res[seg], o.y_type, t * o.ld_res + r, o.res_vec, left, res);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] += res[j];
-            }
-            store8(o.y[seg], o.y_type, t * o.ld_y + r, o.y_vec, left, v);
+            float w[8] = {};
+            Raw8 r;
+            if (o.res[seg] != nullptr) r = load_raw8(o.res[seg], o.y_type, t * o.ld_res, c);
+            finish8(o, seg, t, c, w, b, r);
         }
     }
 }
@@ -779,6 +1077,32 @@ bool encode_all(Maps* m, const ProductArgs& p, int x_rows, int w_rows) {
     return true;
 }
 
+// The outputs, and residuals, that go by tensor memory copies, as boxes of 32 rows; the others' maps are not used.
+bool encode_outputs(OutMaps* m, const ProductArgs& p, const OutArgs& o) {
+    auto type = [](vnm_dtype t) {
+        return t == VNM_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+               : t == VNM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    };
+    const bool gated = p.kind == kGatedPair, eight = p.keep == kKeep8;
+    const int e = p.y_type == VNM_F32 ? 4 : 2;
+    *m = OutMaps{};
+    if (o.y_tma)
+        for (int i = 0; i < (p.kind == kTwoByRows ? 2 : 1); ++i)
+            if (!encode_2d(&m->y[i], type(p.y_type), p.y[i], p.R, p.T, p.ld_y * e, gated ? 32 : 128 / e, 32,
+                           gated ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+                return false;
+    if (p.residual[0] != nullptr && o.res_vec)
+        for (int i = 0; i < (p.kind == kTwoByRows ? 2 : 1); ++i)
+            if (!encode_2d(&m->res[i], type(p.y_type), p.residual[i], p.R, p.T, p.ld_residual * e, 128 / e, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+                return false;
+    if (!o.keep_tma) return true;
+    const CUtensorMapDataType t = eight ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type(p.y_type);
+    const CUtensorMapSwizzle sw = eight ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B;
+    return encode_2d(&m->g, t, p.g.p, p.R, p.T, p.g.ld * (eight ? 1 : 2), 32, 32, sw) &&
+           encode_2d(&m->u, t, p.u.p, p.R, p.T, p.u.ld * (eight ? 1 : 2), 32, 32, sw);
+}
+
 template <typename Kernel>
 cudaError_t prepare(Kernel kernel, int smem, int regs, std::atomic<bool>* set) {
     int dev = 0;
@@ -797,50 +1121,50 @@ cudaError_t prepare(Kernel kernel, int smem, int regs, std::atomic<bool>* set) {
     return cudaSuccess;
 }
 
-template <typename Kernel>
-cudaError_t launch(Kernel kernel, int64_t ctas, int threads, int smem, int cluster, const Maps& maps, const GemmArgs& a,
-                   cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, maps, a);
-}
-
-template <bool GATED, bool SUM>
-cudaError_t run_pair(const ProductArgs& p, GemmArgs a, int sm_count, cudaStream_t stream) {
+template <bool GATED, bool SUM, bool SPLIT, bool ALIGNED>
+cudaError_t run_pair(const ProductArgs& p, GemmArgs a, int tile_n, int splits, int sm_count, cudaStream_t stream) {
     static std::atomic<bool> set[kMaxDevicesDl];
     a.x_tiles = static_cast<int>(ceil_div(p.T, 2 * kTile));
     a.m_tiles = a.x_tiles * (p.kind == kTwoByRows ? 2 : 1);
-    a.n_tiles = static_cast<int>(ceil_div(p.R, GATED ? kTile : 2 * kTile));
+    a.n_tiles = static_cast<int>(ceil_div(p.R, GATED ? tile_n / 2 : tile_n));
+    a.tile_n = tile_n;
+    // (transposed W comes in boxes of 64 rows)
+    a.stage_bytes = kOperandBytes + (a.w_t ? static_cast<int>(ceil_div(tile_n, 128)) * 8192 : tile_n / 2 * 128);
+    a.stages = std::min(kPairMaxStages, kPairRing / a.stage_bytes);
     const int64_t tiles = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
     a.tiles = static_cast<int>(tiles);
-    a.splits = 1;
-    a.kb_per_split = a.total_kb;
-    a.idesc = f16_idesc(2 * kTile, 256, p.bf16, a.x_t, a.w_t);
+    if (tiles * 2 * splits > INT32_MAX) return cudaErrorInvalidValue;
+    a.splits = splits;
+    a.kb_per_split = static_cast<int>(ceil_div(a.total_kb, splits));
+    a.idesc = f16_idesc(2 * kTile, tile_n, p.bf16, a.x_t, a.w_t);
     Maps maps;
-    if (!encode_all(&maps, p, kTile, kTile)) return cudaErrorInvalidValue;
-    const cudaError_t e = prepare(dense_pair_kernel<GATED, SUM>, kPairSmem, SUM ? kSumLaunchRegs : 0, set);
+    OutMaps outs;
+    if (!encode_all(&maps, p, kTile, tile_n / 2) || (!SPLIT && !encode_outputs(&outs, p, a.o))) return cudaErrorInvalidValue;
+    const auto kernel = dense_pair_kernel<GATED, SUM, SPLIT, ALIGNED>;
+    const cudaError_t e = prepare(kernel, kPairSmem, SUM && !SPLIT ? kSumLaunchRegs : 0, set);
     if (e != cudaSuccess) return e;
-    return launch(dense_pair_kernel<GATED, SUM>, 2 * std::min<int64_t>(tiles, std::max(1, sm_count / 2)), kPairThreads, kPairSmem, 2,
-                  maps, a, stream);
+    const int64_t pairs = SPLIT ? tiles * splits : std::min<int64_t>(tiles, std::max(1, sm_count / 2));
+    return launch_early(kernel, 2 * pairs, kPairThreads, kPairSmem, 2 * splits, stream, maps, outs, a);
+}
+
+template <bool GATED>
+cudaError_t run_pair(const ProductArgs& p, const GemmArgs& a, bool sum, bool aligned, int tile_n, int sm_count, cudaStream_t stream) {
+    if (sum)
+        return aligned ? run_pair<GATED, true, false, true>(p, a, tile_n, 1, sm_count, stream)
+                       : run_pair<GATED, true, false, false>(p, a, tile_n, 1, sm_count, stream);
+    return aligned ? run_pair<GATED, false, false, true>(p, a, tile_n, 1, sm_count, stream)
+                   : run_pair<GATED, false, false, false>(p, a, tile_n, 1, sm_count, stream);
 }
 
 template <int BN, bool GATED>
 cudaError_t run_narrow(const ProductArgs& p, GemmArgs a, int splits, cudaStream_t stream) {
-    using Cfg = NarrowCfg<BN, GATED>;
+    using Cfg = NarrowCfg<BN>;
     static std::atomic<bool> set[kMaxDevicesDl];
+    const int twin = p.keep == kKeep8 ? 2 : 1;
     a.x_tiles = static_cast<int>(ceil_div(p.T, BN));
     a.n_tiles = a.x_tiles * (p.kind == kTwoByRows ? 2 : 1);
-    a.m_tiles = static_cast<int>(ceil_div(p.R, kTile));
+    a.m_tiles = static_cast<int>(ceil_div(p.R, GATED ? 64 * twin : kTile)) * twin;
     const int64_t tiles = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
     if (tiles * splits > INT32_MAX) return cudaErrorInvalidValue;
     a.tiles = static_cast<int>(tiles);
@@ -848,10 +1172,10 @@ cudaError_t run_narrow(const ProductArgs& p, GemmArgs a, int splits, cudaStream_
     a.kb_per_split = static_cast<int>(ceil_div(a.total_kb, splits));
     a.idesc = f16_idesc(kTile, BN, p.bf16, a.w_t, a.x_t);
     Maps maps;
-    if (!encode_all(&maps, p, BN, kTile)) return cudaErrorInvalidValue;
+    if (!encode_all(&maps, p, BN, GATED ? 64 : kTile)) return cudaErrorInvalidValue;
     const cudaError_t e = prepare(dense_narrow_kernel<BN, GATED>, Cfg::kSmem, 0, set);
     if (e != cudaSuccess) return e;
-    return launch(dense_narrow_kernel<BN, GATED>, tiles * splits, Cfg::kThreads, Cfg::kSmem, splits, maps, a, stream);
+    return launch_early(dense_narrow_kernel<BN, GATED>, tiles * splits, Cfg::kThreads, Cfg::kSmem, splits * twin, stream, maps, a);
 }
 
 template <bool GATED>
@@ -864,8 +1188,10 @@ cudaError_t run_narrow(int bn, const ProductArgs& p, const GemmArgs& a, int spli
     }
 }
 
+// How a product is tiled: pairs of CTAs (bn = 0), tile_n rows of W a tile, K over `splits` pairs of a
+// cluster; or tiles of bn tokens, K over `splits` CTAs of a cluster.
 struct TilePlan {
-    int bn, splits;
+    int bn, splits, tile_n;
 };
 
 // The times the plan compares, in us: a launch with its first loads and its last stores; then the
@@ -873,24 +1199,38 @@ struct TilePlan {
 TilePlan plan_tiles(const ProductArgs& p, int sm_count) {
     const bool gated = p.kind == kGatedPair, two = p.kind == kTwoByRows;
     const int num_kb = static_cast<int>(ceil_div(p.K, kBlockK)) * (p.kind == kSumOfTwo ? 2 : 1);
-    TilePlan best{0, 1};
-    const int64_t pair_tiles = ceil_div(p.T, 256) * (two ? 2 : 1) * ceil_div(p.R, gated ? 128 : 256);
-    double least = 5.0 + static_cast<double>(ceil_div(pair_tiles, std::max(1, sm_count / 2))) * num_kb * 0.3;
+    const int64_t rows = ceil_div(p.T, 2 * kTile) * (two ? 2 : 1), pairs = std::max(1, sm_count / 2);
+    TilePlan best{0, 1, 256};
+    double least = 1e30;
+    auto consider = [&](const TilePlan& plan, double t) {
+        if (t < least) {
+            least = t;
+            best = plan;
+        }
+    };
+    for (int n = 256; n >= 128; n -= 64) {  // (boxes of 64 columns, 32 features)
+        if (n < 256 && p.keep == kKeep8) break;  // (a group of the 8-bit form is 128 features)
+        const int64_t tiles = rows * ceil_div(p.R, gated ? n / 2 : n);
+        consider({0, 1, n}, 8.0 + static_cast<double>(ceil_div(tiles, pairs)) * num_kb * 0.29 * n / 256);
+    }
+    const int64_t pair_tiles = rows * ceil_div(p.R, gated ? 128 : 256);
+    for (int splits = 2; splits <= kMaxPairSplits; ++splits) {
+        const int64_t clusters = splits == 2 ? sm_count * 36 / 152 : splits == 3 ? sm_count * 23 / 152 : sm_count * 15 / 152;
+        if (splits > num_kb || pair_tiles > clusters) break;
+        consider({0, splits, 256}, 10.0 + static_cast<double>(ceil_div(num_kb, splits)) * 0.29);
+    }
     for (int bn : {16, 32, 64, 128}) {
         if (bn > 16 && bn / 2 >= p.T && !(p.x[0].transposed && bn <= 64)) break;  // the width below holds all tokens
         if (p.x[0].transposed && bn < 64) continue;  // (a box of transposed X is 64 tokens)
-        const int64_t tiles = ceil_div(p.R, kTile) * ceil_div(p.T, bn) * (two ? 2 : 1);
-        const int slots = sm_count * (gated && bn >= 64 ? 1 : 2);
-        for (int splits : {1, 2, 4, 8}) {
+        const int64_t tiles = ceil_div(p.R, gated ? 64 : kTile) * ceil_div(p.T, bn) * (two ? 2 : 1);
+        const int slots = sm_count * 2;
+        for (int splits : {1, 2, 3, 4, 6, 8}) {
+            if (splits * (p.keep == kKeep8 ? 2 : 1) > kMaxSplits) break;  // (two tiles a cluster)
             if (splits > 1 && (splits > num_kb || tiles * splits > slots)) break;
             const int64_t kbs = ceil_div(num_kb, splits), waves = ceil_div(tiles * splits, slots);
-            const double chain = static_cast<double>(waves * kbs) * (bn == 128 ? 0.40 : bn == 64 ? 0.30 : 0.25) * (gated ? 1.6 : 1.0);
-            const double loads = static_cast<double>(tiles * num_kb) * (kTile * (gated ? 2 : 1) + bn) * 128 / 7e6;
-            const double t = 4.9 + std::max(chain, loads) + (splits == 8 ? 1.3 : splits > 1 ? 0.3 : 0.0);
-            if (t < least) {
-                least = t;
-                best = TilePlan{bn, splits};
-            }
+            const double chain = static_cast<double>(waves * kbs) * (bn == 128 ? 0.40 : bn == 64 ? 0.30 : 0.25);
+            const double loads = static_cast<double>(tiles * num_kb) * (kTile + bn) * 128 / 7e6;
+            consider({bn, splits, 0}, 4.9 + std::max(chain, loads) + (splits == 8 ? 1.3 : splits > 1 ? 0.3 : 0.0));
         }
     }
     return best;
@@ -904,7 +1244,7 @@ bool few_tokens(const ProductArgs& p) {
 }  // namespace
 
 void product_plan(const ProductArgs& p, int sm_count, int* tile_tokens, int* splits) {
-    TilePlan plan{kFewTokens, 1};
+    TilePlan plan{kFewTokens, 1, 0};
     if (!few_tokens(p)) plan = plan_tiles(p, sm_count);
     *tile_tokens = plan.bn;
     *splits = plan.splits;
@@ -927,7 +1267,7 @@ cudaError_t launch_product(const ProductArgs& p, int sm_count, cudaStream_t stre
     GemmArgs a{};
     OutArgs& o = a.o;
     auto rows_aligned = [](const void* q, int64_t ld_bytes, int n) {
-        return reinterpret_cast<uintptr_t>(q) % n == 0 && ld_bytes % n == 0;
+        return q == nullptr || (reinterpret_cast<uintptr_t>(q) % n == 0 && ld_bytes % n == 0);
     };
     const int e = p.y_type == VNM_F32 ? 4 : 2, k = p.keep == kKeep8 ? 1 : 2;
     o.T = p.T;
@@ -939,6 +1279,12 @@ cudaError_t launch_product(const ProductArgs& p, int sm_count, cudaStream_t stre
         o.y_vec = o.y_vec && rows_aligned(p.y[i], p.ld_y * e, 16);
         o.res_vec = o.res_vec && rows_aligned(p.residual[i], p.ld_residual * e, 16);
     }
+    o.y_tma = o.y_vec;
+    auto keep_aligned = [&](int n) {
+        return p.keep == kKeepNone || (rows_aligned(p.g.p, p.g.ld * k, n) && rows_aligned(p.u.p, p.u.ld * k, n));
+    };
+    o.keep_vec = keep_aligned(8 * k);
+    o.keep_tma = p.keep != kKeepNone && keep_aligned(16);
     o.bias = p.bias;
     o.ld_y = p.ld_y;
     o.ld_res = p.ld_residual;
@@ -949,27 +1295,28 @@ cudaError_t launch_product(const ProductArgs& p, int sm_count, cudaStream_t stre
     o.e5m2 = p.e5m2;
     o.g = p.g;
     o.u = p.u;
-    o.g_vec = rows_aligned(p.g.p, p.g.ld * k, 8 * k);
-    o.u_vec = rows_aligned(p.u.p, p.u.ld * k, 8 * k);
     if (p.K == 0) {
         const int64_t n = std::min<int64_t>(ceil_div(p.T * ceil_div(p.R, 8), 256), 16 * sm_count);
-        dense_empty_kernel<<<static_cast<unsigned>(n), 256, 0, stream>>>(o, p.kind);
-        return cudaGetLastError();
+        return launch_early(dense_empty_kernel, n, 256, 0, 1, stream, o, static_cast<int>(p.kind));
     }
     a.kind = p.kind;
     a.num_kb = static_cast<int>(ceil_div(p.K, kBlockK));
     a.total_kb = a.num_kb * (p.kind == kSumOfTwo ? 2 : 1);
-    a.chunk_kb = p.y_type == VNM_F32 ? kChunk : a.total_kb;
+    a.chunk_kb = p.y_type == VNM_F32 || p.keep == kKeep8 ? kChunk : a.total_kb;
     a.x_t = p.x[0].transposed;
     a.w_t = p.w[0].transposed;
     a.status = p.status;
     a.skip_stage = p.skip_stage;
     const bool gated = p.kind == kGatedPair;
     const TilePlan plan = plan_tiles(p, sm_count);
-    if (plan.bn == 0)
-        return gated                  ? run_pair<true, false>(p, a, sm_count, stream)
-               : p.y_type == VNM_F32 ? run_pair<false, true>(p, a, sm_count, stream)
-                                     : run_pair<false, false>(p, a, sm_count, stream);
+    if (plan.bn == 0 && plan.splits > 1)
+        return gated ? run_pair<true, true, true, false>(p, a, plan.tile_n, plan.splits, sm_count, stream)
+                     : run_pair<false, true, true, false>(p, a, plan.tile_n, plan.splits, sm_count, stream);
+    if (plan.bn == 0) {
+        const bool aligned = o.y_tma && o.res_vec && (p.keep == kKeepNone || o.keep_tma);
+        if (gated) return run_pair<true>(p, a, p.keep == kKeep8, aligned, plan.tile_n, sm_count, stream);
+        return run_pair<false>(p, a, a.chunk_kb < a.total_kb, aligned, plan.tile_n, sm_count, stream);
+    }
     return gated ? run_narrow<true>(plan.bn, p, a, plan.splits, stream) : run_narrow<false>(plan.bn, p, a, plan.splits, stream);
 }
 

@@ -3,9 +3,9 @@
 //   dg = dy * u * act'(g), du = dy * act(g), h = act(g) * u
 //
 // with g and u as the forward pass kept them, in 16 bits or in the block-scaled
-// 8-bit form. Bound by memory traffic: 8 neighbouring columns a thread, 16-byte loads
-// and stores (8 bytes of an 8-bit checkpoint) where the rows allow them. dg and du are
-// rounded once to 16 bits: the tensor cores take no wider operands at this rate.
+// 8-bit form. Bound by memory traffic: a warp takes 256 columns of a row, 8 neighbours a lane,
+// 16-byte loads and stores (8 bytes of an 8-bit checkpoint) where the rows allow them. dg and du
+// are rounded once to 16 bits: the tensor cores take no wider operands at this rate.
 //   silu'(g) = s (1 + g (1 - s)), s = 1 / (1 + e^-g); gelu'(g) = Phi(g) + g phi(g).
 #include <algorithm>
 
@@ -15,89 +15,149 @@
 namespace vnm {
 namespace {
 
+constexpr int kThreads = 256;
+constexpr int kUnit = 256;  // columns of a row that a warp takes at a time
+
 // act(g) and act'(g)
-__device__ __forceinline__ float2 with_slope(int act, float g) {
-    if (act == VNM_ACT_SILU) {
+template <int ACT>
+__device__ __forceinline__ float2 with_slope(float g) {
+    if (ACT == VNM_ACT_SILU) {
         const float s = sigmoid(g);
         return make_float2(g * s, s * (1.f + g * (1.f - s)));
     }
-    if (act == VNM_ACT_GELU) {
+    if (ACT == VNM_ACT_GELU) {
         const float cdf = 0.5f * (1.f + erff(g * 0.70710678118654752f));
-        return make_float2(g * cdf, cdf + g * (0.39894228040143268f * expf(-0.5f * g * g)));
+        return make_float2(g * cdf, cdf + g * (0.39894228040143268f * __expf(-0.5f * g * g)));
     }
     // (a NaN passes through both)
-    if (act == VNM_ACT_RELU) return make_float2(g < 0.f ? 0.f : g, g > 0.f ? 1.f : g <= 0.f ? 0.f : g);
+    if (ACT == VNM_ACT_RELU) return make_float2(g < 0.f ? 0.f : g, g > 0.f ? 1.f : g <= 0.f ? 0.f : g);
     return make_float2(g, 1.f);
 }
 
-__device__ __forceinline__ void load_kept8(const GatedGradArgs& a, const Kept& k, int type, int64_t t, int64_t f, bool vec,
-                                           int64_t left, float (&v)[8]) {
-    if (a.keep == kKeep16) {
-        load8(k.p, type, t * k.ld + f, vec, left, v);
-        return;
-    }
-    const uint8_t* p = static_cast<const uint8_t*>(k.p) + t * k.ld + f;
-    const float s = k.s[t * k.s_rs + (f >> 7) * k.s_cs];
-    uint32_t w[2] = {0u, 0u};
-    if (vec && left >= 8) {
-        const uint2 q = *reinterpret_cast<const uint2*>(p);
-        w[0] = q.x;
-        w[1] = q.y;
-    } else {
+// A lane's eight elements of a matrix, as they are stored, and their scales: of columns 0 to 3 and of 4 to 7.
+struct Part {
+    uint32_t w[4];
+    float s[2];
+};
+
+template <bool FP8>
+__device__ __forceinline__ Part load_part(const Kept& k, int64_t t, const Cols& c) {
+    Part p{{0u, 0u, 0u, 0u}, {1.f, 1.f}};
+    if (FP8) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < left) w[j >> 2] |= static_cast<uint32_t>(p[j]) << (8 * (j & 3));
+        for (int h = 0; h < 2; ++h)
+            p.s[h] = k.s[t * k.s_rs + (min(c.at(4 * h), c.end - 1) >> 7) * k.s_cs];
+        const uint8_t* row = static_cast<const uint8_t*>(k.p) + t * k.ld;
+        if (c.whole()) {
+            const uint2 q = __ldcs(reinterpret_cast<const uint2*>(row + c.first));
+            p.w[0] = q.x;
+            p.w[1] = q.y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c.at(j) < c.end) p.w[j >> 2] |= static_cast<uint32_t>(row[c.at(j)]) << (8 * (j & 3));
+        }
+    } else {
+        const uint16_t* row = static_cast<const uint16_t*>(k.p) + t * k.ld;
+        if (c.whole()) {
+            const uint4 q = __ldcs(reinterpret_cast<const uint4*>(row + c.first));
+            p.w[0] = q.x;
+            p.w[1] = q.y;
+            p.w[2] = q.z;
+            p.w[3] = q.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c.at(j) < c.end) p.w[j >> 1] |= static_cast<uint32_t>(row[c.at(j)]) << (16 * (j & 1));
+        }
+    }
+    return p;
+}
+
+template <bool FP8>
+__device__ __forceinline__ void widen_part(const Part& p, bool bf16, bool e5m2, float (&v)[8]) {
+    if (!FP8) {
+        widen8(make_uint4(p.w[0], p.w[1], p.w[2], p.w[3]), bf16, v);
+        return;
     }
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[j >> 2] >> (8 * (j & 3))),
-                                                         a.e5m2 ? __NV_E5M2 : __NV_E4M3);
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(p.w[j >> 2] >> (8 * (j & 3))),
+                                                         e5m2 ? __NV_E5M2 : __NV_E4M3);
         const float2 q = __half22float2(__half2(h));
-        v[j] = q.x * s;
-        v[j + 1] = q.y * s;
+        v[j] = q.x * p.s[j >> 2];
+        v[j + 1] = q.y * p.s[j >> 2];
     }
 }
 
-__global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradArgs a, bool dy_vec, bool g_vec, bool u_vec, bool d_vec,
-                                                         bool h_vec) {
-    const int64_t per_row = (a.F + 7) / 8;
-    const int type = a.bf16 ? VNM_BF16 : VNM_F16;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.T * per_row;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t t = i / per_row, f = 8 * (i - t * per_row), left = a.F - f;
-        float dy[8] = {}, g[8], u[8];
-        if (a.dy != nullptr) load8(a.dy, type, t * a.ld_dy + f, dy_vec, left, dy);
-        load_kept8(a, a.g, type, t, f, g_vec, left, g);
-        load_kept8(a, a.u, type, t, f, u_vec, left, u);
-        float h[8];
+// vec: the rows of every matrix start on 16 bytes (8-bit checkpoints: 8); a lane then takes 8 neighbours.
+template <int ACT, bool FP8>
+__global__ void __launch_bounds__(kThreads, 4) gated_grad_kernel(const GatedGradArgs a, bool vec) {
+    const int lane = threadIdx.x & 31, type = a.bf16 ? VNM_BF16 : VNM_F16;
+    const int64_t per_row = (a.F + kUnit - 1) / kUnit, warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+    // units warp, warp + warps, ...; the place of the next one without a division
+    const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t dt = warps / per_row, dn = warps - dt * per_row;
+    int64_t t = warp / per_row, n = warp - t * per_row;
+    const Kept kdy{const_cast<void*>(a.dy), a.ld_dy, nullptr, 0, 0};
+    after_previous_grid();
+#pragma unroll 1
+    while (t < a.T) {
+        const Cols c{n * kUnit + (vec ? 8 * lane : lane), a.F, vec ? 1 : 32, vec};
+        if (!c.none()) {
+            const Part pg = load_part<FP8>(a.g, t, c), pu = load_part<FP8>(a.u, t, c);
+            Part pd{{0u, 0u, 0u, 0u}, {1.f, 1.f}};
+            if (a.dy != nullptr) pd = load_part<false>(kdy, t, c);
+            float dy[8], g[8], u[8], h[8];
+            widen_part<false>(pd, a.bf16, false, dy);
+            widen_part<FP8>(pg, a.bf16, a.e5m2, g);
+            widen_part<FP8>(pu, a.bf16, a.e5m2, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float2 s = with_slope(a.act, g[j]);
-            h[j] = s.x * u[j];
-            g[j] = dy[j] * u[j] * s.y;
-            u[j] = dy[j] * s.x;
+            for (int j = 0; j < 8; ++j) {
+                const float2 s = with_slope<ACT>(g[j]);
+                h[j] = s.x * u[j];
+                g[j] = dy[j] * u[j] * s.y;
+                u[j] = dy[j] * s.x;
+            }
+            if (a.dg != nullptr) {
+                store8(a.dg, type, t * a.ld_d, c, g);
+                store8(a.du, type, t * a.ld_d, c, u);
+            }
+            if (a.h != nullptr) store8(a.h, type, t * a.ld_h, c, h);
         }
-        if (a.dg != nullptr) {
-            store8(a.dg, type, t * a.ld_d + f, d_vec, left, g);
-            store8(a.du, type, t * a.ld_d + f, d_vec, left, u);
+        t += dt;
+        n += dn;
+        if (n >= per_row) {
+            n -= per_row;
+            ++t;
         }
-        if (a.h != nullptr) store8(a.h, type, t * a.ld_h + f, h_vec, left, h);
     }
+}
+
+template <int ACT>
+cudaError_t launch(const GatedGradArgs& a, bool vec, int sm_count, cudaStream_t stream) {
+    const int64_t units = a.T * ((a.F + kUnit - 1) / kUnit);
+    const int64_t blocks = std::min<int64_t>((units + kThreads / 32 - 1) / (kThreads / 32), static_cast<int64_t>(sm_count) * 8);
+    return a.keep == kKeep8 ? launch_early(gated_grad_kernel<ACT, true>, blocks, kThreads, 0, 1, stream, a, vec)
+                            : launch_early(gated_grad_kernel<ACT, false>, blocks, kThreads, 0, 1, stream, a, vec);
 }
 
 }  // namespace
 
 cudaError_t launch_gated_grad(const GatedGradArgs& a, int sm_count, cudaStream_t stream) {
     auto rows_aligned = [](const void* p, int64_t ld_bytes, int n) {
-        return reinterpret_cast<uintptr_t>(p) % n == 0 && ld_bytes % n == 0;
+        return p == nullptr || (reinterpret_cast<uintptr_t>(p) % n == 0 && ld_bytes % n == 0);
     };
     const int k = a.keep == kKeep8 ? 1 : 2;
-    const int64_t n = a.T * ((a.F + 7) / 8);
-    const int64_t blocks = std::min<int64_t>((n + 255) / 256, static_cast<int64_t>(sm_count) * 8);
-    gated_grad_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-        a, rows_aligned(a.dy, a.ld_dy * 2, 16), rows_aligned(a.g.p, a.g.ld * k, 8 * k), rows_aligned(a.u.p, a.u.ld * k, 8 * k),
-        rows_aligned(a.dg, a.ld_d * 2, 16) && rows_aligned(a.du, a.ld_d * 2, 16), rows_aligned(a.h, a.ld_h * 2, 16));
-    return cudaGetLastError();
+    const bool vec = rows_aligned(a.dy, a.ld_dy * 2, 16) && rows_aligned(a.g.p, a.g.ld * k, 8 * k) &&
+                     rows_aligned(a.u.p, a.u.ld * k, 8 * k) && rows_aligned(a.dg, a.ld_d * 2, 16) &&
+                     rows_aligned(a.du, a.ld_d * 2, 16) && rows_aligned(a.h, a.ld_h * 2, 16);
+    switch (a.act) {
+        case VNM_ACT_SILU: return launch<VNM_ACT_SILU>(a, vec, sm_count, stream);
+        case VNM_ACT_GELU: return launch<VNM_ACT_GELU>(a, vec, sm_count, stream);
+        case VNM_ACT_RELU: return launch<VNM_ACT_RELU>(a, vec, sm_count, stream);
+        default: return launch<VNM_ACT_NONE>(a, vec, sm_count, stream);
+    }
 }
 
 }  // namespace vnm

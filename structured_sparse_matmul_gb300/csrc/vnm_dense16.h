@@ -11,6 +11,27 @@
 
 namespace vnm {
 
+// Launches that may start while the stream's previous grid drains (the kernels wait for its end by
+// themselves before they touch global memory): it hides a launch's latency, about 2 us of a chain of small calls.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), int64_t blocks, int threads, size_t smem, int cluster, cudaStream_t stream,
+                         const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // A 16-bit operand of a product, rows x K: stored row-major (a row's K elements
 // are neighbours), or transposed (an element of K is a row of the storage).
 struct Operand16 {
