@@ -9,10 +9,12 @@
 // MMA's k positions may be dealt in any order as long as both operands agree: lane
 // (g, i) = (lane / 4, lane % 4) reads 16 bytes of rows g and g + 8 at column 32 h + 8 i of
 // a block of 64, and the same columns of token g, which are the operands of two MMAs with
-// no shuffle. A CTA takes 16 rows, its 8 warps deal the K blocks among themselves and
+// no shuffle. A CTA takes 16 rows, its warps deal the K blocks among themselves and
 // meet once in shared memory, in a fixed order. The loads of W run kRing blocks ahead,
 // those of x (from L2) one. After every round of the ring the MMAs' sums, which
 // truncate, are added up in fp32.
+#include <type_traits>
+
 #include "vnm_dense16.cuh"
 #include "vnm_internal.h"
 #include "vnm_stream.cuh"
@@ -21,8 +23,16 @@ namespace vnm {
 namespace {
 
 constexpr int kRows = 16;  // rows of W of a CTA
-constexpr int kWarps = 8;
 constexpr int kBlockK = 64;
+
+// 8 warps a CTA, two CTAs an SM; or, where those do not hold all rows of W at once, 4 warps, five CTAs, with
+// fewer loads in flight a warp. 1 and 8 tokens, fp16 (us): 4096 rows of 11008 (256 CTAs) 16.4 and 17.4 with 8 warps,
+// 31.6 and 31.9 with 4; 11008 rows of 4096 (688 CTAs) 18.7 and 20.1, 17.2 and 17.6; gated 32.5 and 33.3, 29.2 and 29.5.
+template <int WARPS, bool GATED>
+struct Cfg {
+    static constexpr int kCtas = WARPS == 8 ? 2 : 5;
+    static constexpr int kRing = WARPS == 8 ? (GATED ? 2 : 4) : (GATED ? 1 : 3);
+};
 
 struct FewArgs {
     const uint8_t *x, *w[2];
@@ -35,6 +45,13 @@ struct FewArgs {
     int64_t ld_y;
     int y_type;
 };
+// (kept apart: with these in the struct the dense kernel took 19.3 us instead of 16.1 for 4096 rows of 11008)
+struct FewGatedArgs : FewArgs {
+    void *g, *u;  // checkpoints of y_type, or NULL
+    int64_t ld_g, ld_u;
+};
+template <bool GATED>
+using ArgsOf = std::conditional_t<GATED, FewGatedArgs, FewArgs>;
 
 // d += A (16 x 16, W) x B (16 x 8, X)
 template <bool BF16>
@@ -56,31 +73,36 @@ template <int NW>
 struct Weights {
     uint4 v[NW][2][2];  // [matrix][row g, g + 8][step]
 };
+template <int NT>
 struct Tokens {
-    uint4 v[2];  // of token g
+    uint4 v[NT][2];  // of tokens g, g + 8
 };
 
-template <bool BF16, bool GATED>
-__global__ void __launch_bounds__(32 * kWarps, 2) dense_decode_kernel(const FewArgs a) {
-    constexpr int NW = GATED ? 2 : 1, kRing = GATED ? 2 : 4;
-    __shared__ float part[NW][kWarps][kFewTokens][kRows + 1];
+// NT: groups of 8 tokens.
+template <bool BF16, bool GATED, int NT, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, Cfg<kWarps, GATED>::kCtas) dense_decode_kernel(const ArgsOf<GATED> a) {
+    constexpr int NW = GATED ? 2 : 1, kRing = Cfg<kWarps, GATED>::kRing;
+    __shared__ float part[NW][kWarps][8 * NT][kRows + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, i = lane & 3;
     const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows;
     // rows and tokens past the edges: the last ones again (their sums are not stored)
     const int64_t row0 = min(r0 + g, a.R - 1), row1 = min(r0 + g + 8, a.R - 1), last = a.T - 1;
     const int full = static_cast<int>(a.K / kBlockK);
-    const uint8_t *w0[NW], *w1[NW];
+    const uint8_t *w0[NW], *w1[NW], *x0[NT];
 #pragma unroll
     for (int m = 0; m < NW; ++m) {
         w0[m] = a.w[m] + row0 * a.ld_w[m] + 16 * i;
         w1[m] = a.w[m] + row1 * a.ld_w[m] + 16 * i;
     }
-    const uint8_t* x0 = a.x + min(static_cast<int64_t>(g), last) * a.ld_x + 16 * i;
-    float sum[NW][4], d[NW][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) x0[n] = a.x + min(static_cast<int64_t>(g + 8 * n), last) * a.ld_x + 16 * i;
+    float sum[NW][NT][4], d[NW][NT][4];
 #pragma unroll
     for (int m = 0; m < NW; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum[m][e] = d[m][e] = 0.f;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[m][n][e] = d[m][n][e] = 0.f;
 
     auto load_w = [&](Weights<NW>& w, int b) {
         const int64_t at = static_cast<int64_t>(b) * 128;
@@ -92,31 +114,39 @@ __global__ void __launch_bounds__(32 * kWarps, 2) dense_decode_kernel(const FewA
                 w.v[m][1][h] = load_once(w1[m] + at + 64 * h);
             }
     };
-    auto load_x = [&](Tokens& x, int b) {
+    auto load_x = [&](Tokens<NT>& x, int b) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) x.v[h] = __ldg(reinterpret_cast<const uint4*>(x0 + static_cast<int64_t>(b) * 128 + 64 * h));
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                x.v[n][h] = __ldg(reinterpret_cast<const uint4*>(x0[n] + static_cast<int64_t>(b) * 128 + 64 * h));
     };
-    auto multiply = [&](const Weights<NW>& w, const Tokens& x) {
+    auto multiply = [&](const Weights<NW>& w, const Tokens<NT>& x) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int m = 0; m < NW; ++m) {
                 const uint4 &p = w.v[m][0][h], &q = w.v[m][1][h];
-                mma<BF16>(d[m], p.x, q.x, p.y, q.y, x.v[h].x, x.v[h].y);
-                mma<BF16>(d[m], p.z, q.z, p.w, q.w, x.v[h].z, x.v[h].w);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    mma<BF16>(d[m][n], p.x, q.x, p.y, q.y, x.v[n][h].x, x.v[n][h].y);
+                    mma<BF16>(d[m][n], p.z, q.z, p.w, q.w, x.v[n][h].z, x.v[n][h].w);
+                }
             }
     };
     auto take = [&] {  // the MMAs' sums: d[0], d[1]: row g, tokens 2i and 2i + 1; d[2], d[3]: row g + 8
 #pragma unroll
         for (int m = 0; m < NW; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                sum[m][e] += d[m][e];
-                d[m][e] = 0.f;
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sum[m][n][e] += d[m][n][e];
+                    d[m][n][e] = 0.f;
+                }
     };
     Weights<NW> ring[kRing];
-    Tokens cur, next;
+    Tokens<NT> cur, next;
     let_next_grid_start();
     after_previous_grid();
 #pragma unroll
@@ -145,7 +175,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) dense_decode_kernel(const FewA
                 ring[0].v[m][0][h] = load_edge(w0[m] - 16 * i, at + 64 * h, end, row0 == a.R - 1);
                 ring[0].v[m][1][h] = load_edge(w1[m] - 16 * i, at + 64 * h, end, row1 == a.R - 1);
             }
-            cur.v[h] = load_edge(x0 - 16 * i, at + 64 * h, end, g >= last);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) cur.v[n][h] = load_edge(x0[n] - 16 * i, at + 64 * h, end, g + 8 * n >= last);
         }
         multiply(ring[0], cur);
         take();
@@ -153,34 +184,52 @@ __global__ void __launch_bounds__(32 * kWarps, 2) dense_decode_kernel(const FewA
 #pragma unroll
     for (int m = 0; m < NW; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) part[m][warp][2 * i + (e & 1)][g + 8 * (e >> 1)] = sum[m][e];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) part[m][warp][8 * n + 2 * i + (e & 1)][g + 8 * (e >> 1)] = sum[m][n][e];
     __syncthreads();
-    const int t = threadIdx.x / kRows, j = threadIdx.x % kRows;
-    if (t >= kFewTokens || t >= a.T || r0 + j >= a.R) return;
-    float v[NW];
+    for (int k = threadIdx.x; k < 8 * NT * kRows; k += 32 * kWarps) {
+        const int t = k / kRows, j = k % kRows;
+        if (t >= a.T || r0 + j >= a.R) continue;
+        float v[NW];
 #pragma unroll
-    for (int m = 0; m < NW; ++m) {
-        v[m] = part[m][0][t][j];
+        for (int m = 0; m < NW; ++m) {
+            v[m] = part[m][0][t][j];
 #pragma unroll
-        for (int k = 1; k < kWarps; ++k) v[m] += part[m][k][t][j];
+            for (int w = 1; w < kWarps; ++w) v[m] += part[m][w][t][j];
+        }
+        if constexpr (GATED) {
+            if (a.g) {
+                store_any(a.g, a.y_type, t * a.ld_g + r0 + j, v[0]);
+                store_any(a.u, a.y_type, t * a.ld_u + r0 + j, v[1]);
+            }
+        }
+        if (a.bias) v[0] += load_any(a.bias, a.bias_type, r0 + j);
+        float y = a.act == VNM_ACT_SILU ? v[0] * sigmoid(v[0]) : activate(a.act, v[0]);
+        if (GATED) y *= v[NW - 1];
+        if (a.res) y += load_any(a.res, a.y_type, t * a.ld_res + r0 + j);
+        store_any(a.y, a.y_type, t * a.ld_y + r0 + j, y);
     }
-    if (a.bias) v[0] += load_any(a.bias, a.bias_type, r0 + j);
-    float y = a.act == VNM_ACT_SILU ? v[0] * sigmoid(v[0]) : activate(a.act, v[0]);
-    if (GATED) y *= v[NW - 1];
-    if (a.res) y += load_any(a.res, a.y_type, t * a.ld_res + r0 + j);
-    store_any(a.y, a.y_type, t * a.ld_y + r0 + j, y);
+}
+
+template <bool BF16, bool GATED, int NT>
+cudaError_t launch(const FewGatedArgs& all, int sm_count, cudaStream_t stream) {
+    const ArgsOf<GATED>& a = all;
+    const int64_t blocks = (a.R + kRows - 1) / kRows;
+    return blocks <= 2 * sm_count ? launch_early(dense_decode_kernel<BF16, GATED, NT, 8>, blocks, 256, 0, 1, stream, a)
+                                  : launch_early(dense_decode_kernel<BF16, GATED, NT, 4>, blocks, 128, 0, 1, stream, a);
 }
 
 template <bool BF16, bool GATED>
-cudaError_t launch(const FewArgs& a, cudaStream_t stream) {
-    return launch_early(dense_decode_kernel<BF16, GATED>, (a.R + kRows - 1) / kRows, 32 * kWarps, 0, 1, stream, a);
+cudaError_t launch(const FewGatedArgs& all, int sm_count, cudaStream_t stream) {
+    return all.T <= 8 ? launch<BF16, GATED, 1>(all, sm_count, stream) : launch<BF16, GATED, 2>(all, sm_count, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_few_tokens(const ProductArgs& p, cudaStream_t stream) {
+cudaError_t launch_few_tokens(const ProductArgs& p, int sm_count, cudaStream_t stream) {
     const bool gated = p.kind == kGatedPair;
-    FewArgs a{};
+    FewGatedArgs a{};
     a.x = static_cast<const uint8_t*>(p.x[0].p);
     a.ld_x = 2 * p.x[0].ld;
     for (int m = 0; m < (gated ? 2 : 1); ++m) {
@@ -198,8 +247,14 @@ cudaError_t launch_few_tokens(const ProductArgs& p, cudaStream_t stream) {
     a.y = p.y[0];
     a.ld_y = p.ld_y;
     a.y_type = p.y_type;
-    if (gated) return p.bf16 ? launch<true, true>(a, stream) : launch<false, true>(a, stream);
-    return p.bf16 ? launch<true, false>(a, stream) : launch<false, false>(a, stream);
+    if (p.keep == kKeep16) {
+        a.g = p.g.p;
+        a.u = p.u.p;
+        a.ld_g = p.g.ld;
+        a.ld_u = p.u.ld;
+    }
+    if (gated) return p.bf16 ? launch<true, true>(a, sm_count, stream) : launch<false, true>(a, sm_count, stream);
+    return p.bf16 ? launch<true, false>(a, sm_count, stream) : launch<false, false>(a, sm_count, stream);
 }
 
 }  // namespace vnm

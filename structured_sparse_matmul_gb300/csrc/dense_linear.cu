@@ -106,6 +106,13 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+// `bytes` of this CTA's shared memory to that of a CTA of the cluster, counted on a barrier there.
+__device__ __forceinline__ void copy_to_cluster(uint32_t cluster_dst, uint32_t src, uint32_t bytes, uint32_t cluster_bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(cluster_dst),
+                 "r"(src), "r"(bytes), "r"(cluster_bar)
+                 : "memory");
+}
+
 // An operand's 128 x 64 part of a stage in shared memory, 128B swizzle. K along the rows: 128-byte
 // rows, 8-row groups 1024 bytes apart; an MMA (16 of K) takes 32 bytes of every row.
 // Transposed: two boxes of 64 operand rows, 8192 bytes apart; in a box 128-byte lines of
@@ -147,14 +154,20 @@ __device__ __forceinline__ void st_shared_f4(uint32_t addr, float a, float b, fl
 
 // ------------------------------------------------------------------ pairs of CTAs
 
-constexpr int kPairRing = 160 * 1024;  // 5 stages of 128 rows of X and 128 of W, or more of less
-constexpr int kPairMaxStages = 6;
+// 6 stages of 128 rows of X and 128 of W, or more of less: a stage's way round (loads of a microsecond, its MMAs, the
+// barriers) takes 1.4 us, its MMAs 0.27 (a K block took 0.42, 0.35 and 0.285 us with 3, 4 and 5 stages).
+constexpr int kPairRing = 192 * 1024;
+constexpr int kPairMaxStages = 8;
 constexpr int kPairHelpers = 4, kPairEpilogue = 8;
 constexpr int kPairThreads = 32 * (kPairHelpers + kPairEpilogue);
-// A warp's staged outputs: two boxes of 32 rows x 128 bytes. Of a gated pair a box holds 32 rows x 32 features
-// of Y and of the checkpoints: 2 KB, or 4 with 8-bit ones (two boxes), or 6 with 16-bit ones (one).
-constexpr int kStageOut = 8192;
+// A warp's staged outputs: two boxes of 32 rows x 64 bytes. Of a gated pair a box holds 32 rows x 32 features
+// of Y, and with 8-bit checkpoints theirs (one box), or 16 features of Y and of 16-bit checkpoints (one).
+constexpr int kStageOut = 4096;
+constexpr int kSumBytes = kTile * 1024;  // a split's sums of a CTA's rows; the rest of the memory takes the other pairs'
 constexpr int kPairSmem = kPairRing + kPairEpilogue * kStageOut + 1024;
+static_assert(kSumBytes + (kMaxPairSplits - 1) * (kTile / kMaxPairSplits) * 1024 <= kPairRing + kPairEpilogue * kStageOut &&
+                  kSumBytes + 2 * ((kTile + 2) / 3) * 1024 <= kPairRing + kPairEpilogue * kStageOut,
+              "the splits' sums fit");
 static_assert(kPairSmem > 116 * 1024 && kPairSmem <= 226 * 1024, "one CTA an SM: each holds all of its TMEM");
 // Registers of the variant that adds chunks up: 128 sums and a load of 32 columns do not fit the 168 that
 // 12 warps get; the epilogue takes what the helper warps leave (in warps: 4 x 56 + 8 x 224 = 12 x 168).
@@ -245,6 +258,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __shared__ __align__(8) uint64_t acce_bar[2];    // and has been read by both CTAs (the first CTA's)
     // of each epilogue warp's two output boxes: the residual's box has landed in it
     __shared__ __align__(8) uint64_t res_bar[GATED ? 1 : kPairEpilogue][2];
+    __shared__ __align__(8) uint64_t split_bar;  // the other pairs' sums of this CTA's rows have landed
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
 
@@ -269,6 +283,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(smem_u32(&acce_bar[s]), 2 * kPairEpilogue);
             for (int w = 0; !GATED && w < kPairEpilogue; ++w) mbar_init(smem_u32(&res_bar[w][s]), 1);
         }
+        mbar_init(smem_u32(&split_bar), 1);
         abort_flag = 0;
         fence_barrier_init();
     }
@@ -418,7 +433,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             // this warp's columns of the tile (a gated pair's features): first .. last - 1
             const int cols = GATED ? a.tile_n / 2 : a.tile_n, first = half * (kTileN / 2), last = min(cols, first + kTileN / 2);
             const int64_t n_tile = static_cast<int64_t>(nt) * cols, end = min(o.R, n_tile + cols);
-            const void* const res = GATED || SPLIT ? nullptr : o.res[seg];
+            // Where sums are added up in registers they may start from the residual, read while the MMAs run.
+            const bool from_res = SUM && !GATED && !SPLIT && o.act == VNM_ACT_NONE && o.res[seg] != nullptr;
+            const void* const res = GATED || SPLIT || from_res ? nullptr : o.res[seg];
             if (!GATED && res != nullptr && o.res_vec && m < o.T && n_tile + first < end) {
                 // the residual's row is on its way to L2 while the MMAs run
                 const int size = o.y_type == VNM_F32 ? 4 : 2;
@@ -439,7 +456,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 return r;
             };
             const bool f32 = o.y_type == VNM_F32, bf16 = o.y_type == VNM_BF16, res_tma = res != nullptr && (ALIGNED || o.res_vec);
-            const int box_cols = f32 ? 32 : 64;
+            const int box_cols = f32 ? 16 : 32;
             // the residual's box from column c on, into output box `at`, whose last store has read it; the outputs then
             // take its place
             auto request = [&](int c, int at) {
@@ -449,8 +466,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (lane == 0) {
                     tma_store_wait_all_read();
                     const uint32_t bar = smem_u32(&res_bar[GATED ? 0 : warp - kPairHelpers][at & 1]);
-                    mbar_arrive_expect_tx(bar, 4096);
-                    tma_load_2d(stage + 4096 * (at & 1), &outs.res[seg], static_cast<int32_t>(n_tile + c), static_cast<int32_t>(m0), bar);
+                    mbar_arrive_expect_tx(bar, 2048);
+                    tma_load_2d(stage + 2048 * (at & 1), &outs.res[seg], static_cast<int32_t>(n_tile + c), static_cast<int32_t>(m0), bar);
                 }
                 __syncwarp();
                 res_pending |= 1u << (at & 1);
@@ -463,6 +480,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 float sum[128];
 #pragma unroll
                 for (int c = 0; c < 128; ++c) sum[c] = 0.f;
+                if constexpr (!GATED && !SPLIT) {
+                    if (from_res && m < o.T) {
+#pragma unroll
+                        for (int c = 0; c < 128; c += 8) {
+                            const Cols at{n_tile + first + c, end, 1, ALIGNED || o.res_vec};
+                            if (at.none()) continue;
+                            float v[8];
+                            widen_raw8(load_raw8(o.res[seg], o.y_type, m * o.ld_res, at), o.y_type, v);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) sum[c + j] = v[j];
+                        }
+                    }
+                }
                 const auto column = [&](int c) { return half * (GATED && !SPLIT ? 64 : 128) + c + (GATED && !SPLIT && c >= 64 ? 64 : 0); };
                 for (int kb0 = kb_first; kb0 < kb_last; kb0 += a.chunk_kb) {
                     if (!wait_sum()) break;
@@ -485,6 +515,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     for (int u = 0; u < 32; ++u)
                         st_shared_f4(sum_piece(smem_base, row, 32 * half + u), sum[4 * u], sum[4 * u + 1], sum[4 * u + 2],
                                      sum[4 * u + 3]);
+                    fence_proxy_async_smem();
                 } else {
                     if constexpr (GATED) {
                         if (o.keep == kKeep8) {
@@ -546,7 +577,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     else
                         release();
                     const int in = c & (box_cols - 1);  // the columns' place in their box
-                    const uint32_t buf = stage + 4096 * (box & 1);
+                    const uint32_t buf = stage + 2048 * (box & 1);
                     const bool landed = res_tma && m0 < o.T && n_tile + c - in < end;
                     if (in == 0) {
                         if (landed) {
@@ -571,7 +602,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     if (landed && f32) {
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
-                            const float4 w = ld_shared_v4(box_piece<128>(buf, lane, in / 4 + u));
+                            const float4 w = ld_shared_v4(box_piece<64>(buf, lane, u));
                             v[4 * u] += w.x, v[4 * u + 1] += w.y, v[4 * u + 2] += w.z, v[4 * u + 3] += w.w;
                         }
                     } else if (landed || (!ALIGNED && res != nullptr && !res_tma)) {
@@ -579,7 +610,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         for (int h = 0; h < 2; ++h) {
                             float w[8];
                             if (ALIGNED || landed) {
-                                const float4 q = ld_shared_v4(box_piece<128>(buf, lane, in / 8 + h));
+                                const float4 q = ld_shared_v4(box_piece<64>(buf, lane, in / 8 + h));
                                 widen8(make_uint4(__float_as_uint(q.x), __float_as_uint(q.y), __float_as_uint(q.z), __float_as_uint(q.w)),
                                        bf16, w);
                             } else {
@@ -592,23 +623,23 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     if (f32) {
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            st_shared_f4(box_piece<128>(buf, lane, in / 4 + u), v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+                            st_shared_f4(box_piece<64>(buf, lane, u), v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
                     } else {
                         uint32_t w[8];
 #pragma unroll
                         for (int u = 0; u < 8; ++u) w[u] = bf16 ? to_bf16x2(v[2 * u], v[2 * u + 1]) : to_f16x2(v[2 * u], v[2 * u + 1]);
-                        st_shared_v4(box_piece<128>(buf, lane, in / 8), w[0], w[1], w[2], w[3]);
-                        st_shared_v4(box_piece<128>(buf, lane, in / 8 + 1), w[4], w[5], w[6], w[7]);
+                        st_shared_v4(box_piece<64>(buf, lane, in / 8), w[0], w[1], w[2], w[3]);
+                        st_shared_v4(box_piece<64>(buf, lane, in / 8 + 1), w[4], w[5], w[6], w[7]);
                     }
-                    // (half way, so that the last box's store has read the other one)
-                    if (in == box_cols / 2 && c - in + box_cols < last) request(c - in + box_cols, box + 1);
+                    // (at the box's end, so that the last box's store has read the other one)
+                    if (in == box_cols - 16 && c + 16 < last) request(c + 16, box + 1);
                     if (in + 16 < box_cols) continue;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (f32)
-                        emit_box<128, 4, ALIGNED>(&outs.y[seg], o.y_tma, o.y[seg], o.ld_y, m0, n_tile + c - 16, o.T, end, buf, lane);
+                        emit_box<64, 4, ALIGNED>(&outs.y[seg], o.y_tma, o.y[seg], o.ld_y, m0, n_tile + c, o.T, end, buf, lane);
                     else
-                        emit_box<128, 2, ALIGNED>(&outs.y[seg], o.y_tma, o.y[seg], o.ld_y, m0, n_tile + c - 48, o.T, end, buf, lane);
+                        emit_box<64, 2, ALIGNED>(&outs.y[seg], o.y_tma, o.y[seg], o.ld_y, m0, n_tile + c - 16, o.T, end, buf, lane);
                     if (lane == 0) tma_store_commit();
                     ++box;
                 }
@@ -619,7 +650,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     tmem_ld(taddr + first, next);
                     tmem_ld(taddr + cols + first, next_u);
                 }
-                const bool twice = o.keep != kKeep16;
+                const bool twice = o.keep == kKeepNone;  // two boxes
+                const int box_cols = o.keep == kKeep16 ? 16 : 32;
 #pragma unroll 1
                 for (int c = first; c < last; c += 16) {
                     float g[16], u[16];
@@ -636,8 +668,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     } else {
                         release();
                     }
-                    const int in = c & 16;
-                    const uint32_t buf = stage + (twice ? 4096 * (box & 1) : 0);
+                    const int in = c & (box_cols - 1);
+                    const uint32_t buf = stage + (twice ? 2048 * (box & 1) : 0);
                     if (in == 0) {
                         if (lane == 0) {
                             if (twice)
@@ -647,12 +679,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         }
                         __syncwarp();
                     }
-                    auto stage16 = [&](uint32_t to, const float (&v)[16]) {
-                        uint32_t w[8];
+                    auto pack16 = [&](const float (&v)[16], uint32_t (&w)[8]) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) w[j] = bf16 ? to_bf16x2(v[2 * j], v[2 * j + 1]) : to_f16x2(v[2 * j], v[2 * j + 1]);
-                        st_shared_v4(box_piece<64>(to, lane, in / 8), w[0], w[1], w[2], w[3]);
-                        st_shared_v4(box_piece<64>(to, lane, in / 8 + 1), w[4], w[5], w[6], w[7]);
+                    };
+                    auto stage16 = [&](uint32_t to, const float (&v)[16]) {  // rows of 32 bytes
+                        uint32_t w[8];
+                        pack16(v, w);
+                        st_shared_v4(box_piece<32>(to, lane, 0), w[0], w[1], w[2], w[3]);
+                        st_shared_v4(box_piece<32>(to, lane, 1), w[4], w[5], w[6], w[7]);
                     };
                     auto stage8 = [&](uint32_t to, const float (&v)[16], float s, float inv) {
                         uint32_t w[4];
@@ -663,8 +698,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         st_shared_v4(box_piece<32>(to, lane, in / 16), w[0], w[1], w[2], w[3]);
                     };
                     if (o.keep == kKeep16) {
-                        stage16(buf + 2048, g);
-                        stage16(buf + 4096, u);
+                        stage16(buf + 1024, g);
+                        stage16(buf + 2048, u);
                     } else if (o.keep == kKeep8) {
                         stage8(buf + 2048, g, scale.g, scale.g_inv);
                         stage8(buf + 3072, u, scale.u, scale.u_inv);
@@ -672,16 +707,26 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     activate_all(o.act, g);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) g[j] *= u[j];
-                    stage16(buf, g);
-                    if (in == 0) continue;
+                    if (o.keep == kKeep16) {
+                        stage16(buf, g);
+                    } else {
+                        uint32_t w[8];
+                        pack16(g, w);
+                        st_shared_v4(box_piece<64>(buf, lane, in / 8), w[0], w[1], w[2], w[3]);
+                        st_shared_v4(box_piece<64>(buf, lane, in / 8 + 1), w[4], w[5], w[6], w[7]);
+                    }
+                    if (in + 16 < box_cols) continue;
                     fence_proxy_async_smem();
                     __syncwarp();
-                    const int64_t n0 = n_tile + c - 16;
-                    emit_box<64, 2, ALIGNED>(&outs.y[0], o.y_tma, o.y[0], o.ld_y, m0, n0, o.T, end, buf, lane);
+                    const int64_t n0 = n_tile + c - in;
                     if (o.keep == kKeep16) {
-                        emit_box<64, 2, ALIGNED>(&outs.g, o.keep_tma, o.g.p, o.g.ld, m0, n0, o.T, end, buf + 2048, lane);
-                        emit_box<64, 2, ALIGNED>(&outs.u, o.keep_tma, o.u.p, o.u.ld, m0, n0, o.T, end, buf + 4096, lane);
-                    } else if (o.keep == kKeep8) {
+                        emit_box<32, 2, ALIGNED>(&outs.y[0], o.y_tma, o.y[0], o.ld_y, m0, n0, o.T, end, buf, lane);
+                        emit_box<32, 2, ALIGNED>(&outs.g, o.keep_tma, o.g.p, o.g.ld, m0, n0, o.T, end, buf + 1024, lane);
+                        emit_box<32, 2, ALIGNED>(&outs.u, o.keep_tma, o.u.p, o.u.ld, m0, n0, o.T, end, buf + 2048, lane);
+                    } else {
+                        emit_box<64, 2, ALIGNED>(&outs.y[0], o.y_tma, o.y[0], o.ld_y, m0, n0, o.T, end, buf, lane);
+                    }
+                    if (o.keep == kKeep8) {
                         emit_box<32, 1, ALIGNED>(&outs.g, o.keep_tma, o.g.p, o.g.ld, m0, n0, o.T, end, buf + 2048, lane);
                         emit_box<32, 1, ALIGNED>(&outs.u, o.keep_tma, o.u.p, o.u.ld, m0, n0, o.T, end, buf + 3072, lane);
                     }
@@ -704,51 +749,58 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tmem_dealloc_group<2>(tmem, 512);
     }
     if constexpr (SPLIT) {
-        // add the pairs' sums, in their order, each pair a share of the rows
+        // Add the pairs' sums, in their order, each pair a share of the rows: every CTA copies the other shares to their
+        // owners, behind the owners' own sums (reading them there instead, 16 bytes a lane, took 7 us).
         const OutArgs& o = a.o;
         const bool vec = all_vec(o);
+        const int share = (kTile + a.splits - 1) / a.splits, row0 = pair * share, row1 = min(kTile, row0 + share);
+        const uint32_t bar = smem_u32(&split_bar), landing = smem_base + kSumBytes;
+        if (threadIdx.x == 0) {
+            mbar_arrive_expect_tx(bar, static_cast<uint32_t>((a.splits - 1) * (row1 - row0) * 1024));
+            for (int p = 0; p < a.splits; ++p) {
+                if (p == pair) continue;
+                const int first = p * share, rows = min(kTile, first + share) - first, slot = pair < p ? pair : pair - 1;
+                copy_to_cluster(dsmem_map(landing + slot * share * 1024, 2 * p + rank), smem_base + first * 1024,
+                                static_cast<uint32_t>(rows * 1024), dsmem_map(bar, 2 * p + rank));
+            }
+        }
         int mt, nt;
         tile_at(a, tile0, mt, nt);
         const int seg = a.kind == kTwoByRows && mt >= a.x_tiles ? 1 : 0;
         const int64_t m0 = static_cast<int64_t>((mt - seg * a.x_tiles) * 2 + rank) * kTile;
-        const int share = (kTile + a.splits - 1) / a.splits, row0 = pair * share, row1 = min(kTile, row0 + share);
         constexpr int kLanes = GATED ? 16 : 32, kRowsAtOnce = 32 / kLanes;  // of a row
         const int q = lane & (kLanes - 1);
         const int local = vec ? 8 * q : q, step = vec ? 1 : kLanes;
         const Cols c{static_cast<int64_t>(nt) * kTileN + local, o.R, step, vec};
         float b[8];
         bias8(o, c, b);
+        const bool landed = mbar_wait_warp(bar, 0, abort);
 #pragma unroll 1
-        for (int base = row0 + kRowsAtOnce * warp; base < row1; base += kRowsAtOnce * (kPairThreads / 32)) {
-            const int row = base + lane / kLanes;
+        for (int base = row0 + kRowsAtOnce * warp; base < row1 && landed; base += kRowsAtOnce * (kPairThreads / 32)) {
+            const int row = min(base + lane / kLanes, row1 - 1);
             const int64_t t = m0 + row;
-            const bool here = row < row1 && t < o.T;
+            const bool here = base + lane / kLanes < row1 && t < o.T;
             float v[GATED ? 2 : 1][8];
             Raw8 r;
             if (!GATED && here && o.res[seg] != nullptr && !c.none()) r = load_raw8(o.res[seg], o.y_type, t * o.ld_res, c);
 #pragma unroll
             for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-                const int at = min(row, kTile - 1), col = 128 * h + local;
-                float w[kMaxPairSplits][8];  // all in flight at once
+                const int col = 128 * h + local;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[h][j] = 0.f;
 #pragma unroll
                 for (int s = 0; s < kMaxPairSplits; ++s) {
                     if (s >= a.splits) break;
-                    const uint32_t from = dsmem_map(smem_base, 2 * s + rank);
+                    // (the pieces keep the order that row & 7 gave them)
+                    const uint32_t from = s == pair ? smem_base : landing + ((s < pair ? s : s - 1) * share - row0) * 1024;
                     if (vec) {
-                        const float4 x = dsmem_ld_v4(sum_piece(from, at, col >> 2)), y = dsmem_ld_v4(sum_piece(from, at, (col >> 2) + 1));
-                        w[s][0] = x.x, w[s][1] = x.y, w[s][2] = x.z, w[s][3] = x.w;
-                        w[s][4] = y.x, w[s][5] = y.y, w[s][6] = y.z, w[s][7] = y.w;
+                        const float4 x = ld_shared_v4(sum_piece(from, row, col >> 2)), y = ld_shared_v4(sum_piece(from, row, (col >> 2) + 1));
+                        v[h][0] += x.x, v[h][1] += x.y, v[h][2] += x.z, v[h][3] += x.w;
+                        v[h][4] += y.x, v[h][5] += y.y, v[h][6] += y.z, v[h][7] += y.w;
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) w[s][j] = dsmem_ld_f32(sum_at(from, at, col + step * j));
+                        for (int j = 0; j < 8; ++j) v[h][j] += ld_shared_f32(sum_at(from, row, col + step * j));
                     }
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    v[h][j] = w[0][j];
-#pragma unroll
-                    for (int s = 1; s < kMaxPairSplits; ++s)
-                        if (s < a.splits) v[h][j] += w[s][j];
                 }
             }
             if constexpr (GATED) {
@@ -762,7 +814,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 finish8(o, seg, t, c, v[0], b, r);
             }
         }
-        cluster_sync_all();  // no CTA leaves while others read its sums
+        cluster_sync_all();  // no CTA leaves while its sums are copied from it
     }
     if (threadIdx.x == 0 && abort_flag) record_error(a.status ? a.status : g_status, VNM_ERR_TIMEOUT, 13);
 }
@@ -1084,23 +1136,23 @@ bool encode_outputs(OutMaps* m, const ProductArgs& p, const OutArgs& o) {
                : t == VNM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                               : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     };
-    const bool gated = p.kind == kGatedPair, eight = p.keep == kKeep8;
-    const int e = p.y_type == VNM_F32 ? 4 : 2;
+    const bool gated = p.kind == kGatedPair, eight = p.keep == kKeep8, sixteen = p.keep == kKeep16;
+    const int e = p.y_type == VNM_F32 ? 4 : 2, wide = sixteen ? 16 : 64 / e;  // columns of a box of Y
     *m = OutMaps{};
     if (o.y_tma)
         for (int i = 0; i < (p.kind == kTwoByRows ? 2 : 1); ++i)
-            if (!encode_2d(&m->y[i], type(p.y_type), p.y[i], p.R, p.T, p.ld_y * e, gated ? 32 : 128 / e, 32,
-                           gated ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+            if (!encode_2d(&m->y[i], type(p.y_type), p.y[i], p.R, p.T, p.ld_y * e, wide, 32,
+                           sixteen ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B))
                 return false;
-    if (p.residual[0] != nullptr && o.res_vec)
+    if (!gated && p.residual[0] != nullptr && o.res_vec)
         for (int i = 0; i < (p.kind == kTwoByRows ? 2 : 1); ++i)
-            if (!encode_2d(&m->res[i], type(p.y_type), p.residual[i], p.R, p.T, p.ld_residual * e, 128 / e, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+            if (!encode_2d(&m->res[i], type(p.y_type), p.residual[i], p.R, p.T, p.ld_residual * e, wide, 32, CU_TENSOR_MAP_SWIZZLE_64B))
                 return false;
     if (!o.keep_tma) return true;
     const CUtensorMapDataType t = eight ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type(p.y_type);
-    const CUtensorMapSwizzle sw = eight ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B;
-    return encode_2d(&m->g, t, p.g.p, p.R, p.T, p.g.ld * (eight ? 1 : 2), 32, 32, sw) &&
-           encode_2d(&m->u, t, p.u.p, p.R, p.T, p.u.ld * (eight ? 1 : 2), 32, 32, sw);
+    const int bytes = eight ? 1 : 2;
+    return encode_2d(&m->g, t, p.g.p, p.R, p.T, p.g.ld * bytes, 32 / bytes, 32, CU_TENSOR_MAP_SWIZZLE_32B) &&
+           encode_2d(&m->u, t, p.u.p, p.R, p.T, p.u.ld * bytes, 32 / bytes, 32, CU_TENSOR_MAP_SWIZZLE_32B);
 }
 
 template <typename Kernel>
@@ -1194,12 +1246,16 @@ struct TilePlan {
     int bn, splits, tile_n;
 };
 
-// The times the plan compares, in us: a launch with its first loads and its last stores; then the
-// longer of a CTA's chain of K blocks and of its tiles' loads from L2.
+// The times that the plan compares, in us. The constants were fitted to 218 products of random sizes (T = 9 .. 8192,
+// R = 64 .. 11008, K = 64 .. 11008, all operand orders, checkpoints or none), each timed with every plan: what the rule
+// picks is 1.6 % slower than the fastest on average, 25 % at worst. They weigh the plans against
+// each other; the absolute times are up to a third off.
 TilePlan plan_tiles(const ProductArgs& p, int sm_count) {
-    const bool gated = p.kind == kGatedPair, two = p.kind == kTwoByRows;
-    const int num_kb = static_cast<int>(ceil_div(p.K, kBlockK)) * (p.kind == kSumOfTwo ? 2 : 1);
-    const int64_t rows = ceil_div(p.T, 2 * kTile) * (two ? 2 : 1), pairs = std::max(1, sm_count / 2);
+    const bool gated = p.kind == kGatedPair, two = p.kind == kTwoByRows, keep8 = p.keep == kKeep8;
+    const int64_t e = p.y_type == VNM_F32 ? 4 : 2;
+    const bool aligned = (reinterpret_cast<uintptr_t>(p.y[0]) | static_cast<uintptr_t>(p.ld_y * e)) % 16 == 0 &&
+                         (!keep8 || (reinterpret_cast<uintptr_t>(p.g.p) | static_cast<uintptr_t>(p.g.ld)) % 16 == 0);
+    const int64_t num_kb = ceil_div(p.K, kBlockK) * (p.kind == kSumOfTwo ? 2 : 1);
     TilePlan best{0, 1, 256};
     double least = 1e30;
     auto consider = [&](const TilePlan& plan, double t) {
@@ -1208,43 +1264,68 @@ TilePlan plan_tiles(const ProductArgs& p, int sm_count) {
             best = plan;
         }
     };
+    // Pairs of CTAs. A K block takes the MMAs' time, or what the running pairs load from L2 (10.3 TB/s) or the
+    // tiles' own rows of W from memory (5.3 TB/s) takes; a tile's epilogue runs under the next one's K blocks.
+    constexpr double kSetup = 5.5, kMma = 0.43, kLeast = 0.32, kL2 = 10.3e6, kMemory = 5.3e6;
+    const int64_t row_tiles = ceil_div(p.T, 2 * kTile) * (two ? 2 : 1), pairs = std::max(1, sm_count / 2);
     for (int n = 256; n >= 128; n -= 64) {  // (boxes of 64 columns, 32 features)
-        if (n < 256 && p.keep == kKeep8) break;  // (a group of the 8-bit form is 128 features)
-        const int64_t tiles = rows * ceil_div(p.R, gated ? n / 2 : n);
-        consider({0, 1, n}, 8.0 + static_cast<double>(ceil_div(tiles, pairs)) * num_kb * 0.29 * n / 256);
+        if (n < 256 && keep8) break;        // (a group of the 8-bit form is 128 features)
+        const int64_t tiles = row_tiles * ceil_div(p.R, gated ? n / 2 : n), full = tiles / pairs, rest = tiles % pairs;
+        const double epilogue = (gated ? (keep8 ? 1.4 : 0.0) + (aligned ? 0.0 : 1.1) : aligned ? 0.9 : 6.0) * n / 256;
+        auto block = [&](int64_t active) {
+            return std::max(std::max(kMma * n / 256, kLeast),
+                            std::max(static_cast<double>(2 * active * (kOperandBytes + 64 * n)) / kL2,
+                                     static_cast<double>(active * n * 128) / static_cast<double>(row_tiles) / kMemory));
+        };
+        double t = kSetup + epilogue + static_cast<double>(full) * std::max(num_kb * block(pairs), epilogue);
+        if (rest > 0) t += std::max(num_kb * block(rest), full > 0 ? epilogue : 0.0);
+        consider({0, 1, n}, t);
     }
-    const int64_t pair_tiles = rows * ceil_div(p.R, gated ? 128 : 256);
-    for (int splits = 2; splits <= kMaxPairSplits; ++splits) {
-        const int64_t clusters = splits == 2 ? sm_count * 36 / 152 : splits == 3 ? sm_count * 23 / 152 : sm_count * 15 / 152;
-        if (splits > num_kb || pair_tiles > clusters) break;
-        consider({0, splits, 256}, 10.0 + static_cast<double>(ceil_div(num_kb, splits)) * 0.29);
+    // K over the pairs of a cluster: as many clusters as fit at once (of 4, 6 and 8 CTAs, one an SM).
+    const int64_t pair_tiles = row_tiles * ceil_div(p.R, gated ? 128 : 256);
+    for (int splits = 2; splits <= kMaxPairSplits && splits <= num_kb; ++splits) {
+        const int64_t clusters = std::max(1, sm_count * (splits == 2 ? 36 : splits == 3 ? 23 : 15) / 152);
+        consider({0, splits, 256}, kSetup + static_cast<double>(ceil_div(pair_tiles, clusters)) *
+                                                (static_cast<double>(ceil_div(num_kb, splits)) * kMma + 6.3));
     }
-    for (int bn : {16, 32, 64, 128}) {
+    // Narrow tiles, two CTAs an SM: a launch, a wave's chain of K blocks (longer where SMs run two CTAs, or as long as
+    // the loads from L2 take), its end; or the operands from memory.
+    const double memory = static_cast<double>((gated ? 2 : 1) * p.R * p.K * 2 + p.T * p.K * 2) / kMemory;
+    for (int i = 0; i < 4; ++i) {
+        const int bn = 16 << i;
+        constexpr double kStart[4] = {1.2, 1.5, 0.7, 6.3}, kBlock[4] = {0.225, 0.242, 0.272, 0.293}, kEnd[4] = {1.2, 1.5, 3.1, 0.0};
         if (bn > 16 && bn / 2 >= p.T && !(p.x[0].transposed && bn <= 64)) break;  // the width below holds all tokens
         if (p.x[0].transposed && bn < 64) continue;  // (a box of transposed X is 64 tokens)
-        const int64_t tiles = ceil_div(p.R, gated ? 64 : kTile) * ceil_div(p.T, bn) * (two ? 2 : 1);
-        const int slots = sm_count * 2;
+        const int64_t tiles = ceil_div(p.R, gated ? 64 : kTile) * ceil_div(p.T, bn) * (two ? 2 : 1), slots = 2 * sm_count;
         for (int splits : {1, 2, 3, 4, 6, 8}) {
-            if (splits * (p.keep == kKeep8 ? 2 : 1) > kMaxSplits) break;  // (two tiles a cluster)
+            if (splits * (keep8 ? 2 : 1) > kMaxSplits) break;  // (two tiles a cluster)
             if (splits > 1 && (splits > num_kb || tiles * splits > slots)) break;
-            const int64_t kbs = ceil_div(num_kb, splits), waves = ceil_div(tiles * splits, slots);
-            const double chain = static_cast<double>(waves * kbs) * (bn == 128 ? 0.40 : bn == 64 ? 0.30 : 0.25);
-            const double loads = static_cast<double>(tiles * num_kb) * (kTile + bn) * 128 / 7e6;
-            consider({bn, splits, 0}, 4.9 + std::max(chain, loads) + (splits == 8 ? 1.3 : splits > 1 ? 0.3 : 0.0));
+            const int64_t blocks = ceil_div(num_kb, splits), full = tiles * splits / slots, rest = tiles * splits % slots;
+            auto wave = [&](int64_t active) {
+                return static_cast<double>(blocks) * std::max(kBlock[i] + (active > sm_count ? 0.49 * bn / 128 : 0.0),
+                                                              static_cast<double>(active * (kOperandBytes + bn * 128)) / 10.8e6) +
+                       kEnd[i];
+            };
+            const double t = static_cast<double>(full) * wave(slots) + (rest > 0 ? wave(rest) : 0.0);
+            consider({bn, splits, 0}, kStart[i] + std::max(t, memory) + (keep8 ? 1.8 : 0.0) +
+                                          (splits > 1 ? 1.1 + (splits > 4 ? 0.7 : 0.0) + 0.0024 * bn * (splits - 1) : 0.0));
         }
     }
     return best;
 }
 
+// Up to 8 tokens; up to kFewTokens where W is so small that the narrow tiles' start weighs more (16 tokens, us: 1024 x
+// 1024 2.8 against 5.1, 4096 x 4096 8.9 and 10.0, 11008 x 4096 21.1 and 20.7; gated 3.7 and 5.8, 15.6 and 15.4, 36.7 and 31.1).
 bool few_tokens(const ProductArgs& p) {
-    return p.T <= kFewTokens && (p.kind == kOneProduct || p.kind == kGatedPair) && p.keep == kKeepNone && !p.x[0].transposed &&
-           !p.w[0].transposed;
+    const bool gated = p.kind == kGatedPair;
+    if ((p.kind != kOneProduct && !gated) || p.keep == kKeep8 || p.x[0].transposed || p.w[0].transposed) return false;
+    return p.T <= 8 || (p.T <= kFewTokens && p.R * p.K * (gated ? 2 : 1) <= (1 << 24));
 }
 
 }  // namespace
 
 void product_plan(const ProductArgs& p, int sm_count, int* tile_tokens, int* splits) {
-    TilePlan plan{kFewTokens, 1, 0};
+    TilePlan plan{8, 1, 0};
     if (!few_tokens(p)) plan = plan_tiles(p, sm_count);
     *tile_tokens = plan.bn;
     *splits = plan.splits;
@@ -1263,7 +1344,7 @@ cudaError_t take_product_status(int* code, cudaStream_t stream) {
 }
 
 cudaError_t launch_product(const ProductArgs& p, int sm_count, cudaStream_t stream) {
-    if (p.K > 0 && p.skip_stage < 0 && few_tokens(p)) return launch_few_tokens(p, stream);
+    if (p.K > 0 && p.skip_stage < 0 && few_tokens(p)) return launch_few_tokens(p, sm_count, stream);
     GemmArgs a{};
     OutArgs& o = a.o;
     auto rows_aligned = [](const void* q, int64_t ld_bytes, int n) {

@@ -81,16 +81,16 @@ struct ProductArgs {
 cudaError_t launch_product(const ProductArgs& a, int sm_count, cudaStream_t stream);
 
 // Which kernel takes a product (K >= 1), by the rule that launch_product goes by: tiles of 16, 32, 64
-// or 128 tokens with K over `splits` CTAs; pairs of CTAs (0); the few-token kernel (kFewTokens).
-constexpr int kFewTokens = 8;
+// or 128 tokens with K over `splits` CTAs; pairs of CTAs (0), K over `splits` pairs; the few-token kernel (8).
+constexpr int kFewTokens = 16;  // the most that it takes
 void product_plan(const ProductArgs& a, int sm_count, int* tile_tokens, int* splits);
 
 // The first error that products without status words recorded on the current device, and clears it.
 cudaError_t take_product_status(int* code, cudaStream_t stream);
 
-// The same product for up to kFewTokens tokens: kOneProduct or kGatedPair without
+// The same product for up to kFewTokens tokens: kOneProduct or kGatedPair without 8-bit
 // checkpoints, both operands row-major.
-cudaError_t launch_few_tokens(const ProductArgs& a, cudaStream_t stream);
+cudaError_t launch_few_tokens(const ProductArgs& a, int sm_count, cudaStream_t stream);
 
 // dg = dy * u * act'(g), du = dy * act(g), h = act(g) * u, element by element.
 struct GatedGradArgs {
