@@ -105,7 +105,7 @@ struct FlArgs {
     void* y;
     int64_t y_ms, y_ns;
     int y_type;
-    bool y_tma;    // Y's rows start on 16 bytes: pairs write it by TMA stores
+    bool y_tma;    // Y's rows start and end on 16 bytes: pairs write it by TMA stores
     const void* bias;
     int bias_type;
     bool bias_on_m;
@@ -624,8 +624,8 @@ __global__ void __launch_bounds__(FlCfg<BN, ONE, CG>::kThreads, FlCfg<BN, ONE, C
             }
             if (CG == 2) {
                 // 128 bytes of 32 rows at a time, 128B-swizzled, then one TMA store (which
-                // leaves out what lies past Y's edges), or, where Y's rows are not 16-byte
-                // aligned, a copy row by row
+                // leaves out what lies past Y's edges), or, where Y's rows do not start and end on
+                // 16 bytes, a copy row by row
                 constexpr int kBoxCols = F32 ? 32 : 64;
                 const bool bf16 = a.y_type == VNM_BF16;
                 const uint32_t bufs = smem_base + ST * Cfg::kStageBytes + (warp - kHelpers) * 2 * kStoreBox;
@@ -891,7 +891,9 @@ cudaError_t launch_fp8_linear(const void* xq, int64_t ld_x, bool x_e5m2, const S
     a.y_ms = g.y_ms;
     a.y_ns = g.y_ns;
     a.y_type = y_type;
-    const uintptr_t align = reinterpret_cast<uintptr_t>(y) | (static_cast<uintptr_t>(ld_y) * (y_type == VNM_F32 ? 4 : 2));
+    // (a TMA store that ends inside 16 bytes writes all of them: Y's rows must end on 16 too)
+    const uintptr_t elem = y_type == VNM_F32 ? 4 : 2;
+    const uintptr_t align = reinterpret_cast<uintptr_t>(y) | static_cast<uintptr_t>(ld_y) * elem | static_cast<uintptr_t>(R) * elem;
     a.y_tma = align % 16 == 0;
     a.bias = bias;
     a.bias_type = bias_type;
