@@ -69,13 +69,16 @@ vnm_status vnm_testing_dense_linear_skip_stage(const void* X, int64_t ld_x, cons
                                                int32_t* status, int32_t skip_stage, vnm_stream_t stream);
 
 /*
- * How the dense 16-bit layers take a product on a GPU of sm_count SMs (host only), as
- * vnm_testing_fp8_linear_plan. kind: 0 one product (T x R over K), 1 the sum of two, 2 two
- * side by side in rows (T each), 3 a gated pair (R features; keep = 1: with checkpoints).
+ * How the dense 16-bit layers take a product with aligned 16-bit outputs on a GPU of sm_count SMs
+ * (host only): tiles of *tile_tokens = 16, 32, 64 or 128 tokens with K over *splits CTAs of a cluster; 0:
+ * pairs of CTAs, 256 tokens by *tile_rows rows of W, K over *splits pairs; 8: the few-token kernel.
+ * kind: 0 one product (T x R over K), 1 the sum of two, 2 two side by side in rows (T each), 3 a gated
+ * pair (R features).
  * Errors: VNM_ERR_INVALID_ARG.
  */
 vnm_status vnm_testing_dense_plan(int32_t kind, int64_t T, int64_t R, int64_t K, int32_t x_transposed, int32_t w_transposed,
-                                  int32_t keep, int32_t sm_count, int32_t* tile_tokens, int32_t* splits);
+                                  vnm_keep keep, int32_t sm_count, int32_t* tile_tokens, int32_t* tile_rows,
+                                  int32_t* splits);
 
 #ifdef __cplusplus
 }

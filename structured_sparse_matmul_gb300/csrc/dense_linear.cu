@@ -226,7 +226,8 @@ template <int RB, int G, bool ALIGNED>
 __device__ __forceinline__ void emit_box(const CUtensorMap* tm, bool tma, void* p, int64_t ld, int64_t m0, int64_t n0, int64_t T,
                                          int64_t end, uint32_t buf, int lane) {
     if (m0 >= T || n0 >= end) return;
-    if (ALIGNED || tma) {
+    // (a tensor memory store that ends inside 16 bytes writes all of them)
+    if (ALIGNED || (tma && (n0 + RB / G <= end || end * G % 16 == 0))) {
         if (lane == 0) tma_store_2d(tm, static_cast<int32_t>(n0), static_cast<int32_t>(m0), buf);
     } else {
         copy_box<RB, G>(static_cast<uint8_t*>(p) + (m0 * ld + n0) * G, ld * G, static_cast<int>(min(static_cast<int64_t>(32), T - m0)),
@@ -243,7 +244,7 @@ struct Raw16 {
 
 // SUM: the sums are taken out every chunk_kb K blocks and added up in registers; SPLIT: K is split over
 // the pairs of a cluster, one tile a cluster; ALIGNED: the outputs' and the residual's rows start on 16 bytes (the
-// code for others, in the same loop, costs the aligned ones a third of their epilogue).
+// code for others, in the same loop, costs the aligned ones a third of their epilogue) and end on 16.
 template <bool GATED, bool SUM, bool SPLIT, bool ALIGNED>
 __global__ void __launch_bounds__(kPairThreads, 1)
     dense_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ OutMaps outs, const __grid_constant__ GemmArgs a) {
@@ -1248,8 +1249,8 @@ struct TilePlan {
 
 // The times that the plan compares, in us. The constants were fitted to 218 products of random sizes (T = 9 .. 8192,
 // R = 64 .. 11008, K = 64 .. 11008, all operand orders, checkpoints or none), each timed with every plan: what the rule
-// picks is 1.6 % slower than the fastest on average, 25 % at worst. They weigh the plans against
-// each other; the absolute times are up to a third off.
+// picks is 1.6 % slower than the fastest on average, 25 % at worst; for 219 other such products 2.2 %, a few 30 %. They
+// weigh the plans against each other; the absolute times are up to a third off.
 TilePlan plan_tiles(const ProductArgs& p, int sm_count) {
     const bool gated = p.kind == kGatedPair, two = p.kind == kTwoByRows, keep8 = p.keep == kKeep8;
     const int64_t e = p.y_type == VNM_F32 ? 4 : 2;
@@ -1286,7 +1287,7 @@ TilePlan plan_tiles(const ProductArgs& p, int sm_count) {
     for (int splits = 2; splits <= kMaxPairSplits && splits <= num_kb; ++splits) {
         const int64_t clusters = std::max(1, sm_count * (splits == 2 ? 36 : splits == 3 ? 23 : 15) / 152);
         consider({0, splits, 256}, kSetup + static_cast<double>(ceil_div(pair_tiles, clusters)) *
-                                                (static_cast<double>(ceil_div(num_kb, splits)) * kMma + 6.3));
+                                                (static_cast<double>(ceil_div(num_kb, splits)) * kMma + 4.5));
     }
     // Narrow tiles, two CTAs an SM: a launch, a wave's chain of K blocks (longer where SMs run two CTAs, or as long as
     // the loads from L2 take), its end; or the operands from memory.
@@ -1304,7 +1305,7 @@ TilePlan plan_tiles(const ProductArgs& p, int sm_count) {
             auto wave = [&](int64_t active) {
                 return static_cast<double>(blocks) * std::max(kBlock[i] + (active > sm_count ? 0.49 * bn / 128 : 0.0),
                                                               static_cast<double>(active * (kOperandBytes + bn * 128)) / 10.8e6) +
-                       kEnd[i];
+                       kEnd[i] + (keep8 ? 0.02 * bn : 0.0);
             };
             const double t = static_cast<double>(full) * wave(slots) + (rest > 0 ? wave(rest) : 0.0);
             consider({bn, splits, 0}, kStart[i] + std::max(t, memory) + (keep8 ? 1.8 : 0.0) +
@@ -1324,10 +1325,11 @@ bool few_tokens(const ProductArgs& p) {
 
 }  // namespace
 
-void product_plan(const ProductArgs& p, int sm_count, int* tile_tokens, int* splits) {
+void product_plan(const ProductArgs& p, int sm_count, int* tile_tokens, int* tile_rows, int* splits) {
     TilePlan plan{8, 1, 0};
     if (!few_tokens(p)) plan = plan_tiles(p, sm_count);
     *tile_tokens = plan.bn;
+    *tile_rows = plan.tile_n;
     *splits = plan.splits;
 }
 
@@ -1394,7 +1396,7 @@ cudaError_t launch_product(const ProductArgs& p, int sm_count, cudaStream_t stre
         return gated ? run_pair<true, true, true, false>(p, a, plan.tile_n, plan.splits, sm_count, stream)
                      : run_pair<false, true, true, false>(p, a, plan.tile_n, plan.splits, sm_count, stream);
     if (plan.bn == 0) {
-        const bool aligned = o.y_tma && o.res_vec && (p.keep == kKeepNone || o.keep_tma);
+        const bool aligned = o.y_tma && o.res_vec && p.R * e % 16 == 0 && (p.keep == kKeepNone || (o.keep_tma && p.R * k % 16 == 0));
         if (gated) return run_pair<true>(p, a, p.keep == kKeep8, aligned, plan.tile_n, sm_count, stream);
         return run_pair<false>(p, a, a.chunk_kb < a.total_kb, aligned, plan.tile_n, sm_count, stream);
     }

@@ -83,7 +83,8 @@ cudaError_t launch_product(const ProductArgs& a, int sm_count, cudaStream_t stre
 // Which kernel takes a product (K >= 1), by the rule that launch_product goes by: tiles of 16, 32, 64
 // or 128 tokens with K over `splits` CTAs; pairs of CTAs (0), K over `splits` pairs; the few-token kernel (8).
 constexpr int kFewTokens = 16;  // the most that it takes
-void product_plan(const ProductArgs& a, int sm_count, int* tile_tokens, int* splits);
+// Pairs: *tile_rows rows of W a tile (both of a gated pair's together).
+void product_plan(const ProductArgs& a, int sm_count, int* tile_tokens, int* tile_rows, int* splits);
 
 // The first error that products without status words recorded on the current device, and clears it.
 cudaError_t take_product_status(int* code, cudaStream_t stream);
