@@ -147,8 +147,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<kWarps, GATED>::kCtas) dense_
     };
     Weights<NW> ring[kRing];
     Tokens<NT> cur, next;
-    let_next_grid_start();
     after_previous_grid();
+    let_next_grid_start();
 #pragma unroll
     for (int u = 0; u < kRing; ++u)
         if (warp + u * kWarps < full) load_w(ring[u], warp + u * kWarps);

@@ -168,6 +168,7 @@ constexpr int kPairSmem = kPairRing + kPairEpilogue * kStageOut + 1024;
 static_assert(kSumBytes + (kMaxPairSplits - 1) * (kTile / kMaxPairSplits) * 1024 <= kPairRing + kPairEpilogue * kStageOut &&
                   kSumBytes + 2 * ((kTile + 2) / 3) * 1024 <= kPairRing + kPairEpilogue * kStageOut,
               "the splits' sums fit");
+static_assert(kPairRing / kPairEpilogue >= 16 * 1024, "a warp's last boxes: 32 rows x 128 columns of fp32");
 static_assert(kPairSmem > 116 * 1024 && kPairSmem <= 226 * 1024, "one CTA an SM: each holds all of its TMEM");
 // Registers of the variant that adds chunks up: 128 sums and a load of 32 columns do not fit the 168 that
 // 12 warps get; the epilogue takes what the helper warps leave (in warps: 4 x 56 + 8 x 224 = 12 x 168).
@@ -293,8 +294,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     cluster_sync_all();  // the CTAs' barriers and TMEM exist
     tc_fence_after_sync();
-    let_next_grid_start();
     after_previous_grid();
+    let_next_grid_start();
     const uint32_t tmem = tmem_slot;
     volatile int* abort = &abort_flag;
 
@@ -456,6 +457,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 }
                 return r;
             };
+            // After the CTA's last tile the ring is free: its boxes all have a place of their own there, and no box waits for
+            // another's store.
+            const bool roomy = tile + tile_step >= a.tiles && res == nullptr;
+            const uint32_t room = smem_base + (warp - kPairHelpers) * (kPairRing / kPairEpilogue);
             const bool f32 = o.y_type == VNM_F32, bf16 = o.y_type == VNM_BF16, res_tma = res != nullptr && (ALIGNED || o.res_vec);
             const int box_cols = f32 ? 16 : 32;
             // the residual's box from column c on, into output box `at`, whose last store has read it; the outputs then
@@ -578,7 +583,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     else
                         release();
                     const int in = c & (box_cols - 1);  // the columns' place in their box
-                    const uint32_t buf = stage + 2048 * (box & 1);
+                    const uint32_t buf = roomy ? room + 2048 * ((c - first) / box_cols) : stage + 2048 * (box & 1);
                     const bool landed = res_tma && m0 < o.T && n_tile + c - in < end;
                     if (in == 0) {
                         if (landed) {
@@ -588,7 +593,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             }
                             res_phase ^= 1u << (box & 1);
                             res_pending &= ~(1u << (box & 1));
-                        } else if (lane == 0) {
+                        } else if (lane == 0 && !roomy) {
                             tma_store_wait_read();
                         }
                         __syncwarp();
@@ -670,9 +675,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         release();
                     }
                     const int in = c & (box_cols - 1);
-                    const uint32_t buf = stage + (twice ? 2048 * (box & 1) : 0);
+                    const uint32_t buf = roomy ? room + 4096 * ((c - first) / box_cols) : stage + (twice ? 2048 * (box & 1) : 0);
                     if (in == 0) {
-                        if (lane == 0) {
+                        if (lane == 0 && !roomy) {
                             if (twice)
                                 tma_store_wait_read();
                             else
@@ -737,7 +742,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
             if (first >= last) release();
         }
-        if (lane == 0) tma_store_wait();
+        if (lane == 0) tma_store_wait_all_read();
         for (int at = 0; at < 2; ++at)  // (after a wait that ran out) copies in flight must land before the CTA exits
             if (res_pending >> at & 1u) mbar_drain(smem_u32(&res_bar[GATED ? 0 : warp - kPairHelpers][at]), res_phase >> at & 1u);
     }
@@ -1269,7 +1274,7 @@ TilePlan plan_tiles(const ProductArgs& p, int sm_count) {
     // tiles' own rows of W from memory (5.3 TB/s) takes; a tile's epilogue runs under the next one's K blocks.
     constexpr double kSetup = 5.5, kMma = 0.43, kLeast = 0.32, kL2 = 10.3e6, kMemory = 5.3e6;
     const int64_t row_tiles = ceil_div(p.T, 2 * kTile) * (two ? 2 : 1), pairs = std::max(1, sm_count / 2);
-    for (int n = 256; n >= 128; n -= 64) {  // (boxes of 64 columns, 32 features)
+    for (int n = 256; n >= 128; n -= gated ? 64 : 32) {  // (boxes of 32 columns or features)
         if (n < 256 && keep8) break;        // (a group of the 8-bit form is 128 features)
         const int64_t tiles = row_tiles * ceil_div(p.R, gated ? n / 2 : n), full = tiles / pairs, rest = tiles % pairs;
         const double epilogue = (gated ? (keep8 ? 1.4 : 0.0) + (aligned ? 0.0 : 1.1) : aligned ? 0.9 : 6.0) * n / 256;

@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(kThreads, 4) gated_grad_kernel(const GatedGrad
         d_next = Part{{0u, 0u, 0u, 0u}, {1.f, 1.f}};
         if (a.dy != nullptr) d_next = load_part<false>(kdy, t, c);
     };
-    let_next_grid_start();
     after_previous_grid();
+    let_next_grid_start();
     fetch();
 #pragma unroll 1
     while (t < a.T) {

@@ -11,7 +11,8 @@ namespace vnm {
 // The launches let this grid start while the stream's previous one drains: nothing of global memory is
 // touched before its end.
 __device__ __forceinline__ void after_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// From here on the next such grid may start (it waits for our end in the same way).
+// From here on the next such grid may start (it waits for our end in the same way). Called after the wait: only one
+// grid is ahead at a time.
 __device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // 1 / (1 + e^-v). __expf is off by a relative 2^-22 (1 + |v|) or so, which 1 + e^-v damps by

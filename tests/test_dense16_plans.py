@@ -25,7 +25,7 @@ def test_every_kernel_is_listed():
     dense, both = {p for p, *_, t in DENSE if not t[0]}, {p for p, *_, t in DENSE if t[0]}
     for found, wide in ((dense, widths), (both, (64, 128))):
         assert {p[0] for p in found if p[0] > 8} == set(wide)
-        assert {(0, n, 1) for n in (128, 192, 256)} | {(0, 256, s) for s in (2, 3, 4)} <= found
+        assert {(0, n, 1) for n in (128, 160, 192, 224, 256)} | {(0, 256, s) for s in (2, 3, 4)} <= found
     assert few in dense
     keeps = {k: {p for p, *_, keep in GATED if keep == k} for k in (0, 1, 2)}
     assert {p[0] for p in keeps[0] | keeps[1]} == {p[0] for p in keeps[2]} | {8} == set(widths) | {0, 8}
@@ -47,7 +47,7 @@ def test_plans_are_ones_that_the_kernels_have(libvnm, sms):  # noqa: F811
         if tile == 8:
             assert T <= 16 and kind in (0, 3) and keep < 2 and not (xt or wt)
         elif tile == 0:
-            assert rows in (128, 192, 256) and splits <= 4 and (splits == 1 or rows == 256) and (keep < 2 or rows == 256)
+            assert rows in ((128, 192, 256) if kind == 3 else (128, 160, 192, 224, 256)) and splits <= 4 and (splits == 1 or rows == 256) and (keep < 2 or rows == 256)
         else:
             assert tile in ((64, 128) if xt else (16, 32, 64, 128)) and splits <= (4 if keep >= 2 else 8)
 
