@@ -10,25 +10,36 @@
 // transposed copy. Two products that add up to one output (dG . Wg + dU . Wu) are one
 // product over both K; two that share an operand (dG^T . X, dU^T . X) are one grid.
 //
-// dense_pair_kernel, many tokens: pairs of CTAs (cta_group::2), 256 rows of X by 256 of W
-// a tile (each CTA loads its own 128 rows of X and 128 of W; of a gated pair, the
+// dense_pair_kernel, many tokens: pairs of CTAs (cta_group::2), 256 rows of X by up to 256 of W
+// a tile (each CTA loads its own 128 rows of X and half of W's; of a gated pair, the
 // first CTA loads Wg's and the second Wu's rows, and a tile is 128 features of
 // both), persistent, two TMEM accumulators of 256 columns, so that a tile's
 // epilogue runs under the next one's MMAs.
-//   warp 0     TMA producer: stages of 64 elements of K, 128B swizzle.
+//   warp 0     TMA producer: six stages of 64 elements of K, 128B swizzle.
 //   warp 1     TMEM owner, MMA issuer (one thread of the first CTA).
-//   warps 4..  epilogue: 32 rows x 128 columns of the tile a warp, by way of shared
-//              memory (fp32), from which 8 neighbouring columns go to a lane: whole
-//              16-byte loads of the residual and stores of Y.
+//   warps 4..  epilogue: 32 rows x half of the columns a warp. A lane has a row, 16 columns at a time; bias,
+//              activation, rounding; then into boxes of 32 rows x 64 bytes, which tensor memory stores bring out
+//              (a residual's boxes came in by the same way). 8 neighbouring columns of a row to a lane, by way of
+//              fp32 rows in shared memory, took 8192 x 11008 over 4096 from 396 to 440 us.
+// Where the outputs' rows do not start and end on 16 bytes, the boxes are copied out by the warps. With
+// few tiles, K is split over the pairs of a cluster, which copy their sums to each other at the end.
+//
+// Measured, bf16 (us; in brackets the operations at the measured rate of a library product):
+// 8192 x 11008 over 4096 with bias and residual 396 (383), gated with 8-bit checkpoints 804 (766); dX of that, 8192 x
+// 4096 over 2 x 11008, 784 (766), dWg and dWu 822 (766). Bound by the MMAs: a K block takes 0.285 us, theirs is 0.27.
+// Products of fewer tiles than pairs are bound by L2: 64 KB a pair and K block, 10.3 TB/s of all.
 //
 // dense_narrow_kernel, few tokens or few tiles: W on the MMA's M side (its rows fill the
-// tensor cores' rows), 16 to 128 tokens a tile, K over the CTAs of a cluster,
-// which add their sums up through distributed shared memory in rank order.
+// tensor cores' rows), 16 to 128 tokens a tile, two CTAs an SM, K over the CTAs of a cluster,
+// which add their sums up through distributed shared memory in rank order. 777 x 1000 over 1041 takes 10.9 us: the
+// launch, a chain of 17 K blocks, whose time is the barriers' latency (0.23 us with 16 tokens, 0.29 with
+// 128), and the exchange of sums.
 //
 // The tensor cores' fp32 sums truncate: over K they lose about K * 2^-30 of
 // random sums and six times that of sums of one sign (measured: 9e-6 and 5e-5 at
-// K = 8192). Nothing next to a rounding to 16 bits, but it is to fp32 outputs, so
-// for those the sums are taken out every kChunk elements of K and added in registers.
+// K = 8192). To fp32 outputs, and to the largest magnitude of a group of 8-bit checkpoints, that is much:
+// there the sums are taken out every kChunk elements of K and added in registers. Next to a rounding to 16 bits
+// it is little up to kLongChunk.
 #include <algorithm>
 #include <atomic>
 
@@ -42,7 +53,7 @@ namespace {
 constexpr int kTile = 128;        // rows of an operand in a CTA's stage
 constexpr int kBlockK = 64;       // elements of K in a stage: 128 bytes
 constexpr int kOperandBytes = kTile * 128;
-constexpr int kChunk = 1024 / kBlockK;
+constexpr int kChunk = 1024 / kBlockK, kLongChunk = 32768 / kBlockK;
 constexpr int kMaxSplits = 8, kMaxPairSplits = 4;
 constexpr int kMaxDevicesDl = 64;
 constexpr int kGroupM = 8;
@@ -781,6 +792,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         float b[8];
         bias8(o, c, b);
         const bool landed = mbar_wait_warp(bar, 0, abort);
+        if (!landed) mbar_drain(bar, 0);  // (after a wait that ran out) no CTA leaves while the others' sums are on their way to it
 #pragma unroll 1
         for (int base = row0 + kRowsAtOnce * warp; base < row1 && landed; base += kRowsAtOnce * (kPairThreads / 32)) {
             const int row = min(base + lane / kLanes, row1 - 1);
@@ -1275,7 +1287,8 @@ TilePlan plan_tiles(const ProductArgs& p, int sm_count) {
     constexpr double kSetup = 5.5, kMma = 0.43, kLeast = 0.32, kL2 = 10.3e6, kMemory = 5.3e6;
     const int64_t row_tiles = ceil_div(p.T, 2 * kTile) * (two ? 2 : 1), pairs = std::max(1, sm_count / 2);
     for (int n = 256; n >= 128; n -= gated ? 64 : 32) {  // (boxes of 32 columns or features)
-        if (n < 256 && keep8) break;        // (a group of the 8-bit form is 128 features)
+        // (a group of the 8-bit form is 128 features; a warp that adds chunks up holds 64 of both products)
+        if (n < 256 && gated && (keep8 || num_kb > kLongChunk)) break;
         const int64_t tiles = row_tiles * ceil_div(p.R, gated ? n / 2 : n), full = tiles / pairs, rest = tiles % pairs;
         const double epilogue = (gated ? (keep8 ? 1.4 : 0.0) + (aligned ? 0.0 : 1.1) : aligned ? 0.9 : 6.0) * n / 256;
         auto block = [&](int64_t active) {
@@ -1296,7 +1309,7 @@ TilePlan plan_tiles(const ProductArgs& p, int sm_count) {
     }
     // Narrow tiles, two CTAs an SM: a launch, a wave's chain of K blocks (longer where SMs run two CTAs, or as long as
     // the loads from L2 take), its end; or the operands from memory.
-    const double memory = static_cast<double>((gated ? 2 : 1) * p.R * p.K * 2 + p.T * p.K * 2) / kMemory;
+    const double memory = 2.0 * static_cast<double>(p.K) * static_cast<double>((gated ? 2 : 1) * p.R + p.T) / kMemory;
     for (int i = 0; i < 4; ++i) {
         const int bn = 16 << i;
         constexpr double kStart[4] = {1.2, 1.5, 0.7, 6.3}, kBlock[4] = {0.225, 0.242, 0.272, 0.293}, kEnd[4] = {1.2, 1.5, 3.1, 0.0};
@@ -1390,7 +1403,7 @@ cudaError_t launch_product(const ProductArgs& p, int sm_count, cudaStream_t stre
     a.kind = p.kind;
     a.num_kb = static_cast<int>(ceil_div(p.K, kBlockK));
     a.total_kb = a.num_kb * (p.kind == kSumOfTwo ? 2 : 1);
-    a.chunk_kb = p.y_type == VNM_F32 || p.keep == kKeep8 ? kChunk : a.total_kb;
+    a.chunk_kb = std::min(a.total_kb, p.y_type == VNM_F32 || p.keep == kKeep8 ? kChunk : kLongChunk);
     a.x_t = p.x[0].transposed;
     a.w_t = p.w[0].transposed;
     a.status = p.status;
@@ -1402,8 +1415,9 @@ cudaError_t launch_product(const ProductArgs& p, int sm_count, cudaStream_t stre
                      : run_pair<false, true, true, false>(p, a, plan.tile_n, plan.splits, sm_count, stream);
     if (plan.bn == 0) {
         const bool aligned = o.y_tma && o.res_vec && p.R * e % 16 == 0 && (p.keep == kKeepNone || (o.keep_tma && p.R * k % 16 == 0));
-        if (gated) return run_pair<true>(p, a, p.keep == kKeep8, aligned, plan.tile_n, sm_count, stream);
-        return run_pair<false>(p, a, a.chunk_kb < a.total_kb, aligned, plan.tile_n, sm_count, stream);
+        const bool sum = a.chunk_kb < a.total_kb || p.keep == kKeep8;
+        return gated ? run_pair<true>(p, a, sum, aligned, plan.tile_n, sm_count, stream)
+                     : run_pair<false>(p, a, sum, aligned, plan.tile_n, sm_count, stream);
     }
     return gated ? run_narrow<true>(plan.bn, p, a, plan.splits, stream) : run_narrow<false>(plan.bn, p, a, plan.splits, stream);
 }
