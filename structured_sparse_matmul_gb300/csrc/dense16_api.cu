@@ -95,7 +95,7 @@ vnm_status dense_linear(const void* X, int64_t ld_x, int32_t x_transposed, const
     p.keep = vnm::kKeepNone;
     p.status = status;
     p.skip_stage = skip_stage;
-    return launched(vnm::launch_product(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+    return launched(vnm::launch_product(p, vnm::plan_product(p, sms), sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int64_t padded(int64_t F) { return (F + 7) / 8 * 8; }
@@ -134,7 +134,11 @@ vnm_status vnm_testing_dense_plan(int32_t kind, int64_t T, int64_t R, int64_t K,
     p.x[0].transposed = x_transposed != 0;
     p.w[0].transposed = w_transposed != 0;
     p.keep = kind_of(keep);
-    vnm::product_plan(p, sm_count, tile_tokens, tile_rows, splits);
+    p.skip_stage = -1;
+    const vnm::TilePlan plan = vnm::plan_product(p, sm_count);
+    *tile_tokens = plan.bn;
+    *tile_rows = plan.tile_n;
+    *splits = plan.splits;
     return VNM_OK;
 }
 
@@ -169,7 +173,7 @@ vnm_status vnm_gated_linear(const void* X, int64_t ld_x, const void* Wg, int64_t
     p.e5m2 = keep == VNM_KEEP_E5M2;
     p.status = status;
     p.skip_stage = -1;
-    return launched(vnm::launch_product(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+    return launched(vnm::launch_product(p, vnm::plan_product(p, sms), sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 vnm_status vnm_gated_linear_backward_workspace_size(int64_t T, int64_t F, size_t* bytes) {
@@ -235,7 +239,8 @@ vnm_status vnm_gated_linear_backward(const void* dY, int64_t ld_dy, const void* 
         e.ld_h = ld_h;
         err = vnm::launch_gated_grad(e, sms, s);
     }
-    if (any_dx && err == cudaSuccess) {
+    const bool dx = any_dx, dw = any_dw && !(T == 0 && accumulate);
+    if (dx) {
         in.kind = vnm::kSumOfTwo;
         in.T = T;
         in.R = K;
@@ -249,9 +254,8 @@ vnm_status vnm_gated_linear_backward(const void* dY, int64_t ld_dy, const void* 
         in.act = VNM_ACT_NONE;
         in.status = status;
         in.skip_stage = -1;
-        err = vnm::launch_product(in, sms, s);
     }
-    if (any_dw && err == cudaSuccess && !(T == 0 && accumulate)) {
+    if (dw) {
         gr.kind = vnm::kTwoByRows;
         gr.T = F;
         gr.R = K;
@@ -271,8 +275,15 @@ vnm_status vnm_gated_linear_backward(const void* dY, int64_t ld_dy, const void* 
         }
         gr.status = status;
         gr.skip_stage = -1;
-        err = vnm::launch_product(gr, sms, s);
     }
+    const vnm::TilePlan in_plan = dx ? vnm::plan_product(in, sms) : vnm::TilePlan{}, gr_plan = dw ? vnm::plan_product(gr, sms) : vnm::TilePlan{};
+    // dX and the weights' gradients share dG and dU, and neither reads what the other writes: their grids run side by side, but
+    // where both are pairs of CTAs, which take whole SMs. The pass in us, one after the other and side by side (bf16 and 8-bit
+    // checkpoints; T x F over K): 42 x 1576 over 125 13.0 and 9.0, 333 x 1001 over 1023 22.8 and 20.5, 2042 x 654 over 684 34.9
+    // and 25.6, 512 x 4096 over 1024 43.2 and 42.7; both pairs: 2048 x 5632 over 2048 135.6 and 136.1, 1024 x 4096 over 1024 53 and 59.
+    in.next_beside = gr.beside = dx && dw && products && (in_plan.bn != 0 || gr_plan.bn != 0);
+    if (dx && err == cudaSuccess) err = vnm::launch_product(in, in_plan, sms, s);
+    if (dw && err == cudaSuccess) err = vnm::launch_product(gr, gr_plan, sms, s);
     return launched(err);
 }
 

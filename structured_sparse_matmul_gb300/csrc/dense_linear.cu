@@ -80,6 +80,7 @@ struct GemmArgs {
     int splits, kb_per_split;
     bool x_t, w_t;
     uint32_t idesc;
+    bool beside, next_beside;
     int* status;
     int skip_stage;
 };
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     cluster_sync_all();  // the CTAs' barriers and TMEM exist
     tc_fence_after_sync();
-    after_previous_grid();
+    if (!a.beside) after_previous_grid();
     let_next_grid_start();
     const uint32_t tmem = tmem_slot;
     volatile int* abort = &abort_flag;
@@ -834,6 +835,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         cluster_sync_all();  // no CTA leaves while its sums are copied from it
     }
+    if (a.beside) after_previous_grid();
     if (threadIdx.x == 0 && abort_flag) record_error(a.status ? a.status : g_status, VNM_ERR_TIMEOUT, 13);
 }
 
@@ -921,7 +923,7 @@ __global__ void __launch_bounds__(NarrowCfg<BN>::kThreads, 2)
         abort_flag = 0;
         fence_barrier_init();
         // the first stages need no other thread: their latency covers the TMEM allocation
-        after_previous_grid();
+        if (!a.beside) after_previous_grid();
         for (int k = 0; k < early; ++k)
             if (k != a.skip_stage || blockIdx.x != 0) load_stage(k, kb0 + k);
     }
@@ -929,7 +931,8 @@ __global__ void __launch_bounds__(NarrowCfg<BN>::kThreads, 2)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    after_previous_grid();
+    if (!a.beside) after_previous_grid();
+    if (a.next_beside) let_next_grid_start();
     const uint32_t tmem = tmem_slot;
     volatile int* abort = &abort_flag;
 
@@ -1096,6 +1099,7 @@ __global__ void __launch_bounds__(NarrowCfg<BN>::kThreads, 2)
         }
     }
     if (a.splits > 1 || twin) cluster_sync_all();  // no CTA leaves while others read its sums
+    if (a.beside) after_previous_grid();
     if (threadIdx.x == 0 && abort_flag) record_error(a.status ? a.status : g_status, VNM_ERR_TIMEOUT, 14);
 }
 
@@ -1258,12 +1262,6 @@ cudaError_t run_narrow(int bn, const ProductArgs& p, const GemmArgs& a, int spli
     }
 }
 
-// How a product is tiled: pairs of CTAs (bn = 0), tile_n rows of W a tile, K over `splits` pairs of a
-// cluster; or tiles of bn tokens, K over `splits` CTAs of a cluster.
-struct TilePlan {
-    int bn, splits, tile_n;
-};
-
 // The times that the plan compares, in us. The constants were fitted to 218 products of random sizes (T = 9 .. 8192,
 // R = 64 .. 11008, K = 64 .. 11008, all operand orders, checkpoints or none), each timed with every plan: what the rule
 // picks is 1.6 % slower than the fastest on average, 25 % at worst; for 219 other such products 2.2 %, a few 30 %. They
@@ -1343,12 +1341,8 @@ bool few_tokens(const ProductArgs& p) {
 
 }  // namespace
 
-void product_plan(const ProductArgs& p, int sm_count, int* tile_tokens, int* tile_rows, int* splits) {
-    TilePlan plan{8, 1, 0};
-    if (!few_tokens(p)) plan = plan_tiles(p, sm_count);
-    *tile_tokens = plan.bn;
-    *tile_rows = plan.tile_n;
-    *splits = plan.splits;
+TilePlan plan_product(const ProductArgs& p, int sm_count) {
+    return few_tokens(p) && p.skip_stage < 0 ? TilePlan{kFewPlan, 1, 0} : plan_tiles(p, sm_count);
 }
 
 cudaError_t take_product_status(int* code, cudaStream_t stream) {
@@ -1363,8 +1357,8 @@ cudaError_t take_product_status(int* code, cudaStream_t stream) {
     return e;
 }
 
-cudaError_t launch_product(const ProductArgs& p, int sm_count, cudaStream_t stream) {
-    if (p.K > 0 && p.skip_stage < 0 && few_tokens(p)) return launch_few_tokens(p, sm_count, stream);
+cudaError_t launch_product(const ProductArgs& p, const TilePlan& plan, int sm_count, cudaStream_t stream) {
+    if (p.K > 0 && plan.bn == kFewPlan) return launch_few_tokens(p, sm_count, stream);
     GemmArgs a{};
     OutArgs& o = a.o;
     auto rows_aligned = [](const void* q, int64_t ld_bytes, int n) {
@@ -1406,10 +1400,11 @@ cudaError_t launch_product(const ProductArgs& p, int sm_count, cudaStream_t stre
     a.chunk_kb = std::min(a.total_kb, p.y_type == VNM_F32 || p.keep == kKeep8 ? kChunk : kLongChunk);
     a.x_t = p.x[0].transposed;
     a.w_t = p.w[0].transposed;
+    a.beside = p.beside;
+    a.next_beside = p.next_beside;
     a.status = p.status;
     a.skip_stage = p.skip_stage;
     const bool gated = p.kind == kGatedPair;
-    const TilePlan plan = plan_tiles(p, sm_count);
     if (plan.bn == 0 && plan.splits > 1)
         return gated ? run_pair<true, true, true, false>(p, a, plan.tile_n, plan.splits, sm_count, stream)
                      : run_pair<false, true, true, false>(p, a, plan.tile_n, plan.splits, sm_count, stream);

@@ -74,17 +74,23 @@ struct ProductArgs {
     KeepKind keep;
     bool e5m2;
     Kept g, u;
+    // Two products that do not need each other, launched one after the other: the second starts its work when all CTAs of the
+    // first run (and have seen the end of what came before it), and waits for the first's end at its own.
+    bool beside, next_beside;  // this is the second; the first (both of K >= 1)
     int* status;
     int skip_stage;  // tests of the bounded waits only (-1: none)
 };
 
-cudaError_t launch_product(const ProductArgs& a, int sm_count, cudaStream_t stream);
-
-// Which kernel takes a product (K >= 1), by the rule that launch_product goes by: tiles of 16, 32, 64
-// or 128 tokens with K over `splits` CTAs; pairs of CTAs (0), K over `splits` pairs; the few-token kernel (8).
+// How a product (K >= 1) is tiled: pairs of CTAs (bn = 0), tile_n rows of W a tile (both of a gated pair's
+// together), K over `splits` pairs of a cluster; tiles of bn = 16, 32, 64 or 128 tokens, K over `splits` CTAs of a cluster; or
+// the few-token kernel.
+struct TilePlan {
+    int bn, splits, tile_n;
+};
+constexpr int kFewPlan = 8;     // bn of the few-token kernel
 constexpr int kFewTokens = 16;  // the most that it takes
-// Pairs: *tile_rows rows of W a tile (both of a gated pair's together).
-void product_plan(const ProductArgs& a, int sm_count, int* tile_tokens, int* tile_rows, int* splits);
+TilePlan plan_product(const ProductArgs& a, int sm_count);
+cudaError_t launch_product(const ProductArgs& a, const TilePlan& plan, int sm_count, cudaStream_t stream);
 
 // The first error that products without status words recorded on the current device, and clears it.
 cudaError_t take_product_status(int* code, cudaStream_t stream);

@@ -6,7 +6,7 @@ from structured_sparse_matmul_gb300 import vnm
 
 pytestmark = pytest.mark.gpu
 
-from dense16_util import BF16, DEV, F16, F32, NONE, ULP, check, generator, whole  # noqa: E402
+from dense16_util import BF16, DEV, F16, F32, NONE, ULP, check, generator, pitched, whole  # noqa: E402
 
 LONG = 262144 + 40
 
@@ -127,3 +127,52 @@ def test_time_out_of_split_pairs(T, R, K, skip):
     vnm.vnm_dense_linear(x, w, Y)
     assert vnm.vnm_dense_get_status() == vnm.VNM_OK
     assert torch.equal(Y, (x.double() @ w.double().t()).half())
+
+
+# (both of dX and of dWg and dWu by narrow tiles; dX by narrow tiles, the others by pairs; both by pairs)
+@pytest.mark.parametrize("T,F,K", [(42, 1576, 125), (1, 79, 125), (736, 1280, 149), (2042, 654, 684), (578, 1346, 1274), (1024, 4096, 1024)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_backward_passes_in_a_row(T, F, K, captured):
+    """Passes one behind the other with one workspace, on changing inputs, and what overwrites their
+    inputs right behind: dX and the weights' gradients, whose grids run side by side, give the bits that they give alone."""
+    g = generator(T, F, K, 26)
+    ins = [[pitched(torch.randn(*s, generator=g, device=DEV).bfloat16()) for s in ((T, F), (T, K), (F, K), (F, K), (T, F), (T, F))]
+           for _ in range(3)]
+    ws = torch.empty(vnm.vnm_gated_linear_backward_workspace_size(T, F), dtype=torch.uint8, device=DEV)
+
+    def outputs():
+        return [torch.full(s, float("nan"), dtype=BF16, device=DEV) for s in ((T, K), (F, K), (F, K))]
+
+    want, outs = [outputs() for _ in ins], [outputs() for _ in ins]
+    for i, o in zip(ins, want):
+        vnm.vnm_gated_linear_backward(*i, dx=o[0], workspace=ws)
+        torch.cuda.synchronize()
+        vnm.vnm_gated_linear_backward(*i, dwg=o[1], dwu=o[2], workspace=ws)
+        torch.cuda.synchronize()
+    held = [pitched(torch.empty_like(v)) for v in ins[0]]
+
+    def run():
+        for _ in range(5):
+            for i, o in zip(ins, outs):
+                for h, v in zip(held, i):
+                    h.copy_(v)
+                vnm.vnm_gated_linear_backward(*held, dx=o[0], dwg=o[1], dwu=o[2], workspace=ws)
+                for h in held:
+                    h.fill_(float("nan"))
+            for i, o in zip(ins, outs):
+                vnm.vnm_gated_linear_backward(*i, dx=o[0], dwg=o[1], dwu=o[2], workspace=ws)
+
+    run()
+    if captured:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        for o in outs:
+            for v in o:
+                v.fill_(float("nan"))
+        for _ in range(3):
+            graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for o, w in zip(outs, want) for p, q in zip(o, w))
+    assert vnm.vnm_dense_get_status() == vnm.VNM_OK
