@@ -29,7 +29,7 @@ __device__ __forceinline__ float2 with_slope(float g) {
         // Phi's tail as e^(-g^2 / 2) times a polynomial in 1 / (1 + 0.3275911 |g| / sqrt 2), within 8e-8 (M. Abramowitz and
         // I. A. Stegun, Handbook of Mathematical Functions, 7.1.26): phi shares the exponential. With erff the pass over
         // 1024 x 4096 took 12.2 us.
-        const float e = __expf(-0.5f * g * g), t = __fdividef(1.f, fmaf(0.23164189f, fabsf(g), 1.f));
+        const float e = exp2_fast(-0.5f * kLog2E * g * g), t = reciprocal_fast(fmaf(0.23164189f, fabsf(g), 1.f));
         const float poly = fmaf(fmaf(fmaf(fmaf(1.061405429f, t, -1.453152027f), t, 1.421413741f), t, -0.284496736f), t, 0.254829592f);
         const float tail = 0.5f * e * t * poly, cdf = g < 0.f ? tail : 1.f - tail;
         return make_float2(g * cdf, cdf + g * (0.39894228040143268f * e));
@@ -49,9 +49,8 @@ template <bool FP8>
 __device__ __forceinline__ Part load_part(const Kept& k, int64_t t, const Cols& c) {
     Part p{{0u, 0u, 0u, 0u}, {1.f, 1.f}};
     if (FP8) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            p.s[h] = k.s[t * k.s_rs + (min(c.at(4 * h), c.end - 1) >> 7) * k.s_cs];
+        p.s[0] = p.s[1] = k.s[t * k.s_rs + (min(c.first, c.end - 1) >> 7) * k.s_cs];
+        if (!c.vec) p.s[1] = k.s[t * k.s_rs + (min(c.at(4), c.end - 1) >> 7) * k.s_cs];
         const uint8_t* row = static_cast<const uint8_t*>(k.p) + t * k.ld;
         if (c.whole()) {
             const uint2 q = __ldcs(reinterpret_cast<const uint2*>(row + c.first));
@@ -95,9 +94,9 @@ __device__ __forceinline__ void widen_part(const Part& p, bool bf16, bool e5m2, 
     }
 }
 
-// vec: the rows of every matrix start on 16 bytes (8-bit checkpoints: 8); a lane then takes 8 neighbours.
-template <int ACT, bool FP8>
-__global__ void __launch_bounds__(kThreads, 4) gated_grad_kernel(const GatedGradArgs a, bool vec) {
+// VEC: the rows of every matrix start on 16 bytes (8-bit checkpoints: 8); a lane then takes 8 neighbours.
+template <int ACT, bool FP8, bool VEC>
+__global__ void __launch_bounds__(kThreads, 4) gated_grad_kernel(const GatedGradArgs a) {
     const int lane = threadIdx.x & 31, type = a.bf16 ? VNM_BF16 : VNM_F16;
     const int64_t per_row = (a.F + kUnit - 1) / kUnit, warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
     // units warp, warp + warps, ...; the place of the next one without a division
@@ -105,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 4) gated_grad_kernel(const GatedGrad
     const int64_t dt = warps / per_row, dn = warps - dt * per_row;
     int64_t t = warp / per_row, n = warp - t * per_row;
     const Kept kdy{const_cast<void*>(a.dy), a.ld_dy, nullptr, 0, 0};
-    auto columns = [&](int64_t at) { return Cols{at * kUnit + (vec ? 8 * lane : lane), a.F, vec ? 1 : 32, vec}; };
+    auto columns = [&](int64_t at) { return Cols{at * kUnit + (VEC ? 8 * lane : lane), a.F, VEC ? 1 : 32, VEC}; };
     Part g_next, u_next, d_next;  // of the unit (t, n): a unit's loads are in flight while the one before it is worked on
     auto fetch = [&] {
         const Cols c = columns(n);
@@ -150,12 +149,17 @@ __global__ void __launch_bounds__(kThreads, 4) gated_grad_kernel(const GatedGrad
     }
 }
 
-template <int ACT>
+template <int ACT, bool FP8>
 cudaError_t launch(const GatedGradArgs& a, bool vec, int sm_count, cudaStream_t stream) {
     const int64_t units = a.T * ((a.F + kUnit - 1) / kUnit);
     const int64_t blocks = std::min<int64_t>((units + kThreads / 32 - 1) / (kThreads / 32), static_cast<int64_t>(sm_count) * 8);
-    return a.keep == kKeep8 ? launch_early(gated_grad_kernel<ACT, true>, blocks, kThreads, 0, 1, stream, a, vec)
-                            : launch_early(gated_grad_kernel<ACT, false>, blocks, kThreads, 0, 1, stream, a, vec);
+    return vec ? launch_early(gated_grad_kernel<ACT, FP8, true>, blocks, kThreads, 0, 1, stream, a)
+               : launch_early(gated_grad_kernel<ACT, FP8, false>, blocks, kThreads, 0, 1, stream, a);
+}
+
+template <int ACT>
+cudaError_t launch(const GatedGradArgs& a, bool vec, int sm_count, cudaStream_t stream) {
+    return a.keep == kKeep8 ? launch<ACT, true>(a, vec, sm_count, stream) : launch<ACT, false>(a, vec, sm_count, stream);
 }
 
 }  // namespace

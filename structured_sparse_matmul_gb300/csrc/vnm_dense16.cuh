@@ -15,10 +15,23 @@ __device__ __forceinline__ void after_previous_grid() { asm volatile("griddepcon
 // grid is ahead at a time.
 __device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// 1 / (1 + e^-v). __expf is off by a relative 2^-22 (1 + |v|) or so, which 1 + e^-v damps by
-// s e^-v <= 1 and, where v is far below 0, v's own factor s; the quotient by 2 ulp, and for v < -87
-// (e^-v above 2^126) it may be 0, where the value is below 2^-126. v * sigmoid(v) is within 8 * 2^-23 |v|.
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+// 2^v and 1 / v by the special-function unit, within 2 ulp and 1 ulp; subnormal arguments and results are 0.
+__device__ __forceinline__ float exp2_fast(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float reciprocal_fast(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+constexpr float kLog2E = 1.4426950408889634f;
+
+// 1 / (1 + e^-v). 2^(-v log2 e) is off by a relative 2^-22 (1 + |v|) or so (the product's rounding), which 1 + e^-v
+// damps by s e^-v <= 1 and, where v is far below 0, v's own factor s; the reciprocal by 1 ulp, and for v < -87
+// (e^-v above 2^126) it is 0, where the value is below 2^-126. v * sigmoid(v) is within 8 * 2^-23 |v|.
+__device__ __forceinline__ float sigmoid(float v) { return reciprocal_fast(1.f + exp2_fast(-kLog2E * v)); }
 
 template <int N>
 __device__ __forceinline__ void activate_all(int act, float (&v)[N]) {
