@@ -276,14 +276,13 @@ vnm_status vnm_gated_linear_backward(const void* dY, int64_t ld_dy, const void* 
         gr.status = status;
         gr.skip_stage = -1;
     }
-    const vnm::TilePlan in_plan = dx ? vnm::plan_product(in, sms) : vnm::TilePlan{}, gr_plan = dw ? vnm::plan_product(gr, sms) : vnm::TilePlan{};
-    // dX and the weights' gradients share dG and dU, and neither reads what the other writes: their grids run side by side, but
-    // where both are pairs of CTAs, which take whole SMs. The pass in us, one after the other and side by side (bf16 and 8-bit
-    // checkpoints; T x F over K): 42 x 1576 over 125 13.0 and 9.0, 333 x 1001 over 1023 22.8 and 20.5, 2042 x 654 over 684 34.9
-    // and 25.6, 512 x 4096 over 1024 43.2 and 42.7; both pairs: 2048 x 5632 over 2048 135.6 and 136.1, 1024 x 4096 over 1024 53 and 59.
-    in.next_beside = gr.beside = dx && dw && products && (in_plan.bn != 0 || gr_plan.bn != 0);
-    if (dx && err == cudaSuccess) err = vnm::launch_product(in, in_plan, sms, s);
-    if (dw && err == cudaSuccess) err = vnm::launch_product(gr, gr_plan, sms, s);
+    // dX and the weights' gradients share dG and dU, and neither reads what the other writes: their grids run side by side.
+    // The pass in us, one after the other and so (T x F over K): 42 x 1576 over 125 13.0 and 9.0, 333 x 1001 over 1023 22.8
+    // and 20.5, 2042 x 654 over 684 34.9 and 25.6, 512 x 4096 over 1024 43.2 and 42.7; where both are pairs of CTAs, which take
+    // whole SMs, the same within 1 %: 1176 x 6308 over 1314 120.9 and 119.4, 2048 x 5632 over 2048 136.9 and 137.5.
+    in.next_beside = gr.beside = dx && dw && products;
+    if (dx && err == cudaSuccess) err = vnm::launch_product(in, vnm::plan_product(in, sms), sms, s);
+    if (dw && err == cudaSuccess) err = vnm::launch_product(gr, vnm::plan_product(gr, sms), sms, s);
     return launched(err);
 }
 

@@ -1039,6 +1039,17 @@ __global__ void __launch_bounds__(NarrowCfg<BN>::kThreads, 2)
         const uint32_t addr = smem_base + 4 * (min(c, BN - 1) * kTile + row0 + local);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        if (a.splits == 1) {  // (this CTA's own)
+            if (vec) {
+                const float4 x = ld_shared_v4(addr), y = ld_shared_v4(addr + 16);
+                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+                v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = ld_shared_f32(addr + 4 * kLanes * j);
+            }
+            return;
+        }
 #pragma unroll
         for (int s = 0; s < kMaxSplits; ++s) {
             if (s >= a.splits) break;
