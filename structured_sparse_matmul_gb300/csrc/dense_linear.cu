@@ -526,6 +526,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     if (SPLIT || kb0 + a.chunk_kb < kb_last) release();
                 }
                 if (!run) break;
+                if constexpr (!GATED && !SPLIT && ALIGNED) {
+                    if (roomy && f32 && o.act == VNM_ACT_NONE && o.bias == nullptr) {
+                        // nothing follows the sums, and the ring is free: all boxes at once
+                        release();
+#pragma unroll
+                        for (int c = 0; c < 128; c += 4)
+                            st_shared_f4(box_piece<64>(room + 2048 * (c / 16), lane, c / 4 % 4), sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        for (int c = 0; first + c < last; c += 16)
+                            emit_box<64, 4, true>(&outs.y[seg], true, nullptr, 0, m0, n_tile + first + c, o.T, end, room + 2048 * (c / 16), lane);
+                        if (lane == 0) tma_store_commit();
+                        continue;
+                    }
+                }
                 if constexpr (SPLIT) {
                     // the ring is free: this cluster's MMAs are done with it
                     const int row = 32 * quarter + lane;
