@@ -531,12 +531,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         // nothing follows the sums, and the ring is free: all boxes at once
                         release();
 #pragma unroll
-                        for (int c = 0; c < 128; c += 4)
-                            st_shared_f4(box_piece<64>(room + 2048 * (c / 16), lane, c / 4 % 4), sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        for (int c = 0; first + c < last; c += 16)
-                            emit_box<64, 4, true>(&outs.y[seg], true, nullptr, 0, m0, n_tile + first + c, o.T, end, room + 2048 * (c / 16), lane);
+                        for (int c = 0; c < 128; c += 32) {
+#pragma unroll
+                            for (int u = c; u < c + 32; u += 4)
+                                st_shared_f4(box_piece<64>(room + 2048 * (u / 16), lane, u / 4 % 4), sum[u], sum[u + 1], sum[u + 2], sum[u + 3]);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (first + c < last) {  // (widths are multiples of 32)
+                                emit_box<64, 4, true>(&outs.y[seg], true, nullptr, 0, m0, n_tile + first + c, o.T, end, room + 128 * c, lane);
+                                emit_box<64, 4, true>(&outs.y[seg], true, nullptr, 0, m0, n_tile + first + c + 16, o.T, end, room + 128 * c + 2048, lane);
+                            }
+                        }
                         if (lane == 0) tma_store_commit();
                         continue;
                     }
