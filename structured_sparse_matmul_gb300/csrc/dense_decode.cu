@@ -12,7 +12,9 @@
 // no shuffle. A CTA takes 16 rows, its warps deal the K blocks among themselves and
 // meet once in shared memory, in a fixed order. The loads of W run kRing blocks ahead,
 // those of x (from L2) one. After every round of the ring the MMAs' sums, which
-// truncate, are added up in fp32.
+// truncate, are added up in fp32. Measured, fp16, one token (us; in brackets the weights at a copy's rate, which is
+// below what reads alone reach): 4096 rows of 11008 15.8 (13.5), 11008 x 2 rows of 4096 27.8 (27.0); what is left is
+// the launch and the first loads' round trip.
 #include <type_traits>
 
 #include "vnm_dense16.cuh"

@@ -19,21 +19,23 @@
 //   warp 1     TMEM owner, MMA issuer (one thread of the first CTA).
 //   warps 4..  epilogue: 32 rows x half of the columns a warp. A lane has a row, 16 columns at a time; bias,
 //              activation, rounding; then into boxes of 32 rows x 64 bytes, which tensor memory stores bring out
-//              (a residual's boxes came in by the same way). 8 neighbouring columns of a row to a lane, by way of
-//              fp32 rows in shared memory, took 8192 x 11008 over 4096 from 396 to 440 us.
+//              (a residual's boxes came in by the same way). Of a CTA's last tile, which nothing hides, fp32 sums that
+//              need no more than storing go to the boxes straight from the registers (4096 x 1024 over 8192 53.5 and
+//              48.5 us).
 // Where the outputs' rows do not start and end on 16 bytes, the boxes are copied out by the warps. With
 // few tiles, K is split over the pairs of a cluster, which copy their sums to each other at the end.
 //
 // Measured, bf16 (us; in brackets the operations at the measured rate of a library product):
-// 8192 x 11008 over 4096 with bias and residual 396 (383), gated with 8-bit checkpoints 804 (766); dX of that, 8192 x
-// 4096 over 2 x 11008, 784 (766), dWg and dWu 822 (766). Bound by the MMAs: a K block takes 0.285 us, theirs is 0.27.
-// Products of fewer tiles than pairs are bound by L2: 64 KB a pair and K block, 10.3 TB/s of all.
+// 8192 x 4096 over 11008 with residual 390 (383), 8192 x 11008 over 4096 gated with 8-bit checkpoints 787 (766); dX of that,
+// 8192 x 4096 over 2 x 11008, 784 (766), dWg and dWu 822 (766). Bound by the MMAs: a K block takes 0.285 us, theirs is 0.27.
+// Products of fewer tiles than pairs wait for L2 as well: 64 KB a pair and K block, 10.3 TB/s of all.
 //
 // dense_narrow_kernel, few tokens or few tiles: W on the MMA's M side (its rows fill the
 // tensor cores' rows), 16 to 128 tokens a tile, two CTAs an SM, K over the CTAs of a cluster,
-// which add their sums up through distributed shared memory in rank order. 777 x 1000 over 1041 takes 10.9 us: the
-// launch, a chain of 17 K blocks, whose time is the barriers' latency (0.23 us with 16 tokens, 0.29 with
-// 128), and the exchange of sums.
+// which add their sums up through distributed shared memory in rank order. 517 x 1001 over 1041 takes 10.8 us: W is
+// read again for every 32 tokens, 36 MB from L2 at 10 TB/s, and a launch, the ring's first loads and
+// the stores of rows of odd length. (A ring twice as deep, one CTA an SM, was 2 to 19 % slower in 30 of 44 products: the
+// next launch's setup no longer runs beside this one's end.)
 //
 // The tensor cores' fp32 sums truncate: over K they lose about K * 2^-30 of
 // random sums and six times that of sums of one sign (measured: 9e-6 and 5e-5 at

@@ -4,8 +4,11 @@
 //
 // with g and u as the forward pass kept them, in 16 bits or in the block-scaled
 // 8-bit form. Bound by memory traffic: a warp takes 256 columns of a row, 8 neighbours a lane,
-// 16-byte loads and stores (8 bytes of an 8-bit checkpoint) where the rows allow them. dg and du
+// 16-byte loads and stores (8 bytes of an 8-bit checkpoint) where the rows allow them, a unit's loads ahead of the
+// work; rows of another alignment go element by element, neighbours to neighbouring lanes. dg and du
 // are rounded once to 16 bits: the tensor cores take no wider operands at this rate.
+// Measured: 8192 x 11008, SiLU, 8-bit checkpoints 141 us (0.9 GB, 135 us at a copy's rate; 42 instructions an element);
+// 1024 x 4096, GELU, 16-bit checkpoints 10 us.
 //   silu'(g) = s (1 + g (1 - s)), s = 1 / (1 + e^-g); gelu'(g) = Phi(g) + g phi(g).
 #include <algorithm>
 
@@ -27,8 +30,8 @@ __device__ __forceinline__ float2 with_slope(float g) {
     }
     if (ACT == VNM_ACT_GELU) {
         // Phi's tail as e^(-g^2 / 2) times a polynomial in 1 / (1 + 0.3275911 |g| / sqrt 2), within 8e-8 (M. Abramowitz and
-        // I. A. Stegun, Handbook of Mathematical Functions, 7.1.26): phi shares the exponential. With erff the pass over
-        // 1024 x 4096 took 12.2 us.
+        // I. A. Stegun, Handbook of Mathematical Functions, 7.1.26): phi shares the exponential, where erff has one of its own
+        // and two branches.
         const float e = exp2_fast(-0.5f * kLog2E * g * g), t = reciprocal_fast(fmaf(0.23164189f, fabsf(g), 1.f));
         const float poly = fmaf(fmaf(fmaf(fmaf(1.061405429f, t, -1.453152027f), t, 1.421413741f), t, -0.284496736f), t, 0.254829592f);
         const float tail = 0.5f * e * t * poly, cdf = g < 0.f ? tail : 1.f - tail;
