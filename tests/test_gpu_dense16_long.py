@@ -176,3 +176,53 @@ def test_backward_passes_in_a_row(T, F, K, captured):
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for o, w in zip(outs, want) for p, q in zip(o, w))
     assert vnm.vnm_dense_get_status() == vnm.VNM_OK
+
+
+@pytest.mark.parametrize("T", [1, 8, 16])
+def test_what_was_added_to_in_place_is_read_by_the_next_call(T):
+    """Calls that add to Y in place, whose neighbouring CTAs read and write parts of the same 32 bytes (Y starts 16 bytes into
+    them), each followed by calls that read Y: as X of few tokens, as X of narrow tiles, as dY of a backward pass. The next grid's CTAs are
+    there before the sums are; they must not see what was cached before."""
+    D, F = 4096, 512
+    g = generator(T, 27)
+    x = whole(g, T, 256, F16, 1)
+    w, w2, wide = whole(g, D, 256, F16, 1), whole(g, F, D, F16, 1), whole(g, 300, D, F16, 1)
+    buf = torch.zeros(T * D + 8, dtype=F16, device=DEV)
+    Y = buf[8:].view(T, D)
+    gg, uu = whole(g, T, D, F16, 1), whole(g, T, D, F16, 1)
+    n = 6
+    Z, V = (torch.empty((n, T, F), dtype=F32, device=DEV) for _ in range(2))
+    dx, wg = torch.empty((n, T, 64), dtype=F16, device=DEV), whole(g, D, 64, F16, 1)
+    ws = torch.empty(vnm.vnm_gated_linear_backward_workspace_size(T, D), dtype=torch.uint8, device=DEV)
+    turned = torch.empty((n, 300, T), dtype=F32, device=DEV)
+
+    def run(wait=lambda: None):
+        Y.zero_()
+        for i in range(n):
+            vnm.vnm_dense_linear(x, w, Y, residual=Y)
+            wait()
+            vnm.vnm_dense_linear(Y, w2, Z[i])
+            wait()
+            vnm.vnm_dense_linear(x, w, Y, residual=Y)
+            wait()
+            vnm.vnm_gated_linear_backward(Y, None, wg, wg, gg, uu, dx=dx[i], workspace=ws)
+            wait()
+            vnm.vnm_dense_linear(x, w, Y, residual=Y)
+            wait()
+            vnm.vnm_dense_linear(wide, Y, turned[i])
+            wait()
+            vnm.vnm_dense_linear(Y, w2, V[i])
+            wait()
+
+    run(torch.cuda.synchronize)
+    want = [v.clone() for v in (Z, V, dx, turned, Y)]
+    total = 3 * (x.double() @ w.double().t())
+    for i in range(n):
+        assert torch.equal(V[i].double(), (i + 1) * total @ w2.double().t())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for way in [run] * 20 + [graph.replay] * 20:
+        way()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, (Z, V, dx, turned, Y)))
