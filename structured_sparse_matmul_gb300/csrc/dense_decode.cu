@@ -11,7 +11,8 @@
 // a block of 64, and the same columns of token g, which are the operands of two MMAs with
 // no shuffle. A CTA takes 16 rows, its warps deal the K blocks among themselves and
 // meet once in shared memory, in a fixed order. The loads of W run kRing blocks ahead,
-// those of x (from L2) one. After every round of the ring the MMAs' sums, which
+// those of x (from L2) one; a last block shorter than 64 is worked on while the first ones are on their way (1500 rows of 500,
+// one token: 4.2 us behind the others and byte by byte, 2.1 so). After every round of the ring the MMAs' sums, which
 // truncate, are added up in fp32. Measured, fp16, one token (us; in brackets the weights at a copy's rate, which is
 // below what reads alone reach): 4096 rows of 11008 15.8 (13.5), 11008 x 2 rows of 4096 27.8 (27.0); what is left is
 // the launch and the first loads' round trip.
@@ -27,13 +28,15 @@ namespace {
 constexpr int kRows = 16;  // rows of W of a CTA
 constexpr int kBlockK = 64;
 
-// 8 warps a CTA, two CTAs an SM; or, where those do not hold all rows of W at once, 4 warps, five CTAs, with
-// fewer loads in flight a warp. 1 and 8 tokens, fp16 (us): 4096 rows of 11008 (256 CTAs) 16.4 and 17.4 with 8 warps,
-// 31.6 and 31.9 with 4; 11008 rows of 4096 (688 CTAs) 18.7 and 20.1, 17.2 and 17.6; gated 32.5 and 33.3, 29.2 and 29.5.
+// 8 warps a CTA, two CTAs an SM; where there are no more CTAs than SMs, 16 warps, as many loads in flight, if K gives each
+// two blocks; or, where those do not hold all rows of W at once, 4 warps, five CTAs, with fewer loads in flight a warp.
+// 1 and 8 tokens, fp16 (us): 1024 rows of 11008 (64 CTAs) 11.4 and 12.1 with 8 warps, 7.6 and 8.1 with 16, 1024 of 1024
+// 2.13 and 2.24, 2.11 and 2.28; 4096 rows of 11008 (256 CTAs) 15.8 and 16.9 with 8 warps, 31.6 and 31.9 with 4; 11008 rows of 4096 (688
+// CTAs) 18.7 and 20.1, 16.3 and 16.4; gated 32.5 and 33.3, 27.8 and 27.9.
 template <int WARPS, bool GATED>
 struct Cfg {
-    static constexpr int kCtas = WARPS == 8 ? 2 : 5;
-    static constexpr int kRing = WARPS == 8 ? (GATED ? 2 : 4) : (GATED ? 1 : 3);
+    static constexpr int kCtas = WARPS == 16 ? 1 : WARPS == 8 ? 2 : 5;
+    static constexpr int kRing = WARPS >= 8 ? (GATED ? 2 : 4) : (GATED ? 1 : 3);
 };
 
 struct FewArgs {
@@ -78,6 +81,28 @@ __device__ __forceinline__ uint4 load_shared_row(const uint8_t* p) {
     return v;
 }
 
+// 16 bytes of a row's last block, `left` bytes (an even number, any) before the row's end; what lies past it is not read. By
+// loads that do not wait for each other: `in_place` puts the pieces there.
+__device__ __forceinline__ uint4 load_end(const uint8_t* p, int left) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    const int n = left >= 16 || left < 0 ? 0 : left;
+    asm volatile(
+        "{\n\t.reg .pred w, a, b, c;\n\t"
+        "setp.ge.s32 w, %5, 16;\n\tsetp.ne.s32 a, %6, 0;\n\tsetp.ne.s32 b, %7, 0;\n\tsetp.ne.s32 c, %8, 0;\n\t"
+        "@w ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t"
+        "@a ld.global.v2.u32 {%0, %1}, [%4];\n\t"
+        "@b ld.global.u32 %2, [%9];\n\t"
+        "@c ld.global.u16 %3, [%10];\n\t}"
+        : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+        : "l"(p), "r"(left), "r"(n & 8), "r"(n & 4), "r"(n & 2), "l"(p + (n & 8)), "l"(p + (n & 12)));
+    return v;
+}
+__device__ __forceinline__ uint4 in_place(const uint4& v, int left) {
+    if (left >= 16 || left <= 0) return v;
+    const uint32_t first = left & 4 ? v.z : v.w, second = left & 4 ? v.w : 0u;
+    return left & 8 ? make_uint4(v.x, v.y, first, second) : make_uint4(first, second, 0u, 0u);
+}
+
 template <int NW>
 struct Weights {
     uint4 v[NW][2][2];  // [matrix][row g, g + 8][step]
@@ -87,8 +112,9 @@ struct Tokens {
     uint4 v[NT][2];  // of tokens g, g + 8
 };
 
-// NT: groups of 8 tokens.
-template <bool BF16, bool GATED, int NT, int kWarps>
+// NT: groups of 8 tokens. TAIL: K is no multiple of kBlockK (the code for its last block costs the others registers: 16
+// tokens, gated, 1024 x 1024 took 3.2 us without it and 3.5 with it).
+template <bool BF16, bool GATED, int NT, int kWarps, bool TAIL>
 __global__ void __launch_bounds__(32 * kWarps, Cfg<kWarps, GATED>::kCtas) dense_decode_kernel(const ArgsOf<GATED> a) {
     constexpr int NW = GATED ? 2 : 1, kRing = Cfg<kWarps, GATED>::kRing;
     __shared__ float part[NW][kWarps][8 * NT][kRows + 1];
@@ -162,6 +188,33 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<kWarps, GATED>::kCtas) dense_
     for (int u = 0; u < kRing; ++u)
         if (warp + u * kWarps < full) load_w(ring[u], warp + u * kWarps);
     if (warp < full) load_x(next, warp);
+    if (TAIL && full % kWarps == warp) {  // the last, shorter block, whose loads are in flight with the first ones
+        const int64_t at = static_cast<int64_t>(full) * 128;
+        const int left = static_cast<int>(2 * a.K - at) - 16 * i;
+        Weights<NW> w;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int m = 0; m < NW; ++m) {
+                w.v[m][0][h] = load_end(w0[m] + at + 64 * h, left - 64 * h);
+                w.v[m][1][h] = load_end(w1[m] + at + 64 * h, left - 64 * h);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) cur.v[n][h] = load_end(x0[n] + at + 64 * h, left - 64 * h);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int m = 0; m < NW; ++m) {
+                w.v[m][0][h] = in_place(w.v[m][0][h], left - 64 * h);
+                w.v[m][1][h] = in_place(w.v[m][1][h], left - 64 * h);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) cur.v[n][h] = in_place(cur.v[n][h], left - 64 * h);
+        }
+        multiply(w, cur);
+        take();
+    }
 #pragma unroll 1
     for (int b0 = warp; b0 < full; b0 += kRing * kWarps) {
 #pragma unroll
@@ -173,21 +226,6 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<kWarps, GATED>::kCtas) dense_
             multiply(ring[u], cur);
             if (b + kRing * kWarps < full) load_w(ring[u], b + kRing * kWarps);
         }
-        take();
-    }
-    if (a.K % kBlockK != 0 && full % kWarps == warp) {
-        const int64_t at = static_cast<int64_t>(full) * 128 + 16 * i, end = 2 * a.K;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int m = 0; m < NW; ++m) {
-                ring[0].v[m][0][h] = load_edge<true>(w0[m] - 16 * i, at + 64 * h, end, row0 == a.R - 1);
-                ring[0].v[m][1][h] = load_edge<true>(w1[m] - 16 * i, at + 64 * h, end, row1 == a.R - 1);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) cur.v[n][h] = load_edge<true>(x0[n] - 16 * i, at + 64 * h, end, g + 8 * n >= last);
-        }
-        multiply(ring[0], cur);
         take();
     }
 #pragma unroll
@@ -221,12 +259,18 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<kWarps, GATED>::kCtas) dense_
     }
 }
 
-template <bool BF16, bool GATED, int NT>
-cudaError_t launch(const FewGatedArgs& all, int sm_count, cudaStream_t stream) {
+template <bool BF16, bool GATED, int NT, int WARPS>
+cudaError_t launch(const FewGatedArgs& all, int64_t blocks, cudaStream_t stream) {
     const ArgsOf<GATED>& a = all;
+    return a.K % kBlockK == 0 ? launch_early(dense_decode_kernel<BF16, GATED, NT, WARPS, false>, blocks, 32 * WARPS, 0, 1, stream, a)
+                              : launch_early(dense_decode_kernel<BF16, GATED, NT, WARPS, true>, blocks, 32 * WARPS, 0, 1, stream, a);
+}
+
+template <bool BF16, bool GATED, int NT>
+cudaError_t launch(const FewGatedArgs& a, int sm_count, cudaStream_t stream) {
     const int64_t blocks = (a.R + kRows - 1) / kRows;
-    return blocks <= 2 * sm_count ? launch_early(dense_decode_kernel<BF16, GATED, NT, 8>, blocks, 256, 0, 1, stream, a)
-                                  : launch_early(dense_decode_kernel<BF16, GATED, NT, 4>, blocks, 128, 0, 1, stream, a);
+    if (blocks <= sm_count && a.K >= 32 * kBlockK) return launch<BF16, GATED, NT, 16>(a, blocks, stream);
+    return blocks <= 2 * sm_count ? launch<BF16, GATED, NT, 8>(a, blocks, stream) : launch<BF16, GATED, NT, 4>(a, blocks, stream);
 }
 
 template <bool BF16, bool GATED>

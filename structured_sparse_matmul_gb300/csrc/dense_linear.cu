@@ -1364,18 +1364,20 @@ TilePlan plan_tiles(const ProductArgs& p, int sm_count) {
     return best;
 }
 
-// Up to 8 tokens; up to kFewTokens where W is so small that the narrow tiles' start weighs more (16 tokens, us: 1024 x
-// 1024 2.8 against 5.1, 4096 x 4096 8.9 and 10.0, 11008 x 4096 21.1 and 20.7; gated 3.7 and 5.8, 15.6 and 15.4, 36.7 and 31.1).
-bool few_tokens(const ProductArgs& p) {
+// Up to 8 tokens; up to kFewTokens where one round of its CTAs, two an SM, holds all rows, and, of a gated pair, where K is
+// short. 12 tokens, few-token kernel and narrow tiles (us): 1024 x 1024 2.5 and 5.2, 2200 x 11008 11.8 and 14.0, 4500 x 11008
+// 20.9 and 22.5, 6000 x 5000 18.4 and 16.0; gated 1024 x 1024 3.4 and 6.0, 1024 x 2500 7.6 and 8.8, 1024 x 11008 17.1 and 14.4,
+// 3000 x 250 4.8 and 3.7. 8 tokens: 0.4 to 0.95 of the narrow tiles' time everywhere (64 .. 9000 rows, K = 250 .. 11008).
+bool few_tokens(const ProductArgs& p, int sm_count) {
     const bool gated = p.kind == kGatedPair;
     if ((p.kind != kOneProduct && !gated) || p.keep == kKeep8 || p.x[0].transposed || p.w[0].transposed) return false;
-    return p.T <= 8 || (p.T <= kFewTokens && p.R * p.K * (gated ? 2 : 1) <= (1 << 24));
+    return p.T <= 8 || (p.T <= kFewTokens && p.R <= static_cast<int64_t>(gated ? 16 : 32) * sm_count && (!gated || p.K <= 2560));
 }
 
 }  // namespace
 
 TilePlan plan_product(const ProductArgs& p, int sm_count) {
-    return few_tokens(p) && p.skip_stage < 0 ? TilePlan{kFewPlan, 1, 0} : plan_tiles(p, sm_count);
+    return few_tokens(p, sm_count) && p.skip_stage < 0 ? TilePlan{kFewPlan, 1, 0} : plan_tiles(p, sm_count);
 }
 
 cudaError_t take_product_status(int* code, cudaStream_t stream) {

@@ -26,12 +26,11 @@ __device__ __forceinline__ uint4 load_once_coherent(const uint8_t* p) {
 // 16 bytes of a row from column k on, 0 from column K on (the last, shorter block).
 // Rows are 16-byte aligned, so the 16 bytes lie within the row's pitch; the last
 // row's pitch may not be all there, and its last bytes are read one by one.
-template <bool COHERENT = false>
 static __device__ __noinline__ uint4 load_edge(const uint8_t* row, int64_t k, int64_t K, bool last_row) {
     const int n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(16), K - k)));  // bytes that exist
     uint32_t u[4] = {0u, 0u, 0u, 0u};
     if (n == 16 || (n > 0 && !last_row)) {
-        const uint4 v = COHERENT ? load_once_coherent(row + k) : load_once(row + k);
+        const uint4 v = load_once(row + k);
         u[0] = v.x;
         u[1] = v.y;
         u[2] = v.z;
