@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     cluster_sync_all();  // the CTAs' barriers and TMEM exist
     tc_fence_after_sync();
-    if (!a.beside) after_previous_grid();
+    after_the_one_before(a.beside, a.o.res[0] != nullptr);
     let_next_grid_start();
     const uint32_t tmem = tmem_slot;
     volatile int* abort = &abort_flag;
@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         stage16(buf + 2048, u);
                     } else if (o.keep == kKeep8) {
                         stage8(buf + 2048, g, scale.g, scale.g_inv);
-                        stage8(buf + 3072, u, scale.u, scale.u_inv);
+                        stage8(buf + 3 * 1024, u, scale.u, scale.u_inv);
                     }
                     activate_all(o.act, g);
 #pragma unroll
@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                     if (o.keep == kKeep8) {
                         emit_box<32, 1, ALIGNED>(&outs.g, o.keep_tma, o.g.p, o.g.ld, m0, n0, o.T, end, buf + 2048, lane);
-                        emit_box<32, 1, ALIGNED>(&outs.u, o.keep_tma, o.u.p, o.u.ld, m0, n0, o.T, end, buf + 3072, lane);
+                        emit_box<32, 1, ALIGNED>(&outs.u, o.keep_tma, o.u.p, o.u.ld, m0, n0, o.T, end, buf + 3 * 1024, lane);
                     }
                     if (lane == 0) tma_store_commit();
                     ++box;
@@ -945,7 +945,7 @@ __global__ void __launch_bounds__(NarrowCfg<BN>::kThreads, 2)
         abort_flag = 0;
         fence_barrier_init();
         // the first stages need no other thread: their latency covers the TMEM allocation
-        if (!a.beside) after_previous_grid();
+        after_the_one_before(a.beside, false);
         for (int k = 0; k < early; ++k)
             if (k != a.skip_stage || blockIdx.x != 0) load_stage(k, kb0 + k);
     }
@@ -953,7 +953,7 @@ __global__ void __launch_bounds__(NarrowCfg<BN>::kThreads, 2)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (!a.beside) after_previous_grid();
+    after_the_one_before(a.beside, a.o.res[0] != nullptr);
     if (a.next_beside) let_next_grid_start();
     const uint32_t tmem = tmem_slot;
     volatile int* abort = &abort_flag;

@@ -11,6 +11,14 @@ namespace vnm {
 // The launches let this grid start while the stream's previous one drains: nothing of global memory is
 // touched before its end.
 __device__ __forceinline__ void after_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The same of a grid that may run beside the one before: what came before that one has ended then. What such a grid reads
+// by way of L1 (`l1`) must not be what an earlier grid read there before its other CTAs wrote it.
+__device__ __forceinline__ void after_the_one_before(bool beside, bool l1) {
+    if (!beside)
+        after_previous_grid();
+    else if (l1)
+        __threadfence();
+}
 // From here on the next such grid may start (it waits for our end in the same way). Called after the wait: only one
 // grid is ahead at a time.
 __device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -226,3 +226,37 @@ def test_what_was_added_to_in_place_is_read_by_the_next_call(T):
         way()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, (Z, V, dx, turned, Y)))
+
+
+@pytest.mark.parametrize("T,F,K", [(42, 1576, 125), (5, 301, 77), (736, 1281, 149), (578, 1346, 1275)])
+@pytest.mark.parametrize("w_type", [BF16, F32])
+def test_gradients_added_up_over_passes(T, F, K, w_type):
+    """The weights' gradients of passes one behind the other, added up in rows whose ends share 32 bytes with their
+    neighbours': the bits of passes that each wait for the one before."""
+    g = generator(T, F, K, 28)
+    dy, x, wg, wu = (pitched(whole(g, *s, BF16, 1)) for s in ((T, F), (T, K), (F, K), (F, K)))
+    gate, up = (whole(g, T, F, BF16, 1) for _ in range(2))
+    ws = torch.empty(vnm.vnm_gated_linear_backward_workspace_size(T, F), dtype=torch.uint8, device=DEV)
+    dx = torch.empty((T, K), dtype=BF16, device=DEV)
+    dwg, dwu = (torch.empty((F, K), dtype=w_type, device=DEV) for _ in range(2))
+
+    def run(wait=lambda: None):
+        dwg.zero_()
+        dwu.zero_()
+        for _ in range(12):
+            wait()
+            vnm.vnm_gated_linear_backward(dy, x, wg, wu, gate, up, act=NONE, dx=dx, dwg=dwg, dwu=dwu, accumulate=True, workspace=ws)
+
+    run(torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    want = [v.clone() for v in (dx, dwg, dwu)]
+    if w_type == F32:
+        assert torch.equal(dwg.double(), 12 * ((dy * up).double().t() @ x.double()))
+        assert torch.equal(dwu.double(), 12 * ((dy * gate).double().t() @ x.double()))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for way in [run] * 20 + [graph.replay] * 20:
+        way()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, (dx, dwg, dwu)))
