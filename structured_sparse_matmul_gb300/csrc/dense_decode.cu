@@ -270,7 +270,10 @@ template <bool BF16, bool GATED, int NT>
 cudaError_t launch(const FewGatedArgs& a, int sm_count, cudaStream_t stream) {
     const int64_t blocks = (a.R + kRows - 1) / kRows;
     if (blocks <= sm_count && a.K >= 32 * kBlockK) return launch<BF16, GATED, NT, 16>(a, blocks, stream);
-    return blocks <= 2 * sm_count ? launch<BF16, GATED, NT, 8>(a, blocks, stream) : launch<BF16, GATED, NT, 4>(a, blocks, stream);
+    if constexpr (NT == 1) {  // (with more than 8 tokens, more rows go to the narrow tiles)
+        if (blocks > 2 * sm_count) return launch<BF16, GATED, NT, 4>(a, blocks, stream);
+    }
+    return launch<BF16, GATED, NT, 8>(a, blocks, stream);
 }
 
 template <bool BF16, bool GATED>
