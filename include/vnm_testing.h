@@ -69,6 +69,28 @@ vnm_status vnm_testing_dense_linear_skip_stage(const void* X, int64_t ld_x, cons
                                                int32_t* status, int32_t skip_stage, vnm_stream_t stream);
 
 /*
+ * vnm_gated_linear with the same change (the few-token kernel is not taken).
+ */
+vnm_status vnm_testing_gated_linear_skip_stage(const void* X, int64_t ld_x, const void* Wg, int64_t ld_wg, const void* Wu,
+                                               int64_t ld_wu, vnm_dtype type, int64_t T, int64_t F, int64_t K,
+                                               vnm_activation act, void* Y, int64_t ld_y, vnm_keep keep, void* g, int64_t ld_g,
+                                               float* g_scale, int64_t gs_rs, int64_t gs_cs, void* u, int64_t ld_u,
+                                               float* u_scale, int64_t us_rs, int64_t us_cs, int32_t* status,
+                                               int32_t skip_stage, vnm_stream_t stream);
+
+/*
+ * vnm_gated_linear_backward with the same change in dX's product (stage skip_dx) and in the weights' (skip_dw); -1: none.
+ */
+vnm_status vnm_testing_gated_linear_backward_skip_stage(const void* dY, int64_t ld_dy, const void* X, int64_t ld_x, const void* Wg,
+                                                        int64_t ld_wg, const void* Wu, int64_t ld_wu, vnm_dtype type, int64_t T, int64_t F,
+                                                        int64_t K, vnm_activation act, vnm_keep keep, const void* g, int64_t ld_g,
+                                                        const float* g_scale, int64_t gs_rs, int64_t gs_cs, const void* u, int64_t ld_u,
+                                                        const float* u_scale, int64_t us_rs, int64_t us_cs, void* dX, int64_t ld_dx, void* dWg,
+                                                        void* dWu, int64_t ld_dw, vnm_dtype w_type, int32_t accumulate, void* H, int64_t ld_h,
+                                                        void* workspace, size_t workspace_bytes, int32_t* status,
+                                                        int32_t skip_dx, int32_t skip_dw, vnm_stream_t stream);
+
+/*
  * How the dense 16-bit layers take a product with aligned 16-bit outputs on a GPU of sm_count SMs
  * (host only): tiles of *tile_tokens = 16, 32, 64 or 128 tokens with K over *splits CTAs of a cluster; 0:
  * pairs of CTAs, 256 tokens by *tile_rows rows of W, K over *splits pairs; 8: the few-token kernel.

@@ -100,53 +100,11 @@ vnm_status dense_linear(const void* X, int64_t ld_x, int32_t x_transposed, const
 
 int64_t padded(int64_t F) { return (F + 7) / 8 * 8; }
 
-}  // namespace
-
-extern "C" {
-
-vnm_status vnm_dense_linear(const void* X, int64_t ld_x, int32_t x_transposed, const void* W, int64_t ld_w,
-                            int32_t w_transposed, vnm_dtype type, int64_t T, int64_t R, int64_t K, const void* bias,
-                            vnm_dtype bias_type, vnm_activation act, const void* residual, int64_t ld_residual, void* Y,
-                            int64_t ld_y, vnm_dtype y_type, int32_t* status, vnm_stream_t stream) {
-    return dense_linear(X, ld_x, x_transposed, W, ld_w, w_transposed, type, T, R, K, bias, bias_type, act, residual,
-                        ld_residual, Y, ld_y, y_type, status, -1, stream);
-}
-
-vnm_status vnm_testing_dense_linear_skip_stage(const void* X, int64_t ld_x, const void* W, int64_t ld_w, vnm_dtype type,
-                                               int64_t T, int64_t R, int64_t K, void* Y, int64_t ld_y, vnm_dtype y_type,
-                                               int32_t* status, int32_t skip_stage, vnm_stream_t stream) {
-    if (skip_stage < 0) return VNM_ERR_INVALID_ARG;
-    return dense_linear(X, ld_x, 0, W, ld_w, 0, type, T, R, K, nullptr, VNM_F32, VNM_ACT_NONE, nullptr, 0, Y, ld_y, y_type, status,
-                        skip_stage, stream);
-}
-
-vnm_status vnm_testing_dense_plan(int32_t kind, int64_t T, int64_t R, int64_t K, int32_t x_transposed, int32_t w_transposed,
-                                  vnm_keep keep, int32_t sm_count, int32_t* tile_tokens, int32_t* tile_rows,
-                                  int32_t* splits) {
-    if (kind < 0 || kind > vnm::kGatedPair || !size_ok(T) || !size_ok(R) || !size_ok(K) || T == 0 || R == 0 || K == 0 ||
-        !keep_ok(keep) || sm_count < 1 || tile_tokens == nullptr || tile_rows == nullptr || splits == nullptr)
-        return VNM_ERR_INVALID_ARG;
-    vnm::ProductArgs p{};
-    p.kind = static_cast<vnm::ProductKind>(kind);
-    p.T = T;
-    p.R = R;
-    p.K = K;
-    p.x[0].transposed = x_transposed != 0;
-    p.w[0].transposed = w_transposed != 0;
-    p.keep = kind_of(keep);
-    p.skip_stage = -1;
-    const vnm::TilePlan plan = vnm::plan_product(p, sm_count);
-    *tile_tokens = plan.bn;
-    *tile_rows = plan.tile_n;
-    *splits = plan.splits;
-    return VNM_OK;
-}
-
-vnm_status vnm_gated_linear(const void* X, int64_t ld_x, const void* Wg, int64_t ld_wg, const void* Wu, int64_t ld_wu,
-                            vnm_dtype type, int64_t T, int64_t F, int64_t K, vnm_activation act, void* Y, int64_t ld_y,
-                            vnm_keep keep, void* g, int64_t ld_g, float* g_scale, int64_t gs_rs, int64_t gs_cs, void* u,
-                            int64_t ld_u, float* u_scale, int64_t us_rs, int64_t us_cs, int32_t* status,
-                            vnm_stream_t stream) {
+vnm_status gated_linear(const void* X, int64_t ld_x, const void* Wg, int64_t ld_wg, const void* Wu, int64_t ld_wu,
+                        vnm_dtype type, int64_t T, int64_t F, int64_t K, vnm_activation act, void* Y, int64_t ld_y,
+                        vnm_keep keep, void* g, int64_t ld_g, float* g_scale, int64_t gs_rs, int64_t gs_cs, void* u,
+                        int64_t ld_u, float* u_scale, int64_t us_rs, int64_t us_cs, int32_t* status,
+                        int skip_stage, vnm_stream_t stream) {
     if ((type != VNM_F16 && type != VNM_BF16) || !act_ok(act) || !keep_ok(keep) || !size_ok(T) || !size_ok(F) || !size_ok(K) ||
         !aligned(status, 4))
         return VNM_ERR_INVALID_ARG;
@@ -172,23 +130,18 @@ vnm_status vnm_gated_linear(const void* X, int64_t ld_x, const void* Wg, int64_t
     p.keep = kind_of(keep);
     p.e5m2 = keep == VNM_KEEP_E5M2;
     p.status = status;
-    p.skip_stage = -1;
+    p.skip_stage = skip_stage;
     return launched(vnm::launch_product(p, vnm::plan_product(p, sms), sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-vnm_status vnm_gated_linear_backward_workspace_size(int64_t T, int64_t F, size_t* bytes) {
-    if (bytes == nullptr || !size_ok(T) || !size_ok(F)) return VNM_ERR_INVALID_ARG;
-    *bytes = 4 * static_cast<size_t>(T) * static_cast<size_t>(padded(F));  // dG and dU side by side
-    return VNM_OK;
-}
-
-vnm_status vnm_gated_linear_backward(const void* dY, int64_t ld_dy, const void* X, int64_t ld_x, const void* Wg,
-                                     int64_t ld_wg, const void* Wu, int64_t ld_wu, vnm_dtype type, int64_t T, int64_t F,
-                                     int64_t K, vnm_activation act, vnm_keep keep, const void* g, int64_t ld_g,
-                                     const float* g_scale, int64_t gs_rs, int64_t gs_cs, const void* u, int64_t ld_u,
-                                     const float* u_scale, int64_t us_rs, int64_t us_cs, void* dX, int64_t ld_dx, void* dWg,
-                                     void* dWu, int64_t ld_dw, vnm_dtype w_type, int32_t accumulate, void* H, int64_t ld_h,
-                                     void* workspace, size_t workspace_bytes, int32_t* status, vnm_stream_t stream) {
+vnm_status gated_linear_backward(const void* dY, int64_t ld_dy, const void* X, int64_t ld_x, const void* Wg,
+                                 int64_t ld_wg, const void* Wu, int64_t ld_wu, vnm_dtype type, int64_t T, int64_t F,
+                                 int64_t K, vnm_activation act, vnm_keep keep, const void* g, int64_t ld_g,
+                                 const float* g_scale, int64_t gs_rs, int64_t gs_cs, const void* u, int64_t ld_u,
+                                 const float* u_scale, int64_t us_rs, int64_t us_cs, void* dX, int64_t ld_dx, void* dWg,
+                                 void* dWu, int64_t ld_dw, vnm_dtype w_type, int32_t accumulate, void* H, int64_t ld_h,
+                                 void* workspace, size_t workspace_bytes, int32_t* status, int skip_dx,
+                                 int skip_dw, vnm_stream_t stream) {
     const bool weights = dWg != nullptr;
     if ((type != VNM_F16 && type != VNM_BF16) || !act_ok(act) || !keep_ok(keep) || keep == VNM_KEEP_NONE || !size_ok(T) ||
         !size_ok(F) || !size_ok(K) || !aligned(status, 4) || (accumulate != 0 && accumulate != 1) ||
@@ -253,7 +206,7 @@ vnm_status vnm_gated_linear_backward(const void* dY, int64_t ld_dy, const void* 
         in.y_type = type;
         in.act = VNM_ACT_NONE;
         in.status = status;
-        in.skip_stage = -1;
+        in.skip_stage = skip_dx;
     }
     if (dw) {
         gr.kind = vnm::kTwoByRows;
@@ -274,7 +227,7 @@ vnm_status vnm_gated_linear_backward(const void* dY, int64_t ld_dy, const void* 
             gr.ld_residual = ld_dw;
         }
         gr.status = status;
-        gr.skip_stage = -1;
+        gr.skip_stage = skip_dw;
     }
     // dX and the weights' gradients share dG and dU, and neither reads what the other writes: their grids run side by side.
     // The pass in us, one after the other and so (T x F over K): 42 x 1576 over 125 13.0 and 9.0, 333 x 1001 over 1023 22.8
@@ -284,6 +237,101 @@ vnm_status vnm_gated_linear_backward(const void* dY, int64_t ld_dy, const void* 
     if (dx && err == cudaSuccess) err = vnm::launch_product(in, vnm::plan_product(in, sms), sms, s);
     if (dw && err == cudaSuccess) err = vnm::launch_product(gr, vnm::plan_product(gr, sms), sms, s);
     return launched(err);
+}
+
+}  // namespace
+
+extern "C" {
+
+vnm_status vnm_dense_linear(const void* X, int64_t ld_x, int32_t x_transposed, const void* W, int64_t ld_w,
+                            int32_t w_transposed, vnm_dtype type, int64_t T, int64_t R, int64_t K, const void* bias,
+                            vnm_dtype bias_type, vnm_activation act, const void* residual, int64_t ld_residual, void* Y,
+                            int64_t ld_y, vnm_dtype y_type, int32_t* status, vnm_stream_t stream) {
+    return dense_linear(X, ld_x, x_transposed, W, ld_w, w_transposed, type, T, R, K, bias, bias_type, act, residual,
+                        ld_residual, Y, ld_y, y_type, status, -1, stream);
+}
+
+vnm_status vnm_testing_dense_linear_skip_stage(const void* X, int64_t ld_x, const void* W, int64_t ld_w, vnm_dtype type,
+                                               int64_t T, int64_t R, int64_t K, void* Y, int64_t ld_y, vnm_dtype y_type,
+                                               int32_t* status, int32_t skip_stage, vnm_stream_t stream) {
+    if (skip_stage < 0) return VNM_ERR_INVALID_ARG;
+    return dense_linear(X, ld_x, 0, W, ld_w, 0, type, T, R, K, nullptr, VNM_F32, VNM_ACT_NONE, nullptr, 0, Y, ld_y, y_type, status,
+                        skip_stage, stream);
+}
+
+vnm_status vnm_testing_dense_plan(int32_t kind, int64_t T, int64_t R, int64_t K, int32_t x_transposed, int32_t w_transposed,
+                                  vnm_keep keep, int32_t sm_count, int32_t* tile_tokens, int32_t* tile_rows,
+                                  int32_t* splits) {
+    if (kind < 0 || kind > vnm::kGatedPair || !size_ok(T) || !size_ok(R) || !size_ok(K) || T == 0 || R == 0 || K == 0 ||
+        !keep_ok(keep) || sm_count < 1 || tile_tokens == nullptr || tile_rows == nullptr || splits == nullptr)
+        return VNM_ERR_INVALID_ARG;
+    vnm::ProductArgs p{};
+    p.kind = static_cast<vnm::ProductKind>(kind);
+    p.T = T;
+    p.R = R;
+    p.K = K;
+    p.x[0].transposed = x_transposed != 0;
+    p.w[0].transposed = w_transposed != 0;
+    p.keep = kind_of(keep);
+    p.skip_stage = -1;
+    const vnm::TilePlan plan = vnm::plan_product(p, sm_count);
+    *tile_tokens = plan.bn;
+    *tile_rows = plan.tile_n;
+    *splits = plan.splits;
+    return VNM_OK;
+}
+
+vnm_status vnm_gated_linear(const void* X, int64_t ld_x, const void* Wg, int64_t ld_wg, const void* Wu, int64_t ld_wu,
+                            vnm_dtype type, int64_t T, int64_t F, int64_t K, vnm_activation act, void* Y, int64_t ld_y,
+                            vnm_keep keep, void* g, int64_t ld_g, float* g_scale, int64_t gs_rs, int64_t gs_cs, void* u,
+                            int64_t ld_u, float* u_scale, int64_t us_rs, int64_t us_cs, int32_t* status,
+                            vnm_stream_t stream) {
+    return gated_linear(X, ld_x, Wg, ld_wg, Wu, ld_wu, type, T, F, K, act, Y, ld_y, keep, g, ld_g, g_scale, gs_rs, gs_cs, u, ld_u,
+                        u_scale, us_rs, us_cs, status, -1, stream);
+}
+
+vnm_status vnm_testing_gated_linear_skip_stage(const void* X, int64_t ld_x, const void* Wg, int64_t ld_wg, const void* Wu,
+                                               int64_t ld_wu, vnm_dtype type, int64_t T, int64_t F, int64_t K,
+                                               vnm_activation act, void* Y, int64_t ld_y, vnm_keep keep, void* g, int64_t ld_g,
+                                               float* g_scale, int64_t gs_rs, int64_t gs_cs, void* u, int64_t ld_u,
+                                               float* u_scale, int64_t us_rs, int64_t us_cs, int32_t* status,
+                                               int32_t skip_stage, vnm_stream_t stream) {
+    if (skip_stage < 0) return VNM_ERR_INVALID_ARG;
+    return gated_linear(X, ld_x, Wg, ld_wg, Wu, ld_wu, type, T, F, K, act, Y, ld_y, keep, g, ld_g, g_scale, gs_rs, gs_cs, u, ld_u,
+                        u_scale, us_rs, us_cs, status, skip_stage, stream);
+}
+
+vnm_status vnm_gated_linear_backward_workspace_size(int64_t T, int64_t F, size_t* bytes) {
+    if (bytes == nullptr || !size_ok(T) || !size_ok(F)) return VNM_ERR_INVALID_ARG;
+    *bytes = 4 * static_cast<size_t>(T) * static_cast<size_t>(padded(F));  // dG and dU side by side
+    return VNM_OK;
+}
+
+vnm_status vnm_gated_linear_backward(const void* dY, int64_t ld_dy, const void* X, int64_t ld_x, const void* Wg,
+                                     int64_t ld_wg, const void* Wu, int64_t ld_wu, vnm_dtype type, int64_t T, int64_t F,
+                                     int64_t K, vnm_activation act, vnm_keep keep, const void* g, int64_t ld_g,
+                                     const float* g_scale, int64_t gs_rs, int64_t gs_cs, const void* u, int64_t ld_u,
+                                     const float* u_scale, int64_t us_rs, int64_t us_cs, void* dX, int64_t ld_dx, void* dWg,
+                                     void* dWu, int64_t ld_dw, vnm_dtype w_type, int32_t accumulate, void* H, int64_t ld_h,
+                                     void* workspace, size_t workspace_bytes, int32_t* status, vnm_stream_t stream) {
+    return gated_linear_backward(dY, ld_dy, X, ld_x, Wg, ld_wg, Wu, ld_wu, type, T, F, K, act, keep, g, ld_g, g_scale, gs_rs, gs_cs, u,
+                                 ld_u, u_scale, us_rs, us_cs, dX, ld_dx, dWg, dWu, ld_dw, w_type, accumulate, H, ld_h, workspace,
+                                 workspace_bytes, status, -1, -1, stream);
+}
+
+vnm_status vnm_testing_gated_linear_backward_skip_stage(const void* dY, int64_t ld_dy, const void* X, int64_t ld_x, const void* Wg,
+                                                        int64_t ld_wg, const void* Wu, int64_t ld_wu, vnm_dtype type, int64_t T, int64_t F,
+                                                        int64_t K, vnm_activation act, vnm_keep keep, const void* g, int64_t ld_g,
+                                                        const float* g_scale, int64_t gs_rs, int64_t gs_cs, const void* u, int64_t ld_u,
+                                                        const float* u_scale, int64_t us_rs, int64_t us_cs, void* dX, int64_t ld_dx, void* dWg,
+                                                        void* dWu, int64_t ld_dw, vnm_dtype w_type, int32_t accumulate, void* H, int64_t ld_h,
+                                                        void* workspace, size_t workspace_bytes, int32_t* status,
+                                                        int32_t skip_dx, int32_t skip_dw, vnm_stream_t stream) {
+    if (skip_dx < -1 || skip_dw < -1) return VNM_ERR_INVALID_ARG;
+    return gated_linear_backward(dY, ld_dy, X, ld_x, Wg, ld_wg, Wu, ld_wu, type, T, F, K, act, keep, g, ld_g, g_scale, gs_rs, gs_cs, u,
+                                 ld_u, u_scale, us_rs, us_cs, dX, ld_dx, dWg, dWu, ld_dw, w_type, accumulate, H, ld_h, workspace,
+                                 workspace_bytes, status, skip_dx,
+                                 skip_dw, stream);
 }
 
 vnm_status vnm_dense_get_status(vnm_stream_t stream) {

@@ -527,7 +527,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                     if (SPLIT || kb0 + a.chunk_kb < kb_last) release();
                 }
-                if (!run) break;
+                // (the warps that share a barrier below leave there, together)
+                if (!run && !(GATED && !SPLIT && o.keep == kKeep8)) break;
                 if constexpr (!GATED && !SPLIT && ALIGNED) {
                     if (roomy && f32 && o.act == VNM_ACT_NONE && o.bias == nullptr) {
                         // nothing follows the sums, and the ring is free: all boxes at once
@@ -571,7 +572,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             if (lane == 0) tma_store_wait_all_read();
                             __syncwarp();
                             st_shared_v2(stage + 8 * lane, g, u);
-                            named_barrier(1 + quarter, 64);
+                            // After a wait that ran out in one of the two warps, the sum may still become complete for
+                            // the other: both have to leave, or the one that goes on waits here for ever.
+                            run = named_barrier_all(1 + quarter, 64, run);
+                            if (!run) break;
                             g = max_magnitude(g, ld_shared_f32(other + 8 * lane));
                             u = max_magnitude(u, ld_shared_f32(other + 8 * lane + 4));
                             named_barrier(1 + quarter, 64);  // (read before the boxes are written)

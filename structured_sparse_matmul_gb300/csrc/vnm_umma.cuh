@@ -146,6 +146,20 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// As named_barrier, and whether `v` holds for all of its threads: they go on, or leave, together.
+__device__ __forceinline__ bool named_barrier_all(uint32_t id, uint32_t threads, bool v) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "bar.red.and.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(id), "r"(threads), "r"(v ? 1u : 0u)
+        : "memory");
+    return all != 0;
+}
+
 __device__ __forceinline__ float4 dsmem_ld_v4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"

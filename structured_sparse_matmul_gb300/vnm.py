@@ -101,6 +101,8 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.vnm_gated_linear_backward_workspace_size.argtypes = [i64, i64, p]
     L.vnm_dense_get_status.argtypes = [p]
     L.vnm_testing_dense_linear_skip_stage.argtypes = [p, i64, p, i64, dt, i64, i64, i64, p, i64, dt, p, i32, p]
+    L.vnm_testing_gated_linear_skip_stage.argtypes = L.vnm_gated_linear.argtypes[:25] + [i32, p]
+    L.vnm_testing_gated_linear_backward_skip_stage.argtypes = L.vnm_gated_linear_backward.argtypes[:36] + [i32, i32, p]
     L.vnm_testing_dense_plan.argtypes = [i32, i64, i64, i64, i32, i32, dt, i32, p, p, p]
     for name in ("vnm_sizes", "vnm_matrix_create", "vnm_matrix_destroy", "vnm_compress", "vnm_decompress",
                  "vnm_spmm", "vnm_spmm_workspace_size", "vnm_spmm_plan_query", "vnm_spmm_with_plan",
@@ -678,6 +680,45 @@ def vnm_testing_dense_linear_skip_stage(X: torch.Tensor, W: torch.Tensor, Y: tor
         X.data_ptr(), _rowmajor(X, "X"), W.data_ptr(), _rowmajor(W, "W"), dt[X.dtype], X.shape[0], W.shape[0], X.shape[1],
         Y.data_ptr(), _rowmajor(Y, "Y"), dt[Y.dtype], status.data_ptr() if status is not None else None, int(skip_stage),
         _stream_ptr(stream)), "vnm_testing_dense_linear_skip_stage")
+
+
+def _testing_kept(g, u, g_scale, u_scale, dtype) -> list:
+    """The arguments (keep, g .. us_cs) of checkpoints g and u, or of none."""
+    if g is None:
+        return [0] + [None, 1, None, 0, 0] * 2
+    keep = {dtype: 1, torch.float8_e4m3fn: 2, torch.float8_e5m2: 3}[g.dtype]
+    out = [keep]
+    for v, s in ((g, g_scale), (u, u_scale)):
+        out += [v.data_ptr(), _rowmajor(v, "g and u")] + ([s.data_ptr(), *s.stride()] if s is not None else [None, 0, 0])
+    return out
+
+
+def vnm_testing_gated_linear_skip_stage(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Y: torch.Tensor, skip_stage: int,
+                                        act: int = VNM_ACT_SILU, g=None, u=None, g_scale=None, u_scale=None,
+                                        status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Test support: vnm_gated_linear with the first CTA's loads of one pipeline stage never issued."""
+    dt = {torch.float16: VNM_F16, torch.bfloat16: VNM_BF16}
+    _check(lib().vnm_testing_gated_linear_skip_stage(
+        X.data_ptr(), _rowmajor(X, "X"), Wg.data_ptr(), _rowmajor(Wg, "Wg"), Wu.data_ptr(), _rowmajor(Wu, "Wu"), dt[X.dtype],
+        X.shape[0], Wg.shape[0], X.shape[1], int(act), Y.data_ptr(), _rowmajor(Y, "Y"),
+        *_testing_kept(g, u, g_scale, u_scale, X.dtype), status.data_ptr() if status is not None else None, int(skip_stage),
+        _stream_ptr(stream)), "vnm_testing_gated_linear_skip_stage")
+
+
+def vnm_testing_gated_linear_backward_skip_stage(dY: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor,
+                                                 g: torch.Tensor, u: torch.Tensor, dx: torch.Tensor, dwg: torch.Tensor,
+                                                 dwu: torch.Tensor, workspace: torch.Tensor, skip_dx: int, skip_dw: int,
+                                                 g_scale=None, u_scale=None, act: int = VNM_ACT_SILU,
+                                                 status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Test support: vnm_gated_linear_backward of dx, dwg and dwu with one pipeline stage's loads of the first CTA never
+    issued in dX's product (skip_dx) and in the weights' (skip_dw); -1: none."""
+    dt = {torch.float16: VNM_F16, torch.bfloat16: VNM_BF16, torch.float32: VNM_F32}
+    _check(lib().vnm_testing_gated_linear_backward_skip_stage(
+        dY.data_ptr(), _rowmajor(dY, "dY"), X.data_ptr(), _rowmajor(X, "X"), Wg.data_ptr(), _rowmajor(Wg, "Wg"), Wu.data_ptr(),
+        _rowmajor(Wu, "Wu"), dt[X.dtype], *g.shape, X.shape[1], int(act), *_testing_kept(g, u, g_scale, u_scale, X.dtype),
+        dx.data_ptr(), _rowmajor(dx, "dx"), dwg.data_ptr(), dwu.data_ptr(), _rowmajor(dwg, "dwg"), dt[dwg.dtype], 0, None, 1,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), status.data_ptr() if status is not None else None,
+        int(skip_dx), int(skip_dw), _stream_ptr(stream)), "vnm_testing_gated_linear_backward_skip_stage")
 
 
 def vnm_testing_dense_plan(kind: int, T: int, R: int, K: int, sm_count: int, x_transposed: bool = False,
