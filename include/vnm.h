@@ -537,7 +537,8 @@ vnm_status vnm_fp8_linear_get_status(vnm_stream_t stream);
 /*
  * Y = act(X . W^T + bias) + residual
  * X: T x K, W: R x K; bias: [R] of bias_type, or NULL; residual: T x R of y_type, or NULL; Y: T x
- * R, of y_type: the operands' type or VNM_F32. Everything after the sum is fp32.
+ * R, of y_type: the operands' type or VNM_F32. Everything after the sum is fp32; the residual is
+ * added to the whole sum, once.
  * The gradients of Y = X . W^T are products of the same form:
  *   dX = dY . W:            X := dY, W := W with w_transposed = 1;
  *   dW = dW0 + dY^T . X:    X := dY, W := X, both transposed, residual := dW0.

@@ -20,8 +20,11 @@
 //   warps 4..  epilogue: 32 rows x half of the columns a warp. A lane has a row, 16 columns at a time; bias,
 //              activation, rounding; then into boxes of 32 rows x 64 bytes, which tensor memory stores bring out
 //              (a residual's boxes came in by the same way). Of a CTA's last tile, which nothing hides, fp32 sums that
-//              need no more than storing go to the boxes straight from the registers (4096 x 1024 over 8192 53.5 and
-//              48.5 us).
+//              need no more than a residual go to the boxes straight from the registers, all of them at once (4096 x 1024
+//              over 8192 53.5 us through the loop and 48.5 so).
+// The residual is added to the whole sum. (Sums of several chunks that start from it, read under the MMAs, are rounded to
+// its spacing once a chunk: 2^24 and eight ones were 2^24. Reading it late is no slower either, us: 4096 x 1024 over 8192
+// 48.7 then and 49.2 now, 4096 x 4096 over 8192 205 and 188, 8192 x 8192 over 2048 313 and 224.)
 // Where the outputs' rows do not start and end on 16 bytes, the boxes are copied out by the warps. With
 // few tiles, K is split over the pairs of a cluster, which copy their sums to each other at the end.
 //
@@ -449,15 +452,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             // this warp's columns of the tile (a gated pair's features): first .. last - 1
             const int cols = GATED ? a.tile_n / 2 : a.tile_n, first = half * (kTileN / 2), last = min(cols, first + kTileN / 2);
             const int64_t n_tile = static_cast<int64_t>(nt) * cols, end = min(o.R, n_tile + cols);
-            // Where sums are added up in registers they may start from the residual, read while the MMAs run.
-            const bool from_res = SUM && !GATED && !SPLIT && o.act == VNM_ACT_NONE && o.res[seg] != nullptr;
-            const void* const res = GATED || SPLIT || from_res ? nullptr : o.res[seg];
-            if (!GATED && res != nullptr && o.res_vec && m < o.T && n_tile + first < end) {
+            // After the CTA's last tile the ring is free: its boxes all have a place of their own there, and no box waits for
+            // another's store. fp32 sums that are held in registers, with nothing to follow but a residual, then go to the boxes at once.
+            const bool last_tile = tile + tile_step >= a.tiles, f32 = o.y_type == VNM_F32;
+            const bool straight = SUM && !GATED && !SPLIT && ALIGNED && last_tile && f32 && o.act == VNM_ACT_NONE && o.bias == nullptr;
+            const void* const res = GATED || SPLIT || straight ? nullptr : o.res[seg];  // that the boxes' loop adds
+            if (!GATED && !SPLIT && o.res[seg] != nullptr && o.res_vec && m < o.T && n_tile + first < end) {
                 // the residual's row is on its way to L2 while the MMAs run
-                const int size = o.y_type == VNM_F32 ? 4 : 2;
+                const int size = f32 ? 4 : 2;
                 const uint32_t bytes =
                     static_cast<uint32_t>(min(static_cast<int64_t>(kTileN / 2), end - n_tile - first) * size) & ~15u;
-                if (bytes > 0) prefetch_l2(static_cast<const uint8_t*>(res) + (m * o.ld_res + n_tile + first) * size, bytes);
+                if (bytes > 0) prefetch_l2(static_cast<const uint8_t*>(o.res[seg]) + (m * o.ld_res + n_tile + first) * size, bytes);
             }
             auto fetch = [&](int c) {  // columns c .. c + 15 of the tile
                 Raw16 r;
@@ -471,11 +476,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 }
                 return r;
             };
-            // After the CTA's last tile the ring is free: its boxes all have a place of their own there, and no box waits for
-            // another's store.
-            const bool roomy = tile + tile_step >= a.tiles && res == nullptr;
+            const bool roomy = last_tile && res == nullptr;
             const uint32_t room = smem_base + (warp - kPairHelpers) * (kPairRing / kPairEpilogue);
-            const bool f32 = o.y_type == VNM_F32, bf16 = o.y_type == VNM_BF16, res_tma = res != nullptr && (ALIGNED || o.res_vec);
+            const bool bf16 = o.y_type == VNM_BF16, res_tma = res != nullptr && (ALIGNED || o.res_vec);
             const int box_cols = f32 ? 16 : 32;
             // the residual's box from column c on, into output box `at`, whose last store has read it; the outputs then
             // take its place
@@ -500,19 +503,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 float sum[128];
 #pragma unroll
                 for (int c = 0; c < 128; ++c) sum[c] = 0.f;
-                if constexpr (!GATED && !SPLIT) {
-                    if (from_res && m < o.T) {
-#pragma unroll
-                        for (int c = 0; c < 128; c += 8) {
-                            const Cols at{n_tile + first + c, end, 1, ALIGNED || o.res_vec};
-                            if (at.none()) continue;
-                            float v[8];
-                            widen_raw8(load_raw8(o.res[seg], o.y_type, m * o.ld_res, at), o.y_type, v);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) sum[c + j] = v[j];
-                        }
-                    }
-                }
                 const auto column = [&](int c) { return half * (GATED && !SPLIT ? 64 : 128) + c + (GATED && !SPLIT && c >= 64 ? 64 : 0); };
                 for (int kb0 = kb_first; kb0 < kb_last; kb0 += a.chunk_kb) {
                     if (!wait_sum()) break;
@@ -530,9 +520,37 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 // (the warps that share a barrier below leave there, together)
                 if (!run && !(GATED && !SPLIT && o.keep == kKeep8)) break;
                 if constexpr (!GATED && !SPLIT && ALIGNED) {
-                    if (roomy && f32 && o.act == VNM_ACT_NONE && o.bias == nullptr) {
-                        // nothing follows the sums, and the ring is free: all boxes at once
+                    if (straight) {
                         release();
+                        if (o.res[seg] != nullptr) {
+                            // its boxes come all at once to where the outputs' will be, half of them on each barrier
+                            const int64_t cols_here = min(static_cast<int64_t>(last), end - n_tile) - first;
+                            const int boxes = m0 < o.T && cols_here > 0 ? static_cast<int>(cols_here + 15) / 16 : 0;
+                            const uint32_t res_at = smem_u32(&res_bar[GATED ? 0 : warp - kPairHelpers][0]);
+                            if (lane == 0 && boxes > 0) {
+                                mbar_arrive_expect_tx(res_at, 2048 * min(boxes, 4));
+                                if (boxes > 4) mbar_arrive_expect_tx(res_at + 8, 2048 * (boxes - 4));
+                                for (int b = 0; b < boxes; ++b)
+                                    tma_load_2d(room + 2048 * b, &outs.res[seg], static_cast<int32_t>(n_tile + first + 16 * b),
+                                                static_cast<int32_t>(m0), res_at + 8 * (b >> 2));
+                            }
+                            __syncwarp();
+                            res_pending = boxes > 4 ? 3u : boxes > 0 ? 1u : 0u;
+#pragma unroll
+                            for (int c = 0; c < 128; c += 64) {
+                                if (!(res_pending >> (c / 64) & 1u)) break;
+                                if (!(run = mbar_wait_warp(res_at + c / 8, res_phase >> (c / 64) & 1u, abort))) break;
+                                res_phase ^= 1u << (c / 64);
+                                res_pending &= ~(1u << (c / 64));
+#pragma unroll
+                                for (int u = c; u < c + 64; u += 4) {
+                                    // (past the last box: sums that are not stored)
+                                    const float4 w = ld_shared_v4(box_piece<64>(room + 2048 * (u / 16), lane, u / 4 % 4));
+                                    sum[u] += w.x, sum[u + 1] += w.y, sum[u + 2] += w.z, sum[u + 3] += w.w;
+                                }
+                            }
+                            if (!run) break;
+                        }
 #pragma unroll
                         for (int c = 0; c < 128; c += 32) {
 #pragma unroll
