@@ -91,15 +91,15 @@ vnm_status vnm_testing_gated_linear_backward_skip_stage(const void* dY, int64_t 
                                                         int32_t skip_dx, int32_t skip_dw, vnm_stream_t stream);
 
 /*
- * How the dense 16-bit layers take a product with aligned 16-bit outputs on a GPU of sm_count SMs
- * (host only): tiles of *tile_tokens = 16, 32, 64 or 128 tokens with K over *splits CTAs of a cluster; 0:
- * pairs of CTAs, 256 tokens by *tile_rows rows of W, K over *splits pairs; 8: the few-token kernel.
+ * How the dense 16-bit layers take a product on a GPU of sm_count SMs (host only): tiles of *tile_tokens = 16, 32, 64 or 128
+ * tokens with K over *splits CTAs of a cluster; 0: pairs of CTAs, 256 tokens by *tile_rows rows of W, K over *splits
+ * pairs; 8: the few-token kernel.
  * kind: 0 one product (T x R over K), 1 the sum of two, 2 two side by side in rows (T each), 3 a gated
- * pair (R features).
+ * pair (R features). aligned: whether Y's rows (and an 8-bit checkpoint's) start on 16 bytes.
  * Errors: VNM_ERR_INVALID_ARG.
  */
 vnm_status vnm_testing_dense_plan(int32_t kind, int64_t T, int64_t R, int64_t K, int32_t x_transposed, int32_t w_transposed,
-                                  vnm_keep keep, int32_t sm_count, int32_t* tile_tokens, int32_t* tile_rows,
+                                  vnm_keep keep, int32_t aligned, int32_t sm_count, int32_t* tile_tokens, int32_t* tile_rows,
                                   int32_t* splits);
 
 #ifdef __cplusplus

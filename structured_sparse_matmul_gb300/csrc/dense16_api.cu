@@ -260,10 +260,10 @@ vnm_status vnm_testing_dense_linear_skip_stage(const void* X, int64_t ld_x, cons
 }
 
 vnm_status vnm_testing_dense_plan(int32_t kind, int64_t T, int64_t R, int64_t K, int32_t x_transposed, int32_t w_transposed,
-                                  vnm_keep keep, int32_t sm_count, int32_t* tile_tokens, int32_t* tile_rows,
+                                  vnm_keep keep, int32_t aligned, int32_t sm_count, int32_t* tile_tokens, int32_t* tile_rows,
                                   int32_t* splits) {
     if (kind < 0 || kind > vnm::kGatedPair || !size_ok(T) || !size_ok(R) || !size_ok(K) || T == 0 || R == 0 || K == 0 ||
-        !keep_ok(keep) || sm_count < 1 || tile_tokens == nullptr || tile_rows == nullptr || splits == nullptr)
+        !keep_ok(keep) || (aligned != 0 && aligned != 1) || sm_count < 1 || tile_tokens == nullptr || tile_rows == nullptr || splits == nullptr)
         return VNM_ERR_INVALID_ARG;
     vnm::ProductArgs p{};
     p.kind = static_cast<vnm::ProductKind>(kind);
@@ -273,6 +273,7 @@ vnm_status vnm_testing_dense_plan(int32_t kind, int64_t T, int64_t R, int64_t K,
     p.x[0].transposed = x_transposed != 0;
     p.w[0].transposed = w_transposed != 0;
     p.keep = kind_of(keep);
+    if (!aligned) p.y[0] = reinterpret_cast<void*>(2);  // (never followed)
     p.skip_stage = -1;
     const vnm::TilePlan plan = vnm::plan_product(p, sm_count);
     *tile_tokens = plan.bn;

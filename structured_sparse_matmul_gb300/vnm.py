@@ -103,7 +103,7 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.vnm_testing_dense_linear_skip_stage.argtypes = [p, i64, p, i64, dt, i64, i64, i64, p, i64, dt, p, i32, p]
     L.vnm_testing_gated_linear_skip_stage.argtypes = L.vnm_gated_linear.argtypes[:25] + [i32, p]
     L.vnm_testing_gated_linear_backward_skip_stage.argtypes = L.vnm_gated_linear_backward.argtypes[:36] + [i32, i32, p]
-    L.vnm_testing_dense_plan.argtypes = [i32, i64, i64, i64, i32, i32, dt, i32, p, p, p]
+    L.vnm_testing_dense_plan.argtypes = [i32, i64, i64, i64, i32, i32, dt, i32, i32, p, p, p]
     for name in ("vnm_sizes", "vnm_matrix_create", "vnm_matrix_destroy", "vnm_compress", "vnm_decompress",
                  "vnm_spmm", "vnm_spmm_workspace_size", "vnm_spmm_plan_query", "vnm_spmm_with_plan",
                  "vnm_get_status", "vnm_spmm_noalloc", "vnm_testing_spmm_skip_stage"):
@@ -722,11 +722,11 @@ def vnm_testing_gated_linear_backward_skip_stage(dY: torch.Tensor, X: torch.Tens
 
 
 def vnm_testing_dense_plan(kind: int, T: int, R: int, K: int, sm_count: int, x_transposed: bool = False,
-                           w_transposed: bool = False, keep: int = 0) -> Tuple[int, int, int]:
+                           w_transposed: bool = False, keep: int = 0, aligned: bool = True) -> Tuple[int, int, int]:
     """Test support: (tokens of a tile, rows of W of a pair's tile, splits of K) that the dense 16-bit
     layers take; 0 tokens: pairs of CTAs, 8: the few-token kernel; keep: 0 none, 1 in 16 bits, 2 or 3 in
-    8 (include/vnm_testing.h)."""
+    8; aligned: whether Y's rows start on 16 bytes (include/vnm_testing.h)."""
     tile, rows, splits = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
-    _check(lib().vnm_testing_dense_plan(kind, T, R, K, int(x_transposed), int(w_transposed), int(keep), sm_count,
+    _check(lib().vnm_testing_dense_plan(kind, T, R, K, int(x_transposed), int(w_transposed), int(keep), int(aligned), sm_count,
                                         ctypes.byref(tile), ctypes.byref(rows), ctypes.byref(splits)), "vnm_testing_dense_plan")
     return tile.value, rows.value, splits.value
