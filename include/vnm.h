@@ -525,9 +525,11 @@ vnm_status vnm_fp8_linear_get_status(vnm_stream_t stream);
  * row); what lies past the last column in the rows' padding is not used. A transposed
  * operand (`*_transposed` = 1) is stored with K along its columns: K x T for X, K x R for W.
  * Outputs, residuals and checkpoints may have any alignment of their type; 16-byte aligned
- * rows run faster. All sums are fp32, added in an order that the sizes alone fix (no
- * atomics), and rounded once; the tensor cores' sums truncate, so they are taken out and added up
- * every 1024 elements of K for fp32 outputs and 8-bit checkpoints, every 32768 for the others.
+ * rows run faster. All sums are fp32 and rounded once. The order of their additions is fixed by the
+ * sizes and types, which operands are transposed, how products are kept, whether the rows of Y (and of g in 8 bits)
+ * start on 16 bytes, and the GPU's number of SMs (no atomics): the same call gives the same bits. The tensor cores'
+ * sums truncate, so they are taken out and added up every 1024 elements of K for fp32 outputs and 8-bit checkpoints,
+ * every 32768 for the others.
  * status: optional device pointer to 3 zeroed int32 words (first error code, detail,
  * count): a bounded wait that runs out records VNM_ERR_TIMEOUT there (the outputs are then
  * undefined). NULL: in words that all such calls on the device share, read by
@@ -579,7 +581,8 @@ vnm_status vnm_gated_linear(const void* X, int64_t ld_x, const void* Wg, int64_t
 /*
  * Backward pass of vnm_gated_linear. dY: gradient of Y (T x F, any alignment; not needed for H alone); X, Wg, Wu as
  * there; g, u and their scales as it kept them (keep: not VNM_KEEP_NONE). With G and U as kept:
- *   dG = dY * U * act'(G), dU = dY * act(G)   (each rounded once to type, past its range to Inf: they are operands)
+ *   dG = dY * U * act'(G), dU = dY * act(G)   (each rounded once to type, past its range to Inf, in fp16
+ *   below 2^-14 to its subnormals: they are operands)
  *   dX = dG . Wg + dU . Wu                    (T x K, type)
  *   dWg = dG^T . X, dWu = dU^T . X            (F x K, of w_type: type or VNM_F32, one leading
  *                                             dimension; with accumulate = 1 added to what is there)

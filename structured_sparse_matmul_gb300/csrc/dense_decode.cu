@@ -112,6 +112,8 @@ struct Tokens {
     uint4 v[NT][2];  // of tokens g, g + 8
 };
 
+// Registers spill with 9 to 16 tokens of a gated pair: 164 bytes of stores and 192 of loads, with TAIL 552 and 520; and up to
+// 60 and 60 in the other variants with TAIL that hold two matrices or two groups of tokens.
 // NT: groups of 8 tokens. TAIL: K is no multiple of kBlockK (the code for its last block costs the others registers: 16
 // tokens, gated, 1024 x 1024 took 3.2 us without it and 3.5 with it).
 template <bool BF16, bool GATED, int NT, int kWarps, bool TAIL>

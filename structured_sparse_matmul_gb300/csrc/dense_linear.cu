@@ -23,13 +23,15 @@
 //              need no more than a residual go to the boxes straight from the registers, all of them at once (4096 x 1024
 //              over 8192 53.5 us through the loop and 48.5 so).
 // The residual is added to the whole sum. (Sums of several chunks that start from it, read under the MMAs, are rounded to
-// its spacing once a chunk: 2^24 and eight ones were 2^24. Reading it late is no slower either, us: 4096 x 1024 over 8192
-// 48.7 then and 49.2 now, 4096 x 4096 over 8192 205 and 188, 8192 x 8192 over 2048 313 and 224.)
+// its spacing once a chunk: 2^24 and eight ones were 2^24. Read late it costs a wait where nothing hides it and less
+// elsewhere, us: 2048 x 2048 over 4096 30.5 then and 34.5 now, 4096 x 1024 over 8192 48.7 and 49.2, 4096 x 4096 over 8192
+// 205 and 188, 8192 x 8192 over 2048 313 and 224.)
 // Where the outputs' rows do not start and end on 16 bytes, the boxes are copied out by the warps. With
 // few tiles, K is split over the pairs of a cluster, which copy their sums to each other at the end.
 //
 // Measured, bf16 (us; in brackets the operations at the measured rate of a library product):
-// 8192 x 4096 over 11008 with residual 390 (383), 8192 x 11008 over 4096 gated with 8-bit checkpoints 787 (766); dX of that,
+// 8192 x 4096 over 11008 with residual 387 (383), 8192 x 11008 over 4096 gated with 8-bit checkpoints 776 (766), 450 and 899 at
+// the 1500 MHz that the power cap leaves after some hundred ms; dX of that,
 // 8192 x 4096 over 2 x 11008, 784 (766), dWg and dWu 822 (766). Bound by the MMAs: a K block takes 0.285 us, theirs is 0.27.
 // Products of fewer tiles than pairs wait for L2 as well: 64 KB a pair and K block, 10.3 TB/s of all.
 //
@@ -1318,9 +1320,12 @@ cudaError_t run_narrow(int bn, const ProductArgs& p, const GemmArgs& a, int spli
 }
 
 // The times that the plan compares, in us. The constants were fitted to 218 products of random sizes (T = 9 .. 8192,
-// R = 64 .. 11008, K = 64 .. 11008, all operand orders, checkpoints or none), each timed with every plan: what the rule
-// picks is 1.6 % slower than the fastest on average, 25 % at worst; for 219 other such products 2.2 %, a few 30 %. They
-// weigh the plans against each other; the absolute times are up to a third off.
+// R = 64 .. 11008, K = 64 .. 11008, all operand orders, checkpoints or none), each timed with every plan that there was: pairs
+// of 256, 192 and 128 columns, all splits, all narrow tiles. What the rule picked was 1.6 % slower than the fastest on average,
+// 25 % at worst; for 219 other such products 2.2 %, a few 30 %, one (which now takes another plan) 82 %. Pairs of 160 and 224
+// columns came later; eleven products were timed with them, where they win by 6 % at most. The constants weigh the plans against
+// each other; the absolute times are up to a third off. `aligned` is about the starts of Y's rows and of an 8-bit G's: rows that
+// end inside 16 bytes, and a residual, U or 16-bit checkpoint off 16 bytes, take the other variant too, which the times leave out.
 TilePlan plan_tiles(const ProductArgs& p, int sm_count) {
     const bool gated = p.kind == kGatedPair, two = p.kind == kTwoByRows, keep8 = p.keep == kKeep8;
     const int64_t e = p.y_type == VNM_F32 ? 4 : 2;
