@@ -24,7 +24,7 @@
 //              over 8192 53.5 us through the loop and 48.5 so).
 // The residual is added to the whole sum. (Sums of several chunks that start from it, read under the MMAs, are rounded to
 // its spacing once a chunk: 2^24 and eight ones were 2^24. Read late it costs a wait where nothing hides it and less
-// elsewhere, us: 2048 x 2048 over 4096 30.5 then and 34.5 now, 4096 x 1024 over 8192 48.7 and 49.2, 4096 x 4096 over 8192
+// elsewhere, us: 2048 x 2048 over 2048 18.4 then and 20.6 now, 4096 x 1024 over 8192 48.7 and 49.2, 4096 x 4096 over 8192
 // 205 and 188, 8192 x 8192 over 2048 313 and 224.)
 // Where the outputs' rows do not start and end on 16 bytes, the boxes are copied out by the warps. With
 // few tiles, K is split over the pairs of a cluster, which copy their sums to each other at the end.
